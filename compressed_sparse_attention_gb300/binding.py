@@ -31,6 +31,15 @@ FLAG_BAD_SEGMENT = 0x04
 FLAG_NVIS_TOO_LARGE = 0x08
 FLAG_WAIT_TIMEOUT = 0x10
 FLAG_BAD_QUERY = 0x20
+FLAG_BAD_PAGE = 0x40
+FLAG_OUT_OF_PAGES = 0x80
+FLAG_BAD_SEQ = 0x100
+
+DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # csa2_dtype
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}  # csa2_rope_layout
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}  # csa2_rope_scaling
+ROPE_MAX_PAIRS = 256
+PAGE_ARRAYS_MAX = 128
 
 
 class Csa2Error(RuntimeError):
@@ -68,6 +77,26 @@ class StepArgs(C.Structure):
                 ("workspace", C.c_void_p), ("workspace_bytes", C.c_size_t),
                 ("append", C.c_int32), ("state_raw", C.c_void_p), ("state_gate", C.c_void_p),
                 ("cand_role", C.c_int32), ("cand", C.c_void_p)]
+
+
+class PagedKVArgs(C.Structure):
+    _fields_ = [("pages", C.c_void_p), ("scales", C.c_void_p), ("page_stride", C.c_int64),
+                ("scale_stride", C.c_int64), ("table", C.c_void_p), ("table_ld", C.c_int64), ("max_pages", C.c_int32),
+                ("n_pages", C.c_int32), ("page_size", C.c_int32), ("n_seq", C.c_int32)]
+
+
+class PagePoolArgs(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("table_ld", C.c_int64), ("seq_len", C.c_void_p), ("ref", C.c_void_p),
+                ("max_pages", C.c_int32), ("n_pages", C.c_int32), ("page_size", C.c_int32), ("n_seq", C.c_int32)]
+
+
+class PageArray(C.Structure):
+    _fields_ = [("base", C.c_void_p), ("page_stride", C.c_int64), ("row_bytes", C.c_int32), ("reserved", C.c_int32)]
+
+
+class RopeTable(C.Structure):
+    _fields_ = [("rope_dim", C.c_int32), ("offset", C.c_int32), ("layout", C.c_int32), ("reserved", C.c_int32),
+                ("amplitude", C.c_double), ("freq", C.c_double * ROPE_MAX_PAIRS)]
 
 
 # name -> (restype, argtypes); every symbol include/csa2.h declares
@@ -126,6 +155,26 @@ SIGNATURES = {
                                       C.c_void_p, C.c_void_p, C.c_void_p]),
     "csa2_attend_combine": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p,
                                       C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
+    "csa2_attend_paged_workspace_size": (C.c_size_t, [C.c_void_p, C.c_int32]),
+    "csa2_attend_paged": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(PagedKVArgs), C.c_int32, C.c_void_p, C.c_void_p,
+                                    C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p, C.c_void_p,
+                                    C.c_void_p, C.c_size_t]),
+    "csa2_append_paged": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(PagedKVArgs), C.c_int32, C.c_void_p, C.c_int64,
+                                    C.c_void_p, C.c_void_p]),
+    "csa2_pages_workspace_size": (C.c_size_t, [C.c_void_p, C.POINTER(PagePoolArgs)]),
+    "csa2_pages_extend": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(PagePoolArgs), C.c_int32, C.c_void_p, C.c_void_p,
+                                    C.c_void_p, C.c_size_t]),
+    "csa2_pages_fork": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(PagePoolArgs), C.c_int32, C.c_void_p, C.c_void_p,
+                                  C.c_int32, C.c_int32, C.POINTER(PageArray), C.c_void_p, C.c_size_t]),
+    "csa2_pages_free": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(PagePoolArgs), C.c_int32, C.c_void_p]),
+    "csa2_pages_trim": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(PagePoolArgs), C.c_int32, C.c_void_p, C.c_int64,
+                                  C.c_int64, C.c_void_p]),
+    "csa2_pages_compact": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(PagePoolArgs), C.c_int32, C.POINTER(PageArray),
+                                     C.c_void_p, C.c_void_p, C.c_size_t]),
+    "csa2_rope_table_init": (C.c_int, [C.POINTER(RopeTable), C.c_int32, C.c_int32, C.c_int32, C.c_double, C.c_int32,
+                                       C.c_double, C.c_double, C.c_double, C.c_double, C.c_double]),
+    "csa2_rope": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(RopeTable), C.c_int32, C.c_int64, C.c_int32, C.c_int32,
+                            C.c_void_p, C.c_int64, C.c_int64, C.c_void_p, C.c_void_p, C.c_int64, C.c_int64, C.c_int32]),
     "csa2_attend_noalloc": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p,
                                       C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
                                       C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p]),
@@ -163,6 +212,19 @@ def default_config(**overrides) -> Config:
             v = {"bf16": KV_BF16, "fp8": KV_FP8, "fp4": KV_FP4, "mxfp4": KV_MXFP4}[v]
         setattr(cfg, k, v)
     return cfg
+
+
+def rope_table(rope_dim, theta=10000.0, layout="interleaved", offset=0, scaling="none", factor=1.0, orig_len=65536.0,
+               beta_fast=32.0, beta_slow=1.0, amplitude=1.0) -> RopeTable:
+    """The frequencies of csa2_rope (csa2_rope_table_init), made once and kept
+    by the caller: `layout` "interleaved" or "half", `scaling` "none",
+    "linear", "ntk" or "yarn", on the channels offset .. offset + rope_dim - 1."""
+    tab = RopeTable()
+    st = load_library().csa2_rope_table_init(C.byref(tab), rope_dim, offset, ROPE_LAYOUTS[layout], theta,
+                                             ROPE_SCALINGS[scaling], factor, orig_len, beta_fast, beta_slow, amplitude)
+    if st != CSA2_OK:
+        raise Csa2Error(st, "csa2_rope_table_init")
+    return tab
 
 
 def _stream() -> int:
@@ -373,6 +435,199 @@ class Context:
             self._p(q_pos, torch.int64, "q_pos"), self._p(sink, torch.float32, "sink"),
             self._p(out, torch.bfloat16, "out"), self._p(lse, torch.float32, "lse")), "csa2_attend_combine")
 
+    # -- paged caches (csa2_attend_paged .. csa2_pages_compact) and csa2_rope
+    #
+    # Each has a prepare_ form that checks the tensors and builds the argument
+    # block once, for a serving loop that reuses its buffers: every
+    # PreparedCall.run() is then a single C call on the current stream. Tensors
+    # are the caller's; a PreparedCall keeps them alive.
+
+    def _strided(self, t, dtype, name):
+        """Pointer and row stride (elements) of a 2-D tensor whose rows are contiguous."""
+        if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+            raise ValueError(f"{name} must be 2-D with contiguous rows")
+        if t.device != self.device or t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype} on {self.device}, is {t.dtype} on {t.device}")
+        return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+    def _page_array(self, t, name):
+        """(pointer, page stride in bytes, row bytes) of [n_pages, page_size, ...] pages, contiguous inside a page."""
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}, is on {t.device}")
+        if t.dim() < 2 or not t[:1].is_contiguous():
+            raise ValueError(f"{name} must be [n_pages, page_size, ...], contiguous inside a page")
+        size = t.element_size()
+        inner = t.shape[1:].numel()
+        stride = t.stride(0) if t.shape[0] > 1 else inner
+        if stride < inner:
+            raise ValueError(f"{name}: pages overlap")
+        return t.data_ptr(), stride * size, inner // max(1, t.shape[1]) * size
+
+    def paged_kv(self, pages, table, scales=None) -> "PagedKV":
+        """A cache in pages: `pages` [n_pages, page_size, 512] bf16, or uint8
+        codes [.., 512] (fp8) / [.., 256] (fp4) with uint8 `scales` [n_pages,
+        page_size, 16 / 32] (the page axis may be strided: pages of several
+        layers side by side); `table` int32 [n_seq, max_pages], the page of
+        each run of page_size positions, -1 for none."""
+        fmt = self.cfg.kv_format
+        dtype, width, sw = {KV_BF16: (torch.bfloat16, 512, 0), KV_FP8: (torch.uint8, 512, 16),
+                            KV_FP4: (torch.uint8, 256, 32)}[fmt]
+        if pages.dim() != 3 or pages.shape[2] != width or pages.dtype != dtype:
+            raise ValueError(f"pages must be {dtype} [n_pages, page_size, {width}] in this context's format")
+        a = PagedKVArgs()
+        a.pages, a.page_stride, _ = self._page_array(pages, "pages")
+        if sw:
+            if scales is None or scales.dtype != torch.uint8 or tuple(scales.shape) != (*pages.shape[:2], sw):
+                raise ValueError(f"scales must be uint8 [n_pages, page_size, {sw}]")
+            a.scales, a.scale_stride, _ = self._page_array(scales, "scales")
+        a.table, a.table_ld = self._strided(table, torch.int32, "table")
+        a.n_seq, a.max_pages = table.shape
+        a.n_pages, a.page_size = pages.shape[:2]
+        return PagedKV(a, (pages, scales, table))
+
+    def attend_paged_workspace_size(self, n_query) -> int:
+        return int(self.lib.csa2_attend_paged_workspace_size(self.h, n_query))
+
+    def prepare_attend_paged(self, kv: "PagedKV", q, q_pos, seq_of_q, out, workspace, *, sink=None, lse=None, lo=None,
+                             window=0, n_first=0) -> "PreparedCall":
+        n = q.shape[0]
+        self._shape(q, (n, 64, 512), "q")
+        self._shape(out, (n, 64, 512), "out")
+        self._shape(q_pos, (n,), "q_pos")
+        self._shape(seq_of_q, (n,), "seq_of_q")
+        self._shape(sink, (64,), "sink")
+        self._shape(lse, (n, 64), "lse")
+        self._shape(lo, (kv.args.n_seq,), "lo")
+        return PreparedCall(self, "csa2_attend_paged", (
+            C.byref(kv.args), n, self._p(q, torch.bfloat16, "q"), self._p(q_pos, torch.int64, "q_pos"),
+            self._p(seq_of_q, torch.int32, "seq_of_q"), self._p(lo, torch.int64, "lo"), int(window), int(n_first),
+            self._p(sink, torch.float32, "sink"), self._p(out, torch.bfloat16, "out"),
+            self._p(lse, torch.float32, "lse"), self._p(workspace, None, "workspace"),
+            0 if workspace is None else workspace.numel() * workspace.element_size()),
+            (kv, q, q_pos, seq_of_q, out, workspace, sink, lse, lo))
+
+    def attend_paged(self, kv, q, q_pos, seq_of_q, out, workspace, **kw):
+        """csa2_attend_paged: every visible row of a paged cache (`window` 0), or
+        the last `window` rows and the first `n_first`."""
+        self.prepare_attend_paged(kv, q, q_pos, seq_of_q, out, workspace, **kw).run()
+
+    def prepare_append_paged(self, kv: "PagedKV", rows, tok_off, first_pos) -> "PreparedCall":
+        self._shape(rows, (rows.shape[0], 512), "rows")
+        self._shape(tok_off, (kv.args.n_seq + 1,), "tok_off")
+        self._shape(first_pos, (kv.args.n_seq,), "first_pos")
+        return PreparedCall(self, "csa2_append_paged", (
+            C.byref(kv.args), DTYPE_CODES.get(rows.dtype, -1), self._p(rows, (torch.bfloat16, torch.float32), "rows"),
+            rows.shape[0], self._p(tok_off, torch.int64, "tok_off"), self._p(first_pos, torch.int64, "first_pos")),
+            (kv, rows, tok_off, first_pos))
+
+    def append_paged(self, kv, rows, tok_off, first_pos):
+        """csa2_append_paged: rows [n, 512] rotated at their positions and stored in their pages."""
+        self.prepare_append_paged(kv, rows, tok_off, first_pos).run()
+
+    def page_pool(self, table, seq_len, ref, page_size) -> "PagePool":
+        """The state of the page operations: `table` int32 [n_seq, max_pages],
+        `seq_len` int64 [n_seq], `ref` int32 [n_pages] (table entries naming
+        each page)."""
+        a = PagePoolArgs()
+        a.table, a.table_ld = self._strided(table, torch.int32, "table")
+        a.n_seq, a.max_pages = table.shape
+        self._shape(seq_len, (a.n_seq,), "seq_len")
+        a.seq_len = self._p(seq_len, torch.int64, "seq_len")
+        a.ref = self._p(ref, torch.int32, "ref")
+        a.n_pages, a.page_size = ref.numel(), page_size
+        return PagePool(a, (table, seq_len, ref))
+
+    def pages_workspace_size(self, pool: "PagePool") -> int:
+        return int(self.lib.csa2_pages_workspace_size(self.h, C.byref(pool.args)))
+
+    def _page_arrays(self, pool, arrays):
+        c = (PageArray * max(1, len(arrays)))()
+        for i, t in enumerate(arrays):
+            if t.dim() < 2 or t.shape[0] != pool.args.n_pages or t.shape[1] != pool.args.page_size:
+                raise ValueError(f"arrays[{i}] must be [{pool.args.n_pages}, {pool.args.page_size}, ...]")
+            c[i].base, c[i].page_stride, c[i].row_bytes = self._page_array(t, f"arrays[{i}]")
+        return c
+
+    def _ws(self, workspace):
+        return self._p(workspace, None, "workspace"), (0 if workspace is None else
+                                                       workspace.numel() * workspace.element_size())
+
+    def prepare_pages_extend(self, pool, seqs, new_len, workspace) -> "PreparedCall":
+        self._shape(new_len, (seqs.shape[0],), "new_len")
+        return PreparedCall(self, "csa2_pages_extend", (
+            C.byref(pool.args), seqs.shape[0], self._p(seqs, torch.int32, "seqs"),
+            self._p(new_len, torch.int64, "new_len"), *self._ws(workspace)), (pool, seqs, new_len, workspace))
+
+    def pages_extend(self, pool, seqs, new_len, workspace):
+        """csa2_pages_extend: sequences grow to new_len tokens, fresh pages where they lack them."""
+        self.prepare_pages_extend(pool, seqs, new_len, workspace).run()
+
+    def prepare_pages_fork(self, pool, parents, children, arrays, workspace, deep=False) -> "PreparedCall":
+        self._shape(children, (parents.shape[0],), "children")
+        c = self._page_arrays(pool, arrays)
+        return PreparedCall(self, "csa2_pages_fork", (
+            C.byref(pool.args), parents.shape[0], self._p(parents, torch.int32, "parents"),
+            self._p(children, torch.int32, "children"), 1 if deep else 0, len(arrays), c, *self._ws(workspace)),
+            (pool, parents, children, tuple(arrays), c, workspace))
+
+    def pages_fork(self, pool, parents, children, arrays, workspace, deep=False):
+        """csa2_pages_fork: children become copies of parents, sharing their full pages (`deep`: none)."""
+        self.prepare_pages_fork(pool, parents, children, arrays, workspace, deep).run()
+
+    def prepare_pages_free(self, pool, seqs) -> "PreparedCall":
+        return PreparedCall(self, "csa2_pages_free", (C.byref(pool.args), seqs.shape[0],
+                                                      self._p(seqs, torch.int32, "seqs")), (pool, seqs))
+
+    def pages_free(self, pool, seqs):
+        """csa2_pages_free: every page of the sequences given back."""
+        self.prepare_pages_free(pool, seqs).run()
+
+    def prepare_pages_trim(self, pool, seqs, window, n_first=0, lo=None) -> "PreparedCall":
+        self._shape(lo, (pool.args.n_seq,), "lo")
+        return PreparedCall(self, "csa2_pages_trim", (
+            C.byref(pool.args), seqs.shape[0], self._p(seqs, torch.int32, "seqs"), int(window), int(n_first),
+            self._p(lo, torch.int64, "lo")), (pool, seqs, lo))
+
+    def pages_trim(self, pool, seqs, window, n_first=0, lo=None):
+        """csa2_pages_trim: the pages no later query sees under the window given back."""
+        self.prepare_pages_trim(pool, seqs, window, n_first, lo).run()
+
+    def prepare_pages_compact(self, pool, arrays, n_live, workspace) -> "PreparedCall":
+        c = self._page_arrays(pool, arrays)
+        self._shape(n_live, (1,), "n_live")
+        return PreparedCall(self, "csa2_pages_compact", (
+            C.byref(pool.args), len(arrays), c, self._p(n_live, torch.int32, "n_live"), *self._ws(workspace)),
+            (pool, tuple(arrays), c, n_live, workspace))
+
+    def pages_compact(self, pool, arrays, n_live, workspace):
+        """csa2_pages_compact: the pages in use moved to the lowest indices; n_live (nullable) receives their number."""
+        self.prepare_pages_compact(pool, arrays, n_live, workspace).run()
+
+    def prepare_rope(self, table: RopeTable, x, pos, out=None, transpose=False) -> "PreparedCall":
+        out = x if out is None else out
+        for t, name in ((x, "x"), (out, "out")):
+            if t.dim() != 3 or (t.shape[2] > 1 and t.stride(2) != 1):
+                raise ValueError(f"{name} must be [n_tokens, n_heads, head_dim] with contiguous channels")
+            if t.device != self.device or t.dtype != x.dtype or t.shape != x.shape:
+                raise ValueError(f"{name} must be {tuple(x.shape)} {x.dtype} on {self.device}")
+        if x.dtype not in DTYPE_CODES:
+            raise TypeError(f"x must be bf16, fp16 or fp32, is {x.dtype}")
+        self._shape(pos, (x.shape[0],), "pos")
+        return PreparedCall(self, "csa2_rope", (
+            C.byref(table), DTYPE_CODES[x.dtype], *x.shape, x.data_ptr(), x.stride(0), x.stride(1),
+            self._p(pos, torch.int64, "pos"), out.data_ptr(), out.stride(0), out.stride(1), 1 if transpose else 0),
+            (table, x, pos, out))
+
+    def rope(self, table, x, pos, out=None, transpose=False):
+        """csa2_rope: x [n_tokens, n_heads, head_dim] rotated at pos into out (in
+        place without one); `transpose` rotates back (the gradient's direction)."""
+        self.prepare_rope(table, x, pos, out, transpose).run()
+
+    @staticmethod
+    def _shape(t, shape, name):
+        if t is not None and tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {tuple(shape)}, is {tuple(t.shape)}")
+
     def step_workspace_size(self, n_query, max_vis) -> int:
         return int(self.lib.csa2_step_workspace_size(self.h, n_query, max_vis))
 
@@ -427,6 +682,37 @@ class Context:
         a.cand_role = cand_role
         a.cand = self._p(cand, torch.int32, "cand")
         return a
+
+
+class PagedKV:
+    """A csa2_paged_kv block kept alive with the tensors it points at."""
+
+    def __init__(self, args: PagedKVArgs, tensors):
+        self.args, self._keep = args, tensors
+
+
+class PagePool:
+    """A csa2_page_pool block kept alive with the tensors it points at."""
+
+    def __init__(self, args: PagePoolArgs, tensors):
+        self.args, self._keep = args, tensors
+
+
+class PreparedCall:
+    """One entry point's arguments, checked and converted once; each run()
+    enqueues the call on the current stream."""
+
+    def __init__(self, ctx: Context, name: str, args: tuple, tensors):
+        self.ctx, self.name, self._keep = ctx, name, tensors
+        self._fn = getattr(ctx.lib, name)
+        types = SIGNATURES[name][1]
+        conv = [C.c_void_p, C.c_int32, C.c_int64, C.c_size_t]
+        self._args = tuple(t(a) if t in conv and not isinstance(a, t) else a for t, a in zip(types[2:], args))
+
+    def run(self):
+        st = self._fn(self.ctx.h, _stream(), *self._args)
+        if st != CSA2_OK:
+            self.ctx._ok(st, self.name)
 
 
 class PreparedStep:

@@ -28,21 +28,24 @@ __device__ __forceinline__ void set_flag(uint32_t* flags, uint32_t bit) {
   if (flags) atomicOr(flags, bit);
 }
 
-// cos / sin of pos * f_i. The angle is formed in double precision and reduced
-// to [-pi, pi] by Cody-Waite reduction with a two-term 2*pi (high part + the
-// rounding remainder), both products fused; the reduced angle then goes to
+// cos / sin of an angle formed in double precision, reduced to [-pi, pi] by
+// Cody-Waite reduction with a two-term 2*pi (high part + the rounding
+// remainder), both products fused; the reduced angle then goes to
 // single-precision sincosf. The reduction error is ~1e-16 * |angle / 2pi|
 // radians, so the result is the correctly rotated float to about 1e-7 even at
 // positions near 2^20, at a few double operations instead of a double sincos.
-__device__ __forceinline__ void rope_cs(const RopeParams& rp, int i, int64_t pos, float& c, float& s) {
+__device__ __forceinline__ void angle_cs(double a, float& c, float& s) {
   constexpr double kTwoPiHi = 6.283185307179586232;     // nearest double to 2*pi
   constexpr double kTwoPiLo = 2.4492935982947064e-16;   // 2*pi - kTwoPiHi
   constexpr double kInvTwoPi = 0.15915494309189533577;
-  const double a = (double)pos * rp.freq[i];
   const double k = rint(a * kInvTwoPi);
   double r = fma(-k, kTwoPiHi, a);
   r = fma(-k, kTwoPiLo, r);
   sincosf((float)r, &s, &c);
+}
+// cos / sin of pos * f_i
+__device__ __forceinline__ void rope_cs(const RopeParams& rp, int i, int64_t pos, float& c, float& s) {
+  angle_cs((double)pos * rp.freq[i], c, s);
 }
 
 // ---------------------------------------------------------------- bf16 packing

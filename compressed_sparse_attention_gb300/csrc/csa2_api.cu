@@ -9,6 +9,32 @@
 #include "ctx.cuh"
 #include "launchers.cuh"
 
+namespace csa2 {
+
+// YaRN ("NTK-by-parts", DeepSeek-V3 ramp) frequencies of the rotated pairs.
+void rope_frequencies(int rope_dim, double theta, double factor, double orig_len, double beta_fast, double beta_slow,
+                      double* f) {
+  const int half = rope_dim / 2;
+  for (int i = 0; i < half; ++i) f[i] = std::pow(theta, -(2.0 * i) / rope_dim);
+  if (!(factor > 1.0)) return;
+  auto boundary = [&](double turns) {
+    return rope_dim * std::log(orig_len / (turns * 2.0 * M_PI)) / (2.0 * std::log(theta));
+  };
+  double lo = std::floor(boundary(beta_fast));
+  double hi = std::ceil(boundary(beta_slow));
+  if (lo < 0) lo = 0;
+  if (hi > rope_dim - 1) hi = rope_dim - 1;
+  if (hi == lo) hi += 0.001;
+  for (int i = 0; i < half; ++i) {
+    double ramp = (i - lo) / (hi - lo);
+    ramp = ramp < 0 ? 0 : (ramp > 1 ? 1 : ramp);
+    // ramp 0 keeps the frequency, 1 divides it by the factor
+    f[i] = f[i] * (1.0 - ramp) + f[i] / factor * ramp;
+  }
+}
+
+}  // namespace csa2
+
 namespace {
 
 constexpr size_t kAlign = 256;
@@ -21,27 +47,6 @@ csa2_status fail(csa2_ctx* c, csa2_status s, const std::string& msg) {
 
 csa2_status cuda_fail(csa2_ctx* c, cudaError_t e, const char* where) {
   return fail(c, CSA2_ERR_CUDA, std::string(where) + ": " + cudaGetErrorString(e));
-}
-
-// YaRN ("NTK-by-parts", DeepSeek-V3 ramp) frequencies of the rotated pairs.
-void rope_frequencies(const csa2_config& c, double* f) {
-  const int half = c.rope_dim / 2;
-  for (int i = 0; i < half; ++i) f[i] = std::pow(c.rope_theta, -(2.0 * i) / c.rope_dim);
-  if (!(c.yarn_factor > 1.0)) return;
-  auto boundary = [&](double turns) {
-    return c.rope_dim * std::log(c.yarn_orig_len / (turns * 2.0 * M_PI)) / (2.0 * std::log(c.rope_theta));
-  };
-  double lo = std::floor(boundary(c.yarn_beta_fast));
-  double hi = std::ceil(boundary(c.yarn_beta_slow));
-  if (lo < 0) lo = 0;
-  if (hi > c.rope_dim - 1) hi = c.rope_dim - 1;
-  if (hi == lo) hi += 0.001;
-  for (int i = 0; i < half; ++i) {
-    double ramp = (i - lo) / (hi - lo);
-    ramp = ramp < 0 ? 0 : (ramp > 1 ? 1 : ramp);
-    // ramp 0 keeps the frequency, 1 divides it by the factor
-    f[i] = f[i] * (1.0 - ramp) + f[i] / c.yarn_factor * ramp;
-  }
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -159,7 +164,8 @@ csa2_status csa2_create(const csa2_config* cfg, csa2_ctx** out) {
   }
   std::memset(&ctx->rope, 0, sizeof(ctx->rope));
   ctx->rope.pairs = c.rope_dim / 2;
-  rope_frequencies(c, ctx->rope.freq);
+  csa2::rope_frequencies(c.rope_dim, c.rope_theta, c.yarn_factor, c.yarn_orig_len, c.yarn_beta_fast, c.yarn_beta_slow,
+                         ctx->rope.freq);
   *out = ctx;
   return CSA2_OK;
 }

@@ -7,6 +7,7 @@
 // from the unrotated latent; the latent is rotated at its group's first token
 // position j*m before it is stored).
 #include "launchers.cuh"
+#include "row_store.cuh"
 
 namespace csa2 {
 
@@ -44,53 +45,8 @@ __global__ void __launch_bounds__(256) store_rows_kernel(const float* __restrict
       }
     }
   }
-  if constexpr (FMT == 0) {
-    uint32_t w[E / 2];
-#pragma unroll
-    for (int k = 0; k < E / 2; ++k) w[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
-    uint2* dst = reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(out) + row * DIM + lane * E);
-#pragma unroll
-    for (int k = 0; k < E / 4; ++k) dst[k] = make_uint2(w[2 * k], w[2 * k + 1]);
-  } else if constexpr (FMT == 1) {
-    constexpr int LPB = 32 / E;  // lanes per 32-channel block
-    float amax = 0.f;
-#pragma unroll
-    for (int k = 0; k < E; ++k) amax = fmaxf(amax, fabsf(v[k]));
-#pragma unroll
-    for (int o = 1; o < LPB; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const uint32_t eb = fp8_scale_byte(amax);
-    const int sh = 127 - (int)eb;  // x / 2^(eb-127), exact
-    uint8_t* dst = reinterpret_cast<uint8_t*>(out) + row * DIM + lane * E;
-#pragma unroll
-    for (int k = 0; k < E; k += 4) {
-      uint32_t word = 0;
-#pragma unroll
-      for (int u = 0; u < 4; ++u) word |= (uint32_t)f32_to_e4m3(ldexpf(v[k + u], sh)) << (8 * u);
-      *reinterpret_cast<uint32_t*>(dst + k) = word;
-    }
-    if ((lane % LPB) == 0) out_scale[row * (DIM / 32) + lane / LPB] = (uint8_t)eb;
-  } else {
-    constexpr int BLK = (FMT == 2) ? 16 : 32;  // channels per scale
-    constexpr int LPB = (BLK / E) > 0 ? BLK / E : 1;  // lanes per block
-    float amax = 0.f;
-#pragma unroll
-    for (int k = 0; k < E; ++k) amax = fmaxf(amax, fabsf(v[k]));
-#pragma unroll
-    for (int o = 1; o < LPB; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    float sc;
-    uint32_t sbyte;
-    if constexpr (FMT == 2) {
-      sbyte = fp4_scale_e4m3(amax);
-      sc = e4m3_value(sbyte);
-    } else {
-      sbyte = mxfp4_scale_byte(amax);
-      sc = ue8m0_value(sbyte);
-    }
-    uint8_t* dst = reinterpret_cast<uint8_t*>(out) + row * (DIM / 2) + lane * (E / 2);
-#pragma unroll
-    for (int k = 0; k < E; k += 2) dst[k / 2] = (uint8_t)(e2m1_code(v[k], sc) | (e2m1_code(v[k + 1], sc) << 4));
-    if ((lane % LPB) == 0) out_scale[row * (DIM / BLK) + lane / LPB] = (uint8_t)sbyte;
-  }
+  store_row<DIM, FMT>(v, lane, reinterpret_cast<uint8_t*>(out) + row * row_code_bytes(DIM, FMT),
+                      out_scale + row * row_scale_bytes(DIM, FMT));
 }
 
 // ---------------------------------------------------------------------------

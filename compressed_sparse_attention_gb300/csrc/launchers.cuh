@@ -2,6 +2,8 @@
 // code (not part of the public interface).
 #pragma once
 #include "common.cuh"
+#include "paged.cuh"
+#include "pages.cuh"
 
 namespace csa2 {
 
@@ -211,5 +213,30 @@ cudaError_t launch_topk_merge(cudaStream_t st, int n_query, int n_lists, int k_i
                               const int32_t* pair_idx, int k, int32_t* out_idx, int* n_launch);
 // one CTA waiting on an mbarrier nothing arrives at, for limit_ns (csa2_debug_wait_timeout)
 cudaError_t launch_wait_probe(cudaStream_t st, uint32_t* flags, uint64_t limit_ns);
+
+// paged caches (csa2_attend_paged, csa2_append_paged, csa2_pages_*)
+size_t attend_paged_workspace_bytes(int num_sms);
+cudaError_t launch_attend_paged(cudaStream_t st, int num_sms, int kv_fmt, AttendParams a, const PagedView& kv,
+                                const int64_t* lo, int64_t window, int64_t n_first, void* ws, int* n_launch);
+cudaError_t launch_append_paged(cudaStream_t st, int dtype, const void* rows, int64_t n_rows, int n_seq,
+                                const int64_t* tok_off, const int64_t* first_pos, const PagedView& kv, int kv_fmt,
+                                const RopeParams& rp, uint32_t* flags);
+size_t pages_workspace_bytes(int n_seq, int n_pages);
+cudaError_t launch_pages_extend(cudaStream_t st, const PagePool& P, int n, const int32_t* seqs, const int64_t* new_len,
+                                void* ws);
+cudaError_t launch_pages_fork(cudaStream_t st, int num_sms, const PagePool& P, int n, const int32_t* parents,
+                              const int32_t* children, bool deep, const PageArrays& A, void* ws);
+// window < 0: every page; otherwise the pages outside the window and the first tokens
+cudaError_t launch_pages_free(cudaStream_t st, const PagePool& P, int n, const int32_t* seqs, int64_t window,
+                              int64_t n_first, const int64_t* lo);
+cudaError_t launch_pages_compact(cudaStream_t st, int num_sms, const PagePool& P, const PageArrays& A, int32_t* n_live,
+                                 void* ws);
+// rotary positions (csa2_rope); strides in elements
+cudaError_t launch_rope(cudaStream_t st, int num_sms, const csa2_rope_table& tab, int dtype, const void* x, void* out,
+                        const int64_t* pos, int64_t n_tok, int n_heads, int head_dim, int64_t x_tok, int64_t x_head,
+                        int64_t o_tok, int64_t o_head, bool transpose, bool in_place, int* n_launch);
+// frequencies of rope_dim / 2 pairs (host); factor <= 1: no ramp
+void rope_frequencies(int rope_dim, double theta, double factor, double orig_len, double beta_fast, double beta_slow,
+                      double* f);
 
 }  // namespace csa2

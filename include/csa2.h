@@ -93,6 +93,11 @@ typedef enum csa2_kv_format {
 #define CSA2_FLAG_NVIS_TOO_LARGE   0x08u /* n_vis larger than the sequence's pool   */
 #define CSA2_FLAG_WAIT_TIMEOUT     0x10u /* a bounded mbarrier wait gave up         */
 #define CSA2_FLAG_BAD_QUERY        0x20u /* seq_of_q outside [0, n_seq)             */
+#define CSA2_FLAG_BAD_PAGE         0x40u /* a needed table entry outside [0, n_pages),
+                                            or more references than counted         */
+#define CSA2_FLAG_OUT_OF_PAGES     0x80u /* an entry refused: not enough free pages  */
+#define CSA2_FLAG_BAD_SEQ          0x100u /* an entry refused: sequence out of range,
+                                            named twice, or of the wrong length      */
 
 /* Geometry and numerics of one CSA2 layer ("DeepSeek-V4.1-Flash on WASTE",
  * section "The shape"; PocketLLM page, geometry table). Supported values:
@@ -571,6 +576,201 @@ csa2_status csa2_attend_noalloc(csa2_ctx* ctx, void* stream, int32_t n_seq, int3
                                 const uint8_t* win_scale, const int64_t* win_off, const int64_t* win_lo,
                                 const void* pool_kv, const uint8_t* pool_scale, const int64_t* pool_off,
                                 const int32_t* topk_idx, const float* sink, uint16_t* out, float* lse);
+
+/* ------------------------------------------------------------------------
+ * Paged caches: rows of the attention formats kept in pages of a shared pool
+ * instead of one packed run a sequence, so that sequences can grow, share
+ * their common beginning and be moved. An engineering addition with no
+ * counterpart in the method's description; the attention formula, the RoPE and
+ * the row formats are csa2_attend's and csa2_store_rows'.
+ *
+ * csa2_paged_kv (host struct): row r of page g has its codes at pages + g *
+ * page_stride + r * row bytes (kv_format: 1024 / 512 / 256) and its scales at
+ * scales + g * scale_stride + r * scale bytes (- / 16 / 32; every row of an
+ * fp4 cache is fp4, no fp8 window). Position p of sequence b is row p mod
+ * page_size of page table[b * table_ld + p / page_size].
+ *   page_size    rows a page, a power of two 1..4096
+ *   page_stride  bytes, a multiple of 16 and at least a page's codes (larger
+ *                for pages of several layers side by side); scale_stride the
+ *                same for the scales, a multiple of 16 (0 for bf16)
+ *   table        [n_seq, table_ld] int32 on the device, max_pages <= table_ld
+ *                columns in use; max_pages * page_size <= 2^30
+ * A table entry outside [0, n_pages) holds no rows. */
+typedef struct csa2_paged_kv {
+  void* pages;
+  uint8_t* scales;
+  int64_t page_stride;
+  int64_t scale_stride;
+  const int32_t* table;
+  int64_t table_ld;
+  int32_t max_pages;
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t n_seq;
+} csa2_paged_kv;
+
+/* csa2_attend_paged: for each query i at t = q_pos[i] of b = seq_of_q[i], per
+ * head: one softmax with the sink over the rows at the visible positions p of
+ * sequence b, with lo_b <= p <= t and (window == 0, or p > t - window, or
+ * p < lo_b + n_first); q rotated at t, the output's rope channels rotated back
+ * (formula as for csa2_attend; rows are stored rotated, as csa2_append_paged
+ * leaves them). Decode queries (one or a few a sequence) and prompt chunks
+ * (every token a query) alike; no row need exist past t.
+ *   q [n_query, 64, 512] bf16 (unrotated); q_pos [n_query] int64;
+ *   seq_of_q [n_query] int32, -1: a padding query, whose out and lse stay as
+ *     they are; another value outside [0, n_seq), or q_pos < -1, is recorded as
+ *     CSA2_FLAG_BAD_QUERY and its output is zero
+ *   lo [n_seq] int64 (nullable: 0) first position that counts (left padding)
+ *   window >= 0, n_first >= 0 (read only when window > 0)
+ *   sink [64] fp32 (nullable: none); out [n_query, 64, 512] bf16; lse
+ *     [n_query, 64] fp32 natural-log denominator (nullable)
+ * A query that sees no row (q_pos -1, or t < lo_b) gives 0, lse = the sink (-inf
+ * without one). A visible row whose page is missing is left out and recorded
+ * as CSA2_FLAG_BAD_PAGE. The denominator sums fp32 weights, the products take
+ * them rounded to bf16; partials of split sequences are fp32.
+ * The result does not depend on timing. Two launches for every 4,096 queries.
+ *   workspace of csa2_attend_paged_workspace_size bytes (whatever the number
+ *   of queries); calls that may overlap on the GPU need one each
+ * q, pages, scales and out must be 16-byte aligned. */
+size_t csa2_attend_paged_workspace_size(const csa2_ctx* ctx, int32_t n_query);
+csa2_status csa2_attend_paged(csa2_ctx* ctx, void* stream, const csa2_paged_kv* kv, int32_t n_query, const uint16_t* q,
+                              const int64_t* q_pos, const int32_t* seq_of_q, const int64_t* lo, int64_t window,
+                              int64_t n_first, const float* sink, uint16_t* out, float* lse, void* workspace,
+                              size_t workspace_bytes);
+
+/* Element types of the operators that take more than one. */
+typedef enum csa2_dtype { CSA2_DTYPE_BF16 = 0, CSA2_DTYPE_FP16 = 1, CSA2_DTYPE_FP32 = 2 } csa2_dtype;
+
+/* csa2_append_paged: new rows rotated at their positions with the context's
+ * RoPE and stored in kv_format where the table says (csa2_store_rows' rounding).
+ *   rows      [n_tokens, 512] bf16 or fp32 (dtype), sequences packed by
+ *   tok_off   [n_seq + 1] int64 (n_seq = kv->n_seq; any counts; rows at or
+ *             past tok_off[n_seq] are not stored)
+ *   first_pos [n_seq] int64 position of sequence b's first row; the others follow
+ * A row whose position has no page is skipped and recorded as
+ * CSA2_FLAG_BAD_PAGE. Two sequences must not append into a page they share.
+ * rows 16-byte aligned. One launch. */
+csa2_status csa2_append_paged(csa2_ctx* ctx, void* stream, const csa2_paged_kv* kv, int32_t dtype, const void* rows,
+                              int64_t n_tokens, const int64_t* tok_off, const int64_t* first_pos);
+
+/* csa2_page_pool (host struct): the state the page operations work on, all of
+ * it the caller's device memory: table as in csa2_paged_kv (written here),
+ * seq_len [n_seq] int64 tokens of each sequence, ref [n_pages] int32 the
+ * number of table entries naming each page (0: free). A sequence's row names
+ * pages for its first ceil(seq_len / page_size) entries and is -1 after them.
+ * csa2_page_array: one array of pages (codes or scales of one layer): row r of
+ * page g at base + g * page_stride + r * row_bytes; arrays of one call must
+ * not overlap. */
+#define CSA2_PAGE_ARRAYS_MAX 128
+typedef struct csa2_page_pool {
+  int32_t* table;
+  int64_t table_ld;
+  int64_t* seq_len;
+  int32_t* ref;
+  int32_t max_pages;
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t n_seq;
+} csa2_page_pool;
+typedef struct csa2_page_array {
+  void* base;
+  int64_t page_stride;
+  int32_t row_bytes;
+  int32_t reserved; /* 0 */
+} csa2_page_array;
+
+/* The page operations. Free pages are handed out lowest index first, in the
+ * order of the entries; n (the entries) is at most n_seq. An entry naming
+ * sequence -1 is skipped. An entry that cannot be carried out (a sequence out
+ * of range or named before in the same call, a length that does not fit) is
+ * left out whole and recorded as CSA2_FLAG_BAD_SEQ; one whose pages are not
+ * there, and every later one that needs any, as CSA2_FLAG_OUT_OF_PAGES. The
+ * state decides on the device: a captured call replays on the state of then.
+ * Calls on one pool must not overlap on the GPU, nor share a workspace.
+ *   csa2_pages_extend  sequence seqs[i] grows to new_len[i] >= seq_len tokens:
+ *                      fresh pages for the entries it lacks. One launch.
+ *   csa2_pages_fork    child children[i] (seq_len 0, and no entry's parent)
+ *                      becomes a copy of parents[i]: the full pages shared
+ *                      (their counts raised), the partly filled last page
+ *                      copied (its rows in use, in every array); deep != 0:
+ *                      every page copied. Pages missing in the parent are
+ *                      missing in the child. Two launches.
+ *   csa2_pages_free    every page of seqs[i] given back, its row -1, its
+ *                      length 0. Naming a sequence twice is harmless. One launch.
+ *   csa2_pages_trim    the pages of seqs[i] given back that no query at
+ *                      position seq_len - 1 or later sees under (window >= 1,
+ *                      n_first, lo), as csa2_attend_paged reads them. One launch.
+ *   csa2_pages_compact the n_live pages in use move to indices 0 .. n_live - 1
+ *                      (those that lie there stay; the others fill the gaps in
+ *                      ascending order), whole, in every array; table and ref
+ *                      follow. n_live (device, nullable) receives the count.
+ *                      A table entry naming a free page from n_live on becomes
+ *                      -1, recorded as CSA2_FLAG_BAD_PAGE. Two launches.
+ * workspace of csa2_pages_workspace_size(pool) bytes, 256-byte aligned. */
+size_t csa2_pages_workspace_size(const csa2_ctx* ctx, const csa2_page_pool* pool);
+csa2_status csa2_pages_extend(csa2_ctx* ctx, void* stream, const csa2_page_pool* pool, int32_t n, const int32_t* seqs,
+                              const int64_t* new_len, void* workspace, size_t workspace_bytes);
+csa2_status csa2_pages_fork(csa2_ctx* ctx, void* stream, const csa2_page_pool* pool, int32_t n, const int32_t* parents,
+                            const int32_t* children, int32_t deep, int32_t n_arrays, const csa2_page_array* arrays,
+                            void* workspace, size_t workspace_bytes);
+csa2_status csa2_pages_free(csa2_ctx* ctx, void* stream, const csa2_page_pool* pool, int32_t n, const int32_t* seqs);
+csa2_status csa2_pages_trim(csa2_ctx* ctx, void* stream, const csa2_page_pool* pool, int32_t n, const int32_t* seqs,
+                            int64_t window, int64_t n_first, const int64_t* lo);
+csa2_status csa2_pages_compact(csa2_ctx* ctx, void* stream, const csa2_page_pool* pool, int32_t n_arrays,
+                               const csa2_page_array* arrays, int32_t* n_live, void* workspace,
+                               size_t workspace_bytes);
+
+/* ------------------------------------------------------------------------
+ * csa2_rope: rotary positions on their own, for layers whose layout or
+ * scaling is not the context's (their attention then runs on a context of
+ * rope_dim 0). csa2_rope_table (host struct) is filled once by
+ * csa2_rope_table_init: pair k < rope_dim / 2 turns by pos * freq[k],
+ *   none    f_k = theta^(-2k / rope_dim)
+ *   linear  f_k / factor
+ *   ntk     theta replaced by theta * factor^(rope_dim / (rope_dim - 2))
+ *           (rope_dim 2: unchanged)
+ *   yarn    the context's ramp between f_k and f_k / factor (orig_len,
+ *           beta_fast, beta_slow)
+ * and the rotated channels are multiplied by `amplitude`. */
+#define CSA2_ROPE_MAX_PAIRS 256
+typedef enum csa2_rope_layout {
+  CSA2_ROPE_INTERLEAVED = 0, /* pair k: channels offset + 2k, offset + 2k + 1            */
+  CSA2_ROPE_HALF = 1         /* pair k: channels offset + k, offset + k + rope_dim / 2   */
+} csa2_rope_layout;
+typedef enum csa2_rope_scaling {
+  CSA2_ROPE_NONE = 0,
+  CSA2_ROPE_LINEAR = 1,
+  CSA2_ROPE_NTK = 2,
+  CSA2_ROPE_YARN = 3
+} csa2_rope_scaling;
+typedef struct csa2_rope_table {
+  int32_t rope_dim;
+  int32_t offset;
+  int32_t layout;
+  int32_t reserved;
+  double amplitude;
+  double freq[CSA2_ROPE_MAX_PAIRS];
+} csa2_rope_table;
+/* rope_dim even, 0..512; offset even; theta > 0 (> 1 for yarn), factor >= 1,
+ * amplitude finite; orig_len and the betas > 0 (read for yarn only). Host only. */
+csa2_status csa2_rope_table_init(csa2_rope_table* table, int32_t rope_dim, int32_t offset, int32_t layout, double theta,
+                                 int32_t scaling, double factor, double orig_len, double beta_fast, double beta_slow,
+                                 double amplitude);
+/* For every token i < n_tokens, pos[i] >= 0, and head h < n_heads: the
+ * channels [offset, offset + rope_dim) of x rotated by +pos (transpose == 0) or
+ * -pos (transpose != 0: the gradient's direction, and for amplitude 1 the
+ * inverse), the others copied, into out. A token with pos < 0 is padding: its
+ * out stays as it is.
+ *   x, out  element (i, h, c) at i * tok_stride + h * head_stride + c, in
+ *           elements of dtype (bf16, fp16, fp32); out may be x itself with the
+ *           same strides (in place) and must not overlap it otherwise; out's
+ *           rows must not overlap each other
+ *   pos     [n_tokens] int64; head_dim even, 2..1024
+ * Rotated in fp32, angles in double precision, rounded once. One launch. */
+csa2_status csa2_rope(csa2_ctx* ctx, void* stream, const csa2_rope_table* table, int32_t dtype, int64_t n_tokens,
+                      int32_t n_heads, int32_t head_dim, const void* x, int64_t x_tok_stride, int64_t x_head_stride,
+                      const int64_t* pos, void* out, int64_t out_tok_stride, int64_t out_head_stride,
+                      int32_t transpose);
 
 /* Number of kernel launches the last entry point call on this context
  * enqueued (host). */

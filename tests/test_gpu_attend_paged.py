@@ -1,0 +1,325 @@
+"""csa2_attend_paged against a plain 64-bit form, at the sizes, masks, layouts
+and streams where it can go wrong. The bounds are derived in
+paged_common.attend_one."""
+import math
+import random
+
+import pytest
+import torch
+
+from gpu_common import context, require_gpu
+from paged_common import DIM, FMT_NAMES, HEADS, U32, check_attend, page_values, random_pages
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+class Case:
+    """A small paged cache and its queries; run() calls the entry point."""
+
+    def __init__(self, lens, fmt="bf16", page=16, per=1, window=0, n_first=0, lo=None, sink=True, seed=0, spare=2,
+                 queries=None, rope=True, layers=0, extra_cols=0, q_scale=1.0):
+        from compressed_sparse_attention_gb300 import binding
+        require_gpu()
+        self.b = binding
+        self.ctx = context(kv_format=fmt, **({} if rope else {"rope_dim": 0}))
+        self.fmt, self.page, self.window, self.n_first = FMT_NAMES[fmt], page, window, n_first
+        rng = random.Random(seed)
+        counts = [-(-n // page) for n in lens]
+        n_pages = sum(counts) + spare
+        order = list(range(n_pages))
+        rng.shuffle(order)
+        width = max(1, max(counts))
+        self.table_rows = [[order.pop() for _ in range(c)] + [-1] * (width - c) for c in counts]
+        self.codes, self.scales = random_pages(self.fmt, n_pages, page, seed, DEV, (layers,) if layers else ())
+        if layers:  # pages of several layers side by side: [n_pages, layers, page, ..], this layer the last
+            self.codes = self.codes.transpose(0, 1).contiguous()[:, -1]
+            self.scales = None if self.scales is None else self.scales.transpose(0, 1).contiguous()[:, -1]
+        full = torch.full((len(lens), width + extra_cols), 7, dtype=torch.int32)
+        full[:, :width] = torch.tensor(self.table_rows, dtype=torch.int32)
+        self.table = full.to(DEV)[:, :width]
+        queries = queries if queries is not None else [(b, n - per + i) for b, n in enumerate(lens) for i in range(per)]
+        self.seq, self.pos = [b for b, _ in queries], [t for _, t in queries]
+        n = len(queries)
+        g = torch.Generator().manual_seed(seed + 1)
+        self.q = (q_scale * torch.randn((n, HEADS, DIM), generator=g)).to(torch.bfloat16).to(DEV)
+        self.sink = torch.randn((HEADS,), generator=g).to(DEV) if sink is True else sink
+        self.lo = lo
+        self.seq_d = torch.tensor(self.seq, dtype=torch.int32, device=DEV)
+        self.pos_d = torch.tensor(self.pos, dtype=torch.int64, device=DEV)
+        self.lo_d = None if lo is None else torch.tensor(lo, dtype=torch.int64, device=DEV)
+        self.out = torch.full((n, HEADS, DIM), 77.0, dtype=torch.bfloat16, device=DEV)
+        self.lse = torch.full((n, HEADS), 77.0, device=DEV)
+        self.ws = binding.workspace(self.ctx.attend_paged_workspace_size(n), DEV)
+        self.kv = self.ctx.paged_kv(self.codes, self.table, self.scales)
+
+    def call(self, out=None, lse=None, ws=None):
+        return self.ctx.prepare_attend_paged(self.kv, self.q, self.pos_d, self.seq_d, self.out if out is None else out,
+                                             self.ws if ws is None else ws, sink=self.sink,
+                                             lse=self.lse if lse is None else lse, lo=self.lo_d, window=self.window,
+                                             n_first=self.n_first)
+
+    def run(self, flags=0):
+        self.call().run()
+        got, _ = self.ctx.check()
+        assert got == flags, f"device error word 0x{got:x}"
+        return self
+
+    def check(self, values=None):
+        if values is None:
+            values = page_values(self.codes, self.scales, self.fmt)
+        check_attend(self.out, self.lse, values, self.table_rows, self.page, self.q, self.pos, self.seq, self.lo,
+                     self.window, self.n_first, self.sink, self.ctx.cfg)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("n", [1, 2, 127, 128, 129, 257, 700])
+def test_lengths_around_the_tile(fmt, n):
+    Case([n], fmt=fmt, page=32, seed=n).run().check()
+
+
+@pytest.mark.parametrize("page", [1, 2, 8, 64, 128, 256, 1024])
+def test_page_sizes(page):
+    Case([333, 1, 140], page=page, seed=page).run().check()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+def test_one_long_sequence_is_split_over_many_ctas(fmt):
+    Case([9000, 5], fmt=fmt, page=64, seed=3).run().check()
+
+
+@pytest.mark.parametrize("fmt,per", [("bf16", 1), ("fp8", 3), ("fp4", 2)])
+def test_ragged_batch(fmt, per):
+    Case([1 + per, 900, 64, 65, 2000, 128, 511], fmt=fmt, per=per, seed=4).run().check()
+
+
+@pytest.mark.parametrize("window,n_first", [(1, 0), (1, 1), (5, 200), (100, 4), (128, 0), (127, 1), (124, 4), (400, 7),
+                                            (10 ** 12, 3), (300, 10 ** 12)])
+def test_windows_and_first_tokens(window, n_first):
+    Case([1, 50, 131, 400, 777], window=window, n_first=n_first, seed=window % 1000).run().check()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+def test_prompt_chunk_under_a_window(fmt):
+    # every token of a chunk is a query: more queries than SMs, several tiles each
+    Case([420, 333], fmt=fmt, per=110, window=150, n_first=4, lo=[0, 9], page=32, seed=6).run().check()
+
+
+def test_left_padding_and_rows_that_see_nothing():
+    # lo past t, lo negative, an empty sequence (t = -1)
+    Case([40, 40, 40, 3], lo=[60, 39, -5, 0], seed=7, queries=[(0, 39), (1, 39), (2, 39), (3, -1)]).run().check()
+    Case([40, 40], lo=[60, 20], window=9, n_first=3, seed=8).run().check()
+
+
+@pytest.mark.parametrize("sink", [None, -math.inf, 80.0, -80.0])
+def test_sinks(sink):
+    s = None if sink is None else torch.full((HEADS,), sink, device=DEV)
+    Case([300, 1, 7], sink=s, lo=[0, 5, 0], seed=9).run().check()
+
+
+def test_large_scores_move_the_reference():
+    # scores in the hundreds: the reference must follow the rows
+    Case([600, 200], q_scale=30.0, seed=10).run().check()
+
+
+def test_padding_queries_stay_as_they_were():
+    c = Case([100, 200], queries=[(0, 99), (-1, 5), (1, 199), (-1, -1)], seed=11)
+    c.run().check()
+    for i in (1, 3):
+        assert (c.out[i] == 77.0).all() and (c.lse[i] == 77.0).all()
+
+
+def test_bad_queries_are_recorded_and_zero():
+    c = Case([100, 200], queries=[(0, 99), (2, 5), (1, -2), (-2, 3)], seed=12)
+    c.run(flags=c.b.FLAG_BAD_QUERY)
+    assert (c.out[1:] == 0).all()
+    # the sink times log2(e) and back by ln 2: two constants and two products, each rounded once
+    assert ((c.lse[1:] - c.sink).abs() <= 4 * U32 * c.sink.abs()).all()
+    c.seq, c.pos = c.seq[:1], c.pos[:1]
+    c.check()
+
+
+def test_missing_pages_are_left_out_and_recorded():
+    c = Case([300, 200], page=32, seed=13)
+    for row, col, v in ((0, 3, -1), (1, 0, 10 ** 6), (1, 2, -7)):
+        c.table_rows[row][col] = v
+        c.table[row, col] = v
+    c.run(flags=c.b.FLAG_BAD_PAGE).check()
+    # a position past the table's columns: what the table holds is read
+    d = Case([64], page=32, queries=[(0, 10 ** 9)], seed=14)
+    d.run(flags=d.b.FLAG_BAD_PAGE)
+    d.pos = [63]
+    values = page_values(d.codes, d.scales, d.fmt)
+    # (the rotation is by the true position, which only the magnitude check below can use)
+    assert torch.isfinite(d.out.float()).all() and values.shape[0] >= 2
+
+
+def test_missing_pages_outside_the_window_are_not_read():
+    c = Case([500], page=16, window=40, n_first=4, seed=15)
+    for j in range(1, 500 // 16 - 3):
+        c.table_rows[0][j] = -1
+        c.table[0, j] = -1
+    c.run().check()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+def test_nan_in_rows_that_are_not_seen(fmt):
+    c = Case([70, 210], fmt=fmt, page=32, lo=[0, 33], window=64, n_first=3, seed=16)
+    values = page_values(c.codes, c.scales, c.fmt)
+    seen = torch.zeros(values.shape[:2], dtype=torch.bool)
+    from paged_common import visible
+    for b, t in zip(c.seq, c.pos):
+        for p in visible(t, c.lo[b], c.window, c.n_first):
+            seen[c.table_rows[b][p // c.page], p % c.page] = True
+    bad = ~seen.to(DEV)
+    if c.fmt == 0:
+        c.codes[bad] = math.nan
+        c.codes[0][bad[0]] = math.inf
+    else:
+        c.codes[bad] = 0x7F
+        c.scales[bad] = 0xFF if c.fmt == 1 else 0x7F
+    c.run().check(values)
+
+
+def test_every_row_of_a_split_missing():
+    # a run of tiles without a single row between tiles that have some
+    c = Case([2000], page=16, seed=17)
+    for j in range(20, 100):
+        c.table_rows[0][j] = -1
+        c.table[0, j] = -1
+    c.run(flags=c.b.FLAG_BAD_PAGE).check()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+def test_strided_pages_and_tables(fmt):
+    Case([100, 333], fmt=fmt, page=32, layers=3, extra_cols=5, seed=18).run().check()
+
+
+def test_context_without_rope():
+    Case([100, 333], rope=False, seed=19).run().check()
+
+
+def test_more_queries_than_one_launch_takes():
+    n = 4100
+    c = Case([300, 40], page=64, queries=[(i % 2, (i * 7) % (300 if i % 2 == 0 else 40)) for i in range(n)], window=60,
+             n_first=2, seed=20)
+    c.run()
+    assert c.ctx.last_launch_count == 4
+    pick = list(range(0, n, 97)) + [4095, 4096, n - 1]
+    c.out, c.lse, c.q = c.out[pick], c.lse[pick], c.q[pick]
+    c.seq, c.pos = [c.seq[i] for i in pick], [c.pos[i] for i in pick]
+    c.check()
+
+
+def test_page_offsets_past_32_bits():
+    # 70,000 pages of 64 KB: codes past 4 GB; only the last pages are used
+    from compressed_sparse_attention_gb300 import binding
+    require_gpu()
+    ctx = context()
+    n_pages = 70000
+    pages = torch.empty((n_pages, 64, DIM), dtype=torch.bfloat16, device=DEV)
+    g = torch.Generator().manual_seed(21)
+    last = torch.randn((3, 64, DIM), generator=g).to(torch.bfloat16)
+    pages[-3:] = last.to(DEV)
+    rows = [[n_pages - 1, n_pages - 3, n_pages - 2]]
+    q = torch.randn((1, HEADS, DIM), generator=g).to(torch.bfloat16).to(DEV)
+    out = torch.empty_like(q)
+    ws = binding.workspace(ctx.attend_paged_workspace_size(1), DEV)
+    kv = ctx.paged_kv(pages, torch.tensor(rows, dtype=torch.int32, device=DEV))
+    ctx.attend_paged(kv, q, torch.tensor([180], device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV), out, ws)
+    assert ctx.check()[0] == 0
+    check_attend(out, None, last.double(), [[2, 0, 1]], 64, q, [180], [0], None, 0, 0, None, ctx.cfg)
+
+
+def test_repeats_bit_for_bit_and_on_another_stream():
+    c = Case([3000, 700, 90, 1], page=32, seed=22).run()
+    out, lse = c.out.clone(), c.lse.clone()
+    for _ in range(3):
+        c.run()
+        assert torch.equal(c.out, out) and torch.equal(c.lse, lse)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        c.out.fill_(5)
+        c.call().run()
+    s.synchronize()
+    assert torch.equal(c.out, out)
+
+
+def test_two_calls_at_once_with_a_workspace_each():
+    a, b = Case([4000, 30], seed=23).run(), Case([2500] * 3, fmt="fp8", seed=24).run()
+    want = [a.out.clone(), b.out.clone()]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, c in zip(streams, (a, b)):
+            with torch.cuda.stream(s):
+                c.out.zero_()
+                c.call().run()
+    torch.cuda.synchronize()
+    assert torch.equal(a.out, want[0]) and torch.equal(b.out, want[1])
+
+
+def test_captured_graphs_share_a_workspace_and_follow_the_state():
+    c = Case([800, 300], page=32, seed=25).run()
+    first = c.out.clone()
+    out2 = torch.zeros_like(c.out)
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        c.call().run()
+    with torch.cuda.graph(g2):  # the same workspace, another output
+        c.call(out=out2).run()
+    for _ in range(3):
+        c.out.zero_()
+        out2.zero_()
+        g1.replay()
+        g2.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(c.out, first) and torch.equal(out2, first)
+    c.pos = [555, 17]
+    c.pos_d.copy_(torch.tensor(c.pos))
+    g1.replay()
+    torch.cuda.synchronize()
+    c.check()
+
+
+def test_no_queries_enqueue_nothing():
+    c = Case([10], queries=[], seed=26)
+    assert c.ctx.attend_paged_workspace_size(0) == 0
+    c.run()
+    assert c.ctx.last_launch_count == 0
+
+
+def test_refusals():
+    from compressed_sparse_attention_gb300 import binding
+    c = Case([100], page=16, seed=27)
+    lib, p = c.ctx.lib, c.call()
+
+    def st(**kw):
+        a = binding.PagedKVArgs.from_buffer_copy(c.kv.args)
+        args = dict(n=1, window=0, n_first=0, q=c.q.data_ptr(), out=c.out.data_ptr(), ws=c.ws.data_ptr(), size=c.ws.numel())
+        for k, v in kw.items():
+            if k in args:
+                args[k] = v
+            else:
+                setattr(a, k, v)
+        return lib.csa2_attend_paged(c.ctx.h, None, binding.C.byref(a), args["n"], args["q"], c.pos_d.data_ptr(),
+                                     c.seq_d.data_ptr(), None, args["window"], args["n_first"], None, args["out"], None,
+                                     args["ws"], args["size"])
+
+    c.out.fill_(3)
+    for kw in (dict(page_size=24), dict(page_size=0), dict(page_size=8192), dict(max_pages=1 << 28, table_ld=1 << 28)):
+        assert st(**kw) == 2, kw
+    for kw in (dict(n_pages=0), dict(n_seq=0), dict(table_ld=1), dict(table=None), dict(pages=None), dict(page_stride=16),
+               dict(page_stride=16 * 1024 + 8), dict(pages=c.codes.data_ptr() + 2), dict(n=-1), dict(window=-1),
+               dict(n_first=-1), dict(q=None), dict(out=None), dict(q=c.q.data_ptr() + 2), dict(ws=c.ws.data_ptr() + 16)):
+        assert st(**kw) == 1, kw
+    assert st(size=c.ws.numel() - 1) == 6 and st(ws=None) == 6
+    f8 = Case([100], fmt="fp8", seed=28)
+    a = binding.PagedKVArgs.from_buffer_copy(f8.kv.args)
+    a.scales = None
+    assert lib.csa2_attend_paged(f8.ctx.h, None, binding.C.byref(a), 1, f8.q.data_ptr(), f8.pos_d.data_ptr(),
+                                 f8.seq_d.data_ptr(), None, 0, 0, None, f8.out.data_ptr(), None, f8.ws.data_ptr(),
+                                 f8.ws.numel()) == 1
+    torch.cuda.synchronize()
+    assert (c.out == 3).all() and c.ctx.last_launch_count == 0 and p is not None
