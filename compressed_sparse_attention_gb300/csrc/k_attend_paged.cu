@@ -5,19 +5,24 @@
 // `n_first`):  s_p = scale q~ . row_p,  o = sum_p e^{s_p} row_p /
 // (sum_p e^{s_p} + e^{sink}), its rope channels rotated back by -t.
 //
-// The visible rows of a query, packed, make 128-row tiles (a query that sees
-// nothing makes one empty tile, which writes its zeros). All queries' tiles,
+// The chunks of a query's visible rows (paged.cuh) make 128-row tiles (a query
+// that sees nothing makes one empty tile, which writes its zeros). All queries' tiles,
 // one query after another, are cut into equal runs, one run per CTA and one
 // CTA per SM: a long sequence is split over many CTAs and a CTA takes many
 // short ones. A query that lies whole in one run is written at once; the runs'
 // ends leave unnormalised fp32 partials, at most two a CTA, which the join
 // kernel sums. The products and softmax of a tile are those of attend_tile.cuh.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "attend_tile.cuh"
 #include "paged.cuh"
 
 namespace csa2 {
 
 struct PagedAttendParams {
+  CUtensorMap q_map;     // Q: [64 n_query heads][512], boxes of 64 heads x 64 channels
+  CUtensorMap kv_map;    // bf16 pages: [n_pages][page_size][512], boxes of one chunk x 64 channels
   AttendParams a;       // q, positions, sink, outputs, scale, RoPE, flags, part_*
   PagedView kv;
   const int64_t* lo;    // [n_seq], nullable
@@ -29,7 +34,7 @@ struct PagedAttendParams {
 
 namespace {
 
-constexpr int kJoinThreads = 512;
+constexpr int kMaxCtas = 512;  // of the tile kernel: the most parts of a query
 
 struct QuerySpan {
   Visible vis;
@@ -46,10 +51,15 @@ __device__ __forceinline__ QuerySpan query_span(const PagedAttendParams& p, int 
   s.ok = s.b >= 0 && s.b < p.kv.n_seq && s.t >= 0;
   const int64_t cap = (int64_t)p.kv.max_pages << p.kv.page_shift;
   const int64_t lo = (s.ok && p.lo != nullptr) ? p.lo[s.b] : 0;
-  s.vis = visible_rows(s.ok ? s.t : -1, lo, p.window, p.n_first, cap);
-  s.n_tiles = max(1, (s.vis.count + kTileRows - 1) / kTileRows);
+  const int cs = chunk_shift(p.kv.page_shift);
+  s.vis = visible_rows(s.ok ? s.t : -1, lo, p.window, p.n_first, cap, cs);
+  s.n_tiles = max(1, (int)((((int64_t)s.vis.n_chunks << cs) + kTileRows - 1) / kTileRows));
   return s;
 }
+
+// A partial O: four heads' values of one dim side by side (what a thread of
+// the tile kernel holds of them), dims next to each other: quad hq = head / 4.
+__device__ __forceinline__ int part_at(int hq, int dim) { return hq * kDim + dim; }
 
 // Slots of the partials: CTA c leaves at most two, 2c for a query that began
 // in an earlier CTA and 2c + 1 for one that it begins and does not end.
@@ -57,356 +67,1166 @@ __device__ __forceinline__ int part_slot(int c, bool begins) { return 2 * c + (b
 
 }  // namespace
 
+// ---------------------------------------------------------------------------
+// The tile kernel. Roles of a CTA's warps:
+//   0 .. 7   math: softmax of a tile, and the outputs at a query's end
+//   8 ..     producers: Q, and the rows of the tiles
+//   last     (bf16) issues the tensor-core products, so that the next query's
+//            scores come while this one's output is written. fp8 and fp4 have
+//            eight producer warps, and a seventeenth warp would take a quarter
+//            of everyone's registers: math warp 0 issues there.
+// A tile's 512 channels are eight 64-channel blocks in eight slots of shared
+// memory (the layout of attend_tile.cuh); full[b] says that block b of a tile
+// has landed, empty[m] that the products of output dims 128 m .. have read
+// blocks 2m and 2m + 1. QK^T runs block by block as they land, PV frees them
+// two at a time, so that the next tile's rows load while this one's PV runs.
+// Everything a role waits for, it waits for with a limit (wait_phase).
+//
+// The code that runs for every tile is kept small, its loops rolled: the roles
+// run different code at the same time, and with everything unrolled the
+// instruction cache missed one request in five (warps without an instruction
+// were 2.3 times those that issued; a tile of bf16 rows took 8,850 cycles).
+// ---------------------------------------------------------------------------
+constexpr int kFirstProducer = kAttWarps;
 template <int KVF>
-__global__ void __launch_bounds__(kAttThreads, 1) attend_paged_kernel(const PagedAttendParams p) {
+struct Roles {
+  // bf16 rows are copied by TMA; fp8 and fp4 rows pass through registers and
+  // are converted there, which takes twice the warps
+  static constexpr int kProducers = KVF == 0 ? 4 : 8;
+  static constexpr int kProducerThreads = 32 * kProducers;
+  static constexpr bool kOwnIssuer = KVF == 0;
+  static constexpr int kIssuer = kFirstProducer + kProducers;  // warp, where it has one
+  static constexpr int kThreads = 32 * (kFirstProducer + kProducers + (kOwnIssuer ? 1 : 0));
+};
+
+// shared memory behind attend_tile.cuh's layout
+constexpr uint32_t SM_BAR = SM_TOTAL;                 // mbarriers
+constexpr uint32_t SM_ROWOK = SM_BAR + 256;           // uint8 [2][128]: rows that are there, by the tile's parity
+constexpr uint32_t SM_DIRTY = SM_ROWOK + 256;         // uint32 [2]: tiles with rows to be cleared
+constexpr uint32_t SM_RUN = SM_DIRTY + 64;            // the CTA's run
+constexpr uint32_t SM_ROWAT = SM_RUN + 256;           // int32 [2][128][2]: page and row in it of a tile's rows
+constexpr uint32_t SM_ROPETAB = SM_ROWAT + 2048;      // float2 [4][32]: cos, sin of four queries' positions
+constexpr uint32_t SM_PAGED_TOTAL = SM_ROPETAB + 1024;
+constexpr uint32_t kPagedSmemBytes = SM_PAGED_TOTAL + 1024;
+
+enum Bar : uint32_t { kFull = 0, kEmpty = 8, kQFull = 12, kQEmpty = 13, kScores = 14, kOut = 15, kCleared = 16, kWeights = 17, kDrained = 18, kBars = 19 };
+
+// Bounded wait on an mbarrier phase: 100,000 suspensions of up to 20 us, then
+// CSA2_FLAG_WAIT_TIMEOUT and false. (mbar_wait with its clock is 40
+// instructions at each of a dozen places; see the note on code size below.)
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t phase, uint32_t* flags) {
+#pragma unroll 1
+  for (int i = 0; i < 100000; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        "selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(phase), "r"(20000u)
+        : "memory");
+    if (ok != 0u) return true;
+  }
+  set_flag(flags, CSA2_FLAG_WAIT_TIMEOUT);
+  return false;
+}
+// A warp arrives once, and waits, by its first lane (an arrival of every lane
+// is one atomic each, in turn).
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0)
+    asm volatile("{\n.reg .b64 t;\nmbarrier.arrive.shared::cta.b64 t, [%0];\n}" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t phase, uint32_t* flags) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = wait_phase(bar, phase, flags);
+  return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+}
+// Tensor-core and TMA instructions take their operands from uniform registers:
+// the warps that issue them run the issuing code whole, one lane's predicate
+// on the instruction itself. (Inside a branch that one thread takes, every
+// operand is moved over one by one: a product took 95 cycles instead of 48, a
+// block's copy 230. The same holds for loops and branches on values that come
+// from memory, which the compiler cannot know to be the same in every lane:
+// they go through a shuffle or a vote first.)
+__device__ __forceinline__ int uniform(int v, int lane = 0) { return __shfl_sync(0xffffffffu, v, lane); }
+__device__ __forceinline__ bool uniform(bool v) { return __any_sync(0xffffffffu, v) != 0; }
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void mma_one(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p, e;\n"
+      "setp.ne.u32 p, %4, 0;\n"
+      "setp.ne.u32 e, %5, 0;\n"
+      "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void commit_one(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred e;\nsetp.ne.u32 e, %1, 0;\n"
+      "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t phase_done(uint32_t bar, uint32_t phase) {
+  uint32_t ok;
+  asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok)
+               : "r"(bar), "r"(phase)
+               : "memory");
+  return ok;
+}
+// wait_phase by every lane of a warp
+__device__ __forceinline__ bool wait_all_lanes(uint32_t bar, uint32_t phase, uint32_t* flags) {
+  return __all_sync(0xffffffffu, wait_phase(bar, phase, flags)) != 0;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+// largest value of the warp's lanes
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// named barrier 1: the 256 math threads
+struct SyncMath {
+  __device__ __forceinline__ void sync() const { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+  __device__ __forceinline__ bool any(bool v) const {
+    uint32_t r;
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, 1, 256, p;\nselp.u32 %0, 1, 0, q;\n}"
+        : "=r"(r)
+        : "r"((uint32_t)v)
+        : "memory");
+    return r != 0;
+  }
+};
+
+// named barrier 2: the producer threads
+template <int N>
+__device__ __forceinline__ void sync_producers() {
+  asm volatile("bar.sync 2, %0;" ::"n"(N) : "memory");
+}
+// The CTA's run of tiles, walked tile by tile; every role has its own.
+struct Cursor {
+  int64_t at, run1, q0;  // tile, end of the run, first tile of query qi
+  int qi;
+  QuerySpan span;
+  __device__ __forceinline__ bool more() const { return at < run1; }
+  __device__ __forceinline__ uint32_t tiles() const { return (uint32_t)uniform((int)(run1 - at)); }
+  __device__ __forceinline__ int tile() const { return (int)(at - q0); }
+  // the last tile of this query in the run
+  __device__ __forceinline__ bool last() const { return uniform(at + 1 == run1 || at + 1 == q0 + span.n_tiles); }
+  __device__ __forceinline__ void next(const PagedAttendParams& p) {
+    ++at;
+    if (at < run1 && at == q0 + span.n_tiles) {
+      q0 = at;
+      span = query_span(p, ++qi);
+    }
+  }
+};
+
+struct Run {
+  Cursor cur;     // at the run's first tile
+  int64_t total;  // tiles of all queries
+  int ctas;       // CTAs with a run
+};
+static_assert(sizeof(Run) <= 256, "SM_RUN");
+
+__device__ __forceinline__ void expect_one(uint32_t leader, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n.reg .b64 t;\n.reg .pred e;\nsetp.ne.u32 e, %2, 0;\n@e mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;\n}" ::"r"(bar),
+      "r"(bytes), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void tma_2d_one(uint32_t leader, uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred e;\nsetp.ne.u32 e, %5, 0;\n"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d_one(uint32_t leader, uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                           uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred e;\nsetp.ne.u32 e, %6, 0;\n"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(leader)
+      : "memory");
+}
+
+// Q of a query: its plain 64-channel blocks by TMA, its rope channels (the
+// last block) rotated and split into hi + lo (see q_rope_split) by the
+// producer threads (t: index among N, warp: a uniform register's t / 32). The
+// (cos, sin) of the query's position are formed once, a pair a lane of the last
+// warp (freq: that lane's frequency), and left for the outputs' rotation back
+// (seg: the query's number in the run; four tables in turn: the output of one
+// query may still be written while the Q of the second after it arrives).
+// kQFull completes when all is there. ask() puts the loads under way, take() waits for them.
+template <int N>
+struct QLoad {
+  uint4 v[8 * kHeads / N];
+  double freq;
+  __device__ __forceinline__ void ask(const PagedAttendParams& p, uint8_t* sm, uint32_t base_s, int qi, int64_t pos, uint32_t seg,
+                                      int t, int warp) {
+    const uint32_t bar = base_s + SM_BAR + 8 * kQFull;
+    const bool rope = p.a.rp.pairs > 0;
+    if (warp == 0) {
+      const uint32_t leader = elect_one();
+      const int plain = rope ? 7 : 8;
+      expect_one(leader, bar, 8192u * plain);
+#pragma unroll 1
+      for (int b = 0; b < plain; ++b) tma_2d_one(leader, base_s + SM_Q + 8192u * b, &p.q_map, 64 * b, kHeads * uniform(qi), bar);
+    }
+    if (rope) {
+      // thread: chunk 56 + (t & 7) of heads t >> 3, ...: always the same four pairs
+      const uint16_t* q = p.a.q + (int64_t)qi * kHeads * kDim + 8 * (56 + (t & 7));
+#pragma unroll
+      for (int u = 0; u < 8 * kHeads / N; ++u) v[u] = *reinterpret_cast<const uint4*>(q + (int64_t)((t >> 3) + u * (N / 8)) * kDim);
+      if (warp == N / 32 - 1) {
+        float cs, sn;
+        angle_cs((double)max(pos, (int64_t)0) * freq, cs, sn);
+        reinterpret_cast<float2*>(sm + SM_ROPETAB)[32 * (seg & 3u) + (t & 31)] = make_float2(cs, sn);
+      }
+    }
+  }
+  __device__ __forceinline__ void take(const PagedAttendParams& p, uint8_t* sm, uint32_t base_s, uint32_t seg, int t) {
+    if (p.a.rp.pairs > 0) {
+      const int c = 56 + (t & 7);
+      const float2* table = reinterpret_cast<const float2*>(sm + SM_ROPETAB) + 32 * (seg & 3u);
+      sync_producers<N>();
+#pragma unroll
+      for (int u = 0; u < 8 * kHeads / N; ++u) {
+        const int h = (t >> 3) + u * (N / 8);
+        uint32_t w[4] = {v[u].x, v[u].y, v[u].z, v[u].w}, lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 cs = table[4 * (t & 7) + k];
+          const float x0 = bf16lo(w[k]), x1 = bf16hi(w[k]);
+          const float y0 = x0 * cs.x - x1 * cs.y, y1 = x0 * cs.y + x1 * cs.x;
+          w[k] = pack_bf16(y0, y1);
+          lo[k] = pack_bf16(y0 - bf16lo(w[k]), y1 - bf16hi(w[k]));
+        }
+        const uint32_t at = (uint32_t)h * 128u + ((uint32_t)((c & 7) ^ (h & 7)) << 4);
+        *reinterpret_cast<uint4*>(sm + SM_Q + 7u * 8192u + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(sm + SM_Q + 8u * 8192u + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      fence_proxy_async_smem();
+    }
+    warp_arrive(base_s + SM_BAR + 8 * kQFull);
+  }
+};
+
+// Row r of the cursor's tile: the page of its chunk and the row in it (page -1:
+// the query has no such chunk, or its page is missing), and whether the query
+// sees it.
+struct RowAt {
+  int32_t page, in_page;
+  bool seen;
+  __device__ __forceinline__ bool there() const { return seen && page >= 0; }
+};
+__device__ __forceinline__ RowAt row_at(const PagedAttendParams& p, const Cursor& cur, int r) {
+  const int cs = chunk_shift(p.kv.page_shift);
+  const Visible& v = cur.span.vis;
+  const int i = cur.tile() * kTileRows + r, k = i >> cs;
+  const bool have = k < v.n_chunks;
+  const int64_t pos = have ? chunk_pos(v, k, i & ((1 << cs) - 1), cs) : 0;
+  RowAt a;
+  a.seen = have && is_seen(v, pos);
+  a.in_page = (int32_t)pos & ((1 << p.kv.page_shift) - 1);
+  a.page = have ? page_of(p.kv, cur.span.b, pos) : -1;
+  return a;
+}
+
+template <int N>
+__device__ __forceinline__ bool any_producer(bool v) {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, 2, %2, p;\nselp.u32 %0, 1, 0, q;\n}"
+               : "=r"(r)
+               : "r"((uint32_t)v), "n"(N)
+               : "memory");
+  return r != 0;
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* ptr, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(ptr), "r"(bytes) : "memory");
+}
+
+// bf16 producers. Thread t finds row t of a tile one tile ahead and the first
+// row of each chunk asks for the chunk in L2: shared memory holds one tile, so
+// that the memory would idle between a tile's last block and its first PV;
+// with the next tile on its way to L2 it does not. Warp w copies blocks 2w and
+// 2w + 1 by TMA, chunk by chunk, as soon as their slots are free (TMA:
+// chunks of at least the 8 rows of a swizzle atom; smaller ones are copied by
+// the threads, 16 bytes each). Rows of a chunk that are not the query's are
+// cleared after they land: their weights are 0, but 0 times a NaN is not.
+template <int N, bool TMA>
+__device__ __forceinline__ void produce_bf16(const PagedAttendParams& p, uint8_t* sm, uint32_t base_s, Cursor cur, int t,
+                                             int warp, double freq) {
+  static_assert(N == kTileRows);
+  const uint32_t bars = base_s + SM_BAR;
+  const int cs = chunk_shift(p.kv.page_shift);
+  const int n_ch = kTileRows >> cs;  // chunks of a tile
+  int2* at = reinterpret_cast<int2*>(sm + SM_ROWAT);
+  uint32_t* dirty = reinterpret_cast<uint32_t*>(sm + SM_DIRTY);
+  QLoad<N> ql;
+  ql.freq = freq;
+  ql.ask(p, sm, base_s, cur.qi, cur.span.t, 0u, t, warp);
+  RowAt mine = row_at(p, cur, t);
+  bool clear = false;
+  // this thread's row of tile n: what math and the copies need to know of it
+  auto publish = [&](uint32_t n) {
+    if (mine.page >= 0 && (t & ((1 << cs) - 1)) == 0)
+      prefetch_l2(p.kv.pages + mine.page * p.kv.page_stride + (int64_t)mine.in_page * 1024, 1024u << cs);
+    if (mine.seen && mine.page < 0) set_flag(p.a.flags, CSA2_FLAG_BAD_PAGE);
+    at[128 * (n & 1u) + t] = make_int2(mine.page, mine.in_page);
+    sm[SM_ROWOK + 128 * (n & 1u) + t] = mine.there();
+    clear = any_producer<N>(!mine.there());
+  };
+  publish(0);
+  bool first = true, live = true;  // live: see math_role
+  uint32_t seg = 0, n = 0;
+  const int lane = t & 31;
+  const uint32_t leader = elect_one();
+  const uint32_t tiles = cur.tiles();
+#pragma unroll 1
+  for (; n < tiles; ++n) {
+    const bool there = mine.there();
+    if (t == 0) dirty[n & 1u] = clear ? 1u : 0u;
+    const bool q_here = first;
+    first = cur.last();
+    // Q comes before the rows, whose slots are free later, except at the
+    // run's start, where both are
+    if (q_here && n > 0) {
+      live = live && wait_all_lanes(bars + 8 * kQEmpty, (seg & 1u) ^ 1u, p.a.flags);
+      ql.ask(p, sm, base_s, cur.qi, cur.span.t, seg, t, warp);
+      ql.take(p, sm, base_s, seg, t);
+    }
+    if constexpr (TMA) {
+      // lane k has chunk k
+      const int2 src = lane < n_ch ? at[128 * (n & 1u) + (lane << cs)] : make_int2(-1, 0);
+      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, src.x >= 0)) << (7 + cs);
+      if (n > 0) live = live && wait_all_lanes(bars + 8 * (kEmpty + warp), (n & 1u) ^ 1u, p.a.flags);
+      if (live) {
+        const uint32_t full = bars + 8 * (kFull + 2 * warp), dst = base_s + SM_KV + (uint32_t)(2 * warp) * 16384u;
+        expect_one(leader, full, bytes);
+        expect_one(leader, full + 8, bytes);
+#pragma unroll 2
+        for (int k = 0; k < n_ch; ++k) {
+          const int page = uniform(src.x, k), row = uniform(src.y, k);
+          if (page >= 0) {
+            tma_3d_one(leader, dst + ((uint32_t)k << (7 + cs)), &p.kv_map, 128 * warp, row, page, full);
+            tma_3d_one(leader, dst + 16384u + ((uint32_t)k << (7 + cs)), &p.kv_map, 128 * warp + 64, row, page, full + 8);
+          }
+        }
+      }
+    } else {
+      int64_t src[8];  // rows t >> 3, + 16, ...: 16-byte chunk t & 7 of every block
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const int r = (t >> 3) + 16 * u;
+        const int2 a = at[128 * (n & 1u) + r];
+        src[u] = sm[SM_ROWOK + 128 * (n & 1u) + r] ? a.x * p.kv.page_stride + (int64_t)a.y * 1024 + 16 * (t & 7) : -1;
+      }
+#pragma unroll 1
+      for (int b = 0; b < 8; ++b) {
+        if (b % 2 == 0 && n > 0) live = live && warp_wait(bars + 8 * (kEmpty + b / 2), (n & 1u) ^ 1u, p.a.flags);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int r = (t >> 3) + 16 * u;
+          cp_async16(base_s + SM_KV + (uint32_t)b * 16384u + (uint32_t)r * 128u + ((uint32_t)((t & 7) ^ (r & 7)) << 4),
+                     p.kv.pages + (src[u] >= 0 ? src[u] + 128 * b : 0), src[u] >= 0 ? 16u : 0u);
+        }
+      }
+      cp_async_wait_all();
+      fence_proxy_async_smem();
+#pragma unroll 1
+      for (int b = 0; b < 8; ++b) warp_arrive(bars + 8 * (kFull + b));
+    }
+    if (q_here && n == 0) ql.take(p, sm, base_s, seg, t);
+    if (q_here) ++seg;
+    cur.next(p);
+    if (cur.more()) mine = row_at(p, cur, t);
+    if (first && t == 0 && cur.more()) prefetch_l2(p.a.q + (int64_t)cur.qi * kHeads * kDim, 2u * kHeads * kDim);
+    if (TMA && clear) {
+      for (int b = 0; b < 8; ++b) live = live && warp_wait(bars + 8 * (kFull + b), n & 1u, p.a.flags);
+      // a warp's rows one after another, its lanes side by side: eight 16-byte
+      // stores a block, four blocks at a time
+      uint8_t* dst = sm + SM_KV + (uint32_t)(lane >> 3) * 16384u + (uint32_t)(32 * warp) * 128u + 16u * (lane & 7);
+      for (uint32_t gone = __ballot_sync(0xffffffffu, !there); gone != 0u; gone &= gone - 1) {
+        const uint32_t r = (uint32_t)(__ffs(gone) - 1) * 128u;
+        *reinterpret_cast<uint4*>(dst + r) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(dst + 4u * 16384u + r) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+    }
+    if (TMA) warp_arrive(bars + 8 * kCleared);
+    if (cur.more()) publish(n + 1);
+  }
+  if (!live && TMA && n > 0) {  // no copy may still be landing when the CTA exits
+    warp_wait(bars + 8 * kQFull, (seg - 1) & 1u, p.a.flags);
+    for (int b = 0; b < 8 && warp_wait(bars + 8 * (kFull + b), (n - 1) & 1u, p.a.flags); ++b) {}
+  }
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// 16 bf16 channels (two 16-byte chunks) from 16 e4m3 codes and their scale.
+// A code's exponent and mantissa in the low bits of bf16's make 2^-120 of its
+// value (subnormal codes included), and one product with 2^(E - 7) the value
+// times 2^(E - 127), exact in bf16: 3 instructions a value, where the hardware
+// conversion issues at an eighth of the rate (a tile's conversion took 4,200
+// cycles with it). NaN codes and scales above 2^7, which 2^(E - 7) cannot
+// hold, take the conversion.
+__device__ __forceinline__ void fp8_to_bf16(const uint4& codes, uint32_t scale, uint32_t (&o)[8]) {
+  const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
+  uint32_t nan = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) nan |= (cw[k] & 0x7F7F7F7Fu) + 0x01010101u;
+  if ((nan & 0x80808080u) != 0u || scale > 134u) {
+    const float sc = ue8m0_value(scale);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 a = e4m3x2_to_float2((uint16_t)(cw[k] & 0xFFFFu));
+      const float2 b = e4m3x2_to_float2((uint16_t)(cw[k] >> 16));
+      o[2 * k] = pack_bf16(a.x * sc, a.y * sc);
+      o[2 * k + 1] = pack_bf16(b.x * sc, b.y * sc);
+    }
+    return;
+  }
+  const uint32_t sc2 = ((scale + 120u) << 7) * 0x00010001u;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const uint32_t x = __byte_perm(cw[k], 0u, u == 0 ? 0x1404 : 0x3424);  // each code in the high byte of a half
+      o[2 * k + u] = mul_bf16x2((x & 0x80008000u) | ((x & 0x7F007F00u) >> 4), sc2);
+    }
+  }
+}
+// 16 bf16 channels from 16 E2M1 codes and their e4m3 scale: the bytes of a
+// code's bf16 from two eight-entry tables held in registers (byte permutes),
+// the sign from a third permute, and one product with the scale (at most 6
+// significant bits: exact).
+__device__ __forceinline__ void fp4_to_bf16(uint32_t lo, uint32_t hi, uint32_t scale, uint32_t (&o)[8]) {
+  const float scf = e4m3_value(scale);
+  const uint32_t sc2 = pack_bf16(scf, scf);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t w = (k < 2 ? lo : hi) >> (16 * (k & 1));  // four codes in the low 16 bits
+    const uint32_t sel = w & 0x7777u;
+    const uint32_t l = __byte_perm(0xC0800000u, 0xC0804000u, sel);
+    // a selector with its top bit set replicates the byte's sign (which
+    // __byte_perm masks off): 0xFF for a negative code, else 0x80
+    uint32_t sg;
+    asm("prmt.b32 %0, %1, %1, %2;" : "=r"(sg) : "r"(0x80808080u), "r"(w));
+    const uint32_t h = __byte_perm(0x3F3F3F00u, 0x40404040u, sel) | ((sg & 0x40404040u) << 1);
+    o[2 * k] = mul_bf16x2(__byte_perm(l, h, 0x5140), sc2);
+    o[2 * k + 1] = mul_bf16x2(__byte_perm(l, h, 0x7362), sc2);
+  }
+}
+
+// fp8 / fp4 producers: a thread's share of the codes passes through registers,
+// four blocks ahead of the conversion (and is asked for in L2 a tile earlier:
+// loads that wait for memory hold up the queue that the math warps'
+// shared-memory and tensor-memory loads go through). fp8: thread t has 16-byte
+// chunk t & 3 (16 channels) of every block for rows t >> 2 and + 64; fp4: chunk
+// t & 1 (32 channels) for row t >> 1.
+template <int KVF, int N>
+__device__ __forceinline__ void produce_codes(const PagedAttendParams& p, uint8_t* sm, uint32_t base_s, Cursor cur, int t,
+                                              int warp, double freq) {
+  constexpr int kChunks = KVF == 1 ? 4 : 2;      // 16-byte chunks of a row's block
+  constexpr int R = kTileRows * kChunks / N;     // rows of a thread
+  constexpr int kRowBytes = KVF == 1 ? 512 : 256, kScaleBytes = KVF == 1 ? 16 : 32;
+  constexpr int kScaleWords = kScaleBytes / 16;
+  const uint32_t bars = base_s + SM_BAR;
+  const int c = t % kChunks;
+  const int cs = chunk_shift(p.kv.page_shift);
+  int2* at = reinterpret_cast<int2*>(sm + SM_ROWAT);
+  Cursor ahead = cur;  // the tile whose rows are found next
+  // threads 0 .. 127: row t of tile n, two tiles before its conversion
+  auto publish = [&](uint32_t n) {
+    if (t < kTileRows && ahead.more()) {
+      const RowAt mine = row_at(p, ahead, t);
+      if (mine.page >= 0 && (t & ((1 << cs) - 1)) == 0) {
+        prefetch_l2(p.kv.pages + mine.page * p.kv.page_stride + (int64_t)mine.in_page * kRowBytes, (uint32_t)kRowBytes << cs);
+        prefetch_l2(p.kv.scales + mine.page * p.kv.scale_stride + (int64_t)mine.in_page * kScaleBytes, (uint32_t)kScaleBytes << cs);
+      }
+      if (mine.seen && mine.page < 0) set_flag(p.a.flags, CSA2_FLAG_BAD_PAGE);
+      at[128 * (n & 1u) + t] = mine.there() ? make_int2(mine.page, mine.in_page) : make_int2(-1, 0);
+    }
+    if (ahead.more()) ahead.next(p);
+    sync_producers<N>();
+  };
+  // a thread's rows of one tile; codes null: the row is not there
+  struct Rows {
+    const uint8_t* codes[R];
+    uint4 scale[R][kScaleWords];
+  };
+  auto find = [&](uint32_t n, Rows& r) {
+#pragma unroll
+    for (int u = 0; u < R; ++u) {
+      const int2 a = at[128 * (n & 1u) + t / kChunks + u * (N / kChunks)];
+      r.codes[u] = a.x >= 0 ? p.kv.pages + a.x * p.kv.page_stride + (int64_t)a.y * kRowBytes + 16 * c : nullptr;
+      const uint8_t* s = p.kv.scales + (a.x >= 0 ? a.x * p.kv.scale_stride + (int64_t)a.y * kScaleBytes : 0);
+#pragma unroll
+      for (int k = 0; k < kScaleWords; ++k)
+        r.scale[u][k] = a.x >= 0 ? *reinterpret_cast<const uint4*>(s + 16 * k) : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  uint4 code[R][4];
+  auto load = [&](const Rows& r, int half, int j) {  // block 4 half + j into the registers of j
+#pragma unroll
+    for (int u = 0; u < R; ++u)
+      code[u][j] = r.codes[u] != nullptr ? ldg_stream16(r.codes[u] + 16 * kChunks * (4 * half + j)) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  Rows now, next;
+  QLoad<N> ql;
+  ql.freq = freq;
+  ql.ask(p, sm, base_s, cur.qi, cur.span.t, 0u, t, warp);
+  publish(0);
+  find(0, now);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) load(now, 0, j);
+  publish(1);
+  bool first = true, live = true;  // live: see math_role
+  const uint32_t tiles = cur.tiles();
+#pragma unroll 1
+  for (uint32_t n = 0, seg = 0; n < tiles; ++n) {
+    const bool more = n + 1 < tiles;
+    if (first) {
+      if (seg > 0) {
+        live = live && warp_wait(bars + 8 * kQEmpty, (seg & 1u) ^ 1u, p.a.flags);
+        ql.ask(p, sm, base_s, cur.qi, cur.span.t, seg, t, warp);
+      }
+      ql.take(p, sm, base_s, seg, t);
+      ++seg;
+    }
+    first = cur.last();
+    next = now;
+    if (more) find(n + 1, next);
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int b = 4 * half + j;
+        if (j % 2 == 0 && n > 0) live = live && warp_wait(bars + 8 * (kEmpty + b / 2), (n & 1u) ^ 1u, p.a.flags);
+#pragma unroll
+        for (int u = 0; u < R; ++u) {
+          const int r = t / kChunks + u * (N / kChunks);
+          if (b == 0 && c == 0) sm[SM_ROWOK + 128 * (n & 1u) + r] = now.codes[u] != nullptr;
+          uint8_t* dst = sm + SM_KV + (uint32_t)b * 16384u + (uint32_t)r * 128u;
+          uint32_t o[8];
+          if constexpr (KVF == 1) {
+            // scale 2b + c / 2 of the row's 16
+            const uint4 sc = now.scale[u][0];
+            const uint32_t w = half == 0 ? (j < 2 ? sc.x : sc.y) : (j < 2 ? sc.z : sc.w);
+            fp8_to_bf16(code[u][j], (w >> (16 * (j & 1) + 8 * (c >> 1))) & 0xFFu, o);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              *reinterpret_cast<uint4*>(dst + (((2 * c + k) ^ (r & 7)) << 4)) =
+                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          } else {
+            // scales 4b + 2c and + 1 of the row's 32
+            const uint4 sc = half == 0 ? now.scale[u][0] : now.scale[u][kScaleWords - 1];
+            const uint32_t two = (j == 0 ? sc.x : (j == 1 ? sc.y : (j == 2 ? sc.z : sc.w))) >> (16 * c);
+            fp4_to_bf16(code[u][j].x, code[u][j].y, two & 0xFFu, o);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              *reinterpret_cast<uint4*>(dst + (((4 * c + k) ^ (r & 7)) << 4)) =
+                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+            fp4_to_bf16(code[u][j].z, code[u][j].w, (two >> 8) & 0xFFu, o);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              *reinterpret_cast<uint4*>(dst + (((4 * c + 2 + k) ^ (r & 7)) << 4)) =
+                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          }
+        }
+        if (half == 0) load(now, 1, j);
+        else if (more) load(next, 0, j);
+        if (j % 2 == 1) {  // two blocks a fence: it takes as long as half a block's conversion
+          fence_proxy_async_smem();
+          warp_arrive(bars + 8 * (kFull + b - 1));
+          warp_arrive(bars + 8 * (kFull + b));
+        }
+      }
+    }
+    now = next;
+    cur.next(p);
+    if (first && t == 0 && more) prefetch_l2(p.a.q + (int64_t)cur.qi * kHeads * kDim, 2u * kHeads * kDim);
+    if (more) publish(n + 2);
+  }
+}
+
+// The products of one tile, by one warp (leader: 1 in the lane that issues);
+// false: a wait ran out and nothing more was issued. n: the tile's number in
+// the run, seg: its query's.
+struct Issuer {
+  uint32_t bars, tmem_s, tmem_o, base_s, leader;
+  uint32_t* flags;
+  const uint32_t* dirty;  // null: no rows are cleared after they land
+  bool rope;
+  // S^T = KV Q^T, block by block as the rows land; the rope channels once more
+  // against q's residual
+  __device__ __forceinline__ bool scores(uint32_t n, uint32_t seg, bool first, bool last) const {
+    const uint64_t kv = sdesc_sw128(base_s + SM_KV, 16u, 1024u), q = sdesc_sw128(base_s + SM_Q, 16u, 1024u);
+    if (first && !wait_all_lanes(bars + 8 * kQFull, seg & 1u, flags)) return false;
+    // a block's barrier is looked at while the products of the block before
+    // are issued (a look takes 200 cycles from the instruction to the branch)
+    uint32_t landed = phase_done(bars + 8 * kFull, n & 1u);
+#pragma unroll
+    for (uint32_t b = 0; b < 8; ++b) {
+      if (!uniform(landed != 0u) && !wait_all_lanes(bars + 8 * (kFull + b), n & 1u, flags)) return false;
+      if (b == 0 && dirty != nullptr && uniform(dirty[n & 1u] != 0u) && !wait_all_lanes(bars + 8 * kCleared, n & 1u, flags)) return false;
+      if (b < 7) landed = phase_done(bars + 8 * (kFull + b + 1), n & 1u);
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k)
+        mma_one(leader, tmem_s, sdesc_add(kv, b * 16384u + 32u * k), sdesc_add(q, b * 8192u + 32u * k), kIdescQK, b | k);
+    }
+    if (rope) {
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k)
+        mma_one(leader, tmem_s, sdesc_add(kv, 7u * 16384u + 32u * k), sdesc_add(q, 8u * 8192u + 32u * k), kIdescQK, 1u);
+    }
+    commit_one(leader, bars + 8 * kScores);
+    if (last) commit_one(leader, bars + 8 * kQEmpty);
+    return true;
+  }
+  // O^T (+)= KV^T P^T, 128 output dims at a time
+  __device__ __forceinline__ void output(bool first, bool last) const {
+    const uint64_t kv = sdesc_sw128(base_s + SM_KV, 16384u, 1024u), pt = sdesc_sw128(base_s + SM_P, 8192u, 1024u);
+    tc_fence_after();
+#pragma unroll
+    for (uint32_t m = 0; m < 4; ++m) {
+#pragma unroll
+      for (uint32_t k = 0; k < 8; ++k)
+        mma_one(leader, tmem_o + 64u * m, sdesc_add(kv, m * 32768u + 2048u * k), sdesc_add(pt, 2048u * k), kIdescPV,
+                k > 0 || !first ? 1u : 0u);
+      commit_one(leader, bars + 8 * (kEmpty + m));
+    }
+    if (last) commit_one(leader, bars + 8 * kOut);
+  }
+  // after a wait that ran out: products still in flight land before tensor memory is freed
+  __device__ __forceinline__ void drain() const {
+    commit_one(leader, bars + 8 * kDrained);
+    wait_phase(bars + 8 * kDrained, 0u, flags);
+  }
+};
+
+// The products of a run, by the issuing warp.
+__device__ __forceinline__ void issue_role(const Issuer& mma, Cursor cur, const PagedAttendParams& p) {
+  const uint32_t tiles = cur.tiles();
+  bool live = true, first = true;
+#pragma unroll 1
+  for (uint32_t n = 0, seg = 0; n < tiles; ++n) {
+    const bool last = cur.last();
+    if (live) live = uniform(mma.scores(n, seg, first, last));
+    if (live) live = wait_all_lanes(mma.bars + 8 * kWeights, n & 1u, mma.flags);
+    if (live) mma.output(first, last);
+    first = last;
+    seg += last ? 1u : 0u;
+    cur.next(p);
+  }
+  if (!live) mma.drain();
+}
+
+// A head's reference moves only when a row's score exceeds it by more than
+// this (log2 units). Weights then reach 2^32, which bf16 and fp32 hold with
+// the same relative precision as weights below 1, and rows whose weight
+// underflows are 2^-126 of the reference's. With 2^8 a few rows four times as
+// large as the others moved some head's reference in nearly every tile, at
+// 1.0 us a move (decode of 128K rows, fp8).
+constexpr float kRefSlack = 32.f;
+
+// Softmax of one tile (thread: row = TMEM lane, heads 32 hh .. +31 of warp w,
+// hh = w / 4) and, at a query's end, its output or partial. Most tiles need
+// one vote on the references and neither a reduction nor a rescale; the
+// weights are summed in fp32 and rounded to bf16 for the product.
+// ISSUE: warp 0 issues the products too.
+template <bool ISSUE>
+__device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* sm, uint32_t base_s, uint32_t tmem_s,
+                                          uint32_t tmem_o, const Issuer& mma, Cursor cur, const Run& run, int warp) {
+  const SyncMath sy;
+  const uint32_t bars = base_s + SM_BAR;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int quad = warp & 3, hh = warp >> 2, row = quad * 32 + lane;
+  const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+  float* red = reinterpret_cast<float*>(sm + SM_RED);
+  float* m_run = reinterpret_cast<float*>(sm + SM_MRUN);
+  float* m_use = reinterpret_cast<float*>(sm + SM_MUSE);
+  float* alpha = reinterpret_cast<float*>(sm + SM_ALPHA);
+  const float4* mu4 = reinterpret_cast<const float4*>(m_use + 32 * hh);
+  const float scale = p.a.scale_log2;
+  const bool by_query = p.a.n_query < (int)gridDim.x;  // a join's index: its query, or the CTA that begins it
+  int2 my_join = make_int2(-1, -1);
+  int my_query = -1;
+  float lsum[32];
+  bool first = true, begins = false;
+  // A wait that ran out is recorded; from then on nothing is waited for or
+  // issued, and the loop only runs out, all threads meeting at its barriers.
+  bool live = true;
+  const uint32_t tiles = cur.tiles();
+#pragma unroll 1
+  for (uint32_t n = 0, seg = 0; n < tiles; ++n) {
+    const bool last = cur.last();
+    if (ISSUE && warp == 0 && live) live = uniform(mma.scores(n, seg, first, last));
+    if (first) {
+      begins = cur.tile() == 0;
+      const bool ends = cur.q0 + cur.span.n_tiles <= cur.run1;
+      if (begins && tid == 0) {
+        const QuerySpan& s = cur.span;
+        const bool seq_ok = s.b >= 0 && s.b < p.kv.n_seq;
+        if (s.b != -1 && !(seq_ok && s.t >= -1)) set_flag(p.a.flags, CSA2_FLAG_BAD_QUERY);
+        if (s.ok && s.vis.past_table) set_flag(p.a.flags, CSA2_FLAG_BAD_PAGE);
+        const int2 jn = ends ? make_int2(-1, -1)
+                             : make_int2((int)blockIdx.x, (int)(((cur.q0 + s.n_tiles) * run.ctas - 1) / run.total));
+        if (by_query) {
+          p.joins[cur.qi] = jn;
+          p.join_query[cur.qi] = cur.qi;
+        } else if (!ends) {
+          my_join = jn;
+          my_query = cur.qi;
+        }
+      }
+      if (tid < kHeads) {
+        m_run[tid] = -INFINITY;
+        m_use[tid] = 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < 32; ++k) lsum[k] = 0.f;
+      sy.sync();
+    }
+    live = live && warp_wait(bars + 8 * kScores, n & 1u, p.a.flags);
+    live = live && warp_wait(bars + 8 * kFull, n & 1u, p.a.flags);  // the producers' row flags and rope table
+    tc_fence_after();
+    const bool valid = sm[SM_ROWOK + 128 * (n & 1u) + row] != 0;
+    // Weights from the references as they stand, and with the barrier that
+    // hands them to the products a vote whether a row exceeded one: then (and
+    // at a query's first tile) the references move and the weights are formed
+    // once more.
+    float x[32];  // score - reference (log2 units) of this row and 32 heads, then its weight
+    bool move = first;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      if (move) {
+        uint32_t r[32];
+        tmem_ld32(tmem_s + lane_base + 32 * hh, r);
+        tmem_wait_ld();
+        // the largest of each head: over this warp's rows (lane k keeps head k), then over the four quadrants
+        float mine = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) {
+          const float v = warp_max(valid ? __uint_as_float(r[k]) * scale : -INFINITY);
+          if (lane == k) mine = v;
+        }
+        red[quad * 64 + 32 * hh + lane] = mine;
+        sy.sync();
+        bool moved = false;
+        if (tid < kHeads) {
+          const float top = fmaxf(fmaxf(red[tid], red[64 + tid]), fmaxf(red[128 + tid], red[192 + tid]));
+          const float mo = m_run[tid];
+          const float mn = (mo == -INFINITY || top > mo + kRefSlack) ? fmaxf(mo, top) : mo;
+          const float al = (mo == -INFINITY) ? 1.f : exp2f(mo - mn);
+          m_use[tid] = mn == -INFINITY ? 0.f : mn;
+          alpha[tid] = al;
+          m_run[tid] = mn;
+          moved = al != 1.f;
+        }
+        if (sy.any(moved)) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) lsum[k] *= alpha[32 * hh + k];
+          // (the products before this tile's scores are complete: they came first)
+#pragma unroll 1
+          for (int mt = 0; mt < 4; ++mt) {
+            const uint32_t a = tmem_o + (uint32_t)(64 * mt + 32 * hh) + lane_base;
+            tmem_ld32(a, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * alpha[32 * hh + k]);
+            tmem_st32(a, r);
+          }
+          tmem_wait_st();
+        }
+      }
+      {
+        uint32_t r[32];
+        tmem_ld32(tmem_s + lane_base + 32 * hh, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float4 m = mu4[k];
+          x[4 * k] = fmaf(__uint_as_float(r[4 * k]), scale, -m.x);
+          x[4 * k + 1] = fmaf(__uint_as_float(r[4 * k + 1]), scale, -m.y);
+          x[4 * k + 2] = fmaf(__uint_as_float(r[4 * k + 2]), scale, -m.z);
+          x[4 * k + 3] = fmaf(__uint_as_float(r[4 * k + 3]), scale, -m.w);
+        }
+      }
+      float over = x[0];
+#pragma unroll
+      for (int k = 1; k < 32; ++k) over = fmaxf(over, x[k]);
+      uint32_t packed[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        x[2 * k] = exp2_approx(x[2 * k]);
+        x[2 * k + 1] = exp2_approx(x[2 * k + 1]);
+        packed[k] = valid ? pack_bf16(x[2 * k], x[2 * k + 1]) : 0u;
+      }
+#pragma unroll
+      for (int c4 = 0; c4 < 4; ++c4) {
+        const int c = 4 * hh + c4;
+        *reinterpret_cast<uint4*>(sm + SM_P + (uint32_t)row * 128u + ((uint32_t)(c ^ (row & 7)) << 4)) =
+            make_uint4(packed[4 * c4], packed[4 * c4 + 1], packed[4 * c4 + 2], packed[4 * c4 + 3]);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      move = sy.any(valid && over > kRefSlack);
+      if (!move) break;
+    }
+    if (!ISSUE) warp_arrive(bars + 8 * kWeights);
+    else if (warp == 0 && live) mma.output(first, last);
+    if (valid) {
+#pragma unroll
+      for (int k = 0; k < 32; ++k) lsum[k] += x[k];
+    }
+    first = false;
+    if (last) {
+      const bool whole = begins && cur.q0 + cur.span.n_tiles <= cur.run1;
+      red[quad * 64 + 32 * hh + lane] = reduce_scatter32<false>(lsum, lane);
+      sy.sync();
+      if (tid < kHeads) {
+        const float l = red[tid] + red[64 + tid] + red[128 + tid] + red[192 + tid];
+        const float mr = m_run[tid];
+        if (whole) {
+          // fo = e^{m - M} / den, den = l e^{m - M} + e^{sink - M}
+          const float sk = p.a.sink != nullptr ? p.a.sink[tid] : -INFINITY, sk2 = sk * 1.4426950408889634f;
+          const float M = fmaxf(mr, sk2);
+          float fo = 0.f, lse = sk;  // no row seen: the denominator is the sink's
+          if (mr != -INFINITY) {
+            const float em = exp2f(mr - M);
+            const float den = l * em + exp2f(sk2 - M);
+            fo = em / den;
+            lse = (M + log2f(den)) * 0.6931471805599453f;
+          }
+          alpha[tid] = fo;
+          if (p.a.lse != nullptr && cur.span.b != -1) p.a.lse[(int64_t)cur.qi * kHeads + tid] = lse;
+        } else {
+          const int64_t at = (int64_t)part_slot((int)blockIdx.x, begins) * kHeads + tid;
+          p.a.part_m[at] = mr;
+          p.a.part_l[at] = l;
+        }
+      }
+      sy.sync();
+      live = live && warp_wait(bars + 8 * kOut, seg & 1u, p.a.flags);
+      tc_fence_after();
+      const float2* rope_tab = reinterpret_cast<const float2*>(sm + SM_ROPETAB) + 32 * (seg & 3u);
+      const int first_rope = kDim - 2 * p.a.rp.pairs;
+      if (!whole) {
+        float* po = p.a.part_o + (int64_t)part_slot((int)blockIdx.x, begins) * kHeads * kDim;
+#pragma unroll 1
+        for (int mt = 0; mt < 4; ++mt) {
+          uint32_t r[32];
+          tmem_ld32(tmem_o + (uint32_t)(64 * mt + 32 * hh) + lane_base, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            reinterpret_cast<uint4*>(po)[part_at(8 * hh + k, 128 * mt + row)] =
+                make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+        }
+      } else if (cur.span.b != -1) {
+        uint16_t* out = p.a.out + (int64_t)cur.qi * kHeads * kDim;
+#pragma unroll 1
+        for (int mt = 0; mt < 4; ++mt) {
+          const int d = 128 * mt + row;
+          uint32_t r[32];
+          tmem_ld32(tmem_o + (uint32_t)(64 * mt + 32 * hh) + lane_base, r);
+          tmem_wait_ld();
+          float v[32];
+#pragma unroll
+          for (int k = 0; k < 32; ++k) v[k] = alpha[32 * hh + k] == 0.f ? 0.f : __uint_as_float(r[k]) * alpha[32 * hh + k];
+          // rope channels rotated back by -t: only warps that hold some
+          // exchange values with the pair's other lane (warp-uniform test)
+          if (p.a.rp.pairs > 0 && 128 * mt + 32 * quad + 31 >= first_rope) {
+            const bool rope = d >= first_rope;
+            const float2 cs = rope ? rope_tab[(d - first_rope) >> 1] : make_float2(1.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const float partner = __shfl_xor_sync(0xffffffffu, v[k], 1);
+              if (rope) v[k] = (d & 1) ? (v[k] * cs.x - partner * cs.y) : (v[k] * cs.x + partner * cs.y);
+            }
+          }
+          store_out_block(sm, v, mt, out, sy);
+        }
+      }
+      ++seg;
+      first = true;
+      tc_fence_before();  // O^T has been read
+      sy.sync();          // and red, alpha and the rope table are free for the next query
+    }
+    cur.next(p);
+  }
+  if (ISSUE && warp == 0 && !live) mma.drain();
+  if (!by_query && tid == 0) {
+    p.joins[blockIdx.x] = my_join;
+    p.join_query[blockIdx.x] = my_query;
+  }
+}
+
+// TMA: of bf16 rows (see produce_bf16)
+template <int KVF, bool TMA>
+__global__ void __launch_bounds__(Roles<KVF>::kThreads, 1) attend_paged_kernel(const __grid_constant__ PagedAttendParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_s = smem_u32(smem_raw);
   const uint32_t base_s = (raw_s + 1023u) & ~1023u;
   uint8_t* sm = smem_raw + (base_s - raw_s);
-  float* m_run = reinterpret_cast<float*>(sm + SM_MRUN);
-  float* l_run = reinterpret_cast<float*>(sm + SM_LRUN);
-  int64_t* rows = reinterpret_cast<int64_t*>(sm + SM_ROWS);  // page << 16 | row in the page, -1 for none
+  const uint32_t bars = base_s + SM_BAR;
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + SM_MISC);
-  float2* rope_tab = reinterpret_cast<float2*>(sm + SM_ROPE);
-  const uint32_t mbar = base_s + SM_MISC;
-  const uint32_t tslot = base_s + SM_MISC + 8;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int quad = warp & 3;
-  const int row = quad * 32 + lane;
+  Run* run = reinterpret_cast<Run*>(sm + SM_RUN);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // in a uniform register
 
   pdl_trigger();
+  // frequencies of the last producer warp's lanes (parameters come from memory
+  // the first time, a line at a time)
+  const double freq = warp == kFirstProducer + Roles<KVF>::kProducers - 1 && lane < p.a.rp.pairs ? p.a.rp.freq[lane] : 0.0;
   if (warp == 0) {
-    tmem_alloc(tslot, kTmemCols);
+    tmem_alloc(base_s + SM_MISC + 8, kTmemCols);
     tmem_relinquish();
   }
-  if (tid == 0) {
-    mbar_init(mbar, 1);
+  if (tid == kFirstProducer * 32) {
+    constexpr uint32_t np = Roles<KVF>::kProducers;
+    for (uint32_t b = 0; b < kBars; ++b)
+      mbar_init(bars + 8 * b, b < kEmpty ? (TMA ? 1u : np) : (b == kQFull ? np + 1 : (b == kCleared ? np : (b == kWeights ? (uint32_t)kAttWarps : 1u))));
     fence_mbar_init();
-    misc[3] = 0;
   }
   pdl_wait();
-
-  // ---- this CTA's run of tiles: thread x counts the tiles of its share of
-  // the queries, a scan places the shares, and the thread whose share holds
-  // the run's first tile finds its query
+  // ---- this CTA's run of tiles: math thread x counts the tiles of its share
+  // of the queries, a scan places the shares, and the thread whose share
+  // holds the run's first tile finds its query
   const int Q = p.a.n_query;
   __shared__ int64_t warp_sum[kAttWarps];
-  __shared__ int64_t s_first_tile;  // first tile of query s_query among all
-  __shared__ int s_query;
   const int per = (Q + kAttThreads - 1) / kAttThreads;
   const int q_lo = min(Q, tid * per), q_hi = min(Q, q_lo + per);
-  int64_t mine = 0;
-  for (int i = q_lo; i < q_hi; ++i) mine += query_span(p, i).n_tiles;
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) warp_sum[warp] = incl;
-  __syncthreads();
-  int64_t base = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kAttWarps; ++w) {
-    if (w < warp) base += warp_sum[w];
-    total += warp_sum[w];
-  }
-  // no run is empty: the CTAs of a split query are neighbours
-  const int c = (int)blockIdx.x;
-  const int G = (int)min((int64_t)gridDim.x, total);
-  const int64_t run0 = c < G ? (int64_t)c * total / G : total, run1 = c < G ? (int64_t)(c + 1) * total / G : total;
-  const int64_t before = base + incl - mine;
-  if (run0 >= before && run0 < before + mine) {
-    int64_t at = before;
-    int i = q_lo;
-    for (;; ++i) {
-      const int n = query_span(p, i).n_tiles;
-      if (run0 < at + n) break;
-      at += n;
+  QuerySpan span;
+  int64_t mine = 0, incl = 0;
+  if (warp < kAttWarps) {
+#pragma unroll 4
+    for (int i = q_lo; i < q_hi; ++i) {
+      span = query_span(p, i);
+      mine += span.n_tiles;
     }
-    s_query = i;
-    s_first_tile = at;
+    incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
   }
-  const float sink_l2 = (tid < kHeads && p.a.sink != nullptr) ? p.a.sink[tid] * 1.4426950408889634f : -INFINITY;
+  __syncthreads();
+  if (warp < kAttWarps) {
+    int64_t before = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kAttWarps; ++w) {
+      if (w < warp) before += warp_sum[w];
+      total += warp_sum[w];
+    }
+    // no run is empty: the CTAs of a split query are neighbours
+    const int c = (int)blockIdx.x, G = (int)min((int64_t)gridDim.x, total);
+    const int64_t run0 = c < G ? (int64_t)c * total / G : total, run1 = c < G ? (int64_t)(c + 1) * total / G : total;
+    if (tid == 0) {
+      run->total = total;
+      run->ctas = G;
+      if (run0 == run1) run->cur.at = run->cur.run1 = total;
+    }
+    if (run0 < run1 && run0 >= before && run0 < before + mine) {
+      int i = q_lo;
+      if (per > 1) {
+        for (;; ++i) {
+          span = query_span(p, i);
+          if (run0 < before + span.n_tiles) break;
+          before += span.n_tiles;
+        }
+      }
+      run->cur.at = run0;
+      run->cur.run1 = run1;
+      run->cur.q0 = before;
+      run->cur.qi = i;
+      run->cur.span = span;
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t taddr = misc[2];
+  const uint32_t taddr = (uint32_t)uniform((int)misc[2]);
   const uint32_t tmem_s = taddr, tmem_o = taddr + 64;
-  const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-  uint32_t phase = 0;
-  bool aborted = false;
-  const bool rope = p.a.rp.pairs > 0;
-  const bool by_query = Q < (int)gridDim.x;  // the index of a join: its query, or the CTA that begins it
-
-  int qi = 0;
-  int64_t q0 = 0;
-  if (run0 < run1) {
-    qi = s_query;
-    q0 = s_first_tile;
+  Cursor cur = run->cur;
+  if (uniform(cur.more())) {
+    const Issuer mma{bars, tmem_s, tmem_o, base_s, elect_one(), p.a.flags,
+                     TMA ? reinterpret_cast<const uint32_t*>(sm + SM_DIRTY) : nullptr, p.a.rp.pairs > 0};
+    if (Roles<KVF>::kOwnIssuer && warp == Roles<KVF>::kIssuer) {
+      issue_role(mma, cur, p);
+    } else if (warp >= kFirstProducer) {
+      const int t = tid - 32 * kFirstProducer;
+      if constexpr (KVF == 0) produce_bf16<Roles<KVF>::kProducerThreads, TMA>(p, sm, base_s, cur, t, warp - kFirstProducer, freq);
+      else produce_codes<KVF, Roles<KVF>::kProducerThreads>(p, sm, base_s, cur, t, warp - kFirstProducer, freq);
+      cp_async_wait_all();  // no copy may still be landing when the CTA exits
+    } else {
+      math_role<!Roles<KVF>::kOwnIssuer>(p, sm, base_s, tmem_s, tmem_o, mma, cur, *run, warp);
+    }
   }
-  int my_join_query = -1;
-  int2 my_join = make_int2(-1, -1);
-  for (int64_t at = run0; at < run1 && !aborted; ++qi) {
-    const QuerySpan qs = query_span(p, qi);
-    const int tile_begin = (int)(at - q0);
-    const int tile_end = (int)min((int64_t)qs.n_tiles, run1 - q0);
-    const bool begins = tile_begin == 0, ends = tile_end == qs.n_tiles;
-    const bool has_rows = qs.vis.count > 0;
-    if (begins && tid == 0) {
-      if (!qs.ok && !(qs.b == -1) && !(qs.b >= 0 && qs.b < p.kv.n_seq && qs.t == -1))
-        set_flag(p.a.flags, CSA2_FLAG_BAD_QUERY);
-      if (qs.ok && qs.vis.past_table) set_flag(p.a.flags, CSA2_FLAG_BAD_PAGE);
-    }
-    const int2 jn = (begins && !ends) ? make_int2(c, (int)(((q0 + qs.n_tiles) * G - 1) / total)) : make_int2(-1, -1);
-    if (by_query) {
-      if (begins && tid == 0) {
-        p.joins[qi] = jn;
-        p.join_query[qi] = qi;
-      }
-    } else if (begins && !ends) {
-      my_join = jn;
-      my_join_query = qi;
-    }
-    if (has_rows) {
-      copy_q_async(p.a, base_s, qi);
-      cp_async_commit();
-    }
-    if (tid < p.a.rp.pairs) {
-      float cc = 1.f, sn = 0.f;
-      if (qs.ok) rope_cs(p.a.rp, tid, qs.t, cc, sn);
-      rope_tab[tid] = make_float2(cc, sn);
-    }
-    if (tid < kHeads) {
-      m_run[tid] = -INFINITY;
-      l_run[tid] = 0.f;
-    }
-    float lsum[32];
-#pragma unroll
-    for (int k = 0; k < 32; ++k) lsum[k] = 0.f;
-    for (int tile = tile_begin; has_rows && tile < tile_end; ++tile) {
-      if (tid < kTileRows) {
-        const int i = tile * kTileRows + tid;
-        int64_t src = -1;
-        if (i < qs.vis.count) {
-          const int64_t pos = visible_pos(qs.vis, i);
-          const int32_t g = page_of(p.kv, qs.b, pos);
-          if (g >= 0) src = ((int64_t)g << 16) | (pos & ((1 << p.kv.page_shift) - 1));
-          else set_flag(p.a.flags, CSA2_FLAG_BAD_PAGE);
-        }
-        rows[tid] = src;
-      }
-      __syncthreads();
-      // a warp takes rows warp, warp + 8, ..., eight rows' loads in flight
-      constexpr int kBatch = 8;
-#pragma unroll 1
-      for (int r0 = warp; r0 < kTileRows; r0 += kAttWarps * kBatch) {
-        if constexpr (KVF == 0) {
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            const int r = r0 + kAttWarps * j;
-            const int64_t src = rows[r];
-            const uint8_t* g = p.kv.pages + (src >= 0 ? (src >> 16) * p.kv.page_stride + (src & 0xFFFF) * 1024 : 0);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int cc = lane + 32 * u;
-              const uint32_t dst = base_s + SM_KV + (uint32_t)(cc >> 3) * 16384u + (uint32_t)r * 128u +
-                                   ((uint32_t)((cc & 7) ^ (r & 7)) << 4);
-              cp_async16(dst, g + 16 * cc, src >= 0 ? 16u : 0u);
-            }
-          }
-        } else {
-          uint4 codes[kBatch];
-          uint32_t sb[kBatch];
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            const int64_t src = rows[r0 + kAttWarps * j];
-            codes[j] = make_uint4(0u, 0u, 0u, 0u);
-            sb[j] = 0;
-            if (src >= 0) {
-              const int64_t g = src >> 16, r = src & 0xFFFF;
-              if constexpr (KVF == 1) {
-                codes[j] = ldg_stream16(p.kv.pages + g * p.kv.page_stride + r * 512 + 16 * lane);
-                sb[j] = p.kv.scales[g * p.kv.scale_stride + r * 16 + (lane >> 1)];
-              } else {
-                const uint2 w = ldg_stream8(p.kv.pages + g * p.kv.page_stride + r * 256 + 8 * lane);
-                codes[j].x = w.x;
-                codes[j].y = w.y;
-                sb[j] = p.kv.scales[g * p.kv.scale_stride + r * 32 + lane];
-              }
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < kBatch; ++j) {
-            const int r = r0 + kAttWarps * j;
-            uint32_t o[8];
-            if constexpr (KVF == 1) {
-              const float sc = ue8m0_value(sb[j]);
-              const uint32_t cw[4] = {codes[j].x, codes[j].y, codes[j].z, codes[j].w};
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const float2 a = e4m3x2_to_float2((uint16_t)(cw[k] & 0xFFFFu));
-                const float2 b = e4m3x2_to_float2((uint16_t)(cw[k] >> 16));
-                o[2 * k] = pack_bf16(a.x * sc, a.y * sc);
-                o[2 * k + 1] = pack_bf16(b.x * sc, b.y * sc);
-              }
-            } else {
-              const float sc = e4m3_value(sb[j]) * kE2M1Unscale;
-#pragma unroll
-              for (int b = 0; b < 8; ++b) {
-                const float2 f = e2m1x2_to_float2_scaled(((b < 4 ? codes[j].x : codes[j].y) >> (8 * (b & 3))) & 0xFFu);
-                o[b] = pack_bf16(f.x * sc, f.y * sc);  // exact: <= 6 significant bits
-              }
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const int cc = 2 * lane + u;
-              const uint32_t off = SM_KV + (uint32_t)(cc >> 3) * 16384u + (uint32_t)r * 128u +
-                                   ((uint32_t)((cc & 7) ^ (r & 7)) << 4);
-              *reinterpret_cast<uint4*>(sm + off) = make_uint4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-            }
-          }
-        }
-      }
-      cp_async_wait_all();
-      if (tile == tile_begin && rope) {
-        __syncthreads();
-        q_rope_split(sm, p.a.rp);
-      }
-      fence_proxy_async_smem();
-      __syncthreads();
-      if (tid == 0) {
-        tc_fence_after();
-        issue_qk(base_s, tmem_s, 0, 1, rope);
-        mma_commit(mbar);
-      }
-      bool ok = mbar_wait(mbar, phase, p.a.flags);
-      phase ^= 1u;
-      if (!__syncthreads_and(ok)) { aborted = true; break; }
-      tc_fence_after();
-      tile_softmax<true>(p.a, sm, tmem_s, tmem_o, lane_base, rows[row] >= 0, tile == tile_begin, &misc[3], lsum, SyncCta{});
-      if (tid == 0) {
-        tc_fence_after();
-        issue_pv(base_s, tmem_o, tile > tile_begin);
-        mma_commit(mbar);
-      }
-      ok = mbar_wait(mbar, phase, p.a.flags);
-      phase ^= 1u;
-      if (!__syncthreads_and(ok)) { aborted = true; break; }
-      tc_fence_after();
-    }
-    __syncthreads();
-    if (!aborted && qs.b != -1) {
-      AttendParams st = p.a;
-      st.direct = (begins && ends) ? 1 : 2;
-      attend_store(st, sm, st.direct == 1 ? qi : part_slot(c, begins), 0, has_rows, lsum, tmem_o, lane_base, sink_l2,
-                   SyncCta{});
-    }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    at = q0 + tile_end;
-    q0 += qs.n_tiles;
-  }
-  if (!by_query && tid == 0) {
-    p.joins[c] = my_join;
-    p.join_query[c] = my_join_query;
-  }
-  cp_async_wait_all();
-  if (aborted) mbar_wait(mbar, phase ^ 1u, p.a.flags, 1000000000ull);  // tensor-core work in flight lands first
+  if (cur.at >= cur.run1 && Q >= (int)gridDim.x && tid == 0) p.joins[blockIdx.x] = make_int2(-1, -1);
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(taddr, kTmemCols);
 }
 
-// Join of a split query's partials: one CTA per (query, head). With M the
-// largest reference of its parts and the sink, o = sum_g e^(m_g - M) O_g /
-// (sum_g e^(m_g - M) l_g + e^(sink - M)), its rope channels rotated back.
-// Four groups of 128 threads take every fourth part, 4 channels a thread.
-__global__ void __launch_bounds__(kJoinThreads) attend_paged_join_kernel(const PagedAttendParams p) {
-  __shared__ float wpart[512];
-  __shared__ float red[kJoinThreads / 32];
-  __shared__ float4 acc_s[4][128];
+// Join of a split query's partials. With M the largest reference of its parts
+// and the sink, o = sum_g e^(m_g - M) O_g / (sum_g e^(m_g - M) l_g +
+// e^(sink - M)), its rope channels rotated back. Latency-bound (128 KB a part,
+// from L2): a warp takes four heads and 32 dims and needs no barrier; lanes
+// (part, head) hold the weights of eight parts, which the lanes' dims take by
+// shuffles, and the first eight parts are under way before their weights are
+// known. GROUPS 1: four warps a CTA, next to each other in dims. GROUPS 8: the
+// eight warps of a CTA share the dims and take every eighth batch of parts, for
+// the few queries that have many.
+constexpr int kJoinBatch = 8;
+template <int GROUPS>
+__global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS) attend_paged_join_kernel(const __grid_constant__ PagedAttendParams p) {
+  constexpr int kWarps = GROUPS == 1 ? 4 : GROUPS, kSpan = GROUPS == 1 ? 128 : 32;  // warps and dims of a CTA
   pdl_wait();
   const int2 jn = p.joins[blockIdx.x];
   if (jn.x < 0) return;
   const int qi = p.join_query[blockIdx.x];
-  const int h = blockIdx.y;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = GROUPS == 1 ? 0 : warp;
+  const int hq = blockIdx.y / (kDim / kSpan);
+  const int d = (blockIdx.y % (kDim / kSpan)) * kSpan + (GROUPS == 1 ? 32 * warp : 0) + lane;
   const int n = jn.y - jn.x + 1;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const float sk = p.a.sink != nullptr ? p.a.sink[h] : -INFINITY;
   auto slot = [&](int k) { return (int64_t)(k == 0 ? part_slot(jn.x, true) : part_slot(jn.x + k, false)); };
-  // n <= gridDim of the tile kernel <= 512 parts: one a thread
-  const float m = tid < n ? p.a.part_m[slot(tid) * kHeads + h] : -INFINITY;
-  const float l = tid < n ? p.a.part_l[slot(tid) * kHeads + h] : 0.f;
-  float M = m;
+  float4 v[kJoinBatch];
+  auto fetch = [&](int k0) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (lane == 0) red[warp] = M;
-  __syncthreads();
-  M = sk;
-#pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) M = fmaxf(M, red[w]);
-  const float e = (M == -INFINITY || m == -INFINITY) ? 0.f : expf(m - M);
-  wpart[tid] = e;
-  float den = e * l;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-  __syncthreads();
-  if (lane == 0) red[warp] = den;
-  __syncthreads();
-  den = M == -INFINITY ? 0.f : expf(sk - M);
-#pragma unroll
-  for (int w = 0; w < kJoinThreads / 32; ++w) den += red[w];
-  const int g = tid >> 7, ch = 4 * (tid & 127);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = g; k < n; k += 4) {
-    const float w = wpart[k];
-    const float4 v = *reinterpret_cast<const float4*>(p.a.part_o + (slot(k) * kHeads + h) * kDim + ch);
-    acc.x = fmaf(w, v.x, acc.x);
-    acc.y = fmaf(w, v.y, acc.y);
-    acc.z = fmaf(w, v.z, acc.z);
-    acc.w = fmaf(w, v.w, acc.w);
-  }
-  acc_s[g][tid & 127] = acc;
-  __syncthreads();
-  if (g != 0) return;
-#pragma unroll
-  for (int k = 1; k < 4; ++k) {
-    const float4 v = acc_s[k][tid];
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
-  }
-  const float inv = den > 0.f ? 1.f / den : 0.f;
-  acc.x *= inv;
-  acc.y *= inv;
-  acc.z *= inv;
-  acc.w *= inv;
+    for (int u = 0; u < kJoinBatch; ++u)
+      v[u] = k0 + u < n ? reinterpret_cast<const float4*>(p.a.part_o + slot(k0 + u) * kHeads * kDim)[part_at(hq, d)]
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  fetch(kJoinBatch * group);
+  const int head = 4 * hq + (lane & 3), mine = lane >> 2;  // this lane's head, and its part of a batch
   const int first_rope = kDim - 2 * p.a.rp.pairs;
-  if (ch >= first_rope) {
-    const int64_t t = p.a.q_pos[qi];
-    float c0, s0, c1, s1;
-    rope_cs(p.a.rp, (ch - first_rope) >> 1, t, c0, s0);
-    rope_cs(p.a.rp, ((ch - first_rope) >> 1) + 1, t, c1, s1);
-    acc = make_float4(acc.x * c0 + acc.y * s0, acc.y * c0 - acc.x * s0, acc.z * c1 + acc.w * s1,
-                      acc.w * c1 - acc.z * s1);
+  const int64_t t = p.a.q_pos[qi];
+  const float sink = p.a.sink != nullptr ? p.a.sink[head] : -INFINITY;
+  const float sk = sink * 1.4426950408889634f;  // references and scores are in log2 units
+  // every warp forms the head's maximum and denominator over all parts
+  float M = -INFINITY;
+  for (int k = mine; k < n; k += kJoinBatch) M = fmaxf(M, p.a.part_m[slot(k) * kHeads + head]);
+#pragma unroll
+  for (int o = 16; o >= 4; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  const bool none = M == -INFINITY;  // no row in any part
+  M = fmaxf(M, sk);
+  float den = 0.f;
+  for (int k = mine; k < n; k += kJoinBatch) {
+    const float m = p.a.part_m[slot(k) * kHeads + head];
+    den += m == -INFINITY ? 0.f : exp2f(m - M) * p.a.part_l[slot(k) * kHeads + head];
   }
-  *reinterpret_cast<uint2*>(p.a.out + ((int64_t)qi * kHeads + h) * kDim + ch) =
-      make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
-  if (tid == 0 && p.a.lse != nullptr) p.a.lse[(int64_t)qi * kHeads + h] = M == -INFINITY ? -INFINITY : M + logf(den);
+#pragma unroll
+  for (int o = 16; o >= 4; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
+  den = none ? 1.f : den + exp2f(sk - M);
+  float cs = 1.f, sn = 0.f;
+  if (d >= first_rope) rope_cs(p.a.rp, (d - first_rope) >> 1, t, cs, sn);
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int k0 = kJoinBatch * group; k0 < n; k0 += kJoinBatch * GROUPS) {
+    if (k0 != kJoinBatch * group) fetch(k0);
+    const float m = k0 + mine < n ? p.a.part_m[slot(k0 + mine) * kHeads + head] : -INFINITY;
+    const float e = m == -INFINITY ? 0.f : exp2f(m - M);
+#pragma unroll
+    for (int u = 0; u < kJoinBatch; ++u) {
+      o[0] = fmaf(__shfl_sync(0xffffffffu, e, 4 * u), v[u].x, o[0]);
+      o[1] = fmaf(__shfl_sync(0xffffffffu, e, 4 * u + 1), v[u].y, o[1]);
+      o[2] = fmaf(__shfl_sync(0xffffffffu, e, 4 * u + 2), v[u].z, o[2]);
+      o[3] = fmaf(__shfl_sync(0xffffffffu, e, 4 * u + 3), v[u].w, o[3]);
+    }
+  }
+  if constexpr (GROUPS > 1) {
+    __shared__ float4 acc[kWarps - 1][32];
+    if (warp > 0) acc[warp - 1][lane] = make_float4(o[0], o[1], o[2], o[3]);
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int k = 0; k < kWarps - 1; ++k) {
+      const float4 a = acc[k][lane];
+      o[0] += a.x;
+      o[1] += a.y;
+      o[2] += a.z;
+      o[3] += a.w;
+    }
+  }
+  if (d < 4 && p.a.lse != nullptr)  // lanes 0 .. 3 of the warp of dims 0 ..: a head each
+    p.a.lse[(int64_t)qi * kHeads + head] = none ? sink : (M + log2f(den)) * 0.6931471805599453f;
+  const float inv = none ? 0.f : 1.f / den;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) o[u] *= __shfl_sync(0xffffffffu, inv, u);  // lane u holds head u's
+  if ((d | 31) >= first_rope) {  // whole warps: a warp's dims are 32 in a row
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float partner = __shfl_xor_sync(0xffffffffu, o[u], 1);
+      o[u] = (d & 1) ? o[u] * cs - partner * sn : o[u] * cs + partner * sn;
+    }
+  }
+  // even lanes store heads 0 and 1, odd lanes heads 2 and 3, two dims a store
+  uint32_t* out = reinterpret_cast<uint32_t*>(p.a.out + ((int64_t)qi * kHeads + 4 * hq) * kDim);
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const float give = (d & 1) ? o[u] : o[2 + u], keep = (d & 1) ? o[2 + u] : o[u];
+    const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+    const int h = (d & 1) ? 2 + u : u;
+    out[(h * kDim + (d & ~1)) >> 1] = (d & 1) ? pack_bf16(got, keep) : pack_bf16(keep, got);
+  }
 }
 
 namespace {
 constexpr size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
+// Tensor map of bf16 rows, boxes of 64 channels (128 bytes, the swizzle's width).
+cudaError_t encode_bf16_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                            const uint32_t* box) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  if (encode == nullptr) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
+    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  const uint32_t ones[3] = {1u, 1u, 1u};
+  cuuint64_t d[3], st[2];
+  cuuint32_t bx[3], es[3];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    es[i] = ones[i];
+    if (i + 1 < rank) st[i] = strides[i];
+  }
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, st, bx, es,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
 // Every CTA sums the tile counts of all queries before it starts: 16 a thread
 // at this many. More queries go in launches of this many, one after another.
 constexpr int kMaxQueries = 4096;
 }  // namespace
 
-int attend_paged_ctas(int num_sms) { return num_sms < 512 ? num_sms : 512; }
+int attend_paged_ctas(int num_sms) { return num_sms < kMaxCtas ? num_sms : kMaxCtas; }
 
 size_t attend_paged_workspace_bytes(int num_sms) {
   const size_t slots = 2 * (size_t)attend_paged_ctas(num_sms);
@@ -434,6 +1254,10 @@ cudaError_t launch_attend_paged(cudaStream_t st, int num_sms, int kv_fmt, Attend
   w += al256(slots * 8);
   p.join_query = reinterpret_cast<int32_t*>(w);
   const int Q = a.n_query;
+  const int chunk = 1 << chunk_shift(kv.page_shift);
+  const uint64_t kv_dims[3] = {(uint64_t)kDim, 1ull << kv.page_shift, (uint64_t)kv.n_pages};
+  const uint64_t kv_strides[2] = {2u * kDim, (uint64_t)kv.page_stride};
+  const uint32_t kv_box[3] = {64u, (uint32_t)chunk, 1u};
   for (int q0 = 0; q0 < Q; q0 += kMaxQueries) {
     const int nq = Q - q0 < kMaxQueries ? Q - q0 : kMaxQueries;
     p.a.n_query = nq;
@@ -442,20 +1266,30 @@ cudaError_t launch_attend_paged(cudaStream_t st, int num_sms, int kv_fmt, Attend
     p.a.seq_of_q = a.seq_of_q + q0;
     p.a.out = a.out + (int64_t)q0 * kHeads * kDim;
     p.a.lse = a.lse != nullptr ? a.lse + (int64_t)q0 * kHeads : nullptr;
-    cudaError_t e;
-#define CSA2_PAGED(F)                                                                                              \
-  do {                                                                                                             \
-    e = cudaFuncSetAttribute(attend_paged_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kAttSmemBytes); \
-    if (e == cudaSuccess)                                                                                          \
-      e = launch_ex(attend_paged_kernel<F>, dim3(G), dim3(kAttThreads), kAttSmemBytes, st, false, 0, p);             \
+    const uint64_t q_dims[2] = {(uint64_t)kDim, (uint64_t)kHeads * nq}, q_strides[1] = {2u * kDim};
+    const uint32_t q_box[2] = {64u, (uint32_t)kHeads};
+    cudaError_t e = encode_bf16_map(&p.q_map, 2, p.a.q, q_dims, q_strides, q_box);
+    if (e == cudaSuccess && kv_fmt == 0) e = encode_bf16_map(&p.kv_map, 3, kv.pages, kv_dims, kv_strides, kv_box);
+    if (e != cudaSuccess) return e;
+#define CSA2_PAGED(F, T)                                                                                               \
+  do {                                                                                                                \
+    e = cudaFuncSetAttribute(attend_paged_kernel<F, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kPagedSmemBytes); \
+    if (e == cudaSuccess)                                                                                             \
+      e = launch_ex(attend_paged_kernel<F, T>, dim3(G), dim3(Roles<F>::kThreads), kPagedSmemBytes, st, true, 0, p);  \
   } while (0)
-    if (kv_fmt == 0) CSA2_PAGED(0);
-    else if (kv_fmt == 1) CSA2_PAGED(1);
-    else CSA2_PAGED(2);
+    if (kv_fmt == 0 && chunk >= 8) CSA2_PAGED(0, true);
+    else if (kv_fmt == 0) CSA2_PAGED(0, false);
+    else if (kv_fmt == 1) CSA2_PAGED(1, false);
+    else CSA2_PAGED(2, false);
 #undef CSA2_PAGED
     if (e != cudaSuccess) return e;
     *n_launch += 1;
-    e = launch_ex(attend_paged_join_kernel, dim3((unsigned)(nq < G ? nq : G), kHeads), dim3(kJoinThreads), 0, st, true, 0, p);
+    const int joins = nq < G ? nq : G;
+    // a query has more than two batches of parts only where there are few queries
+    if (joins * 2 * kJoinBatch <= G)
+      e = launch_ex(attend_paged_join_kernel<8>, dim3((unsigned)joins, kHeads / 4 * (kDim / 32)), dim3(256), 0, st, true, 0, p);
+    else
+      e = launch_ex(attend_paged_join_kernel<1>, dim3((unsigned)joins, kHeads / 4 * (kDim / 128)), dim3(128), 0, st, true, 0, p);
     if (e != cudaSuccess) return e;
     *n_launch += 1;
   }
