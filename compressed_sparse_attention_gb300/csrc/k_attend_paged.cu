@@ -14,6 +14,7 @@
 // kernel sums. The products and softmax of a tile are those of attend_tile.cuh.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <type_traits>
 
 #include "attend_tile.cuh"
 #include "paged.cuh"
@@ -102,14 +103,14 @@ struct Roles {
 // shared memory behind attend_tile.cuh's layout
 constexpr uint32_t SM_BAR = SM_TOTAL;                 // mbarriers
 constexpr uint32_t SM_ROWOK = SM_BAR + 256;           // uint8 [2][128]: rows that are there, by the tile's parity
-constexpr uint32_t SM_DIRTY = SM_ROWOK + 256;         // uint32 [2]: tiles with rows to be cleared
-constexpr uint32_t SM_RUN = SM_DIRTY + 64;            // the CTA's run
+constexpr uint32_t SM_GONE = SM_ROWOK + 256;          // uint32 [2][4]: rows to be cleared, by the tile's parity
+constexpr uint32_t SM_RUN = SM_GONE + 64;            // the CTA's run
 constexpr uint32_t SM_ROWAT = SM_RUN + 256;           // int32 [2][128][2]: page and row in it of a tile's rows
 constexpr uint32_t SM_ROPETAB = SM_ROWAT + 2048;      // float2 [4][32]: cos, sin of four queries' positions
 constexpr uint32_t SM_PAGED_TOTAL = SM_ROPETAB + 1024;
 constexpr uint32_t kPagedSmemBytes = SM_PAGED_TOTAL + 1024;
 
-enum Bar : uint32_t { kFull = 0, kEmpty = 8, kQFull = 12, kQEmpty = 13, kScores = 14, kOut = 15, kCleared = 16, kWeights = 17, kDrained = 18, kBars = 19 };
+enum Bar : uint32_t { kFull = 0, kEmpty = 8, kQFull = 12, kQEmpty = 13, kScores = 14, kOut = 15, kWeights = 16, kDrained = 17, kCleared = 18, kBars = 22 };
 
 // Bounded wait on an mbarrier phase: 100,000 suspensions of up to 20 us, then
 // CSA2_FLAG_WAIT_TIMEOUT and false. (mbar_wait with its clock is 40
@@ -346,14 +347,10 @@ __device__ __forceinline__ RowAt row_at(const PagedAttendParams& p, const Cursor
   return a;
 }
 
-template <int N>
-__device__ __forceinline__ bool any_producer(bool v) {
-  uint32_t r;
-  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, 2, %2, p;\nselp.u32 %0, 1, 0, q;\n}"
-               : "=r"(r)
-               : "r"((uint32_t)v), "n"(N)
+// 16 zero bytes into shared memory if hit != 0, without a branch
+__device__ __forceinline__ void zero16_if(uint32_t hit, uint32_t dst) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %0, 0;\n@p st.shared.v4.u32 [%1], {%2, %2, %2, %2};\n}" ::"r"(hit), "r"(dst), "r"(0u)
                : "memory");
-  return r != 0;
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* ptr, uint32_t bytes) {
@@ -366,22 +363,24 @@ __device__ __forceinline__ void prefetch_l2(const void* ptr, uint32_t bytes) {
 // with the next tile on its way to L2 it does not. Warp w copies blocks 2w and
 // 2w + 1 by TMA, chunk by chunk, as soon as their slots are free (TMA:
 // chunks of at least the 8 rows of a swizzle atom; smaller ones are copied by
-// the threads, 16 bytes each). Rows of a chunk that are not the query's are
-// cleared after they land: their weights are 0, but 0 times a NaN is not.
+// the threads, 16 bytes each). Chunks that the tile lacks, or whose pages are
+// missing, are read past the pages' end, where TMA writes zeros; rows of a
+// chunk that are not the query's are cleared after they land: their weights are
+// 0, but 0 times a NaN is not.
 template <int N, bool TMA>
 __device__ __forceinline__ void produce_bf16(const PagedAttendParams& p, uint8_t* sm, uint32_t base_s, Cursor cur, int t,
                                              int warp, double freq) {
   static_assert(N == kTileRows);
   const uint32_t bars = base_s + SM_BAR;
+  const int lane = t & 31;
   const int cs = chunk_shift(p.kv.page_shift);
   const int n_ch = kTileRows >> cs;  // chunks of a tile
   int2* at = reinterpret_cast<int2*>(sm + SM_ROWAT);
-  uint32_t* dirty = reinterpret_cast<uint32_t*>(sm + SM_DIRTY);
+  uint32_t* gone = reinterpret_cast<uint32_t*>(sm + SM_GONE);  // rows to be cleared, a bit each
   QLoad<N> ql;
   ql.freq = freq;
   ql.ask(p, sm, base_s, cur.qi, cur.span.t, 0u, t, warp);
   RowAt mine = row_at(p, cur, t);
-  bool clear = false;
   // this thread's row of tile n: what math and the copies need to know of it
   auto publish = [&](uint32_t n) {
     if (mine.page >= 0 && (t & ((1 << cs) - 1)) == 0)
@@ -389,18 +388,17 @@ __device__ __forceinline__ void produce_bf16(const PagedAttendParams& p, uint8_t
     if (mine.seen && mine.page < 0) set_flag(p.a.flags, CSA2_FLAG_BAD_PAGE);
     at[128 * (n & 1u) + t] = make_int2(mine.page, mine.in_page);
     sm[SM_ROWOK + 128 * (n & 1u) + t] = mine.there();
-    clear = any_producer<N>(!mine.there());
+    const uint32_t bits = __ballot_sync(0xffffffffu, mine.page >= 0 && !mine.seen);
+    if (lane == 0) gone[4 * (n & 1u) + warp] = bits;
+    sync_producers<N>();
   };
   publish(0);
   bool first = true, live = true;  // live: see math_role
   uint32_t seg = 0, n = 0;
-  const int lane = t & 31;
   const uint32_t leader = elect_one();
   const uint32_t tiles = cur.tiles();
 #pragma unroll 1
   for (; n < tiles; ++n) {
-    const bool there = mine.there();
-    if (t == 0) dirty[n & 1u] = clear ? 1u : 0u;
     const bool q_here = first;
     first = cur.last();
     // Q comes before the rows, whose slots are free later, except at the
@@ -412,20 +410,18 @@ __device__ __forceinline__ void produce_bf16(const PagedAttendParams& p, uint8_t
     }
     if constexpr (TMA) {
       // lane k has chunk k
-      const int2 src = lane < n_ch ? at[128 * (n & 1u) + (lane << cs)] : make_int2(-1, 0);
-      const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, src.x >= 0)) << (7 + cs);
+      int2 src = lane < n_ch ? at[128 * (n & 1u) + (lane << cs)] : make_int2(0, 0);
+      if (src.x < 0) src = make_int2(p.kv.n_pages, 0);  // past the end: zeros
       if (n > 0) live = live && wait_all_lanes(bars + 8 * (kEmpty + warp), (n & 1u) ^ 1u, p.a.flags);
       if (live) {
         const uint32_t full = bars + 8 * (kFull + 2 * warp), dst = base_s + SM_KV + (uint32_t)(2 * warp) * 16384u;
-        expect_one(leader, full, bytes);
-        expect_one(leader, full + 8, bytes);
+        expect_one(leader, full, 16384u);
+        expect_one(leader, full + 8, 16384u);
 #pragma unroll 2
         for (int k = 0; k < n_ch; ++k) {
           const int page = uniform(src.x, k), row = uniform(src.y, k);
-          if (page >= 0) {
-            tma_3d_one(leader, dst + ((uint32_t)k << (7 + cs)), &p.kv_map, 128 * warp, row, page, full);
-            tma_3d_one(leader, dst + 16384u + ((uint32_t)k << (7 + cs)), &p.kv_map, 128 * warp + 64, row, page, full + 8);
-          }
+          tma_3d_one(leader, dst + ((uint32_t)k << (7 + cs)), &p.kv_map, 128 * warp, row, page, full);
+          tma_3d_one(leader, dst + 16384u + ((uint32_t)k << (7 + cs)), &p.kv_map, 128 * warp + 64, row, page, full + 8);
         }
       }
     } else {
@@ -453,22 +449,26 @@ __device__ __forceinline__ void produce_bf16(const PagedAttendParams& p, uint8_t
     }
     if (q_here && n == 0) ql.take(p, sm, base_s, seg, t);
     if (q_here) ++seg;
+    if constexpr (TMA) {
+      // this warp's two blocks, four rows a store: eight lanes a row
+      const uint4 g = *reinterpret_cast<const uint4*>(gone + 4 * (n & 1u));
+      if (uniform((g.x | g.y | g.z | g.w) != 0u)) {
+        for (int b = 2 * warp; b < 2 * warp + 2; ++b) live = live && wait_all_lanes(bars + 8 * (kFull + b), n & 1u, p.a.flags);
+        const uint32_t dst = base_s + SM_KV + (uint32_t)(2 * warp) * 16384u + 16u * lane;
+#pragma unroll
+        for (int i = 0; i < kTileRows / 4; ++i) {
+          const uint32_t bits = i < 8 ? g.x : (i < 16 ? g.y : (i < 24 ? g.z : g.w));
+          const uint32_t hit = (bits >> (4 * (i & 7) + (lane >> 3))) & 1u;
+          zero16_if(hit, dst + 512u * i);
+          zero16_if(hit, dst + 512u * i + 16384u);
+        }
+        fence_proxy_async_smem();
+      }
+      warp_arrive(bars + 8 * (kCleared + warp));
+    }
     cur.next(p);
     if (cur.more()) mine = row_at(p, cur, t);
     if (first && t == 0 && cur.more()) prefetch_l2(p.a.q + (int64_t)cur.qi * kHeads * kDim, 2u * kHeads * kDim);
-    if (TMA && clear) {
-      for (int b = 0; b < 8; ++b) live = live && warp_wait(bars + 8 * (kFull + b), n & 1u, p.a.flags);
-      // a warp's rows one after another, its lanes side by side: eight 16-byte
-      // stores a block, four blocks at a time
-      uint8_t* dst = sm + SM_KV + (uint32_t)(lane >> 3) * 16384u + (uint32_t)(32 * warp) * 128u + 16u * (lane & 7);
-      for (uint32_t gone = __ballot_sync(0xffffffffu, !there); gone != 0u; gone &= gone - 1) {
-        const uint32_t r = (uint32_t)(__ffs(gone) - 1) * 128u;
-        *reinterpret_cast<uint4*>(dst + r) = make_uint4(0u, 0u, 0u, 0u);
-        *reinterpret_cast<uint4*>(dst + 4u * 16384u + r) = make_uint4(0u, 0u, 0u, 0u);
-      }
-      fence_proxy_async_smem();
-    }
-    if (TMA) warp_arrive(bars + 8 * kCleared);
     if (cur.more()) publish(n + 1);
   }
   if (!live && TMA && n > 0) {  // no copy may still be landing when the CTA exits
@@ -477,81 +477,53 @@ __device__ __forceinline__ void produce_bf16(const PagedAttendParams& p, uint8_t
   }
 }
 
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-// 16 bf16 channels (two 16-byte chunks) from 16 e4m3 codes and their scale.
-// A code's exponent and mantissa in the low bits of bf16's make 2^-120 of its
-// value (subnormal codes included), and one product with 2^(E - 7) the value
-// times 2^(E - 127), exact in bf16: 3 instructions a value, where the hardware
-// conversion issues at an eighth of the rate (a tile's conversion took 4,200
-// cycles with it). NaN codes and scales above 2^7, which 2^(E - 7) cannot
-// hold, take the conversion.
+// 16 bf16 channels (two 16-byte chunks) from 16 e4m3 codes and their scale, by
+// the hardware's conversions (72 cycles a warp and 16 values; assembling the
+// bits with integer operations and one bf16 product took 91).
 __device__ __forceinline__ void fp8_to_bf16(const uint4& codes, uint32_t scale, uint32_t (&o)[8]) {
+  const float sc = ue8m0_value(scale);
   const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
-  uint32_t nan = 0;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) nan |= (cw[k] & 0x7F7F7F7Fu) + 0x01010101u;
-  if ((nan & 0x80808080u) != 0u || scale > 134u) {
-    const float sc = ue8m0_value(scale);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float2 a = e4m3x2_to_float2((uint16_t)(cw[k] & 0xFFFFu));
-      const float2 b = e4m3x2_to_float2((uint16_t)(cw[k] >> 16));
-      o[2 * k] = pack_bf16(a.x * sc, a.y * sc);
-      o[2 * k + 1] = pack_bf16(b.x * sc, b.y * sc);
-    }
-    return;
-  }
-  const uint32_t sc2 = ((scale + 120u) << 7) * 0x00010001u;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint32_t x = __byte_perm(cw[k], 0u, u == 0 ? 0x1404 : 0x3424);  // each code in the high byte of a half
-      o[2 * k + u] = mul_bf16x2((x & 0x80008000u) | ((x & 0x7F007F00u) >> 4), sc2);
-    }
+    const float2 a = e4m3x2_to_float2((uint16_t)(cw[k] & 0xFFFFu));
+    const float2 b = e4m3x2_to_float2((uint16_t)(cw[k] >> 16));
+    o[2 * k] = pack_bf16(a.x * sc, a.y * sc);
+    o[2 * k + 1] = pack_bf16(b.x * sc, b.y * sc);
   }
 }
-// 16 bf16 channels from 16 E2M1 codes and their e4m3 scale: the bytes of a
-// code's bf16 from two eight-entry tables held in registers (byte permutes),
-// the sign from a third permute, and one product with the scale (at most 6
-// significant bits: exact).
+// 16 bf16 channels from 16 E2M1 codes and their e4m3 scale (at most 6
+// significant bits: exact)
 __device__ __forceinline__ void fp4_to_bf16(uint32_t lo, uint32_t hi, uint32_t scale, uint32_t (&o)[8]) {
-  const float scf = e4m3_value(scale);
-  const uint32_t sc2 = pack_bf16(scf, scf);
+  const float sc = e4m3_value(scale);
+  uint32_t h[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t w = (k < 2 ? lo : hi) >> (16 * (k & 1));  // four codes in the low 16 bits
-    const uint32_t sel = w & 0x7777u;
-    const uint32_t l = __byte_perm(0xC0800000u, 0xC0804000u, sel);
-    // a selector with its top bit set replicates the byte's sign (which
-    // __byte_perm masks off): 0xFF for a negative code, else 0x80
-    uint32_t sg;
-    asm("prmt.b32 %0, %1, %1, %2;" : "=r"(sg) : "r"(0x80808080u), "r"(w));
-    const uint32_t h = __byte_perm(0x3F3F3F00u, 0x40404040u, sel) | ((sg & 0x40404040u) << 1);
-    o[2 * k] = mul_bf16x2(__byte_perm(l, h, 0x5140), sc2);
-    o[2 * k + 1] = mul_bf16x2(__byte_perm(l, h, 0x7362), sc2);
+  for (int k = 0; k < 2; ++k) {
+    e2m1x8_to_f16x2x4_cvt(k == 0 ? lo : hi, h);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      __half2_raw r;
+      r.x = (unsigned short)(h[u] & 0xFFFFu);
+      r.y = (unsigned short)(h[u] >> 16);
+      const float2 f = __half22float2(__half2(r));
+      o[4 * k + u] = pack_bf16(f.x * sc, f.y * sc);
+    }
   }
 }
 
-// fp8 / fp4 producers: a thread's share of the codes passes through registers,
-// four blocks ahead of the conversion (and is asked for in L2 a tile earlier:
-// loads that wait for memory hold up the queue that the math warps'
-// shared-memory and tensor-memory loads go through). fp8: thread t has 16-byte
-// chunk t & 3 (16 channels) of every block for rows t >> 2 and + 64; fp4: chunk
-// t & 1 (32 channels) for row t >> 1.
+// fp8 / fp4 producers: the codes pass through registers, a pair of blocks ahead
+// of the conversion, and are asked for in L2 two tiles earlier (loads that
+// wait for memory hold up the queue that the math warps' shared-memory and
+// tensor-memory loads go through). Of a pair of blocks thread t has 16
+// channels, chunk t & 7, of rows t >> 3, + 32, ...: a load takes whole 128-byte
+// lines (fp8) of four rows.
 template <int KVF, int N>
 __device__ __forceinline__ void produce_codes(const PagedAttendParams& p, uint8_t* sm, uint32_t base_s, Cursor cur, int t,
                                               int warp, double freq) {
-  constexpr int kChunks = KVF == 1 ? 4 : 2;      // 16-byte chunks of a row's block
-  constexpr int R = kTileRows * kChunks / N;     // rows of a thread
   constexpr int kRowBytes = KVF == 1 ? 512 : 256, kScaleBytes = KVF == 1 ? 16 : 32;
-  constexpr int kScaleWords = kScaleBytes / 16;
+  constexpr int R = kTileRows * 8 / N;  // rows of a thread
+  using Code = typename std::conditional<KVF == 1, uint4, uint2>::type;
   const uint32_t bars = base_s + SM_BAR;
-  const int c = t % kChunks;
+  const int c = t & 7, row0 = t >> 3;
   const int cs = chunk_shift(p.kv.page_shift);
   int2* at = reinterpret_cast<int2*>(sm + SM_ROWAT);
   Cursor ahead = cur;  // the tile whose rows are found next
@@ -569,36 +541,37 @@ __device__ __forceinline__ void produce_codes(const PagedAttendParams& p, uint8_
     if (ahead.more()) ahead.next(p);
     sync_producers<N>();
   };
-  // a thread's rows of one tile; codes null: the row is not there
+  // a thread's codes and scale bytes of one tile; codes null: the row is not there
   struct Rows {
     const uint8_t* codes[R];
-    uint4 scale[R][kScaleWords];
+    const uint8_t* scale[R];
   };
   auto find = [&](uint32_t n, Rows& r) {
 #pragma unroll
     for (int u = 0; u < R; ++u) {
-      const int2 a = at[128 * (n & 1u) + t / kChunks + u * (N / kChunks)];
-      r.codes[u] = a.x >= 0 ? p.kv.pages + a.x * p.kv.page_stride + (int64_t)a.y * kRowBytes + 16 * c : nullptr;
-      const uint8_t* s = p.kv.scales + (a.x >= 0 ? a.x * p.kv.scale_stride + (int64_t)a.y * kScaleBytes : 0);
-#pragma unroll
-      for (int k = 0; k < kScaleWords; ++k)
-        r.scale[u][k] = a.x >= 0 ? *reinterpret_cast<const uint4*>(s + 16 * k) : make_uint4(0u, 0u, 0u, 0u);
+      const int2 a = at[128 * (n & 1u) + row0 + u * (N / 8)];
+      r.codes[u] = a.x >= 0 ? p.kv.pages + a.x * p.kv.page_stride + (int64_t)a.y * kRowBytes + (kRowBytes / 32) * c : nullptr;
+      r.scale[u] = a.x >= 0 ? p.kv.scales + a.x * p.kv.scale_stride + (int64_t)a.y * kScaleBytes + (KVF == 1 ? c >> 1 : c) : nullptr;
     }
   };
-  uint4 code[R][4];
-  auto load = [&](const Rows& r, int half, int j) {  // block 4 half + j into the registers of j
+  Code code[2][R];
+  uint8_t scale[2][R];
+  auto load = [&](const Rows& r, int m, int slot) {  // pair m into register set `slot`
 #pragma unroll
-    for (int u = 0; u < R; ++u)
-      code[u][j] = r.codes[u] != nullptr ? ldg_stream16(r.codes[u] + 16 * kChunks * (4 * half + j)) : make_uint4(0u, 0u, 0u, 0u);
+    for (int u = 0; u < R; ++u) {
+      if constexpr (KVF == 1) code[slot][u] = r.codes[u] != nullptr ? ldg_stream16(r.codes[u] + 128 * m) : make_uint4(0u, 0u, 0u, 0u);
+      else code[slot][u] = r.codes[u] != nullptr ? ldg_stream8(r.codes[u] + 64 * m) : make_uint2(0u, 0u);
+      scale[slot][u] = r.codes[u] != nullptr ? __ldg(r.scale[u] + (kScaleBytes / 4) * m) : 0;
+    }
   };
-  Rows now, next;
   QLoad<N> ql;
   ql.freq = freq;
   ql.ask(p, sm, base_s, cur.qi, cur.span.t, 0u, t, warp);
+  Rows now;
   publish(0);
   find(0, now);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) load(now, 0, j);
+  load(now, 0, 0);
+  load(now, 1, 1);
   publish(1);
   bool first = true, live = true;  // live: see math_role
   const uint32_t tiles = cur.tiles();
@@ -614,55 +587,36 @@ __device__ __forceinline__ void produce_codes(const PagedAttendParams& p, uint8_
       ++seg;
     }
     first = cur.last();
-    next = now;
-    if (more) find(n + 1, next);
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int b = 4 * half + j;
-        if (j % 2 == 0 && n > 0) live = live && warp_wait(bars + 8 * (kEmpty + b / 2), (n & 1u) ^ 1u, p.a.flags);
+      for (int j = 0; j < 2; ++j) {
+        const int m = 2 * half + j;
+        if (n > 0) live = live && warp_wait(bars + 8 * (kEmpty + m), (n & 1u) ^ 1u, p.a.flags);
 #pragma unroll
         for (int u = 0; u < R; ++u) {
-          const int r = t / kChunks + u * (N / kChunks);
-          if (b == 0 && c == 0) sm[SM_ROWOK + 128 * (n & 1u) + r] = now.codes[u] != nullptr;
-          uint8_t* dst = sm + SM_KV + (uint32_t)b * 16384u + (uint32_t)r * 128u;
+          const int r = row0 + u * (N / 8);
+          if (m == 0 && c == 0) sm[SM_ROWOK + 128 * (n & 1u) + r] = now.codes[u] != nullptr;
           uint32_t o[8];
-          if constexpr (KVF == 1) {
-            // scale 2b + c / 2 of the row's 16
-            const uint4 sc = now.scale[u][0];
-            const uint32_t w = half == 0 ? (j < 2 ? sc.x : sc.y) : (j < 2 ? sc.z : sc.w);
-            fp8_to_bf16(code[u][j], (w >> (16 * (j & 1) + 8 * (c >> 1))) & 0xFFu, o);
+          if constexpr (KVF == 1) fp8_to_bf16(code[j][u], scale[j][u], o);
+          else fp4_to_bf16(code[j][u].x, code[j][u].y, scale[j][u], o);
+          uint8_t* dst = sm + SM_KV + (uint32_t)(2 * m + (c >> 2)) * 16384u + (uint32_t)r * 128u;
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
-              *reinterpret_cast<uint4*>(dst + (((2 * c + k) ^ (r & 7)) << 4)) =
-                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          } else {
-            // scales 4b + 2c and + 1 of the row's 32
-            const uint4 sc = half == 0 ? now.scale[u][0] : now.scale[u][kScaleWords - 1];
-            const uint32_t two = (j == 0 ? sc.x : (j == 1 ? sc.y : (j == 2 ? sc.z : sc.w))) >> (16 * c);
-            fp4_to_bf16(code[u][j].x, code[u][j].y, two & 0xFFu, o);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              *reinterpret_cast<uint4*>(dst + (((4 * c + k) ^ (r & 7)) << 4)) =
-                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-            fp4_to_bf16(code[u][j].z, code[u][j].w, (two >> 8) & 0xFFu, o);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              *reinterpret_cast<uint4*>(dst + (((4 * c + 2 + k) ^ (r & 7)) << 4)) =
-                  make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          }
+          for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<uint4*>(dst + (((2 * (c & 3) + k) ^ (r & 7)) << 4)) =
+                make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
-        if (half == 0) load(now, 1, j);
-        else if (more) load(next, 0, j);
-        if (j % 2 == 1) {  // two blocks a fence: it takes as long as half a block's conversion
-          fence_proxy_async_smem();
-          warp_arrive(bars + 8 * (kFull + b - 1));
-          warp_arrive(bars + 8 * (kFull + b));
+        fence_proxy_async_smem();
+        warp_arrive(bars + 8 * (kFull + 2 * m));
+        warp_arrive(bars + 8 * (kFull + 2 * m + 1));
+        if (half == 0) {
+          load(now, 2 + j, j);
+        } else if (more) {
+          if (j == 0) find(n + 1, now);
+          load(now, j, j);
         }
       }
     }
-    now = next;
     cur.next(p);
     if (first && t == 0 && more) prefetch_l2(p.a.q + (int64_t)cur.qi * kHeads * kDim, 2u * kHeads * kDim);
     if (more) publish(n + 2);
@@ -675,7 +629,7 @@ __device__ __forceinline__ void produce_codes(const PagedAttendParams& p, uint8_
 struct Issuer {
   uint32_t bars, tmem_s, tmem_o, base_s, leader;
   uint32_t* flags;
-  const uint32_t* dirty;  // null: no rows are cleared after they land
+  const uint4* gone;  // by the tile's parity; null: no rows are cleared after they land
   bool rope;
   // S^T = KV Q^T, block by block as the rows land; the rope channels once more
   // against q's residual
@@ -685,10 +639,15 @@ struct Issuer {
     // a block's barrier is looked at while the products of the block before
     // are issued (a look takes 200 cycles from the instruction to the branch)
     uint32_t landed = phase_done(bars + 8 * kFull, n & 1u);
+    bool clear = false;
 #pragma unroll
     for (uint32_t b = 0; b < 8; ++b) {
       if (!uniform(landed != 0u) && !wait_all_lanes(bars + 8 * (kFull + b), n & 1u, flags)) return false;
-      if (b == 0 && dirty != nullptr && uniform(dirty[n & 1u] != 0u) && !wait_all_lanes(bars + 8 * kCleared, n & 1u, flags)) return false;
+      if (b == 0 && gone != nullptr) {
+        const uint4 g = gone[n & 1u];
+        clear = uniform((g.x | g.y | g.z | g.w) != 0u);
+      }
+      if (b % 2 == 0 && clear && !wait_all_lanes(bars + 8 * (kCleared + b / 2), n & 1u, flags)) return false;
       if (b < 7) landed = phase_done(bars + 8 * (kFull + b + 1), n & 1u);
 #pragma unroll
       for (uint32_t k = 0; k < 4; ++k)
@@ -732,11 +691,11 @@ __device__ __forceinline__ void issue_role(const Issuer& mma, Cursor cur, const 
   for (uint32_t n = 0, seg = 0; n < tiles; ++n) {
     const bool last = cur.last();
     if (live) live = uniform(mma.scores(n, seg, first, last));
+    cur.next(p);  // the next query is looked up while the weights are formed
     if (live) live = wait_all_lanes(mma.bars + 8 * kWeights, n & 1u, mma.flags);
     if (live) mma.output(first, last);
     first = last;
     seg += last ? 1u : 0u;
-    cur.next(p);
   }
   if (!live) mma.drain();
 }
@@ -927,6 +886,9 @@ __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* s
         }
       }
       sy.sync();
+      const int qi = cur.qi;
+      const bool padding = cur.span.b == -1;
+      cur.next(p);  // the next query is looked up while the products run
       live = live && warp_wait(bars + 8 * kOut, seg & 1u, p.a.flags);
       tc_fence_after();
       const float2* rope_tab = reinterpret_cast<const float2*>(sm + SM_ROPETAB) + 32 * (seg & 3u);
@@ -943,8 +905,14 @@ __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* s
             reinterpret_cast<uint4*>(po)[part_at(8 * hh + k, 128 * mt + row)] =
                 make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
         }
-      } else if (cur.span.b != -1) {
-        uint16_t* out = p.a.out + (int64_t)cur.qi * kHeads * kDim;
+      } else if (!padding) {
+        // Lanes hold neighbouring dims: a pair of lanes swaps so that the even
+        // one has two dims of one head and the odd one of the next, and each
+        // store instruction writes 64 bytes of two heads. (Staged through shared
+        // memory for 16-byte stores, with two barriers a block of 128 dims, an
+        // output took 8,200 cycles, more than a tile.)
+        uint32_t* out = reinterpret_cast<uint32_t*>(p.a.out + (int64_t)qi * kHeads * kDim);
+        const bool odd = (lane & 1) != 0;
 #pragma unroll 1
         for (int mt = 0; mt < 4; ++mt) {
           const int d = 128 * mt + row;
@@ -953,7 +921,13 @@ __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* s
           tmem_wait_ld();
           float v[32];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) v[k] = alpha[32 * hh + k] == 0.f ? 0.f : __uint_as_float(r[k]) * alpha[32 * hh + k];
+          for (int k = 0; k < 8; ++k) {
+            const float4 f = *reinterpret_cast<const float4*>(alpha + 32 * hh + 4 * k);
+            v[4 * k] = __uint_as_float(r[4 * k]) * f.x;
+            v[4 * k + 1] = __uint_as_float(r[4 * k + 1]) * f.y;
+            v[4 * k + 2] = __uint_as_float(r[4 * k + 2]) * f.z;
+            v[4 * k + 3] = __uint_as_float(r[4 * k + 3]) * f.w;
+          }
           // rope channels rotated back by -t: only warps that hold some
           // exchange values with the pair's other lane (warp-uniform test)
           if (p.a.rp.pairs > 0 && 128 * mt + 32 * quad + 31 >= first_rope) {
@@ -962,18 +936,24 @@ __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* s
 #pragma unroll
             for (int k = 0; k < 32; ++k) {
               const float partner = __shfl_xor_sync(0xffffffffu, v[k], 1);
-              if (rope) v[k] = (d & 1) ? (v[k] * cs.x - partner * cs.y) : (v[k] * cs.x + partner * cs.y);
+              if (rope) v[k] = odd ? (v[k] * cs.x - partner * cs.y) : (v[k] * cs.x + partner * cs.y);
             }
           }
-          store_out_block(sm, v, mt, out, sy);
+          uint32_t* dst = out + ((32 * hh + (odd ? 1 : 0)) * kDim + (d & ~1)) / 2;
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const float recv = __shfl_xor_sync(0xffffffffu, odd ? v[k] : v[k + 1], 1);
+            dst[k * (kDim / 2)] = odd ? pack_bf16(recv, v[k + 1]) : pack_bf16(v[k], recv);
+          }
         }
       }
       ++seg;
       first = true;
       tc_fence_before();  // O^T has been read
       sy.sync();          // and red, alpha and the rope table are free for the next query
+    } else {
+      cur.next(p);
     }
-    cur.next(p);
   }
   if (ISSUE && warp == 0 && !live) mma.drain();
   if (!by_query && tid == 0) {
@@ -1006,7 +986,7 @@ __global__ void __launch_bounds__(Roles<KVF>::kThreads, 1) attend_paged_kernel(c
   if (tid == kFirstProducer * 32) {
     constexpr uint32_t np = Roles<KVF>::kProducers;
     for (uint32_t b = 0; b < kBars; ++b)
-      mbar_init(bars + 8 * b, b < kEmpty ? (TMA ? 1u : np) : (b == kQFull ? np + 1 : (b == kCleared ? np : (b == kWeights ? (uint32_t)kAttWarps : 1u))));
+      mbar_init(bars + 8 * b, b < kEmpty ? (TMA ? 1u : np) : (b == kQFull ? np + 1 : (b == kWeights ? (uint32_t)kAttWarps : 1u)));
     fence_mbar_init();
   }
   pdl_wait();
@@ -1073,7 +1053,7 @@ __global__ void __launch_bounds__(Roles<KVF>::kThreads, 1) attend_paged_kernel(c
   Cursor cur = run->cur;
   if (uniform(cur.more())) {
     const Issuer mma{bars, tmem_s, tmem_o, base_s, elect_one(), p.a.flags,
-                     TMA ? reinterpret_cast<const uint32_t*>(sm + SM_DIRTY) : nullptr, p.a.rp.pairs > 0};
+                     TMA ? reinterpret_cast<const uint4*>(sm + SM_GONE) : nullptr, p.a.rp.pairs > 0};
     if (Roles<KVF>::kOwnIssuer && warp == Roles<KVF>::kIssuer) {
       issue_role(mma, cur, p);
     } else if (warp >= kFirstProducer) {
@@ -1097,20 +1077,23 @@ __global__ void __launch_bounds__(Roles<KVF>::kThreads, 1) attend_paged_kernel(c
 // from L2): a warp takes four heads and 32 dims and needs no barrier; lanes
 // (part, head) hold the weights of eight parts, which the lanes' dims take by
 // shuffles, and the first eight parts are under way before their weights are
-// known. GROUPS 1: four warps a CTA, next to each other in dims. GROUPS 8: the
-// eight warps of a CTA share the dims and take every eighth batch of parts, for
-// the few queries that have many.
+// known. GROUPS 1: four warps a CTA, next to each other in dims, each `spans`
+// times 32 of them one after another (CTAs start at 0.6 a nanosecond: 9,728 of
+// them took 17 us). GROUPS 8: the eight warps of a CTA share the dims and take
+// every eighth batch of parts, for the few queries that have many.
 constexpr int kJoinBatch = 8;
 template <int GROUPS>
-__global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS) attend_paged_join_kernel(const __grid_constant__ PagedAttendParams p) {
-  constexpr int kWarps = GROUPS == 1 ? 4 : GROUPS, kSpan = GROUPS == 1 ? 128 : 32;  // warps and dims of a CTA
+__global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS) attend_paged_join_kernel(const __grid_constant__ PagedAttendParams p, int spans) {
+  constexpr int kWarps = GROUPS == 1 ? 4 : GROUPS;
   pdl_wait();
   const int2 jn = p.joins[blockIdx.x];
   if (jn.x < 0) return;
   const int qi = p.join_query[blockIdx.x];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = GROUPS == 1 ? 0 : warp;
-  const int hq = blockIdx.y / (kDim / kSpan);
-  const int d = (blockIdx.y % (kDim / kSpan)) * kSpan + (GROUPS == 1 ? 32 * warp : 0) + lane;
+  // this warp's dims: `spans` times 32 from d on
+  const int unit = GROUPS == 1 ? (int)blockIdx.y * kWarps + warp : (int)blockIdx.y, per_head = kDim / 32 / spans;
+  const int hq = unit / per_head;
+  int d = (unit % per_head) * 32 * spans + lane;
   const int n = jn.y - jn.x + 1;
   auto slot = [&](int k) { return (int64_t)(k == 0 ? part_slot(jn.x, true) : part_slot(jn.x + k, false)); };
   float4 v[kJoinBatch];
@@ -1141,6 +1124,12 @@ __global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS) attend_paged_
 #pragma unroll
   for (int o = 16; o >= 4; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
   den = none ? 1.f : den + exp2f(sk - M);
+  const float inv = none ? 0.f : 1.f / den;
+  if (d < 4 && group == 0 && p.a.lse != nullptr)  // lanes 0 .. 3 of the warp of dims 0 ..: a head each
+    p.a.lse[(int64_t)qi * kHeads + head] = none ? sink : (M + log2f(den)) * 0.6931471805599453f;
+  uint32_t* out = reinterpret_cast<uint32_t*>(p.a.out + ((int64_t)qi * kHeads + 4 * hq) * kDim);
+  for (int span = 0; span < spans; ++span, d += 32) {
+  if (span > 0) fetch(kJoinBatch * group);
   float cs = 1.f, sn = 0.f;
   if (d >= first_rope) rope_cs(p.a.rp, (d - first_rope) >> 1, t, cs, sn);
   float o[4] = {0.f, 0.f, 0.f, 0.f};
@@ -1170,9 +1159,6 @@ __global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS) attend_paged_
       o[3] += a.w;
     }
   }
-  if (d < 4 && p.a.lse != nullptr)  // lanes 0 .. 3 of the warp of dims 0 ..: a head each
-    p.a.lse[(int64_t)qi * kHeads + head] = none ? sink : (M + log2f(den)) * 0.6931471805599453f;
-  const float inv = none ? 0.f : 1.f / den;
 #pragma unroll
   for (int u = 0; u < 4; ++u) o[u] *= __shfl_sync(0xffffffffu, inv, u);  // lane u holds head u's
   if ((d | 31) >= first_rope) {  // whole warps: a warp's dims are 32 in a row
@@ -1183,13 +1169,13 @@ __global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS) attend_paged_
     }
   }
   // even lanes store heads 0 and 1, odd lanes heads 2 and 3, two dims a store
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.a.out + ((int64_t)qi * kHeads + 4 * hq) * kDim);
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const float give = (d & 1) ? o[u] : o[2 + u], keep = (d & 1) ? o[2 + u] : o[u];
     const float got = __shfl_xor_sync(0xffffffffu, give, 1);
     const int h = (d & 1) ? 2 + u : u;
     out[(h * kDim + (d & ~1)) >> 1] = (d & 1) ? pack_bf16(got, keep) : pack_bf16(keep, got);
+  }
   }
 }
 
@@ -1285,11 +1271,16 @@ cudaError_t launch_attend_paged(cudaStream_t st, int num_sms, int kv_fmt, Attend
     if (e != cudaSuccess) return e;
     *n_launch += 1;
     const int joins = nq < G ? nq : G;
-    // a query has more than two batches of parts only where there are few queries
-    if (joins * 2 * kJoinBatch <= G)
-      e = launch_ex(attend_paged_join_kernel<8>, dim3((unsigned)joins, kHeads / 4 * (kDim / 32)), dim3(256), 0, st, true, 0, p);
-    else
-      e = launch_ex(attend_paged_join_kernel<1>, dim3((unsigned)joins, kHeads / 4 * (kDim / 128)), dim3(128), 0, st, true, 0, p);
+    // A query has more than two batches of parts only where there are few
+    // queries. Otherwise spans of 32 dims a warp until at most 64 warps an SM are
+    // left: fewer CTAs to start, the same loads under way.
+    if (joins * 2 * kJoinBatch <= G) {
+      e = launch_ex(attend_paged_join_kernel<8>, dim3((unsigned)joins, kHeads / 4 * (kDim / 32)), dim3(256), 0, st, true, 0, p, 1);
+    } else {
+      int spans = 1;
+      while (spans < kDim / 32 && joins * (kHeads / 4) * (kDim / 32) / spans > 64 * num_sms) spans *= 2;
+      e = launch_ex(attend_paged_join_kernel<1>, dim3((unsigned)joins, kHeads / 4 * (kDim / 32) / 4 / spans), dim3(128), 0, st, true, 0, p, spans);
+    }
     if (e != cudaSuccess) return e;
     *n_launch += 1;
   }
