@@ -9,7 +9,8 @@
 // that sees nothing makes one empty tile, which writes its zeros). All queries' tiles,
 // one query after another, are cut into equal runs, one run per CTA and one
 // CTA per SM: a long sequence is split over many CTAs and a CTA takes many
-// short ones. A query that lies whole in one run is written at once; the runs'
+// short ones (a run that crosses into another query is made shorter by the
+// time that this takes: kQueryCost). A query that lies whole in one run is written at once; the runs'
 // ends leave unnormalised fp32 partials, at most two a CTA, which the join
 // kernel sums. The products and softmax of a tile are those of attend_tile.cuh.
 #include <cuda.h>
@@ -29,8 +30,7 @@ struct PagedAttendParams {
   const int64_t* lo;    // [n_seq], nullable
   int64_t window;       // 0: every row
   int64_t n_first;
-  int2* joins;          // [min(n_query, gridDim.x)]: first and last CTA of a query to be joined (-1: none)
-  int32_t* join_query;  // the query of each
+  int4* joins;          // [min(n_query, gridDim.x)]: first and last CTA of a query to be joined (-1: none), the query
 };
 
 namespace {
@@ -216,6 +216,35 @@ template <int N>
 __device__ __forceinline__ void sync_producers() {
   asm volatile("bar.sync 2, %0;" ::"n"(N) : "memory");
 }
+// How the tiles are cut into runs. On a line where a tile is kTileCost long and
+// a query starts with kQueryCost (its Q, its first tile's references, an
+// output or partial more), CTA c of `ctas` has the tiles that start in the
+// c-th of equal parts. With fewer tiles than two a CTA, the queries' starts are
+// left out: one tile a CTA where they suffice. Parts of a query lie in
+// neighbouring CTAs, none of them empty: the parts are longer than a tile.
+constexpr int kTileCost = 2, kQueryCost = 3;
+struct RunCut {
+  int64_t cost;
+  int ctas, start;  // start: kQueryCost or 0
+  // where query i starts, b tiles coming before it
+  __device__ __forceinline__ int64_t at(int64_t b, int i) const { return kTileCost * b + (int64_t)start * i; }
+  // tiles of a query of n that start before x of its start
+  __device__ __forceinline__ int tiles_before(int64_t x, int n) const {
+    return (int)min((int64_t)n, (max(x - start, (int64_t)0) + kTileCost - 1) / kTileCost);
+  }
+  // CTA of tile j of query i
+  __device__ __forceinline__ int cta(int64_t b, int i, int j) const {
+    return (int)(((at(b, i) + start + (int64_t)kTileCost * j + 1) * ctas - 1) / cost);
+  }
+};
+__device__ __forceinline__ RunCut run_cut(int64_t tiles, int n_query, int grid) {
+  RunCut r;
+  r.start = tiles > 2 * (int64_t)grid ? kQueryCost : 0;
+  r.cost = kTileCost * tiles + (int64_t)r.start * n_query;
+  r.ctas = (int)min((int64_t)grid, tiles);
+  return r;
+}
+
 // The CTA's run of tiles, walked tile by tile; every role has its own.
 struct Cursor {
   int64_t at, run1, q0;  // tile, end of the run, first tile of query qi
@@ -238,7 +267,6 @@ struct Cursor {
 struct Run {
   Cursor cur;     // at the run's first tile
   int64_t total;  // tiles of all queries
-  int ctas;       // CTAs with a run
 };
 static_assert(sizeof(Run) <= 256, "SM_RUN");
 
@@ -749,10 +777,9 @@ __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* s
         if (s.b != -1 && !(seq_ok && s.t >= -1)) set_flag(p.a.flags, CSA2_FLAG_BAD_QUERY);
         if (s.ok && s.vis.past_table) set_flag(p.a.flags, CSA2_FLAG_BAD_PAGE);
         const int2 jn = ends ? make_int2(-1, -1)
-                             : make_int2((int)blockIdx.x, (int)(((cur.q0 + s.n_tiles) * run.ctas - 1) / run.total));
+                             : make_int2((int)blockIdx.x, run_cut(run.total, p.a.n_query, (int)gridDim.x).cta(cur.q0, cur.qi, s.n_tiles - 1));
         if (by_query) {
-          p.joins[cur.qi] = jn;
-          p.join_query[cur.qi] = cur.qi;
+          p.joins[cur.qi] = make_int4(jn.x, jn.y, cur.qi, 0);
         } else if (!ends) {
           my_join = jn;
           my_query = cur.qi;
@@ -957,8 +984,7 @@ __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* s
   }
   if (ISSUE && warp == 0 && !live) mma.drain();
   if (!by_query && tid == 0) {
-    p.joins[blockIdx.x] = my_join;
-    p.join_query[blockIdx.x] = my_query;
+    p.joins[blockIdx.x] = make_int4(my_join.x, my_join.y, my_query, 0);
   }
 }
 
@@ -1021,14 +1047,33 @@ __global__ void __launch_bounds__(Roles<KVF>::kThreads, 1) attend_paged_kernel(c
       if (w < warp) before += warp_sum[w];
       total += warp_sum[w];
     }
-    // no run is empty: the CTAs of a split query are neighbours
-    const int c = (int)blockIdx.x, G = (int)min((int64_t)gridDim.x, total);
-    const int64_t run0 = c < G ? (int64_t)c * total / G : total, run1 = c < G ? (int64_t)(c + 1) * total / G : total;
+    const int c = (int)blockIdx.x;
+    const RunCut cut = run_cut(total, Q, (int)gridDim.x);
+    const int64_t x0 = c < cut.ctas ? (int64_t)c * cut.cost / cut.ctas : cut.cost;
+    const int64_t x1 = c < cut.ctas ? (int64_t)(c + 1) * cut.cost / cut.ctas : cut.cost;
     if (tid == 0) {
       run->total = total;
-      run->ctas = G;
-      if (run0 == run1) run->cur.at = run->cur.run1 = total;
+      run->cur.at = run->cur.run1 = total;  // unless found below
     }
+    __shared__ int64_t ends[2];  // first tile of this run and of the next
+    if (tid == 0) ends[0] = ends[1] = total;
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    // the thread whose share holds a cut finds the first tile from it on
+    for (int e = 0; e < 2; ++e) {
+      const int64_t x = e == 0 ? x0 : x1;
+      if (x >= cut.at(before, q_lo) && x < cut.at(before + mine, q_hi)) {
+        int64_t b = before;
+        int i = q_lo;
+        int n = per > 1 ? query_span(p, i).n_tiles : span.n_tiles;
+        while (x >= cut.at(b + n, i + 1)) {
+          b += n;
+          n = query_span(p, ++i).n_tiles;
+        }
+        ends[e] = b + cut.tiles_before(x - cut.at(b, i), n);
+      }
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const int64_t run0 = ends[0], run1 = ends[1];
     if (run0 < run1 && run0 >= before && run0 < before + mine) {
       int i = q_lo;
       if (per > 1) {
@@ -1065,7 +1110,7 @@ __global__ void __launch_bounds__(Roles<KVF>::kThreads, 1) attend_paged_kernel(c
       math_role<!Roles<KVF>::kOwnIssuer>(p, sm, base_s, tmem_s, tmem_o, mma, cur, *run, warp);
     }
   }
-  if (cur.at >= cur.run1 && Q >= (int)gridDim.x && tid == 0) p.joins[blockIdx.x] = make_int2(-1, -1);
+  if (cur.at >= cur.run1 && Q >= (int)gridDim.x && tid == 0) p.joins[blockIdx.x] = make_int4(-1, -1, -1, 0);
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(taddr, kTmemCols);
@@ -1081,19 +1126,25 @@ __global__ void __launch_bounds__(Roles<KVF>::kThreads, 1) attend_paged_kernel(c
 // times 32 of them one after another (CTAs start at 0.6 a nanosecond: 9,728 of
 // them took 17 us). GROUPS 8: the eight warps of a CTA share the dims and take
 // every eighth batch of parts, for the few queries that have many.
-constexpr int kJoinBatch = 8;
+constexpr int kJoinLanes = 8;  // parts whose weights a warp's lanes hold at once
+constexpr int kJoinBatch = 4;  // parts whose values are under way at once
 template <int GROUPS>
-__global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS) attend_paged_join_kernel(const __grid_constant__ PagedAttendParams p, int spans) {
+__global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS, GROUPS == 1 ? 8 : 4)
+    attend_paged_join_kernel(const __grid_constant__ PagedAttendParams p, int spans) {
   constexpr int kWarps = GROUPS == 1 ? 4 : GROUPS;
-  pdl_wait();
-  const int2 jn = p.joins[blockIdx.x];
-  if (jn.x < 0) return;
-  const int qi = p.join_query[blockIdx.x];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = GROUPS == 1 ? 0 : warp;
   // this warp's dims: `spans` times 32 from d on
   const int unit = GROUPS == 1 ? (int)blockIdx.y * kWarps + warp : (int)blockIdx.y, per_head = kDim / 32 / spans;
   const int hq = unit / per_head;
   int d = (unit % per_head) * 32 * spans + lane;
+  // the frequency of this lane's rope channel, if its last span has one, and
+  // the line of parameters it lies in, before the wait
+  const int first_rope = kDim - 2 * p.a.rp.pairs, d_last = d + 32 * (spans - 1);
+  const double freq = d_last >= first_rope ? p.a.rp.freq[(d_last - first_rope) >> 1] : 0.0;
+  pdl_wait();
+  const int4 jn = p.joins[blockIdx.x];
+  if (jn.x < 0) return;
+  const int qi = jn.z;
   const int n = jn.y - jn.x + 1;
   auto slot = [&](int k) { return (int64_t)(k == 0 ? part_slot(jn.x, true) : part_slot(jn.x + k, false)); };
   float4 v[kJoinBatch];
@@ -1103,21 +1154,23 @@ __global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS) attend_paged_
       v[u] = k0 + u < n ? reinterpret_cast<const float4*>(p.a.part_o + slot(k0 + u) * kHeads * kDim)[part_at(hq, d)]
                         : make_float4(0.f, 0.f, 0.f, 0.f);
   };
-  fetch(kJoinBatch * group);
+  fetch(kJoinLanes * group);
   const int head = 4 * hq + (lane & 3), mine = lane >> 2;  // this lane's head, and its part of a batch
-  const int first_rope = kDim - 2 * p.a.rp.pairs;
-  const int64_t t = p.a.q_pos[qi];
+  // the first of the head's references and sums that this lane reads
+  const float m0 = mine < n ? p.a.part_m[slot(mine) * kHeads + head] : -INFINITY;
+  const float l0 = mine < n ? p.a.part_l[slot(mine) * kHeads + head] : 0.f;
+  const double t = (double)p.a.q_pos[qi];
   const float sink = p.a.sink != nullptr ? p.a.sink[head] : -INFINITY;
   const float sk = sink * 1.4426950408889634f;  // references and scores are in log2 units
   // every warp forms the head's maximum and denominator over all parts
-  float M = -INFINITY;
-  for (int k = mine; k < n; k += kJoinBatch) M = fmaxf(M, p.a.part_m[slot(k) * kHeads + head]);
+  float M = m0;
+  for (int k = mine + kJoinLanes; k < n; k += kJoinLanes) M = fmaxf(M, p.a.part_m[slot(k) * kHeads + head]);
 #pragma unroll
   for (int o = 16; o >= 4; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const bool none = M == -INFINITY;  // no row in any part
   M = fmaxf(M, sk);
-  float den = 0.f;
-  for (int k = mine; k < n; k += kJoinBatch) {
+  float den = m0 == -INFINITY ? 0.f : exp2f(m0 - M) * l0;
+  for (int k = mine + kJoinLanes; k < n; k += kJoinLanes) {
     const float m = p.a.part_m[slot(k) * kHeads + head];
     den += m == -INFINITY ? 0.f : exp2f(m - M) * p.a.part_l[slot(k) * kHeads + head];
   }
@@ -1129,20 +1182,22 @@ __global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS) attend_paged_
     p.a.lse[(int64_t)qi * kHeads + head] = none ? sink : (M + log2f(den)) * 0.6931471805599453f;
   uint32_t* out = reinterpret_cast<uint32_t*>(p.a.out + ((int64_t)qi * kHeads + 4 * hq) * kDim);
   for (int span = 0; span < spans; ++span, d += 32) {
-  if (span > 0) fetch(kJoinBatch * group);
-  float cs = 1.f, sn = 0.f;
-  if (d >= first_rope) rope_cs(p.a.rp, (d - first_rope) >> 1, t, cs, sn);
+  if (span > 0) fetch(kJoinLanes * group);
   float o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int k0 = kJoinBatch * group; k0 < n; k0 += kJoinBatch * GROUPS) {
-    if (k0 != kJoinBatch * group) fetch(k0);
-    const float m = k0 + mine < n ? p.a.part_m[slot(k0 + mine) * kHeads + head] : -INFINITY;
+  for (int k8 = kJoinLanes * group; k8 < n; k8 += kJoinLanes * GROUPS) {
+    const float m = k8 == 0 ? m0 : (k8 + mine < n ? p.a.part_m[slot(k8 + mine) * kHeads + head] : -INFINITY);
     const float e = m == -INFINITY ? 0.f : exp2f(m - M);
 #pragma unroll
-    for (int u = 0; u < kJoinBatch; ++u) {
-      o[0] = fmaf(__shfl_sync(0xffffffffu, e, 4 * u), v[u].x, o[0]);
-      o[1] = fmaf(__shfl_sync(0xffffffffu, e, 4 * u + 1), v[u].y, o[1]);
-      o[2] = fmaf(__shfl_sync(0xffffffffu, e, 4 * u + 2), v[u].z, o[2]);
-      o[3] = fmaf(__shfl_sync(0xffffffffu, e, 4 * u + 3), v[u].w, o[3]);
+    for (int k4 = 0; k4 < kJoinLanes; k4 += kJoinBatch) {
+      if (k8 + k4 >= n) break;
+      if (k4 > 0 || k8 > kJoinLanes * group) fetch(k8 + k4);
+#pragma unroll
+      for (int u = 0; u < kJoinBatch; ++u) {
+        o[0] = fmaf(__shfl_sync(0xffffffffu, e, 4 * (k4 + u)), v[u].x, o[0]);
+        o[1] = fmaf(__shfl_sync(0xffffffffu, e, 4 * (k4 + u) + 1), v[u].y, o[1]);
+        o[2] = fmaf(__shfl_sync(0xffffffffu, e, 4 * (k4 + u) + 2), v[u].z, o[2]);
+        o[3] = fmaf(__shfl_sync(0xffffffffu, e, 4 * (k4 + u) + 3), v[u].w, o[3]);
+      }
     }
   }
   if constexpr (GROUPS > 1) {
@@ -1162,6 +1217,8 @@ __global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS) attend_paged_
 #pragma unroll
   for (int u = 0; u < 4; ++u) o[u] *= __shfl_sync(0xffffffffu, inv, u);  // lane u holds head u's
   if ((d | 31) >= first_rope) {  // whole warps: a warp's dims are 32 in a row
+    float cs = 1.f, sn = 0.f;
+    if (d >= first_rope) angle_cs(t * (d == d_last ? freq : p.a.rp.freq[(d - first_rope) >> 1]), cs, sn);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const float partner = __shfl_xor_sync(0xffffffffu, o[u], 1);
@@ -1216,7 +1273,7 @@ int attend_paged_ctas(int num_sms) { return num_sms < kMaxCtas ? num_sms : kMaxC
 
 size_t attend_paged_workspace_bytes(int num_sms) {
   const size_t slots = 2 * (size_t)attend_paged_ctas(num_sms);
-  return al256(slots * kHeads * kDim * 4) + 2 * al256(slots * kHeads * 4) + al256(slots * 8) + al256(slots * 4);
+  return al256(slots * kHeads * kDim * 4) + 2 * al256(slots * kHeads * 4) + al256(slots * 16);
 }
 
 cudaError_t launch_attend_paged(cudaStream_t st, int num_sms, int kv_fmt, AttendParams a, const PagedView& kv,
@@ -1236,9 +1293,7 @@ cudaError_t launch_attend_paged(cudaStream_t st, int num_sms, int kv_fmt, Attend
   w += al256(slots * kHeads * 4);
   p.a.part_l = reinterpret_cast<float*>(w);
   w += al256(slots * kHeads * 4);
-  p.joins = reinterpret_cast<int2*>(w);
-  w += al256(slots * 8);
-  p.join_query = reinterpret_cast<int32_t*>(w);
+  p.joins = reinterpret_cast<int4*>(w);
   const int Q = a.n_query;
   const int chunk = 1 << chunk_shift(kv.page_shift);
   const uint64_t kv_dims[3] = {(uint64_t)kDim, 1ull << kv.page_shift, (uint64_t)kv.n_pages};
@@ -1272,13 +1327,13 @@ cudaError_t launch_attend_paged(cudaStream_t st, int num_sms, int kv_fmt, Attend
     *n_launch += 1;
     const int joins = nq < G ? nq : G;
     // A query has more than two batches of parts only where there are few
-    // queries. Otherwise spans of 32 dims a warp until at most 64 warps an SM are
-    // left: fewer CTAs to start, the same loads under way.
-    if (joins * 2 * kJoinBatch <= G) {
+    // queries. Otherwise spans of 32 dims a warp until the CTAs are resident at once
+    // (32 warps an SM): fewer CTAs to start, the same loads under way.
+    if (joins * 2 * kJoinLanes <= G) {
       e = launch_ex(attend_paged_join_kernel<8>, dim3((unsigned)joins, kHeads / 4 * (kDim / 32)), dim3(256), 0, st, true, 0, p, 1);
     } else {
       int spans = 1;
-      while (spans < kDim / 32 && joins * (kHeads / 4) * (kDim / 32) / spans > 64 * num_sms) spans *= 2;
+      while (spans < kDim / 32 && joins * (kHeads / 4) * (kDim / 32) / spans > 32 * num_sms) spans *= 2;
       e = launch_ex(attend_paged_join_kernel<1>, dim3((unsigned)joins, kHeads / 4 * (kDim / 32) / 4 / spans), dim3(128), 0, st, true, 0, p, spans);
     }
     if (e != cudaSuccess) return e;
