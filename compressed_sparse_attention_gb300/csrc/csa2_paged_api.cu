@@ -325,6 +325,10 @@ csa2_status csa2_rope(csa2_ctx* ctx, void* stream, const csa2_rope_table* table,
     return fail(ctx, CSA2_ERR_INVALID_ARG, "rope: the table's channels must lie inside the head");
   if (table->layout != CSA2_ROPE_INTERLEAVED && table->layout != CSA2_ROPE_HALF)
     return fail(ctx, CSA2_ERR_INVALID_ARG, "rope: the table's layout");
+  if (!std::isfinite(table->amplitude)) return fail(ctx, CSA2_ERR_INVALID_ARG, "rope: the table's amplitude");
+  for (int k = 0; k < table->rope_dim / 2; ++k)
+    if (!(std::fabs(table->freq[k]) < 4294967296.0))
+      return fail(ctx, CSA2_ERR_INVALID_ARG, "rope: a frequency of the table is not finite or 2^32 and more");
   if (n_tokens == 0 || n_heads == 0) return CSA2_OK;
   const uintptr_t size = dtype == CSA2_DTYPE_FP32 ? 4 : 2;
   if (!x || !out || !pos || !aligned(x, size) || !aligned(out, size))

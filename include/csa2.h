@@ -766,7 +766,9 @@ csa2_status csa2_rope_table_init(csa2_rope_table* table, int32_t rope_dim, int32
  *           same strides (in place) and must not overlap it otherwise; out's
  *           rows must not overlap each other
  *   pos     [n_tokens] int64; head_dim even, 2..1024
- * Rotated in fp32, angles in double precision, rounded once. One launch. */
+ * Rotated in fp32, rounded once. A position's turn is freq[k] / 2 pi in 64-bit
+ * fixed point (|freq| < 2^32), so an angle is off by pos * 2^-65 turns at most
+ * before its float cosine and sine. One launch. */
 csa2_status csa2_rope(csa2_ctx* ctx, void* stream, const csa2_rope_table* table, int32_t dtype, int64_t n_tokens,
                       int32_t n_heads, int32_t head_dim, const void* x, int64_t x_tok_stride, int64_t x_head_stride,
                       const int64_t* pos, void* out, int64_t out_tok_stride, int64_t out_head_stride,
