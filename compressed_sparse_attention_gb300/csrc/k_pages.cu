@@ -23,6 +23,27 @@ constexpr int kScanPages = 16;  // pages a thread of the plan scans in one round
 constexpr int kCopyThreads = 256;
 constexpr int kCopyChunk = 16384;  // bytes of a page that a CTA copies in one go: 4 x 16 a thread
 constexpr int kNoOwner = 0x7FFFFFFF;
+constexpr int kSharedSeqs = 2048;  // sequences whose plan fits shared memory, 24 KB
+
+// What the plan keeps of its entries: in shared memory, which spares it a round
+// trip to the L2 after each of its barriers, or for very many sequences in the
+// workspace.
+struct Entries {
+  int32_t *owner, *need, *off;
+};
+struct EntriesShared {
+  int32_t owner[kSharedSeqs], need[kSharedSeqs], off[kSharedSeqs];
+};
+__device__ __forceinline__ Entries entries_of(const PagePool& P, const PagePlan& W, EntriesShared& sh) {
+  return P.n_seq <= kSharedSeqs ? Entries{sh.owner, sh.need, sh.off} : Entries{W.owner, W.need, W.off};
+}
+
+// The counts and lengths that the plan reads late, on their way to the L2.
+__device__ __forceinline__ void plan_prefetch(const PagePool& P) {
+  const int64_t t = threadIdx.x;
+  if (t * 32 < P.n_pages) asm volatile("prefetch.global.L2 [%0];" ::"l"(P.ref + t * 32));
+  if (t * 16 < P.n_seq) asm volatile("prefetch.global.L2 [%0];" ::"l"(P.seq_len + t * 16));
+}
 
 // Exclusive scan of one value a thread over the plan's CTA; total: the sum.
 template <typename N>
@@ -104,24 +125,24 @@ __device__ __forceinline__ bool is_page(const PagePool& P, int32_t g) { return (
 // Offsets of the entries' fresh pages and the pages themselves. need[i] < 0:
 // an entry that is not carried out. An entry whose pages are not there, and
 // with it every later one that needs any, is refused (need[i] = -1).
-__device__ void place_entries(const PagePool& P, const PagePlan& W, int n) {
+__device__ void place_entries(const PagePool& P, const PagePlan& W, const Entries& E, int n) {
   __shared__ int64_t sums64[32];
   __shared__ int sums32[32];
   int64_t carry = 0;
   for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
     const int i = i0 + (int)threadIdx.x;
-    const int64_t x = i < n ? max(W.need[i], 0) : 0;
+    const int64_t x = i < n ? max(E.need[i], 0) : 0;
     int64_t total;
     const int64_t at = carry + cta_scan<int64_t>(x, total, sums64);
     carry += total;
     // offsets past the pool mean that the entry is refused below
-    if (i < n) W.off[i] = (int32_t)min(at, (int64_t)P.n_pages + 1);
+    if (i < n) E.off[i] = (int32_t)min(at, (int64_t)P.n_pages + 1);
   }
   const int n_free = take_free(P, min(carry, (int64_t)P.n_pages), W.fresh, sums32);
   for (int i = threadIdx.x; i < n; i += kPlanThreads) {
-    const int need = W.need[i];
-    if (need > 0 && (int64_t)W.off[i] + need > n_free) {
-      W.need[i] = -1;
+    const int need = E.need[i];
+    if (need > 0 && (int64_t)E.off[i] + need > n_free) {
+      E.need[i] = -1;
       set_flag(P.flags, CSA2_FLAG_OUT_OF_PAGES);
     }
   }
@@ -129,31 +150,34 @@ __device__ void place_entries(const PagePool& P, const PagePlan& W, int n) {
 }
 
 // ---------------------------------------------------------------- extend
-__global__ void __launch_bounds__(kPlanThreads) pages_extend_kernel(const PagePool P, const PagePlan W, int n,
+__global__ void __launch_bounds__(kPlanThreads, 1) pages_extend_kernel(const PagePool P, const PagePlan W, int n,
                                                                     const int32_t* __restrict__ seqs,
                                                                     const int64_t* __restrict__ new_len) {
-  claim(P, seqs, n, W.owner);
+  __shared__ EntriesShared sh;
+  const Entries E = entries_of(P, W, sh);
+  plan_prefetch(P);
+  claim(P, seqs, n, E.owner);
   for (int i = threadIdx.x; i < n; i += kPlanThreads) {
     const int b = seqs[i];
     int need = -1;
-    if (b >= 0 && b < P.n_seq && W.owner[b] == i) {
+    if (b >= 0 && b < P.n_seq && E.owner[b] == i) {
       const int64_t len = P.seq_len[b], to = new_len[i];
       if (to >= len && len >= 0 && to <= ((int64_t)P.max_pages << P.page_shift))
         need = (int)(pages_for(P, to) - pages_for(P, len));
     }
-    W.need[i] = need;
+    E.need[i] = need;
     if (need < 0 && b != -1) set_flag(P.flags, CSA2_FLAG_BAD_SEQ);
   }
   __syncthreads();
-  place_entries(P, W, n);
+  place_entries(P, W, E, n);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int i = warp; i < n; i += kPlanWarps) {
-    const int need = W.need[i];
+    const int need = E.need[i];
     if (need < 0) continue;
     const int b = seqs[i];
     int32_t* row = P.table + (int64_t)b * P.table_ld + pages_for(P, P.seq_len[b]);
     for (int k = lane; k < need; k += 32) {
-      const int g = W.fresh[W.off[i] + k];
+      const int g = W.fresh[E.off[i] + k];
       row[k] = g;
       P.ref[g] = 1;
     }
@@ -165,20 +189,22 @@ __global__ void __launch_bounds__(kPlanThreads) pages_extend_kernel(const PagePo
 // ---------------------------------------------------------------- fork
 // The plan: what each entry needs, where its fresh pages lie, and the pairs
 // (source page, rows in use) to be copied into them, in the order of the pages.
-__global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(const PagePool P, const PagePlan W, int n,
+__global__ void __launch_bounds__(kPlanThreads, 1) pages_fork_plan_kernel(const PagePool P, const PagePlan W, int n,
                                                                        const int32_t* __restrict__ parents,
                                                                        const int32_t* __restrict__ children, int deep) {
   pdl_trigger();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  claim(P, children, n, W.owner);
+  __shared__ EntriesShared sh;
+  const Entries E = entries_of(P, W, sh);
+  plan_prefetch(P);
+  claim(P, children, n, E.owner);
   for (int i = warp; i < n; i += kPlanWarps) {
     const int p = parents[i], c = children[i];
     int need = -1;
-    if (p >= 0 && p < P.n_seq && c >= 0 && c < P.n_seq && W.owner[c] == i && W.owner[p] == kNoOwner &&
-        P.seq_len[c] == 0) {
-      const int64_t len = P.seq_len[p];
+    if (p >= 0 && p < P.n_seq && c >= 0 && c < P.n_seq) {
+      const int64_t len = P.seq_len[p], child_len = P.seq_len[c];
       const int64_t np = pages_for(P, len);
-      if (len >= 0 && np <= P.max_pages) {
+      if (E.owner[c] == i && E.owner[p] == kNoOwner && child_len == 0 && len >= 0 && np <= P.max_pages) {
         const int32_t* row = P.table + (int64_t)p * P.table_ld;
         if (deep) {
           int mine = 0;
@@ -190,22 +216,22 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(const Pag
       }
     }
     if (lane == 0) {
-      W.need[i] = need;
+      E.need[i] = need;
       if (need < 0 && c != -1) set_flag(P.flags, CSA2_FLAG_BAD_SEQ);
     }
   }
   __syncthreads();
-  place_entries(P, W, n);
+  place_entries(P, W, E, n);
   __shared__ int s_pairs;
   if (threadIdx.x == 0) s_pairs = 0;
   __syncthreads();
   for (int i = warp; i < n; i += kPlanWarps) {
-    const int need = W.need[i];
+    const int need = E.need[i];
     if (need <= 0) continue;
     const int64_t len = P.seq_len[parents[i]];
     const int np = (int)pages_for(P, len), ps = 1 << P.page_shift;
     const int32_t* row = P.table + (int64_t)parents[i] * P.table_ld;
-    int at = W.off[i];
+    int at = E.off[i];
     for (int j0 = deep ? 0 : np - 1; j0 < np; j0 += 32) {
       const int j = j0 + lane;
       const int32_t g = j < np ? row[j] : -1;
@@ -221,6 +247,11 @@ __global__ void __launch_bounds__(kPlanThreads) pages_fork_plan_kernel(const Pag
   }
   __syncthreads();
   if (threadIdx.x == 0) W.count[0] = s_pairs;
+  if (E.need != W.need)
+    for (int i = threadIdx.x; i < n; i += kPlanThreads) {
+      W.need[i] = E.need[i];
+      W.off[i] = E.off[i];
+    }
 }
 
 // Copies `count` pages (rows[k] rows of page src[k], all rows where rows is
@@ -365,7 +396,7 @@ __global__ void __launch_bounds__(256) pages_free_kernel(const PagePool P, const
 // The plan: with L pages in use, the free pages below L in ascending order
 // take the pages in use from L on in ascending order. map[g] (g >= L) is a
 // page's new index, -1 for a free one.
-__global__ void __launch_bounds__(kPlanThreads) pages_compact_plan_kernel(const PagePool P, const PagePlan W,
+__global__ void __launch_bounds__(kPlanThreads, 1) pages_compact_plan_kernel(const PagePool P, const PagePlan W,
                                                                           int32_t* __restrict__ n_live_out) {
   pdl_trigger();
   __shared__ int sums32[32];
@@ -460,8 +491,14 @@ PagePlan plan_of(const PagePool& P, void* ws) {
   return W;
 }
 
-// CTAs that copy: eight resident a SM keep 128 KB of loads under way on each
-int copy_ctas(int num_sms, const PageArrays& A) { return A.n > 0 ? 8 * num_sms : 0; }
+// CTAs that copy `pages` pages at most: eight resident a SM keep 128 KB of
+// loads under way on each, and no more than there are units
+int copy_ctas(int num_sms, const PageArrays& A, int64_t pages, int page_rows) {
+  int64_t units = 0;
+  for (int a = 0; a < A.n; ++a)
+    units += pages * (((int64_t)page_rows * A.a[a].row_bytes + kCopyChunk - 1) / kCopyChunk);
+  return (int)(units < 8 * num_sms ? units : 8 * num_sms);
+}
 
 }  // namespace
 
@@ -481,7 +518,7 @@ cudaError_t launch_pages_fork(cudaStream_t st, int num_sms, const PagePool& P, i
   pages_fork_plan_kernel<<<1, kPlanThreads, 0, st>>>(P, W, n, parents, children, deep ? 1 : 0);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_ex(pages_fork_apply_kernel, dim3((unsigned)(n + copy_ctas(num_sms, A))), dim3(kCopyThreads), 0, st, true,
+  return launch_ex(pages_fork_apply_kernel, dim3((unsigned)(n + copy_ctas(num_sms, A, deep ? P.n_pages : n, 1 << P.page_shift))), dim3(kCopyThreads), 0, st, true,
                    0, P, W, n, parents, children, deep ? 1 : 0, A);
 }
 
@@ -500,7 +537,7 @@ cudaError_t launch_pages_compact(cudaStream_t st, int num_sms, const PagePool& P
   const int64_t entries = (int64_t)P.n_seq * P.max_pages;
   const int64_t want = (entries + kRemapEach - 1) / kRemapEach;
   const int remap = (int)(want < num_sms ? want : num_sms);
-  return launch_ex(pages_compact_apply_kernel, dim3((unsigned)(remap + copy_ctas(num_sms, A))), dim3(kCopyThreads), 0, st,
+  return launch_ex(pages_compact_apply_kernel, dim3((unsigned)(remap + copy_ctas(num_sms, A, P.n_pages, 1 << P.page_shift))), dim3(kCopyThreads), 0, st,
                    true, 0, P, W, remap, A);
 }
 
