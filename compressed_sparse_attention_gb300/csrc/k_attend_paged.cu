@@ -615,12 +615,16 @@ __device__ __forceinline__ void produce_codes(const PagedAttendParams& p, uint8_
       ++seg;
     }
     first = cur.last();
+    // (a look at a barrier takes some 300 cycles: the next pair's is under way
+    // while this one is converted)
+    uint32_t free = n == 0 ? 1u : phase_done(bars + 8 * kEmpty, (n & 1u) ^ 1u);
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int m = 2 * half + j;
-        if (n > 0) live = live && warp_wait(bars + 8 * (kEmpty + m), (n & 1u) ^ 1u, p.a.flags);
+        if (!uniform(free != 0u)) live = live && warp_wait(bars + 8 * (kEmpty + m), (n & 1u) ^ 1u, p.a.flags);
+        if (n > 0 && m < 3) free = phase_done(bars + 8 * (kEmpty + m + 1), (n & 1u) ^ 1u);
 #pragma unroll
         for (int u = 0; u < R; ++u) {
           const int r = row0 + u * (N / 8);
@@ -637,13 +641,13 @@ __device__ __forceinline__ void produce_codes(const PagedAttendParams& p, uint8_
         fence_proxy_async_smem();
         warp_arrive(bars + 8 * (kFull + 2 * m));
         warp_arrive(bars + 8 * (kFull + 2 * m + 1));
-        if (half == 0) {
-          load(now, 2 + j, j);
-        } else if (more) {
-          if (j == 0) find(n + 1, now);
-          load(now, j, j);
-        }
+        if (half == 0) load(now, 2 + j, j);
       }
+    }
+    if (more) {
+      find(n + 1, now);
+      load(now, 0, 0);
+      load(now, 1, 1);
     }
     cur.next(p);
     if (first && t == 0 && more) prefetch_l2(p.a.q + (int64_t)cur.qi * kHeads * kDim, 2u * kHeads * kDim);
