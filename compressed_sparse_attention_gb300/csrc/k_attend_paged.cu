@@ -223,6 +223,11 @@ __device__ __forceinline__ void sync_producers() {
 // left out: one tile a CTA where they suffice. Parts of a query lie in
 // neighbouring CTAs, none of them empty: the parts are longer than a tile.
 constexpr int kTileCost = 2, kQueryCost = 3;
+// a / b of values >= 0: 32-bit where they fit (a 64-bit division is several
+// hundred cycles, before any row is asked for)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 struct RunCut {
   int64_t cost;
   int ctas, start;  // start: kQueryCost or 0
@@ -234,7 +239,7 @@ struct RunCut {
   }
   // CTA of tile j of query i
   __device__ __forceinline__ int cta(int64_t b, int i, int j) const {
-    return (int)(((at(b, i) + start + (int64_t)kTileCost * j + 1) * ctas - 1) / cost);
+    return (int)quotient((at(b, i) + start + (int64_t)kTileCost * j + 1) * ctas - 1, cost);
   }
 };
 __device__ __forceinline__ RunCut run_cut(int64_t tiles, int n_query, int grid) {
@@ -381,6 +386,7 @@ __device__ __forceinline__ void zero16_if(uint32_t hit, uint32_t dst) {
                : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2_line(const void* ptr) { asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr)); }
 __device__ __forceinline__ void prefetch_l2(const void* ptr, uint32_t bytes) {
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(ptr), "r"(bytes) : "memory");
 }
@@ -407,7 +413,6 @@ __device__ __forceinline__ void produce_bf16(const PagedAttendParams& p, uint8_t
   uint32_t* gone = reinterpret_cast<uint32_t*>(sm + SM_GONE);  // rows to be cleared, a bit each
   QLoad<N> ql;
   ql.freq = freq;
-  ql.ask(p, sm, base_s, cur.qi, cur.span.t, 0u, t, warp);
   RowAt mine = row_at(p, cur, t);
   // this thread's row of tile n: what math and the copies need to know of it
   auto publish = [&](uint32_t n) {
@@ -429,8 +434,8 @@ __device__ __forceinline__ void produce_bf16(const PagedAttendParams& p, uint8_t
   for (; n < tiles; ++n) {
     const bool q_here = first;
     first = cur.last();
-    // Q comes before the rows, whose slots are free later, except at the
-    // run's start, where both are
+    // Q comes before the rows, whose slots are free later; at the run's start,
+    // where both are, the rows come first: memory is the slower
     if (q_here && n > 0) {
       live = live && wait_all_lanes(bars + 8 * kQEmpty, (seg & 1u) ^ 1u, p.a.flags);
       ql.ask(p, sm, base_s, cur.qi, cur.span.t, seg, t, warp);
@@ -475,7 +480,10 @@ __device__ __forceinline__ void produce_bf16(const PagedAttendParams& p, uint8_t
 #pragma unroll 1
       for (int b = 0; b < 8; ++b) warp_arrive(bars + 8 * (kFull + b));
     }
-    if (q_here && n == 0) ql.take(p, sm, base_s, seg, t);
+    if (q_here && n == 0) {
+      ql.ask(p, sm, base_s, cur.qi, cur.span.t, seg, t, warp);
+      ql.take(p, sm, base_s, seg, t);
+    }
     if (q_here) ++seg;
     if constexpr (TMA) {
       // this warp's two blocks, four rows a store: eight lanes a row
@@ -594,9 +602,9 @@ __device__ __forceinline__ void produce_codes(const PagedAttendParams& p, uint8_
   };
   QLoad<N> ql;
   ql.freq = freq;
-  ql.ask(p, sm, base_s, cur.qi, cur.span.t, 0u, t, warp);
   Rows now;
   publish(0);
+  ql.ask(p, sm, base_s, cur.qi, cur.span.t, 0u, t, warp);
   find(0, now);
   load(now, 0, 0);
   load(now, 1, 1);
@@ -1009,6 +1017,9 @@ __global__ void __launch_bounds__(Roles<KVF>::kThreads, 1) attend_paged_kernel(c
   // frequencies of the last producer warp's lanes (parameters come from memory
   // the first time, a line at a time)
   const double freq = warp == kFirstProducer + Roles<KVF>::kProducers - 1 && lane < p.a.rp.pairs ? p.a.rp.freq[lane] : 0.0;
+  if (tid * 16 < p.a.n_query) prefetch_l2_line(p.a.q_pos + tid * 16);
+  if (tid * 32 < p.a.n_query) prefetch_l2_line(p.a.seq_of_q + tid * 32);
+  if (p.lo != nullptr && tid * 16 < p.kv.n_seq) prefetch_l2_line(p.lo + tid * 16);
   if (warp == 0) {
     tmem_alloc(base_s + SM_MISC + 8, kTmemCols);
     tmem_relinquish();
@@ -1053,8 +1064,8 @@ __global__ void __launch_bounds__(Roles<KVF>::kThreads, 1) attend_paged_kernel(c
     }
     const int c = (int)blockIdx.x;
     const RunCut cut = run_cut(total, Q, (int)gridDim.x);
-    const int64_t x0 = c < cut.ctas ? (int64_t)c * cut.cost / cut.ctas : cut.cost;
-    const int64_t x1 = c < cut.ctas ? (int64_t)(c + 1) * cut.cost / cut.ctas : cut.cost;
+    const int64_t x0 = c < cut.ctas ? quotient((int64_t)c * cut.cost, cut.ctas) : cut.cost;
+    const int64_t x1 = c < cut.ctas ? quotient((int64_t)(c + 1) * cut.cost, cut.ctas) : cut.cost;
     if (tid == 0) {
       run->total = total;
       run->cur.at = run->cur.run1 = total;  // unless found below
