@@ -230,9 +230,7 @@ __device__ __forceinline__ void q_rope_split(uint8_t* sm, const RopeParams& rp) 
 // sums lsum (scaled with the reference when it moves), rescales O^T in
 // tensor memory where needed, and ends with the async-proxy fence and a
 // barrier of the math threads: P^T and O^T are then ready for the PV product.
-// kExactSums: the row sums take the fp32 weights instead of the rounded ones
-// (the denominator, and with it lse, then carries no bf16 rounding).
-template <bool kExactSums = false, class Sync>
+template <class Sync>
 __device__ __forceinline__ void tile_softmax(const AttendParams& p, uint8_t* sm, uint32_t tmem_s, uint32_t tmem_o,
                                              uint32_t lane_base, bool valid, bool first, uint32_t* rescale,
                                              float (&lsum)[32], const Sync& sy) {
@@ -291,8 +289,8 @@ __device__ __forceinline__ void tile_softmax(const AttendParams& p, uint8_t* sm,
       const float p0 = exp2f(s[2 * k] - m_use[32 * hh + 2 * k]);
       const float p1 = exp2f(s[2 * k + 1] - m_use[32 * hh + 2 * k + 1]);
       packed[k] = pack_bf16(p0, p1);
-      lsum[2 * k] += kExactSums ? p0 : bf16lo(packed[k]);  // the weights PV sums, rounded to bf16
-      lsum[2 * k + 1] += kExactSums ? p1 : bf16hi(packed[k]);
+      lsum[2 * k] += bf16lo(packed[k]);  // the weights PV sums, rounded to bf16
+      lsum[2 * k + 1] += bf16hi(packed[k]);
     }
     // P^T row `row`: 64 heads = 8 chunks of 16 B; this thread writes chunks
     // 4 hh .. 4 hh + 3

@@ -37,7 +37,7 @@ __device__ __forceinline__ int32_t page_of(const PagedView& v, int b, int64_t p)
 // masked.
 struct Visible {
   int64_t lo, tail, end;  // end: one past the last position (t + 1, or the table's end)
-  int32_t head, count;    // count: rows seen
+  int32_t head;           // first tokens seen
   int32_t head_chunk, n_head, tail_chunk, n_chunks;
   bool past_table;  // t lies beyond the table's last column: those rows are not there
 };
@@ -53,7 +53,6 @@ __host__ __device__ __forceinline__ Visible visible_rows(int64_t t, int64_t lo_i
   s.end = s.past_table ? cap : t + 1;
   s.head = 0;
   s.tail = s.lo;
-  s.count = 0;
   s.head_chunk = s.n_head = s.tail_chunk = s.n_chunks = 0;
   if (s.end <= s.lo) return s;
   if (window > 0) {
@@ -64,7 +63,6 @@ __host__ __device__ __forceinline__ Visible visible_rows(int64_t t, int64_t lo_i
     const int64_t from = t - window + 1;
     s.tail = s.lo + s.head > from ? s.lo + s.head : from;
   }
-  s.count = s.head + (s.end > s.tail ? (int32_t)(s.end - s.tail) : 0);
   if (s.head > 0) {
     s.head_chunk = (int32_t)(s.lo >> shift);
     s.n_head = (int32_t)((s.lo + s.head - 1) >> shift) - s.head_chunk + 1;
