@@ -22,6 +22,12 @@ csa2_status cuda_fail(csa2_ctx* c, cudaError_t e, const char* where) {
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// every pointer a multiple of `size` (a power of two); null ones are
+template <class... P>
+bool aligned_all(uintptr_t size, const P*... p) {
+  return (aligned(p, size) && ...);
+}
+
 // A launch goes to the current device: it must be the context's.
 csa2_status begin(csa2_ctx* ctx, const char* where) {
   ctx->last_launches = 0;
@@ -146,7 +152,7 @@ csa2_status csa2_attend_paged(csa2_ctx* ctx, void* stream, const csa2_paged_kv* 
   if (n_query < 0 || window < 0 || n_first < 0)
     return fail(ctx, CSA2_ERR_INVALID_ARG, "attend_paged: n_query, window and n_first must not be negative");
   if (n_query == 0) return CSA2_OK;
-  if (!q || !q_pos || !seq_of_q || !out || !aligned(q, 16) || !aligned(out, 16))
+  if (!q || !q_pos || !seq_of_q || !out || !aligned_all(16, q, out) || !aligned_all(8, q_pos, lo) || !aligned_all(4, seq_of_q, sink, lse))
     return fail(ctx, CSA2_ERR_INVALID_ARG, "attend_paged: null or misaligned buffer");
   s = check_ws(ctx, "attend_paged", workspace, workspace_bytes, csa2::attend_paged_workspace_bytes(ctx->num_sms));
   if (s != CSA2_OK) return s;
@@ -181,7 +187,7 @@ csa2_status csa2_append_paged(csa2_ctx* ctx, void* stream, const csa2_paged_kv* 
     return fail(ctx, CSA2_ERR_UNSUPPORTED, "append_paged: rows must be bf16 or fp32");
   if (n_tokens < 0) return fail(ctx, CSA2_ERR_INVALID_ARG, "append_paged: n_tokens");
   if (n_tokens == 0) return CSA2_OK;
-  if (!rows || !tok_off || !first_pos || !aligned(rows, 16))
+  if (!rows || !tok_off || !first_pos || !aligned(rows, 16) || !aligned_all(8, tok_off, first_pos))
     return fail(ctx, CSA2_ERR_INVALID_ARG, "append_paged: null or misaligned buffer");
   const cudaError_t e = csa2::launch_append_paged(reinterpret_cast<cudaStream_t>(stream), dtype, rows, n_tokens, kv->n_seq,
                                                   tok_off, first_pos, v, ctx->cfg.kv_format, ctx->rope, ctx->d_flags);
@@ -203,7 +209,8 @@ csa2_status csa2_pages_extend(csa2_ctx* ctx, void* stream, const csa2_page_pool*
   csa2::PagePool P{};
   if ((s = check_pool(ctx, "pages_extend", pool, n, &P)) != CSA2_OK) return s;
   if (n == 0) return CSA2_OK;
-  if (!seqs || !new_len) return fail(ctx, CSA2_ERR_INVALID_ARG, "pages_extend: null pointer");
+  if (!seqs || !new_len || !aligned(seqs, 4) || !aligned(new_len, 8))
+    return fail(ctx, CSA2_ERR_INVALID_ARG, "pages_extend: null or misaligned buffer");
   s = check_ws(ctx, "pages_extend", workspace, workspace_bytes, csa2::pages_workspace_bytes(P.n_seq, P.n_pages));
   if (s != CSA2_OK) return s;
   const cudaError_t e = csa2::launch_pages_extend(reinterpret_cast<cudaStream_t>(stream), P, n, seqs, new_len, workspace);
@@ -223,7 +230,8 @@ csa2_status csa2_pages_fork(csa2_ctx* ctx, void* stream, const csa2_page_pool* p
   if ((s = check_pool(ctx, "pages_fork", pool, n, &P)) != CSA2_OK) return s;
   if ((s = check_arrays(ctx, "pages_fork", pool->page_size, n_arrays, arrays, &A)) != CSA2_OK) return s;
   if (n == 0) return CSA2_OK;
-  if (!parents || !children) return fail(ctx, CSA2_ERR_INVALID_ARG, "pages_fork: null pointer");
+  if (!parents || !children || !aligned_all(4, parents, children))
+    return fail(ctx, CSA2_ERR_INVALID_ARG, "pages_fork: null or misaligned buffer");
   s = check_ws(ctx, "pages_fork", workspace, workspace_bytes, csa2::pages_workspace_bytes(P.n_seq, P.n_pages));
   if (s != CSA2_OK) return s;
   const cudaError_t e = csa2::launch_pages_fork(reinterpret_cast<cudaStream_t>(stream), ctx->num_sms, P, n, parents,
@@ -240,7 +248,8 @@ static csa2_status do_free(csa2_ctx* ctx, const char* where, void* stream, const
   csa2::PagePool P{};
   if ((s = check_pool(ctx, where, pool, n, &P)) != CSA2_OK) return s;
   if (n == 0) return CSA2_OK;
-  if (!seqs) return fail(ctx, CSA2_ERR_INVALID_ARG, std::string(where) + ": null pointer");
+  if (!seqs || !aligned(seqs, 4) || !aligned(lo, 8))
+    return fail(ctx, CSA2_ERR_INVALID_ARG, std::string(where) + ": null or misaligned buffer");
   const cudaError_t e = csa2::launch_pages_free(reinterpret_cast<cudaStream_t>(stream), P, n, seqs, window, n_first, lo);
   if (e != cudaSuccess) return cuda_fail(ctx, e, where);
   ctx->last_launches = 1;
@@ -274,6 +283,7 @@ csa2_status csa2_pages_compact(csa2_ctx* ctx, void* stream, const csa2_page_pool
   csa2::PageArrays A{};
   if ((s = check_pool(ctx, "pages_compact", pool, 0, &P)) != CSA2_OK) return s;
   if ((s = check_arrays(ctx, "pages_compact", pool->page_size, n_arrays, arrays, &A)) != CSA2_OK) return s;
+  if (!aligned(n_live, 4)) return fail(ctx, CSA2_ERR_INVALID_ARG, "pages_compact: misaligned buffer");
   s = check_ws(ctx, "pages_compact", workspace, workspace_bytes, csa2::pages_workspace_bytes(P.n_seq, P.n_pages));
   if (s != CSA2_OK) return s;
   const cudaError_t e = csa2::launch_pages_compact(reinterpret_cast<cudaStream_t>(stream), ctx->num_sms, P, A, n_live, workspace);
@@ -331,11 +341,15 @@ csa2_status csa2_rope(csa2_ctx* ctx, void* stream, const csa2_rope_table* table,
       return fail(ctx, CSA2_ERR_INVALID_ARG, "rope: a frequency of the table is not finite or 2^32 and more");
   if (n_tokens == 0 || n_heads == 0) return CSA2_OK;
   const uintptr_t size = dtype == CSA2_DTYPE_FP32 ? 4 : 2;
-  if (!x || !out || !pos || !aligned(x, size) || !aligned(out, size))
+  if (!x || !out || !pos || !aligned_all(size, x, out) || !aligned(pos, 8))
     return fail(ctx, CSA2_ERR_INVALID_ARG, "rope: null or misaligned buffer");
   // strides of axes of one are never used
   if (n_tokens == 1) x_tok_stride = out_tok_stride = 0;
   if (n_heads == 1) x_head_stride = out_head_stride = 0;
+  // extents are sums of products below 2^63
+  const double far = (double)n_tokens * (double)std::max(x_tok_stride, out_tok_stride) +
+                     (double)n_heads * (double)std::max(x_head_stride, out_head_stride);
+  if (far > 0x1p56) return fail(ctx, CSA2_ERR_UNSUPPORTED, "rope: a tensor of more than 2^56 elements");
   const bool in_place = out == x;
   if (in_place && (x_tok_stride != out_tok_stride || x_head_stride != out_head_stride))
     return fail(ctx, CSA2_ERR_INVALID_ARG, "rope: in place, x and out must have the same strides");

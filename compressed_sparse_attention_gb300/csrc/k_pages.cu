@@ -365,7 +365,7 @@ __global__ void __launch_bounds__(256) pages_free_kernel(const PagePool P, const
   int64_t head_lo = 0, head_hi = 0, tail = 0;
   int n_cols = P.max_pages;
   if (window >= 0) {
-    head_lo = lo_of != nullptr ? max(lo_of[b], (int64_t)0) : 0;
+    head_lo = lo_of != nullptr ? min(max(lo_of[b], (int64_t)0), (int64_t)1 << 40) : 0;  // past any row
     head_hi = head_lo + n_first;
     tail = max(head_lo, len - window);
     n_cols = (int)min((int64_t)P.max_pages, pages_for(P, max(len, (int64_t)0)));

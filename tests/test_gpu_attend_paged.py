@@ -323,3 +323,40 @@ def test_refusals():
                                  f8.ws.numel()) == 1
     torch.cuda.synchronize()
     assert (c.out == 3).all() and c.ctx.last_launch_count == 0 and p is not None
+
+
+def test_refuses_misaligned_elements():
+    from compressed_sparse_attention_gb300 import binding
+    c = Case([100], page=16, seed=29)
+    c.out.fill_(3)
+    good = dict(pos=c.pos_d.data_ptr(), seq=c.seq_d.data_ptr(), lo=None, sink=c.sink.data_ptr(), lse=c.lse.data_ptr())
+    for k, by in (("pos", 4), ("seq", 2), ("lo", 4), ("sink", 1), ("lse", 2)):
+        a = dict(good, **{k: (good[k] or good["pos"]) + by})
+        assert c.ctx.lib.csa2_attend_paged(c.ctx.h, None, binding.C.byref(c.kv.args), 1, c.q.data_ptr(), a["pos"], a["seq"],
+                                           a["lo"], 0, 0, a["sink"], c.out.data_ptr(), a["lse"], c.ws.data_ptr(),
+                                           c.ws.numel()) == 1, k
+    torch.cuda.synchronize()
+    assert (c.out == 3).all() and c.ctx.last_launch_count == 0
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("page", [8, 32])
+def test_more_tiles_than_two_a_cta(fmt, page):
+    # runs are then cut by cost: many short sequences, some of one row, and long ones that cross many runs
+    rng = random.Random(30)
+    lens = [rng.choice([1, 3, 130, rng.randint(100, 900), rng.randint(100, 900)]) for _ in range(80)] + [9001, 1, 6000]
+    rng.shuffle(lens)
+    Case(lens, fmt, page=page, seed=31).run().check()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp4"])
+def test_long_and_empty_queries_in_turn_under_a_window(fmt):
+    # every third query sees nothing, neighbours see one to eleven tiles
+    rng = random.Random(32)
+    lens = [rng.randint(1, 1500) for _ in range(40)]
+    queries = []
+    for b, n in enumerate(lens):
+        queries += [(b, n - 1), (b, -1), (b, rng.randint(0, n - 1)), (-1, 5)]
+    c = Case(lens, fmt, page=16, window=1300, n_first=3, lo=[rng.choice([0, 0, 7]) for _ in lens], queries=queries, seed=33)
+    c.run().check()
+    assert (c.out.view(-1, 4, HEADS, DIM)[:, 3] == 77.0).all() and (c.lse.view(-1, 4, HEADS)[:, 3] == 77.0).all()

@@ -297,3 +297,35 @@ def test_refusals():
         p.ctx.pages_fork(p.pool, ids, ids, [p.arrays[0][:, :8]], p.ws)
     torch.cuda.synchronize()
     assert torch.equal(p.table, before) and p.ctx.check()[0] == 0
+
+
+def test_more_sequences_than_the_plan_holds_in_shared_memory():
+    n = 2500
+    p = Pool([3] * 6 + [0] * (n - 6), page=4, n_pages=6000, cols=3, seed=19, arrays=((torch.uint8, 16),))
+    p.do("extend", list(range(n)), [5 if b % 2 else 3 for b in range(n)])
+    p.do("free", list(range(6, n, 3)))
+    p.do("fork", [1, 1, 5], [6, 9, 12])
+    p.do("fork", [0, 4, 4], [15, 18, 21], deep=True)
+    p.compact()
+
+
+def test_trim_where_the_first_position_lies_past_every_row():
+    p = Pool([40, 33, 8], page=8, seed=20)
+    p.do("trim", [0, 1, 2], 16, 10 ** 15, [2 ** 62 + 5, 20, -3])
+
+
+def test_refuses_misaligned_elements():
+    from compressed_sparse_attention_gb300 import binding
+    p = Pool([40, 0], page=16, seed=21)
+    lib, h, a = p.ctx.lib, p.ctx.h, binding.C.byref(p.pool.args)
+    ids, lens, ws, size = p.ids([0, 1]).data_ptr(), p.seq_len.data_ptr(), p.ws.data_ptr(), p.ws.numel()
+    before = p.table.clone()
+    assert lib.csa2_pages_extend(h, None, a, 1, ids + 2, lens, ws, size) == 1
+    assert lib.csa2_pages_extend(h, None, a, 1, ids, lens + 4, ws, size) == 1
+    assert lib.csa2_pages_fork(h, None, a, 1, ids + 2, ids, 0, 0, None, ws, size) == 1
+    assert lib.csa2_pages_fork(h, None, a, 1, ids, ids + 1, 0, 0, None, ws, size) == 1
+    assert lib.csa2_pages_free(h, None, a, 1, ids + 2) == 1
+    assert lib.csa2_pages_trim(h, None, a, 1, ids, 4, 0, lens + 4) == 1
+    assert lib.csa2_pages_compact(h, None, a, 0, None, ids + 2, ws, size) == 1
+    torch.cuda.synchronize()
+    assert torch.equal(p.table, before) and p.ctx.check()[0] == 0

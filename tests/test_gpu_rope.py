@@ -1,8 +1,8 @@
 """csa2_rope and csa2_append_paged against plain 64-bit forms.
 
 csa2_rope's bound: the rotated value is u cos - v sin in fp32 from a (cos, sin)
-within 2^-22 of the exact one (sincosf of a reduced angle that is rounded to
-fp32: 2^-24 * pi for the argument, one ulp for the function) scaled by the
+within 2^-22 of the exact one (a turn in 64-bit fixed point, rounded to fp32:
+2^-24 * pi for the argument, one ulp for the function) scaled by the
 amplitude: |error| <= (2^-22 + 4 * 2^-24)(|u| + |v|) amplitude, then one
 rounding to the type, half a step of the result. Channels that are not
 rotated are equal."""
@@ -221,6 +221,56 @@ def test_rope_refusals():
     assert (out == 5).all()
 
 
+def test_angles_of_very_far_positions():
+    # against pi to 100 digits. A frequency's turn is rounded to 2^-64: off by
+    # 2^-65 turns a position; the turn (at most a half) to fp32 by 2^-24 of itself
+    from decimal import Decimal, getcontext
+    require_gpu()
+    getcontext().prec = 100
+    pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798")
+    r = 64
+    tab = table(r, theta=5.0e5)
+    pos = [2 ** 20 + 1, 2 ** 31 - 1, 2 ** 33 + 12345, 2 ** 38 + 7, 3 * 2 ** 37 + 11]
+    x = torch.zeros((len(pos), 1, r), device=DEV)
+    x[..., 0::2] = 1.0  # (1, 0) -> (cos, sin)
+    out = torch.empty_like(x)
+    for sign in (1, -1):
+        context().rope(tab, x, torch.tensor(pos, device=DEV), out, transpose=sign < 0)
+        got = out.cpu().double()
+        for i, p in enumerate(pos):
+            for k in range(r // 2):
+                turn = Decimal(p) * Decimal(tab.freq[k]) / (2 * pi)
+                a = float((turn - turn.to_integral_value()) * 2 * pi) * sign
+                tol = 2 * math.pi * p * 2.0 ** -65 + math.pi * 2.0 ** -24 + 2.0 ** -23
+                assert abs(got[i, 0, 2 * k].item() - math.cos(a)) <= tol and \
+                    abs(got[i, 0, 2 * k + 1].item() - math.sin(a)) <= tol, (p, k)
+
+
+def test_rope_refuses_bad_tables_pointers_and_extents():
+    from compressed_sparse_attention_gb300 import binding
+    require_gpu()
+    ctx = context()
+    tab = table(32)
+    x = torch.full((4, 3, 64), 2.0, device=DEV)
+    pos = torch.zeros(5, dtype=torch.int64, device=DEV)
+
+    def call(t=tab, p=pos.data_ptr(), n=4, stride=192):
+        return ctx.lib.csa2_rope(ctx.h, None, binding.C.byref(t), 2, n, 3, 64, x.data_ptr(), stride, 64, p, x.data_ptr(), stride,
+                                 64, 0)
+
+    for k, v in ((0, math.inf), (15, math.nan), (3, 2.0 ** 32), (3, -2.0 ** 40)):
+        broken = binding.RopeTable.from_buffer_copy(tab)
+        broken.freq[k] = v
+        assert call(broken) == 1, (k, v)
+    broken = binding.RopeTable.from_buffer_copy(tab)
+    broken.amplitude = math.nan
+    assert call(broken) == 1
+    assert call(p=pos.data_ptr() + 4) == 1
+    assert call(n=2 ** 40, stride=2 ** 30) == 2
+    torch.cuda.synchronize()
+    assert (x == 2).all() and ctx.last_launch_count == 0
+
+
 # ---------------------------------------------------------------- append
 
 @pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
@@ -332,3 +382,7 @@ def test_append_refusals():
         ctx.h, None, binding.C.byref(kv.args), dt, p, n, off.data_ptr(), first.data_ptr())
     assert call(dt=1) == 2 and call(n=-1) == 1 and call(p=None) == 1 and call(p=rows.data_ptr() + 4) == 1
     assert call(n=0) == 0 and ctx.last_launch_count == 0
+    assert lib.csa2_append_paged(ctx.h, None, binding.C.byref(kv.args), 2, rows.data_ptr(), 3, off.data_ptr() + 4,
+                                 first.data_ptr()) == 1
+    assert lib.csa2_append_paged(ctx.h, None, binding.C.byref(kv.args), 2, rows.data_ptr(), 3, off.data_ptr(),
+                                 first.data_ptr() + 4) == 1
