@@ -765,6 +765,9 @@ __device__ __forceinline__ void issue_role(const Issuer& mma, Cursor cur, const 
 // large as the others moved some head's reference in nearly every tile, at
 // 1.0 us a move (decode of 128K rows, fp8).
 constexpr float kRefSlack = 32.f;
+// What scores are taken against while no row has set a head's reference (its
+// rows so far are missing, or -inf or NaN): the first finite one exceeds it.
+constexpr float kNoRef = -1e38f;
 
 // Softmax of one tile (thread: row = TMEM lane, heads 32 hh .. +31 of warp w,
 // hh = w / 4) and, at a query's end, its output or partial. Most tiles need
@@ -817,7 +820,7 @@ __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* s
       }
       if (tid < kHeads) {
         m_run[tid] = -INFINITY;
-        m_use[tid] = 0.f;
+        m_use[tid] = kNoRef;
       }
 #pragma unroll
       for (int k = 0; k < 32; ++k) lsum[k] = 0.f;
@@ -854,7 +857,7 @@ __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* s
           const float mo = m_run[tid];
           const float mn = (mo == -INFINITY || top > mo + kRefSlack) ? fmaxf(mo, top) : mo;
           const float al = (mo == -INFINITY) ? 1.f : exp2f(mo - mn);
-          m_use[tid] = mn == -INFINITY ? 0.f : mn;
+          m_use[tid] = mn == -INFINITY ? kNoRef : mn;
           alpha[tid] = al;
           m_run[tid] = mn;
           moved = al != 1.f;

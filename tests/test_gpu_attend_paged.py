@@ -360,3 +360,25 @@ def test_long_and_empty_queries_in_turn_under_a_window(fmt):
     c = Case(lens, fmt, page=16, window=1300, n_first=3, lo=[rng.choice([0, 0, 7]) for _ in lens], queries=queries, seed=33)
     c.run().check()
     assert (c.out.view(-1, 4, HEADS, DIM)[:, 3] == 77.0).all() and (c.lse.view(-1, 4, HEADS)[:, 3] == 77.0).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp4"])
+def test_first_tiles_without_a_row_before_tiles_with_some(fmt):
+    # several tiles a CTA; the first one or two of every second query have no page, and its scores lie below the
+    # reference that nothing has set (a weight of 2^-150 and less against 1)
+    from compressed_sparse_attention_gb300 import binding
+    rng = random.Random(36)
+    lens = [rng.randint(300, 520) for _ in range(330)]
+    c = Case(lens, fmt, page=16, seed=37, sink=None)
+    for b in range(0, 330, 2):
+        n = rng.choice([8, 9, 16])
+        c.table_rows[b][:n] = [-1] * n
+        c.table[b, :n] = -1
+    c.run(flags=binding.FLAG_BAD_PAGE).check()
+    values = page_values(c.codes, c.scales, c.fmt)
+    # one direction of the rows, far below zero for every query of the second half
+    side = values.mean((0, 1))
+    side = side / side.norm()
+    low = -(3000.0 * side).to(torch.bfloat16).to(DEV)
+    c.q[165:] = low
+    c.run(flags=binding.FLAG_BAD_PAGE).check()
