@@ -931,7 +931,7 @@ __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* s
           const float sk = p.a.sink != nullptr ? p.a.sink[tid] : -INFINITY, sk2 = sk * 1.4426950408889634f;
           const float M = fmaxf(mr, sk2);
           float fo = 0.f, lse = sk;  // no row seen: the denominator is the sink's
-          if (mr != -INFINITY) {
+          if (mr != -INFINITY || l != l) {  // (scores that are all NaN set no reference)
             const float em = exp2f(mr - M);
             const float den = l * em + exp2f(sk2 - M);
             fo = em / den;
@@ -1205,17 +1205,17 @@ __global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS, GROUPS == 1 ?
   for (int o = 16; o >= 4; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const bool none = M == -INFINITY;  // no row in any part
   M = fmaxf(M, sk);
-  float den = m0 == -INFINITY ? 0.f : exp2f(m0 - M) * l0;
+  float den = (m0 == -INFINITY ? 0.f : exp2f(m0 - M)) * l0;  // 0 times NaN stays
   for (int k = mine + kJoinLanes; k < n; k += kJoinLanes) {
     const float m = p.a.part_m[slot(k) * kHeads + head];
-    den += m == -INFINITY ? 0.f : exp2f(m - M) * p.a.part_l[slot(k) * kHeads + head];
+    den += (m == -INFINITY ? 0.f : exp2f(m - M)) * p.a.part_l[slot(k) * kHeads + head];
   }
 #pragma unroll
   for (int o = 16; o >= 4; o >>= 1) den += __shfl_xor_sync(0xffffffffu, den, o);
-  den = none ? 1.f : den + exp2f(sk - M);
+  den = none ? den + 1.f : den + exp2f(sk - M);
   const float inv = none ? 0.f : 1.f / den;
   if (d < 4 && group == 0 && p.a.lse != nullptr)  // lanes 0 .. 3 of the warp of dims 0 ..: a head each
-    p.a.lse[(int64_t)qi * kHeads + head] = none ? sink : (M + log2f(den)) * 0.6931471805599453f;
+    p.a.lse[(int64_t)qi * kHeads + head] = none && den == 1.f ? sink : (M + log2f(den)) * 0.6931471805599453f;
   uint32_t* out = reinterpret_cast<uint32_t*>(p.a.out + ((int64_t)qi * kHeads + 4 * hq) * kDim);
   for (int span = 0; span < spans; ++span, d += 32) {
   if (span > 0) fetch(kJoinLanes * group);

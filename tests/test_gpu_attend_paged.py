@@ -362,6 +362,23 @@ def test_long_and_empty_queries_in_turn_under_a_window(fmt):
     assert (c.out.view(-1, 4, HEADS, DIM)[:, 3] == 77.0).all() and (c.lse.view(-1, 4, HEADS)[:, 3] == 77.0).all()
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_a_query_of_nans_leaves_its_neighbours_alone(fmt):
+    # two queries a CTA and more: every other one NaN or infinite
+    rng = random.Random(34)
+    c = Case([rng.randint(1, 400) for _ in range(330)], fmt, page=16, seed=35)
+    clean = c.q.clone()
+    c.q[1::4] = math.nan
+    c.q[3::4, :, :7] = math.inf
+    c.run()
+    bad, bad_lse = c.out[1::2].clone(), c.lse[1::2].clone()
+    assert torch.isnan(bad[0::2]).all() and torch.isnan(bad_lse[0::2]).all()
+    good = c.out[0::2].clone(), c.lse[0::2].clone()
+    c.q = clean
+    c.run().check()
+    assert torch.equal(c.out[0::2], good[0]) and torch.equal(c.lse[0::2], good[1])
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "fp4"])
 def test_first_tiles_without_a_row_before_tiles_with_some(fmt):
     # several tiles a CTA; the first one or two of every second query have no page, and its scores lie below the
