@@ -21,11 +21,11 @@
 // shared memory's 128 bytes a clock), the scores' weights (1,000) and the
 // waits between them, with one tile in shared memory at a time. fp8 and fp4
 // rows: the same chain with the conversion's stores in it, 8,700 cycles. Short
-// calls: launch, cut, first rows and join, 16 us together. Calls of many short
+// calls: launch, cut, first rows and join, 14 us together. Calls of many short
 // queries: an output leaves an SM at 32 bytes a clock, 2,000 cycles (a partial
 // 4,000), and its Q takes as long to arrive. Measured: 32 ragged sequences to
 // 8K 50 us (3.1 TB/s), 8 x 128K fp8 265 us, 1,200 prompt queries under a window of
-// 512 170 us, one query over 2K rows 16 us.
+// 512 170 us, one query over 2K rows 14.5 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <type_traits>
@@ -241,9 +241,15 @@ constexpr int kTileCost = 2, kQueryCost = 3;
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
+// CTAs that share a tile, each with as many of its output dims: with fewer
+// tiles than half or a quarter of the CTAs two or four of them form the same
+// scores, and each has a share of the output's products and stores (a partial
+// leaves an SM in 4,600 cycles whole and 1,200 in quarters; one query over 2K
+// rows 16.6 -> 14.5 us). As a shift: 2, 1 or 0.
+__device__ __forceinline__ int dim_shift(int64_t tiles, int grid) { return 4 * tiles <= grid ? 2 : (2 * tiles <= grid ? 1 : 0); }
 struct RunCut {
   int64_t cost;
-  int ctas, start;  // start: kQueryCost or 0
+  int ctas, start;  // ctas: runs (of 1 << dim_shift CTAs each); start: kQueryCost or 0
   // where query i starts, b tiles coming before it
   __device__ __forceinline__ int64_t at(int64_t b, int i) const { return kTileCost * b + (int64_t)start * i; }
   // tiles of a query of n that start before x of its start
@@ -259,7 +265,7 @@ __device__ __forceinline__ RunCut run_cut(int64_t tiles, int n_query, int grid) 
   RunCut r;
   r.start = tiles > 2 * (int64_t)grid ? kQueryCost : 0;
   r.cost = kTileCost * tiles + (int64_t)r.start * n_query;
-  r.ctas = (int)min((int64_t)grid, tiles);
+  r.ctas = (int)min((int64_t)(grid >> dim_shift(tiles, grid)), tiles);
   return r;
 }
 
@@ -285,6 +291,8 @@ struct Cursor {
 struct Run {
   Cursor cur;     // at the run's first tile
   int64_t total;  // tiles of all queries
+  int index;      // the run's number
+  int m0, m1;     // this CTA's output dims, 128 m0 .. 128 m1
 };
 static_assert(sizeof(Run) <= 256, "SM_RUN");
 
@@ -684,11 +692,13 @@ __device__ __forceinline__ void produce_codes(const PagedAttendParams& p, uint8_
 // The products of one tile, by one warp (leader: 1 in the lane that issues);
 // false: a wait ran out and nothing more was issued. n: the tile's number in
 // the run, seg: its query's.
+template <bool SPLIT>  // whether CTAs share tiles (dim_shift)
 struct Issuer {
   uint32_t bars, tmem_s, tmem_o, base_s, leader;
   uint32_t* flags;
   const uint4* gone;  // by the tile's parity; null: no rows are cleared after they land
   bool rope;
+  uint32_t m0, m1;  // this CTA's output dims, 128 m0 .. 128 m1
   // S^T = KV Q^T, block by block as the rows land; the rope channels once more
   // against q's residual
   __device__ __forceinline__ bool scores(uint32_t n, uint32_t seg, bool first, bool last) const {
@@ -724,13 +734,23 @@ struct Issuer {
   __device__ __forceinline__ void output(bool first, bool last) const {
     const uint64_t kv = sdesc_sw128(base_s + SM_KV, 16384u, 1024u), pt = sdesc_sw128(base_s + SM_P, 8192u, 1024u);
     tc_fence_after();
-#pragma unroll
-    for (uint32_t m = 0; m < 4; ++m) {
+    auto dims = [&](uint32_t m) {
 #pragma unroll
       for (uint32_t k = 0; k < 8; ++k)
         mma_one(leader, tmem_o + 64u * m, sdesc_add(kv, m * 32768u + 2048u * k), sdesc_add(pt, 2048u * k), kIdescPV,
                 k > 0 || !first ? 1u : 0u);
-      commit_one(leader, bars + 8 * (kEmpty + m));
+    };
+    if constexpr (SPLIT) {
+#pragma unroll 1
+      for (uint32_t m = m0; m < m1; ++m) dims(m);
+#pragma unroll 1
+      for (uint32_t m = 0; m < 4; ++m) commit_one(leader, bars + 8 * (kEmpty + m));
+    } else {
+#pragma unroll
+      for (uint32_t m = 0; m < 4; ++m) {
+        dims(m);
+        commit_one(leader, bars + 8 * (kEmpty + m));
+      }
     }
     if (last) commit_one(leader, bars + 8 * kOut);
   }
@@ -742,7 +762,8 @@ struct Issuer {
 };
 
 // The products of a run, by the issuing warp.
-__device__ __forceinline__ void issue_role(const Issuer& mma, Cursor cur, const PagedAttendParams& p) {
+template <bool SPLIT>
+__device__ __forceinline__ void issue_role(const Issuer<SPLIT>& mma, Cursor cur, const PagedAttendParams& p) {
   const uint32_t tiles = cur.tiles();
   bool live = true, first = true;
 #pragma unroll 1
@@ -774,9 +795,9 @@ constexpr float kNoRef = -1e38f;
 // one vote on the references and neither a reduction nor a rescale; the
 // weights are summed in fp32 and rounded to bf16 for the product.
 // ISSUE: warp 0 issues the products too.
-template <bool ISSUE>
+template <bool ISSUE, bool SPLIT>
 __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* sm, uint32_t base_s, uint32_t tmem_s,
-                                          uint32_t tmem_o, const Issuer& mma, Cursor cur, const Run& run, int warp) {
+                                          uint32_t tmem_o, const Issuer<SPLIT>& mma, Cursor cur, const Run& run, int warp) {
   const SyncMath sy;
   const uint32_t bars = base_s + SM_BAR;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -789,6 +810,7 @@ __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* s
   const float4* mu4 = reinterpret_cast<const float4*>(m_use + 32 * hh);
   const float scale = p.a.scale_log2;
   const bool by_query = p.a.n_query < (int)gridDim.x;  // a join's index: its query, or the CTA that begins it
+  const int m0 = SPLIT ? run.m0 : 0, m1 = SPLIT ? run.m1 : 4;
   int2 my_join = make_int2(-1, -1);
   int my_query = -1;
   float lsum[32];
@@ -804,13 +826,13 @@ __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* s
     if (first) {
       begins = cur.tile() == 0;
       const bool ends = cur.q0 + cur.span.n_tiles <= cur.run1;
-      if (begins && tid == 0) {
+      if (begins && tid == 0 && m0 == 0) {
         const QuerySpan& s = cur.span;
         const bool seq_ok = s.b >= 0 && s.b < p.kv.n_seq;
         if (s.b != -1 && !(seq_ok && s.t >= -1)) set_flag(p.a.flags, CSA2_FLAG_BAD_QUERY);
         if (s.ok && s.vis.past_table) set_flag(p.a.flags, CSA2_FLAG_BAD_PAGE);
         const int2 jn = ends ? make_int2(-1, -1)
-                             : make_int2((int)blockIdx.x, run_cut(run.total, p.a.n_query, (int)gridDim.x).cta(cur.q0, cur.qi, s.n_tiles - 1));
+                             : make_int2(run.index, run_cut(run.total, p.a.n_query, (int)gridDim.x).cta(cur.q0, cur.qi, s.n_tiles - 1));
         if (by_query) {
           p.joins[cur.qi] = make_int4(jn.x, jn.y, cur.qi, 0);
         } else if (!ends) {
@@ -867,7 +889,7 @@ __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* s
           for (int k = 0; k < 32; ++k) lsum[k] *= alpha[32 * hh + k];
           // (the products before this tile's scores are complete: they came first)
 #pragma unroll 1
-          for (int mt = 0; mt < 4; ++mt) {
+          for (int mt = m0; mt < m1; ++mt) {
             const uint32_t a = tmem_o + (uint32_t)(64 * mt + 32 * hh) + lane_base;
             tmem_ld32(a, r);
             tmem_wait_ld();
@@ -938,11 +960,13 @@ __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* s
             lse = (M + log2f(den)) * 0.6931471805599453f;
           }
           alpha[tid] = fo;
-          if (p.a.lse != nullptr && cur.span.b != -1) p.a.lse[(int64_t)cur.qi * kHeads + tid] = lse;
+          if (p.a.lse != nullptr && cur.span.b != -1 && m0 == 0) p.a.lse[(int64_t)cur.qi * kHeads + tid] = lse;
         } else {
-          const int64_t at = (int64_t)part_slot((int)blockIdx.x, begins) * kHeads + tid;
-          p.a.part_m[at] = mr;
-          p.a.part_l[at] = l;
+          const int64_t at = (int64_t)part_slot(run.index, begins) * kHeads + tid;
+          if (m0 == 0) {
+            p.a.part_m[at] = mr;
+            p.a.part_l[at] = l;
+          }
         }
       }
       sy.sync();
@@ -954,9 +978,9 @@ __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* s
       const float2* rope_tab = reinterpret_cast<const float2*>(sm + SM_ROPETAB) + 32 * (seg & 3u);
       const int first_rope = kDim - 2 * p.a.rp.pairs;
       if (!whole) {
-        float* po = p.a.part_o + (int64_t)part_slot((int)blockIdx.x, begins) * kHeads * kDim;
+        float* po = p.a.part_o + (int64_t)part_slot(run.index, begins) * kHeads * kDim;
 #pragma unroll 1
-        for (int mt = 0; mt < 4; ++mt) {
+        for (int mt = m0; mt < m1; ++mt) {
           uint32_t r[32];
           tmem_ld32(tmem_o + (uint32_t)(64 * mt + 32 * hh) + lane_base, r);
           tmem_wait_ld();
@@ -974,7 +998,7 @@ __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* s
         uint32_t* out = reinterpret_cast<uint32_t*>(p.a.out + (int64_t)qi * kHeads * kDim);
         const bool odd = (lane & 1) != 0;
 #pragma unroll 1
-        for (int mt = 0; mt < 4; ++mt) {
+        for (int mt = m0; mt < m1; ++mt) {
           const int d = 128 * mt + row;
           uint32_t r[32];
           tmem_ld32(tmem_o + (uint32_t)(64 * mt + 32 * hh) + lane_base, r);
@@ -1083,12 +1107,15 @@ __global__ void __launch_bounds__(Roles<KVF>::kThreads, 1) attend_paged_kernel(c
       if (w < warp) before += warp_sum[w];
       total += warp_sum[w];
     }
-    const int c = (int)blockIdx.x;
+    const int shift = dim_shift(total, (int)gridDim.x), c = (int)blockIdx.x >> shift;
     const RunCut cut = run_cut(total, Q, (int)gridDim.x);
     const int64_t x0 = c < cut.ctas ? quotient((int64_t)c * cut.cost, cut.ctas) : cut.cost;
     const int64_t x1 = c < cut.ctas ? quotient((int64_t)(c + 1) * cut.cost, cut.ctas) : cut.cost;
     if (tid == 0) {
       run->total = total;
+      run->index = c;
+      run->m0 = ((int)blockIdx.x - (c << shift)) * (4 >> shift);
+      run->m1 = run->m0 + (4 >> shift);
       run->cur.at = run->cur.run1 = total;  // unless found below
     }
     __shared__ int64_t ends[2];  // first tile of this run and of the next
@@ -1133,17 +1160,23 @@ __global__ void __launch_bounds__(Roles<KVF>::kThreads, 1) attend_paged_kernel(c
   const uint32_t tmem_s = taddr, tmem_o = taddr + 64;
   Cursor cur = run->cur;
   if (uniform(cur.more())) {
-    const Issuer mma{bars, tmem_s, tmem_o, base_s, elect_one(), p.a.flags,
-                     TMA ? reinterpret_cast<const uint4*>(sm + SM_GONE) : nullptr, p.a.rp.pairs > 0};
-    if (Roles<KVF>::kOwnIssuer && warp == Roles<KVF>::kIssuer) {
-      issue_role(mma, cur, p);
-    } else if (warp >= kFirstProducer) {
+    auto work = [&](auto split) {  // products, weights and outputs
+      constexpr bool kSplit = decltype(split)::value;
+      const Issuer<kSplit> mma{bars, tmem_s, tmem_o, base_s, elect_one(), p.a.flags,
+                               TMA ? reinterpret_cast<const uint4*>(sm + SM_GONE) : nullptr, p.a.rp.pairs > 0,
+                               (uint32_t)run->m0, (uint32_t)run->m1};
+      if (Roles<KVF>::kOwnIssuer && warp == Roles<KVF>::kIssuer) issue_role(mma, cur, p);
+      else math_role<!Roles<KVF>::kOwnIssuer>(p, sm, base_s, tmem_s, tmem_o, mma, cur, *run, warp);
+    };
+    if (warp >= kFirstProducer && !(Roles<KVF>::kOwnIssuer && warp == Roles<KVF>::kIssuer)) {
       const int t = tid - 32 * kFirstProducer;
       if constexpr (KVF == 0) produce_bf16<Roles<KVF>::kProducerThreads, TMA>(p, sm, base_s, cur, t, warp - kFirstProducer, freq);
       else produce_codes<KVF, Roles<KVF>::kProducerThreads>(p, sm, base_s, cur, t, warp - kFirstProducer, freq);
       cp_async_wait_all();  // no copy may still be landing when the CTA exits
+    } else if (uniform(run->m1 - run->m0 == 4)) {
+      work(std::false_type{});
     } else {
-      math_role<!Roles<KVF>::kOwnIssuer>(p, sm, base_s, tmem_s, tmem_o, mma, cur, *run, warp);
+      work(std::true_type{});
     }
   }
   if (cur.at >= cur.run1 && Q >= (int)gridDim.x && tid == 0) p.joins[blockIdx.x] = make_int4(-1, -1, -1, 0);

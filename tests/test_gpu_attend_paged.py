@@ -399,3 +399,14 @@ def test_first_tiles_without_a_row_before_tiles_with_some(fmt):
     low = -(3000.0 * side).to(torch.bfloat16).to(DEV)
     c.q[165:] = low
     c.run(flags=binding.FLAG_BAD_PAGE).check()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+@pytest.mark.parametrize("share,more", [(4, 0), (4, 1), (2, 0), (2, 1)])
+def test_tiles_around_a_share_of_the_ctas(fmt, share, more):
+    # with fewer tiles than half or a quarter of the CTAs several of them share a tile's output dims
+    require_gpu()
+    tiles = torch.cuda.get_device_properties(0).multi_processor_count // share + more
+    rng = random.Random(38)
+    Case([rng.randint(1, 128) for _ in range(tiles)], fmt, page=16, seed=39).run().check()
+    Case([128 * (tiles - 3) - 5, 129, 1], fmt, page=64, seed=40).run().check()
