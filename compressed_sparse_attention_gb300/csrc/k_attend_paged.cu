@@ -231,7 +231,7 @@ __device__ __forceinline__ void sync_producers() {
 }
 // How the tiles are cut into runs. On a line where a tile is kTileCost long and
 // a query starts with kQueryCost (its Q, its first tile's references, an
-// output or partial more), CTA c of `ctas` has the tiles that start in the
+// output or partial more), run c of `ctas` has the tiles that start in the
 // c-th of equal parts. With fewer tiles than two a CTA, the queries' starts are
 // left out: one tile a CTA where they suffice. Parts of a query lie in
 // neighbouring CTAs, none of them empty: the parts are longer than a tile.
@@ -252,13 +252,16 @@ struct RunCut {
   int ctas, start;  // ctas: runs (of 1 << dim_shift CTAs each); start: kQueryCost or 0
   // where query i starts, b tiles coming before it
   __device__ __forceinline__ int64_t at(int64_t b, int i) const { return kTileCost * b + (int64_t)start * i; }
-  // tiles of a query of n that start before x of its start
-  __device__ __forceinline__ int tiles_before(int64_t x, int n) const {
-    return (int)min((int64_t)n, (max(x - start, (int64_t)0) + kTileCost - 1) / kTileCost);
+  // Run c begins with the first tile whose place, ctas-fold, is y = c * cost
+  // or more (products where the quotient's division would take as long as all
+  // else); of a query of n tiles, this many come before it
+  __device__ __forceinline__ int tiles_before(int64_t y, int64_t b, int i, int n) const {
+    const int64_t left = y - ctas * (at(b, i) + start), step = kTileCost * ctas;
+    return left <= 0 ? 0 : (int)min((int64_t)n, quotient(left + step - 1, step));
   }
-  // CTA of tile j of query i
-  __device__ __forceinline__ int cta(int64_t b, int i, int j) const {
-    return (int)quotient((at(b, i) + start + (int64_t)kTileCost * j + 1) * ctas - 1, cost);
+  // run of tile j of query i
+  __device__ __forceinline__ int run_of(int64_t b, int i, int j) const {
+    return (int)quotient((at(b, i) + start + (int64_t)kTileCost * j) * ctas, cost);
   }
 };
 __device__ __forceinline__ RunCut run_cut(int64_t tiles, int n_query, int grid) {
@@ -832,7 +835,7 @@ __device__ __forceinline__ void math_role(const PagedAttendParams& p, uint8_t* s
         if (s.b != -1 && !(seq_ok && s.t >= -1)) set_flag(p.a.flags, CSA2_FLAG_BAD_QUERY);
         if (s.ok && s.vis.past_table) set_flag(p.a.flags, CSA2_FLAG_BAD_PAGE);
         const int2 jn = ends ? make_int2(-1, -1)
-                             : make_int2(run.index, run_cut(run.total, p.a.n_query, (int)gridDim.x).cta(cur.q0, cur.qi, s.n_tiles - 1));
+                             : make_int2(run.index, run_cut(run.total, p.a.n_query, (int)gridDim.x).run_of(cur.q0, cur.qi, s.n_tiles - 1));
         if (by_query) {
           p.joins[cur.qi] = make_int4(jn.x, jn.y, cur.qi, 0);
         } else if (!ends) {
@@ -1109,8 +1112,6 @@ __global__ void __launch_bounds__(Roles<KVF>::kThreads, 1) attend_paged_kernel(c
     }
     const int shift = dim_shift(total, (int)gridDim.x), c = (int)blockIdx.x >> shift;
     const RunCut cut = run_cut(total, Q, (int)gridDim.x);
-    const int64_t x0 = c < cut.ctas ? quotient((int64_t)c * cut.cost, cut.ctas) : cut.cost;
-    const int64_t x1 = c < cut.ctas ? quotient((int64_t)(c + 1) * cut.cost, cut.ctas) : cut.cost;
     if (tid == 0) {
       run->total = total;
       run->index = c;
@@ -1122,17 +1123,19 @@ __global__ void __launch_bounds__(Roles<KVF>::kThreads, 1) attend_paged_kernel(c
     if (tid == 0) ends[0] = ends[1] = total;
     asm volatile("bar.sync 1, 256;" ::: "memory");
     // the thread whose share holds a cut finds the first tile from it on
+#pragma unroll 1
     for (int e = 0; e < 2; ++e) {
-      const int64_t x = e == 0 ? x0 : x1;
-      if (x >= cut.at(before, q_lo) && x < cut.at(before + mine, q_hi)) {
+      const int64_t y = min(c + e, cut.ctas) * cut.cost;
+      if (y >= cut.ctas * cut.at(before, q_lo) && y < cut.ctas * cut.at(before + mine, q_hi)) {
         int64_t b = before;
-        int i = q_lo;
-        int n = per > 1 ? query_span(p, i).n_tiles : span.n_tiles;
-        while (x >= cut.at(b + n, i + 1)) {
+        for (int i = q_lo;; ++i) {
+          const int n = per > 1 ? query_span(p, i).n_tiles : span.n_tiles;
+          if (y < cut.ctas * cut.at(b + n, i + 1)) {
+            ends[e] = b + cut.tiles_before(y, b, i, n);
+            break;
+          }
           b += n;
-          n = query_span(p, ++i).n_tiles;
         }
-        ends[e] = b + cut.tiles_before(x - cut.at(b, i), n);
       }
     }
     asm volatile("bar.sync 1, 256;" ::: "memory");
