@@ -17,9 +17,8 @@ namespace csa2 {
 
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 512;
 constexpr int kPlanWarps = kPlanThreads / 32;
-constexpr int kScanPages = 16;  // pages a thread of the plan scans in one round
 constexpr int kCopyThreads = 256;
 constexpr int kCopyChunk = 16384;  // bytes of a page that a CTA copies in one go: 4 x 16 a thread
 constexpr int kNoOwner = 0x7FFFFFFF;
@@ -45,72 +44,82 @@ __device__ __forceinline__ void plan_prefetch(const PagePool& P) {
   if (t * 16 < P.n_seq) asm volatile("prefetch.global.L2 [%0];" ::"l"(P.seq_len + t * 16));
 }
 
+// The plans run once, on instructions that come from memory, each issued as
+// often as there are warps: short code, one scan for all of them and 512
+// threads (free, fork of 24 children and extend over 2,048 pages: 18.5 us, and
+// 20.1 with 1,024 threads and a scan inlined at each place).
+
 // Exclusive scan of one value a thread over the plan's CTA; total: the sum.
-template <typename N>
-__device__ N cta_scan(N x, N& total, N* warp_sums) {
+// Sums stop at cap (values at most cap, cap below 2^31).
+__device__ __noinline__ uint32_t cta_scan(uint32_t x, uint32_t cap, uint32_t* total) {
+  __shared__ uint32_t sums[kPlanWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  N incl = x;
+  uint32_t before = 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const N v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  __syncthreads();  // the sums of the scan before have been read
-  if (lane == 31) warp_sums[warp] = incl;
-  __syncthreads();
-  if (warp == 0) {
-    N w = warp_sums[lane];
+  for (int level = 0; level < 2; ++level) {  // the warp's threads, then the warps
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const N v = __shfl_up_sync(0xffffffffu, w, o);
-      if (lane >= o) w += v;
+      const uint32_t v = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x = min(x + v, cap);
     }
-    warp_sums[lane] = w;  // inclusive
+    if (level == 0) {
+      const uint32_t left = __shfl_up_sync(0xffffffffu, x, 1);
+      before = lane > 0 ? left : 0u;
+      if (lane == 31) sums[warp] = x;
+      __syncthreads();
+      x = lane < kPlanWarps ? sums[lane] : 0u;
+    }
   }
-  __syncthreads();
-  total = warp_sums[kPlanWarps - 1];
-  return (warp > 0 ? warp_sums[warp - 1] : (N)0) + incl - x;
+  *total = __shfl_sync(0xffffffffu, x, 31);
+  const uint32_t left = __shfl_sync(0xffffffffu, x, warp > 0 ? warp - 1 : 0);
+  __syncthreads();  // sums is free for the next scan
+  return warp > 0 ? min(before + left, cap) : before;
 }
 
 // The lowest `want` free pages in ascending order into list; returns how many
-// there are (at most want). By the plan's CTA.
-__device__ int take_free(const PagePool& P, int64_t want, int32_t* list, int* warp_sums) {
+// there are (at most want). By the plan's CTA, in rounds of 4 counts a thread,
+// or of 16 for pools of more than four such rounds, whose barriers then count
+// (a million counts: 0.34 ms with 4).
+__device__ int take_free(const PagePool& P, int want, int32_t* list) {
+  const int each = P.n_pages > 16 * kPlanThreads ? 16 : 4;
+  const bool wide = (reinterpret_cast<uintptr_t>(P.ref) & 15u) == 0;
   int found = 0;
-  for (int base = 0; base < P.n_pages && found < want; base += kPlanThreads * kScanPages) {
-    const int first = base + (int)threadIdx.x * kScanPages;
+#pragma unroll 1
+  for (int64_t base = 0; base < P.n_pages && found < want; base += kPlanThreads * each) {
+    const int64_t first = base + (int64_t)threadIdx.x * each;
     uint32_t free_bits = 0;
-    if (first + kScanPages <= P.n_pages && (reinterpret_cast<uintptr_t>(P.ref) & 15u) == 0) {
-      const int4* r4 = reinterpret_cast<const int4*>(P.ref + first);
-      int4 r[kScanPages / 4];
-#pragma unroll
-      for (int u = 0; u < kScanPages / 4; ++u) r[u] = r4[u];
-#pragma unroll
-      for (int u = 0; u < kScanPages / 4; ++u)
-        free_bits |= (uint32_t)((r[u].x == 0) | (r[u].y == 0) << 1 | (r[u].z == 0) << 2 | (r[u].w == 0) << 3) << (4 * u);
-    } else {
-      for (int u = 0; u < kScanPages; ++u)
-        if (first + u < P.n_pages && P.ref[first + u] == 0) free_bits |= 1u << u;
+#pragma unroll 4
+    for (int u = 0; u < each; u += 4) {
+      const int64_t g = first + u;
+      int4 r = make_int4(1, 1, 1, 1);
+      if (wide && g + 4 <= P.n_pages) {
+        r = *reinterpret_cast<const int4*>(P.ref + g);
+      } else {
+        if (g < P.n_pages) r.x = P.ref[g];
+        if (g + 1 < P.n_pages) r.y = P.ref[g + 1];
+        if (g + 2 < P.n_pages) r.z = P.ref[g + 2];
+        if (g + 3 < P.n_pages) r.w = P.ref[g + 3];
+      }
+      free_bits |= (uint32_t)((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3) << u;
     }
-    int total;
-    int at = found + cta_scan<int>(__popc(free_bits), total, warp_sums);
-    while (free_bits != 0u) {
-      const int u = __ffs(free_bits) - 1;
-      free_bits &= free_bits - 1;
-      if (at < want) list[at] = first + u;
-      ++at;
-    }
-    found += total;
+    uint32_t total;
+    int at = found + (int)cta_scan(__popc(free_bits), 0x7FFFFFFFu, &total);
+    for (; free_bits != 0u && at < want; free_bits &= free_bits - 1) list[at++] = (int32_t)first + __ffs(free_bits) - 1;
+    found += (int)total;
   }
   __syncthreads();
-  return (int)min((int64_t)found, want);
+  return min(found, want);
 }
 
 // Marks every valid sequence named in `seqs` with the first entry naming it.
 __device__ void claim(const PagePool& P, const int32_t* seqs, int n, int32_t* owner) {
-  for (int b = threadIdx.x; b < P.n_seq; b += kPlanThreads) owner[b] = kNoOwner;
+  int b = (int)threadIdx.x < n ? seqs[threadIdx.x] : -1;  // on its way during the reset
+#pragma unroll 1
+  for (int k = threadIdx.x; k < P.n_seq; k += kPlanThreads) owner[k] = kNoOwner;
   __syncthreads();
+#pragma unroll 1
   for (int i = threadIdx.x; i < n; i += kPlanThreads) {
-    const int b = seqs[i];
+    if (i >= kPlanThreads) b = seqs[i];
     if (b >= 0 && b < P.n_seq) atomicMin(&owner[b], i);
   }
   __syncthreads();
@@ -126,19 +135,18 @@ __device__ __forceinline__ bool is_page(const PagePool& P, int32_t g) { return (
 // an entry that is not carried out. An entry whose pages are not there, and
 // with it every later one that needs any, is refused (need[i] = -1).
 __device__ void place_entries(const PagePool& P, const PagePlan& W, const Entries& E, int n) {
-  __shared__ int64_t sums64[32];
-  __shared__ int sums32[32];
-  int64_t carry = 0;
+  // offsets past the pool mean that the entry is refused below
+  const uint32_t cap = (uint32_t)P.n_pages + 1u;
+  uint32_t carry = 0;
+#pragma unroll 1
   for (int i0 = 0; i0 < n; i0 += kPlanThreads) {
     const int i = i0 + (int)threadIdx.x;
-    const int64_t x = i < n ? max(E.need[i], 0) : 0;
-    int64_t total;
-    const int64_t at = carry + cta_scan<int64_t>(x, total, sums64);
-    carry += total;
-    // offsets past the pool mean that the entry is refused below
-    if (i < n) E.off[i] = (int32_t)min(at, (int64_t)P.n_pages + 1);
+    uint32_t total;
+    const uint32_t at = cta_scan(i < n ? min((uint32_t)max(E.need[i], 0), cap) : 0u, cap, &total);
+    if (i < n) E.off[i] = (int32_t)min(carry + at, cap);
+    carry = min(carry + total, cap);
   }
-  const int n_free = take_free(P, min(carry, (int64_t)P.n_pages), W.fresh, sums32);
+  const int n_free = take_free(P, (int)min(carry, (uint32_t)P.n_pages), W.fresh);
   for (int i = threadIdx.x; i < n; i += kPlanThreads) {
     const int need = E.need[i];
     if (need > 0 && (int64_t)E.off[i] + need > n_free) {
@@ -198,6 +206,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_fork_plan_kernel(const 
   const Entries E = entries_of(P, W, sh);
   plan_prefetch(P);
   claim(P, children, n, E.owner);
+#pragma unroll 1
   for (int i = warp; i < n; i += kPlanWarps) {
     const int p = parents[i], c = children[i];
     int need = -1;
@@ -208,6 +217,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_fork_plan_kernel(const 
         const int32_t* row = P.table + (int64_t)p * P.table_ld;
         if (deep) {
           int mine = 0;
+#pragma unroll 4
           for (int j = lane; j < np; j += 32) mine += is_page(P, row[j]) ? 1 : 0;
           need = __reduce_add_sync(0xffffffffu, mine);
         } else {
@@ -232,6 +242,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_fork_plan_kernel(const 
     const int np = (int)pages_for(P, len), ps = 1 << P.page_shift;
     const int32_t* row = P.table + (int64_t)parents[i] * P.table_ld;
     int at = E.off[i];
+#pragma unroll 1
     for (int j0 = deep ? 0 : np - 1; j0 < np; j0 += 32) {
       const int j = j0 + lane;
       const int32_t g = j < np ? row[j] : -1;
@@ -399,11 +410,12 @@ __global__ void __launch_bounds__(256) pages_free_kernel(const PagePool P, const
 __global__ void __launch_bounds__(kPlanThreads, 1) pages_compact_plan_kernel(const PagePool P, const PagePlan W,
                                                                           int32_t* __restrict__ n_live_out) {
   pdl_trigger();
-  __shared__ int sums32[32];
-  int live = 0;
+  uint32_t live = 0;
+#pragma unroll 4
   for (int g = threadIdx.x; g < P.n_pages; g += kPlanThreads) live += P.ref[g] > 0 ? 1 : 0;
-  int L;
-  cta_scan<int>(live, L, sums32);
+  uint32_t total;
+  cta_scan(live, 0x7FFFFFFFu, &total);
+  const int L = (int)total;
   int n_dst = 0, n_src = 0;
   constexpr int kEach = 8;
   for (int base = 0; base < P.n_pages; base += kPlanThreads * kEach) {
@@ -422,13 +434,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_compact_plan_kernel(con
       }
     }
     // both counts in one scan: at most 8,192 of each a round
-    int total;
-    const int at = cta_scan<int>(__popc(dst_bits) | __popc(src_bits) << 16, total, sums32);
-    int d = n_dst + (at & 0xFFFF), s = n_src + (at >> 16);
+    const uint32_t at = cta_scan((uint32_t)(__popc(dst_bits) | __popc(src_bits) << 16), 0x7FFFFFFFu, &total);
+    int d = n_dst + (int)(at & 0xFFFFu), s = n_src + (int)(at >> 16);
     for (; dst_bits != 0u; dst_bits &= dst_bits - 1) W.fresh[d++] = first + __ffs(dst_bits) - 1;
     for (; src_bits != 0u; src_bits &= src_bits - 1) W.src[s++] = first + __ffs(src_bits) - 1;
-    n_dst += total & 0xFFFF;
-    n_src += total >> 16;
+    n_dst += (int)(total & 0xFFFFu);
+    n_src += (int)(total >> 16);
   }
   __syncthreads();  // the lists, of equal length, are complete
   for (int k = threadIdx.x; k < n_src; k += kPlanThreads) {
