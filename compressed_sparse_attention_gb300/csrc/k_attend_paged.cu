@@ -24,8 +24,8 @@
 // calls: launch, cut, first rows and join, 14 us together. Calls of many short
 // queries: an output leaves an SM at 32 bytes a clock, 2,000 cycles (a partial
 // 4,000), and its Q takes as long to arrive. Measured: 32 ragged sequences to
-// 8K 50 us (3.1 TB/s), 8 x 128K fp8 265 us, 1,200 prompt queries under a window of
-// 512 170 us, one query over 2K rows 14.5 us.
+// 8K 49 us (3.1 TB/s), 8 x 128K fp8 260 us, 1,200 prompt queries under a
+// window of 512 169 us, one query over 2K rows 14.4 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <type_traits>
@@ -235,7 +235,7 @@ __device__ __forceinline__ void sync_producers() {
 // c-th of equal parts. With fewer tiles than two a CTA, the queries' starts are
 // left out: one tile a CTA where they suffice. Parts of a query lie in
 // neighbouring CTAs, none of them empty: the parts are longer than a tile.
-constexpr int kTileCost = 2, kQueryCost = 3;
+constexpr int kTileCost = 4, kQueryCost = 5;
 // a / b of values >= 0: 32-bit where they fit (a 64-bit division is several
 // hundred cycles, before any row is asked for)
 __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
@@ -1089,7 +1089,7 @@ __global__ void __launch_bounds__(Roles<KVF>::kThreads, 1) attend_paged_kernel(c
   QuerySpan span;
   int64_t mine = 0, incl = 0;
   if (warp < kAttWarps) {
-#pragma unroll 4
+#pragma unroll 2  // (code before the first row is asked for comes from memory: unrolled by 4, 1 us more)
     for (int i = q_lo; i < q_hi; ++i) {
       span = query_span(p, i);
       mine += span.n_tiles;
