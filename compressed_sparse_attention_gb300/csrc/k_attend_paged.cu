@@ -24,8 +24,8 @@
 // calls: launch, cut, first rows and join, 14 us together. Calls of many short
 // queries: an output leaves an SM at 32 bytes a clock, 2,000 cycles (a partial
 // 4,000), and its Q takes as long to arrive. Measured: 32 ragged sequences to
-// 8K 49 us (3.1 TB/s), 8 x 128K fp8 260 us, 1,200 prompt queries under a
-// window of 512 169 us, one query over 2K rows 14.4 us.
+// 8K 48 us (3.2 TB/s), 8 x 128K fp8 261 us, 1,200 prompt queries under a
+// window of 512 167 us, one query over 2K rows 14.4 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <type_traits>
@@ -63,11 +63,11 @@ __device__ __forceinline__ QuerySpan query_span(const PagedAttendParams& p, int 
   s.t = p.a.q_pos[qi];
   s.b = p.a.seq_of_q[qi];
   s.ok = s.b >= 0 && s.b < p.kv.n_seq && s.t >= 0;
-  const int64_t cap = (int64_t)p.kv.max_pages << p.kv.page_shift;
+  const int32_t cap = p.kv.max_pages << p.kv.page_shift;  // at most 2^30
   const int64_t lo = (s.ok && p.lo != nullptr) ? p.lo[s.b] : 0;
   const int cs = chunk_shift(p.kv.page_shift);
   s.vis = visible_rows(s.ok ? s.t : -1, lo, p.window, p.n_first, cap, cs);
-  s.n_tiles = max(1, (int)((((int64_t)s.vis.n_chunks << cs) + kTileRows - 1) / kTileRows));
+  s.n_tiles = max(1, ((s.vis.n_chunks << cs) + kTileRows - 1) / kTileRows);
   return s;
 }
 
@@ -396,10 +396,10 @@ __device__ __forceinline__ RowAt row_at(const PagedAttendParams& p, const Cursor
   const Visible& v = cur.span.vis;
   const int i = cur.tile() * kTileRows + r, k = i >> cs;
   const bool have = k < v.n_chunks;
-  const int64_t pos = have ? chunk_pos(v, k, i & ((1 << cs) - 1), cs) : 0;
+  const int32_t pos = have ? chunk_pos(v, k, i & ((1 << cs) - 1), cs) : 0;
   RowAt a;
   a.seen = have && is_seen(v, pos);
-  a.in_page = (int32_t)pos & ((1 << p.kv.page_shift) - 1);
+  a.in_page = pos & ((1 << p.kv.page_shift) - 1);
   a.page = have ? page_of(p.kv, cur.span.b, pos) : -1;
   return a;
 }

@@ -34,9 +34,10 @@ __device__ __forceinline__ int32_t page_of(const PagedView& v, int b, int64_t p)
 // rows are taken in chunks, aligned runs of 2^shift positions that lie in one
 // page (chunk_shift): first the chunks that the first tokens touch, then those
 // of [tail, t] that are left. Rows of a chunk that the query does not see are
-// masked.
+// masked. Positions are 32 bits: a table holds at most 2^30 rows, and what lies
+// past them is cut to that first (64-bit ones cost 2% of a window's decode).
 struct Visible {
-  int64_t lo, tail, end;  // end: one past the last position (t + 1, or the table's end)
+  int32_t lo, tail, end;  // end: one past the last position (t + 1, or the table's end)
   int32_t head;           // first tokens seen
   int32_t head_chunk, n_head, tail_chunk, n_chunks;
   bool past_table;  // t lies beyond the table's last column: those rows are not there
@@ -45,43 +46,45 @@ struct Visible {
 // rows of a chunk: a page, or 64 rows of a larger one
 __host__ __device__ __forceinline__ int chunk_shift(int page_shift) { return page_shift < 6 ? page_shift : 6; }
 
+// t >= -1; cap: rows of the table, at most 2^30
 __host__ __device__ __forceinline__ Visible visible_rows(int64_t t, int64_t lo_in, int64_t window, int64_t n_first,
-                                                         int64_t cap, int shift) {
+                                                         int32_t cap, int shift) {
   Visible s;
-  s.lo = lo_in > 0 ? lo_in : 0;
+  s.lo = lo_in > 0 ? (lo_in < cap ? (int32_t)lo_in : cap) : 0;
   s.past_table = t >= cap;
-  s.end = s.past_table ? cap : t + 1;
+  s.end = s.past_table ? cap : (int32_t)t + 1;
   s.head = 0;
   s.tail = s.lo;
   s.head_chunk = s.n_head = s.tail_chunk = s.n_chunks = 0;
   if (s.end <= s.lo) return s;
   if (window > 0) {
-    const int64_t all = s.end - s.lo;
-    s.head = (int32_t)(n_first < all ? n_first : all);
+    const int32_t all = s.end - s.lo;
+    s.head = n_first < all ? (int32_t)n_first : all;
     // the window counts from t itself; a window that starts inside the first
     // tokens continues after them, so that no row is seen twice
     const int64_t from = t - window + 1;
-    s.tail = s.lo + s.head > from ? s.lo + s.head : from;
+    s.tail = s.lo + s.head;
+    if (from > s.tail) s.tail = from < cap ? (int32_t)from : cap;
   }
   if (s.head > 0) {
-    s.head_chunk = (int32_t)(s.lo >> shift);
-    s.n_head = (int32_t)((s.lo + s.head - 1) >> shift) - s.head_chunk + 1;
+    s.head_chunk = s.lo >> shift;
+    s.n_head = ((s.lo + s.head - 1) >> shift) - s.head_chunk + 1;
   }
   s.n_chunks = s.n_head;
   if (s.end > s.tail) {
-    const int32_t first = (int32_t)(s.tail >> shift), after = s.head_chunk + s.n_head;
+    const int32_t first = s.tail >> shift, after = s.head_chunk + s.n_head;
     s.tail_chunk = s.n_head > 0 && after > first ? after : first;
-    s.n_chunks += (int32_t)((s.end - 1) >> shift) - s.tail_chunk + 1;
+    s.n_chunks += ((s.end - 1) >> shift) - s.tail_chunk + 1;
   }
   return s;
 }
 
 // Position of row r of the query's chunk k < n_chunks, and whether it is seen.
-__host__ __device__ __forceinline__ int64_t chunk_pos(const Visible& s, int k, int r, int shift) {
-  const int64_t c = k < s.n_head ? s.head_chunk + k : s.tail_chunk + (k - s.n_head);
+__host__ __device__ __forceinline__ int32_t chunk_pos(const Visible& s, int k, int r, int shift) {
+  const int32_t c = k < s.n_head ? s.head_chunk + k : s.tail_chunk + (k - s.n_head);
   return (c << shift) + r;
 }
-__host__ __device__ __forceinline__ bool is_seen(const Visible& s, int64_t p) {
+__host__ __device__ __forceinline__ bool is_seen(const Visible& s, int32_t p) {
   return (p >= s.lo && p < s.lo + s.head) || (p >= s.tail && p < s.end);
 }
 
