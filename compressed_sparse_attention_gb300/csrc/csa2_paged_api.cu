@@ -154,6 +154,11 @@ csa2_status csa2_attend_paged(csa2_ctx* ctx, void* stream, const csa2_paged_kv* 
   if (n_query == 0) return CSA2_OK;
   if (!q || !q_pos || !seq_of_q || !out || !aligned_all(16, q, out) || !aligned_all(8, q_pos, lo) || !aligned_all(4, seq_of_q, sink, lse))
     return fail(ctx, CSA2_ERR_INVALID_ARG, "attend_paged: null or misaligned buffer");
+  // CTAs that share a query's output dims each read its whole Q: one may store
+  // its share of out before another has read q
+  const uint64_t qb = reinterpret_cast<uintptr_t>(q), ob = reinterpret_cast<uintptr_t>(out);
+  if ((ob > qb ? ob - qb : qb - ob) < (uint64_t)n_query * csa2::kHeads * csa2::kDim * 2)
+    return fail(ctx, CSA2_ERR_INVALID_ARG, "attend_paged: out overlaps q");
   s = check_ws(ctx, "attend_paged", workspace, workspace_bytes, csa2::attend_paged_workspace_bytes(ctx->num_sms));
   if (s != CSA2_OK) return s;
   csa2::AttendParams a{};

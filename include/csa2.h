@@ -631,7 +631,8 @@ typedef struct csa2_paged_kv {
  * The result does not depend on timing. Two launches for every 4,096 queries.
  *   workspace of csa2_attend_paged_workspace_size bytes (whatever the number
  *   of queries); calls that may overlap on the GPU need one each
- * q, pages, scales and out must be 16-byte aligned. */
+ * q, pages, scales and out must be 16-byte aligned; out must not overlap q
+ * (refused: there is no form in place). */
 size_t csa2_attend_paged_workspace_size(const csa2_ctx* ctx, int32_t n_query);
 csa2_status csa2_attend_paged(csa2_ctx* ctx, void* stream, const csa2_paged_kv* kv, int32_t n_query, const uint16_t* q,
                               const int64_t* q_pos, const int32_t* seq_of_q, const int64_t* lo, int64_t window,

@@ -410,3 +410,27 @@ def test_tiles_around_a_share_of_the_ctas(fmt, share, more):
     rng = random.Random(38)
     Case([rng.randint(1, 128) for _ in range(tiles)], fmt, page=16, seed=39).run().check()
     Case([128 * (tiles - 3) - 5, 129, 1], fmt, page=64, seed=40).run().check()
+
+
+def test_refuses_an_output_over_its_queries():
+    # CTAs that share a query's output dims each read its whole Q, so nothing may be stored over it
+    from compressed_sparse_attention_gb300 import binding
+    c = Case([100, 30, 7], page=16, seed=41)
+    row = HEADS * DIM
+    buf = torch.zeros((8 * row,), dtype=torch.bfloat16, device=DEV)
+    buf[2 * row:5 * row] = c.q.view(-1)
+    keep = buf.clone()
+    c.q = buf[2 * row:5 * row].view(3, HEADS, DIM)
+    for at in (2 * row, row, 3 * row, 5 * row - 8, 8):  # the same place, a query earlier and later, 16 bytes of overlap
+        with pytest.raises(binding.Csa2Error) as e:
+            c.call(out=buf[at:at + 3 * row].view(3, HEADS, DIM)).run()
+        assert e.value.status == 1
+    torch.cuda.synchronize()
+    assert torch.equal(buf, keep) and c.ctx.last_launch_count == 0
+    # right behind q and right before it
+    wide = torch.zeros((9 * row,), dtype=torch.bfloat16, device=DEV)
+    c.q = wide[3 * row:6 * row].view(3, HEADS, DIM)
+    c.q.copy_(keep[2 * row:5 * row].view(3, HEADS, DIM))
+    for at in (0, 6 * row):
+        c.out = wide[at:at + 3 * row].view(3, HEADS, DIM)
+        c.run().check()
