@@ -62,6 +62,9 @@ csa2_status check_table(csa2_ctx* c, const std::string& where, const void* table
     return fail(c, CSA2_ERR_UNSUPPORTED, where + ": page_size must be a power of two, 1..4096");
   if (n_seq < 1 || n_pages < 1 || max_pages < 1 || ld < max_pages)
     return fail(c, CSA2_ERR_INVALID_ARG, where + ": n_seq, n_pages, max_pages or table_ld");
+  // the plans step 32-bit counters past them by up to 4,096 and add one to n_pages
+  if (n_seq > 1 << 30 || n_pages > 1 << 30)
+    return fail(c, CSA2_ERR_UNSUPPORTED, where + ": at most 2^30 sequences and 2^30 pages");
   if ((int64_t)max_pages * page_size > (int64_t)1 << 30)
     return fail(c, CSA2_ERR_UNSUPPORTED, where + ": a table row may hold at most 2^30 rows");
   if (!table || !aligned(table, 4)) return fail(c, CSA2_ERR_INVALID_ARG, where + ": table");

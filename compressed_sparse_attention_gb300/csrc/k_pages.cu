@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) pages_compact_plan_kernel(con
         }
       }
     }
-    // both counts in one scan: at most 8,192 of each a round
+    // both counts in one scan: at most 4,096 of each a round
     const uint32_t at = cta_scan((uint32_t)(__popc(dst_bits) | __popc(src_bits) << 16), 0x7FFFFFFFu, &total);
     int d = n_dst + (int)(at & 0xFFFFu), s = n_src + (int)(at >> 16);
     for (; dst_bits != 0u; dst_bits &= dst_bits - 1) W.fresh[d++] = first + __ffs(dst_bits) - 1;

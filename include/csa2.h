@@ -595,6 +595,7 @@ csa2_status csa2_attend_noalloc(csa2_ctx* ctx, void* stream, int32_t n_seq, int3
  *                same for the scales, a multiple of 16 (0 for bf16)
  *   table        [n_seq, table_ld] int32 on the device, max_pages <= table_ld
  *                columns in use; max_pages * page_size <= 2^30
+ *   n_pages, n_seq  at most 2^30 each (pools alike)
  * A table entry outside [0, n_pages) holds no rows. */
 typedef struct csa2_paged_kv {
   void* pages;

@@ -329,3 +329,33 @@ def test_refuses_misaligned_elements():
     assert lib.csa2_pages_compact(h, None, a, 0, None, ids + 2, ws, size) == 1
     torch.cuda.synchronize()
     assert torch.equal(p.table, before) and p.ctx.check()[0] == 0
+
+
+@pytest.mark.parametrize("field", ["n_pages", "n_seq"])
+def test_refuses_more_pages_or_sequences_than_the_plans_count(field):
+    # in the last thousands below 2^31 a plan's 32-bit counters pass the end; refused before anything is read
+    from compressed_sparse_attention_gb300 import binding
+    p = Pool([40, 0], page=16, seed=22, arrays=((torch.bfloat16, 512),))
+    lib, h, C = p.ctx.lib, p.ctx.h, binding.C
+    ids, lens, ws, size = p.ids([0, 1]).data_ptr(), p.seq_len.data_ptr(), p.ws.data_ptr(), p.ws.numel()
+    before = p.table.clone(), p.ref.clone(), p.seq_len.clone()
+    a = binding.PagePoolArgs.from_buffer_copy(p.pool.args)
+    pages = torch.zeros((64, 16, 512), dtype=torch.bfloat16, device=DEV)
+    kv = binding.PagedKVArgs.from_buffer_copy(p.ctx.paged_kv(pages, p.table).args)
+    q = torch.zeros((2, 64, 512), dtype=torch.bfloat16, device=DEV)
+    out = torch.full_like(q, 3.0)
+    aws = binding.workspace(p.ctx.attend_paged_workspace_size(1), DEV)
+    for n in (2 ** 30 + 1, 2 ** 31 - 4096, 2 ** 31 - 1):
+        setattr(a, field, n)
+        setattr(kv, field, n)
+        assert lib.csa2_pages_extend(h, None, C.byref(a), 1, ids, lens, ws, size) == 2
+        assert lib.csa2_pages_fork(h, None, C.byref(a), 1, ids, ids + 4, 0, 0, None, ws, size) == 2
+        assert lib.csa2_pages_free(h, None, C.byref(a), 1, ids) == 2
+        assert lib.csa2_pages_trim(h, None, C.byref(a), 1, ids, 4, 0, None) == 2
+        assert lib.csa2_pages_compact(h, None, C.byref(a), 0, None, None, ws, size) == 2
+        assert lib.csa2_attend_paged(h, None, C.byref(kv), 1, q.data_ptr(), lens, ids, None, 0, 0, None, out.data_ptr(),
+                                     None, aws.data_ptr(), aws.numel()) == 2
+        assert lib.csa2_append_paged(h, None, C.byref(kv), 0, q.data_ptr(), 1, lens, lens) == 2
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(before, (p.table, p.ref, p.seq_len)))
+    assert (out == 3).all() and p.ctx.last_launch_count == 0 and p.ctx.check()[0] == 0
