@@ -2,6 +2,7 @@
 // and launches.
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 #include <string>
 
@@ -133,6 +134,30 @@ csa2_status check_arrays(csa2_ctx* c, const std::string& where, int32_t page_siz
     out->a[i].wide = aligned(in[i].base, 16) && in[i].page_stride % 16 == 0 ? 1 : 0;
   }
   return CSA2_OK;
+}
+
+// Whether two tensors of the same strides share an element: rows of `width`
+// elements at a * outer + b * inner, a < n_outer, b < n_inner, the second
+// tensor's `delta` elements on. Rows of one tensor lie apart, inner ones within
+// an outer stride; an axis of one has stride 0.
+bool share_elements(int64_t delta, int64_t n_outer, int64_t outer, int64_t n_inner, int64_t inner, int64_t width) {
+  // the row pairs (difference of a) that can meet leave a rest below a stride,
+  // and so do, of those, the ones by b: the two multiples on either side of 0
+  auto nearest = [](int64_t rest, int64_t stride, int64_t n, int64_t (&k)[2]) {
+    k[0] = k[1] = 0;
+    if (stride == 0) return;
+    const int64_t down = rest >= 0 ? rest / stride : -((-rest + stride - 1) / stride);
+    for (int i = 0; i < 2; ++i) k[i] = std::min(std::max(down + i, 1 - n), n - 1);
+  };
+  int64_t a[2], b[2];
+  nearest(delta, outer, n_outer, a);
+  for (const int64_t ka : a) {
+    const int64_t rest = delta - ka * outer;
+    nearest(rest, inner, n_inner, b);
+    for (const int64_t kb : b)
+      if (std::abs(rest - kb * inner) < width) return true;
+  }
+  return false;
 }
 
 }  // namespace
@@ -372,7 +397,16 @@ csa2_status csa2_rope(csa2_ctx* ctx, void* stream, const csa2_rope_table* table,
     const uintptr_t xb = reinterpret_cast<uintptr_t>(x), ob = reinterpret_cast<uintptr_t>(out);
     const uintptr_t xe = xb + size * ((n_tokens - 1) * x_tok_stride + (n_heads - 1) * x_head_stride + head_dim);
     const uintptr_t oe = ob + size * ((n_tokens - 1) * out_tok_stride + (n_heads - 1) * out_head_stride + head_dim);
-    if (xb < oe && ob < xe) return fail(ctx, CSA2_ERR_INVALID_ARG, "rope: x and out overlap without being the same");
+    if (xb < oe && ob < xe) {
+      // one inside the other's span: parts of one buffer, as the queries and keys of a fused projection, lie apart
+      if (x_tok_stride != out_tok_stride || x_head_stride != out_head_stride)
+        return fail(ctx, CSA2_ERR_INVALID_ARG, "rope: x and out of different strides lie within each other's span");
+      const int64_t delta = ((int64_t)ob - (int64_t)xb) / (int64_t)size;
+      const bool tok_outer = n_heads == 1 || (n_tokens > 1 && out_tok_stride >= head_span);
+      if (tok_outer ? share_elements(delta, n_tokens, out_tok_stride, n_heads, out_head_stride, head_dim)
+                    : share_elements(delta, n_heads, out_head_stride, n_tokens, out_tok_stride, head_dim))
+        return fail(ctx, CSA2_ERR_INVALID_ARG, "rope: x and out overlap without being the same");
+    }
   }
   int nl = 0;
   const cudaError_t e = csa2::launch_rope(reinterpret_cast<cudaStream_t>(stream), ctx->num_sms, *table, dtype, x, out, pos,

@@ -765,8 +765,10 @@ csa2_status csa2_rope_table_init(csa2_rope_table* table, int32_t rope_dim, int32
  * out stays as it is.
  *   x, out  element (i, h, c) at i * tok_stride + h * head_stride + c, in
  *           elements of dtype (bf16, fp16, fp32); out may be x itself with the
- *           same strides (in place) and must not overlap it otherwise; out's
- *           rows must not overlap each other
+ *           same strides (in place) and must not overlap it otherwise: parts of
+ *           one buffer with the same strides may lie between each other (heads
+ *           of a fused projection), with other strides their spans, first to
+ *           last element, must not meet; out's rows must not overlap each other
  *   pos     [n_tokens] int64; head_dim even, 2..1024
  * Rotated in fp32, rounded once. A position's turn is freq[k] / 2 pi in 64-bit
  * fixed point (|freq| < 2^32), so an angle is off by pos * 2^-65 turns at most

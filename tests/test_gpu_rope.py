@@ -386,3 +386,57 @@ def test_append_refusals():
                                  first.data_ptr()) == 1
     assert lib.csa2_append_paged(ctx.h, None, binding.C.byref(kv.args), 2, rows.data_ptr(), 3, off.data_ptr(),
                                  first.data_ptr() + 4) == 1
+
+
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("tokens,heads,dim", [(1, 5, 64), (6, 1, 64), (6, 5, 64), (300, 4, 24)])
+def test_rope_between_parts_of_one_buffer(layout, tokens, heads, dim):
+    # x and out are parts of one buffer that share no element, though the span of one holds elements of the other
+    require_gpu()
+    ctx = context()
+    tab = table(16, layout=layout, offset=8, theta=10000.0)
+    g = torch.Generator().manual_seed(7)
+    pos = torch.randint(0, 4000, (tokens,), generator=g).to(DEV)
+    make = lambda *shape: torch.randn(shape, generator=g).to(torch.bfloat16).to(DEV)  # noqa: E731
+    fused, by_head, wide = make(tokens, 3 * heads, dim), make(2 * heads, tokens, dim), make(tokens, heads, 2 * dim)
+    parts = [(fused, fused[:, heads:2 * heads], fused[:, 2 * heads:]), (fused, fused[:, 2 * heads:], fused[:, heads:2 * heads]),
+             (by_head, by_head[:heads].transpose(0, 1), by_head[heads:].transpose(0, 1)),
+             (by_head, by_head[0::2].transpose(0, 1), by_head[1::2].transpose(0, 1)),
+             (wide, wide[..., dim:], wide[..., :dim])]
+    for buf, x, out in parts:
+        before = buf.clone()
+        want = torch.empty((tokens, heads, dim), dtype=buf.dtype, device=DEV)
+        ctx.rope(tab, x.clone(), pos, want)
+        ctx.rope(tab, x, pos, out)
+        assert torch.equal(out, want)
+        out.copy_(before.as_strided(out.shape, out.stride(), out.storage_offset()))
+        assert torch.equal(buf, before)
+
+
+def test_rope_refuses_parts_that_overlap():
+    from compressed_sparse_attention_gb300 import binding
+    require_gpu()
+    ctx = context()
+    tab = table(16)
+    pos = torch.arange(6, device=DEV)
+    buf = torch.full((8, 12, 64), 2.0, device=DEV)
+    flat = buf.view(-1)
+    view = lambda at, tok, head: flat[at:].as_strided((4, 3, 32), (tok, head, 1), flat.storage_offset() + at)  # noqa: E731
+    x = view(256, 768, 64)
+    for at, tok, head in ((256 + 31, 768, 64), (256 - 31, 768, 64), (256 + 128, 768, 64), (256 + 768, 768, 64),
+                          (256 + 64 + 2, 768, 64), (256 + 768 * 3 - 64, 768, 64),  # equal strides: an element in common
+                          (256 + 32, 768, 128), (256 + 32, 512, 64)):              # others: within the other's span
+        with pytest.raises(binding.Csa2Error) as e:
+            ctx.rope(tab, x, pos[:4], view(at, tok, head))
+        assert e.value.status == 1, (at, tok, head)
+    torch.cuda.synchronize()
+    assert (buf == 2).all() and ctx.last_launch_count == 0
+    for at in (256 + 32, 256 - 32, 256 + 192, 256 + 768 * 3 + 192):
+        out = view(at, 768, 64)
+        before = buf.clone()
+        ctx.rope(tab, x, pos[:4], out)
+        want = torch.empty((4, 3, 32), device=DEV)
+        ctx.rope(tab, x.clone(), pos[:4], want)
+        assert torch.equal(out, want)
+        out.fill_(2.0)
+        assert torch.equal(buf, before)
