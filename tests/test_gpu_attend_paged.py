@@ -434,3 +434,29 @@ def test_refuses_an_output_over_its_queries():
     for at in (0, 6 * row):
         c.out = wide[at:at + 3 * row].view(3, HEADS, DIM)
         c.run().check()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_the_first_call_of_a_host_thread(fmt):
+    # a thread that has made no CUDA call has no current driver context, which a tensor map's encoding wants
+    import threading
+    c = Case([100, 300], fmt=fmt, page=16, seed=42).run()
+    want = c.out.clone()
+    call = c.call()
+    for _ in range(2):
+        c.out.zero_()
+        torch.cuda.synchronize()
+        bad = []
+
+        def work():
+            try:
+                call.run()
+            except Exception as e:  # noqa: BLE001
+                bad.append(e)
+
+        t = threading.Thread(target=work)
+        t.start()
+        t.join()
+        torch.cuda.synchronize()
+        assert not bad, bad
+        assert torch.equal(c.out, want)
