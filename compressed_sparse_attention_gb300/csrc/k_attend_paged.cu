@@ -28,6 +28,7 @@
 // window of 512 167 us, one query over 2K rows 14.4 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
+#include <atomic>
 #include <type_traits>
 
 #include "attend_tile.cuh"
@@ -1313,7 +1314,9 @@ constexpr size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 // Tensor map of bf16 rows, boxes of 64 channels (128 bytes, the swizzle's width).
 cudaError_t encode_bf16_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
                             const uint32_t* box) {
-  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  // looked up by the first call; host threads with contexts of their own may make it at once
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> looked_up{nullptr};
+  PFN_cuTensorMapEncodeTiled_v12000 encode = looked_up.load(std::memory_order_acquire);
   if (encode == nullptr) {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult found;
@@ -1321,6 +1324,7 @@ cudaError_t encode_bf16_map(CUtensorMap* map, int rank, const void* base, const 
     if (e != cudaSuccess) return e;
     if (found != cudaDriverEntryPointSuccess) return cudaErrorNotSupported;
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    looked_up.store(encode, std::memory_order_release);
   }
   const uint32_t ones[3] = {1u, 1u, 1u};
   cuuint64_t d[3], st[2];

@@ -460,3 +460,44 @@ def test_the_first_call_of_a_host_thread(fmt):
         torch.cuda.synchronize()
         assert not bad, bad
         assert torch.equal(c.out, want)
+
+
+def test_first_calls_of_two_host_threads():
+    # a fresh process, whose first calls of the library come from two threads at once, each on a context and a stream of its own
+    import os
+    import subprocess
+    import sys
+    require_gpu()
+    code = """
+import threading, torch
+from compressed_sparse_attention_gb300 import binding
+g = torch.Generator().manual_seed(0)
+pages = torch.randn((8, 16, 512), generator=g).to(torch.bfloat16).cuda()
+table = torch.arange(8, dtype=torch.int32, device='cuda').view(1, 8)
+q = torch.randn((1, 64, 512), generator=g).to(torch.bfloat16).cuda()
+pos, seq = torch.tensor([120], device='cuda'), torch.zeros(1, dtype=torch.int32, device='cuda')
+made = []
+for _ in range(2):
+    ctx = binding.Context()
+    ws = binding.workspace(ctx.attend_paged_workspace_size(1), 'cuda')
+    out = torch.zeros_like(q)
+    made.append((ctx, out, ctx.prepare_attend_paged(ctx.paged_kv(pages, table), q, pos, seq, out, ws), torch.cuda.Stream()))
+torch.cuda.synchronize()
+gate, bad = threading.Barrier(2), []
+def work(i):
+    try:
+        with torch.cuda.stream(made[i][3]):
+            gate.wait()
+            made[i][2].run()
+    except Exception as e:
+        bad.append(e)
+threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+for t in threads: t.start()
+for t in threads: t.join()
+torch.cuda.synchronize()
+assert not bad, bad
+assert torch.equal(made[0][1], made[1][1]) and made[0][1].abs().max() > 0 and all(m[0].check()[0] == 0 for m in made)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
