@@ -501,3 +501,43 @@ assert torch.equal(made[0][1], made[1][1]) and made[0][1].abs().max() > 0 and al
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("window,n_first", [(0, 0), (20, 0), (20, 4), (500, 3)])
+def test_positions_past_the_table(window, n_first):
+    # the table holds 64 rows; a query past it sees those of them that its mask leaves, and the rest are missing
+    queries = [(0, 63), (0, 64), (0, 70), (0, 83), (0, 84), (0, 95), (1, 100), (0, 1000), (1, 30), (0, 300000)]
+    c = Case([64, 50], page=32, window=window, n_first=n_first, lo=[0, 9], queries=queries, seed=43)
+    c.run(flags=c.b.FLAG_BAD_PAGE).check()
+    # a first position at the table's end and past it: no row that the table holds is seen
+    d = Case([64, 64], page=32, window=window, n_first=n_first, lo=[64, 70], queries=[(0, 64), (0, 90), (1, 90), (1, 69)], seed=44)
+    d.run(flags=d.b.FLAG_BAD_PAGE).check()
+    assert (d.out == 0).all()
+
+
+@pytest.mark.parametrize("fmt,page", [("bf16", 4), ("fp8", 4), ("fp4", 4), ("fp8", 1), ("fp4", 2), ("bf16", 4096), ("fp8", 4096),
+                                      ("fp4", 4096)])
+def test_small_and_large_pages(fmt, page):
+    Case([333, 1, 140], fmt=fmt, page=page, seed=page + 45).run().check()
+    Case([300, 77], fmt=fmt, page=page, per=2, window=90, n_first=5, lo=[3, 0], seed=page + 46).run().check()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+def test_dense_prompt_chunk(fmt):
+    # every token of a chunk over a prefix is a query and sees all rows up to its own: more tiles than two a CTA
+    lens, per = [333, 210, 128], [130, 90, 60]
+    queries = [(b, n - k + i) for b, (n, k) in enumerate(zip(lens, per)) for i in range(k)]
+    c = Case(lens, fmt=fmt, page=32, lo=[0, 5, 0], queries=queries, seed=47).run()
+    pick = sorted({*range(0, len(queries), 9), 129, 130, 219, 220, len(queries) - 1})
+    c.out, c.lse, c.q = c.out[pick], c.lse[pick], c.q[pick]
+    c.seq, c.pos = [c.seq[i] for i in pick], [c.pos[i] for i in pick]
+    c.check()
+
+
+def test_dense_prompt_chunk_from_an_empty_cache():
+    # the first chunk of a prompt: query i sees i + 1 rows
+    c = Case([200, 1, 131], page=16, queries=[(b, t) for b, n in enumerate([200, 1, 131]) for t in range(n)], seed=48).run()
+    pick = [0, 1, 2, 63, 64, 127, 128, 129, 199, 200, 201, 202, 328, 329, 330, 331]
+    c.out, c.lse, c.q = c.out[pick], c.lse[pick], c.q[pick]
+    c.seq, c.pos = [c.seq[i] for i in pick], [c.pos[i] for i in pick]
+    c.check()

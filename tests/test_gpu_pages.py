@@ -359,3 +359,28 @@ def test_refuses_more_pages_or_sequences_than_the_plans_count(field):
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(before, (p.table, p.ref, p.seq_len)))
     assert (out == 3).all() and p.ctx.last_launch_count == 0 and p.ctx.check()[0] == 0
+
+
+@pytest.mark.parametrize("n_pages", [2047, 2048, 2049, 4095, 4096, 4097, 8191, 8192, 8193])
+def test_pools_around_the_plans_rounds(n_pages):
+    # fresh pages are looked for 2,048 counts a round, 8,192 in pools above that size; compaction goes by 4,096
+    p = Pool([0] * 6, page=1, n_pages=n_pages, cols=n_pages, seed=23, arrays=((torch.uint8, 16),))
+    p.do("extend", [0, 1, 2], [n_pages // 2, n_pages // 3, 1])
+    p.do("free", [0])
+    p.compact()
+    p.do("fork", [1, 2], [5, 0], deep=True)
+    p.do("free", [1])
+    p.do("extend", [4, 3], [min(n_pages, 5), n_pages])  # the second: not enough pages
+    p.do("extend", [3], [p.host.ref.count(0)])          # exactly all that are left
+    p.do("free", [4, 5])
+    p.compact()
+
+
+@pytest.mark.parametrize("n", [2047, 2048, 2049])
+def test_sequences_around_what_the_plan_holds_in_shared_memory(n):
+    p = Pool([3] * 6 + [0] * (n - 6), page=4, n_pages=6000, cols=3, seed=24, arrays=((torch.uint8, 16),))
+    p.do("extend", list(range(n - 1, -1, -1)), [5 if b % 2 else 3 for b in range(n)])
+    p.do("free", list(range(6, n, 3)) + [n - 1])
+    p.do("fork", [1, 1, 5], [6, 9, n - 1])
+    p.do("fork", [0, 4, 4], [15, 18, 21], deep=True)
+    p.compact()

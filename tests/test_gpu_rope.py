@@ -440,3 +440,23 @@ def test_rope_refuses_parts_that_overlap():
         assert torch.equal(out, want)
         out.fill_(2.0)
         assert torch.equal(buf, before)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("layout", ["interleaved", "half"])
+@pytest.mark.parametrize("dim,r,offset", [(1024, 512, 512), (1024, 512, 0), (1022, 2, 600), (1024, 0, 0)])
+def test_more_units_a_head_than_threads(dtype, layout, dim, r, offset):
+    # one element off every wider alignment: one pair (interleaved) or one element of each member (half) a unit
+    require_gpu()
+    ctx = context()
+    g = torch.Generator().manual_seed(dim + r + offset)
+    make = lambda: torch.randn((5 * 3 * dim + 1,), generator=g).to(dtype).to(DEV)[1:].view(5, 3, dim)  # noqa: E731
+    x, out = make(), make()
+    before = out.clone()
+    pos = torch.tensor([0, 17, -1, 4000, 123456], device=DEV)
+    tab = table(r, layout=layout, offset=offset, theta=10000.0)
+    ctx.rope(tab, x, pos, out)
+    check_rope(x, out, pos, r, offset, layout, exact_freq(r, 10000.0, "none", 1, 1, 1, 1), before=before)
+    keep = x.clone()
+    ctx.rope(tab, x, pos)
+    assert torch.equal(x, torch.where((pos >= 0)[:, None, None], out, keep))
