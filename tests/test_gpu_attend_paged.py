@@ -541,3 +541,29 @@ def test_dense_prompt_chunk_from_an_empty_cache():
     c.out, c.lse, c.q = c.out[pick], c.lse[pick], c.q[pick]
     c.seq, c.pos = [c.seq[i] for i in pick], [c.pos[i] for i in pick]
     c.check()
+
+
+@pytest.mark.parametrize("fmt,page", [("bf16", 4096), ("fp8", 64)])
+def test_the_last_rows_of_the_largest_table(fmt, page):
+    # 2^30 rows a sequence: positions, chunks and columns at the end of 32 bits
+    from compressed_sparse_attention_gb300 import binding
+    end, cols = 2 ** 30, 2 ** 30 // page
+    n = -(-400 // page) + 1
+    # the window starts 400 rows before the end; the first tokens lie right behind lo
+    lens, lo = [1], [end - 300]
+    c = Case(lens, fmt=fmt, page=page, window=150, n_first=5, lo=lo, queries=[(0, end - 1), (0, end - 140), (0, end - 300)],
+             seed=49, spare=n + 1)
+    c.table = torch.full((1, cols), -1, dtype=torch.int32, device=DEV)
+    c.table[0, cols - n:] = torch.arange(n, dtype=torch.int32)
+    c.kv = c.ctx.paged_kv(c.codes, c.table, c.scales)
+    c.table_rows = [c.table[0].tolist()]
+    c.run().check()
+    c.window = 0  # every row from lo on
+    c.run().check()
+    c.pos = [end, end + 7, end - 2]
+    c.pos_d.copy_(torch.tensor(c.pos))
+    c.run(flags=binding.FLAG_BAD_PAGE).check()
+
+
+def test_one_position_asked_for_by_several_queries():
+    Case([900, 40], page=16, queries=[(0, 899), (1, 39), (0, 899), (0, 899), (1, 39)], seed=50).run().check()

@@ -384,3 +384,42 @@ def test_sequences_around_what_the_plan_holds_in_shared_memory(n):
     p.do("fork", [1, 1, 5], [6, 9, n - 1])
     p.do("fork", [0, 4, 4], [15, 18, 21], deep=True)
     p.compact()
+
+
+def test_copies_past_32_bits():
+    # pages of 128 KB: the source past 8 GB, the copies from the pool's start and back again
+    from compressed_sparse_attention_gb300 import binding
+    require_gpu()
+    ctx = context()
+    n_pages, page, width = 70000, 64, 2048
+    a = torch.empty((n_pages, page, width), dtype=torch.uint8, device=DEV)
+    a[-2:] = torch.randint(0, 256, (2, page, width), generator=torch.Generator().manual_seed(25), dtype=torch.uint8).to(DEV)
+    a[:3] = 7
+    want = a[-2:].clone()
+    table = torch.full((2, 3), -1, dtype=torch.int32, device=DEV)
+    table[0, :2] = torch.tensor([n_pages - 1, n_pages - 2], dtype=torch.int32)
+    ref = torch.zeros(n_pages, dtype=torch.int32, device=DEV)
+    ref[-2:] = 1
+    seq_len = torch.tensor([page + 9, 0], dtype=torch.int64, device=DEV)
+    pool = ctx.page_pool(table, seq_len, ref, page)
+    ws = binding.workspace(ctx.pages_workspace_size(pool), DEV)
+    ids = Pool.ids
+    ctx.pages_fork(pool, ids([0]), ids([1]), [a], ws, deep=True)
+    assert ctx.check()[0] == 0 and table[1].tolist() == [0, 1, -1]
+    assert torch.equal(a[0], want[1]) and torch.equal(a[1, :9], want[0, :9]) and (a[1, 9:] == 7).all()
+    n_live = ids([0])
+    ctx.pages_compact(pool, [a], n_live, ws)
+    assert ctx.check()[0] == 0 and n_live.item() == 4 and table.tolist() == [[3, 2, -1], [0, 1, -1]]
+    assert torch.equal(a[2:4], want) and ref.sum().item() == 4
+
+
+def test_a_table_row_of_the_largest_length():
+    # 2^30 rows of 4,096 a page
+    page, cols = 4096, 2 ** 30 // 4096
+    p = Pool([0, 0, 0], page=page, n_pages=cols + 40, cols=cols, seed=26, arrays=())
+    p.do("extend", [0, 1], [2 ** 30 - 5000, 17])
+    p.do("extend", [0, 1], [2 ** 30, 2 ** 30 + 1])  # the second: past the table
+    p.do("fork", [0], [2])
+    p.do("free", [0])
+    p.do("extend", [1], [4097])
+    p.compact()

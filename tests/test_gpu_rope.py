@@ -460,3 +460,44 @@ def test_more_units_a_head_than_threads(dtype, layout, dim, r, offset):
     keep = x.clone()
     ctx.rope(tab, x, pos)
     assert torch.equal(x, torch.where((pos >= 0)[:, None, None], out, keep))
+
+
+def test_rope_offsets_past_32_bits():
+    # 2^31 and more elements, 4 GB and more: the last tokens against a small call
+    require_gpu()
+    ctx = context()
+    n, heads, dim = 262200, 64, 128
+    x = torch.empty((n, heads, dim), dtype=torch.bfloat16, device=DEV)
+    x[-40:] = torch.randn((40, heads, dim), generator=torch.Generator().manual_seed(8)).to(torch.bfloat16).to(DEV)
+    pos = torch.arange(n, device=DEV)
+    for layout in ("interleaved", "half"):
+        tab = table(96, layout=layout, offset=16)
+        small = torch.empty((40, heads, dim), dtype=torch.bfloat16, device=DEV)
+        ctx.rope(tab, x[-40:].clone(), pos[-40:].clone(), small)
+        out = torch.empty_like(x)
+        ctx.rope(tab, x, pos, out)
+        assert torch.equal(out[-40:], small)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp4"])
+def test_append_past_32_bits(fmt):
+    # pages past 4 GB, and the last rows of a table of 2^30
+    require_gpu()
+    ctx = context(kv_format=fmt)
+    f = FMT_NAMES[fmt]
+    page, cols = 64, 2 ** 24
+    n_pages = 70000 if f == 0 else 270000
+    width = 512 if f == 0 else 256
+    codes = torch.zeros((n_pages, page, width), dtype=torch.bfloat16 if f == 0 else torch.uint8, device=DEV)
+    scales = None if f == 0 else torch.zeros((n_pages, page, 32), dtype=torch.uint8, device=DEV)
+    tab = torch.full((1, cols), -1, dtype=torch.int32, device=DEV)
+    tab[0, -2:] = torch.tensor([n_pages - 1, n_pages - 3], dtype=torch.int32)
+    rows = torch.randn((70, DIM), generator=torch.Generator().manual_seed(9)).to(DEV)
+    first = 2 ** 30 - 70
+    ctx.append_paged(ctx.paged_kv(codes, tab, scales), rows, torch.tensor([0, 70], device=DEV), torch.tensor([first], device=DEV))
+    assert ctx.check()[0] == 0
+    exact = torch.stack([layer_turned(rows[i].double().cpu(), first + i, ctx.cfg) for i in range(70)])
+    got = torch.cat((codes[n_pages - 1, 58:], codes[n_pages - 3])).cpu()
+    sc = None if scales is None else torch.cat((scales[n_pages - 1, 58:], scales[n_pages - 3])).cpu()
+    assert_rows_close_stored(got, sc, exact.numpy(), f, "append")
+    assert (codes[n_pages - 2] == 0).all() and (codes[n_pages - 1, :58] == 0).all() and (codes[:n_pages - 3:997] == 0).all()
