@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const int64_t turn = (int64_t)((uint64_t)a.pos[tok0 + tk] * a.turns[k]);
     float c, s;
     sincospif((float)turn * 0x1p-63f, &s, &c);
-    tab[tk * table_row + (VEC > 2 || (HALF && VEC > 1) ? table_at(k) : k)] = make_float2(a.amplitude * c, a.amplitude * s);
+    tab[tk * table_row + (VEC > 2 ? table_at(k) : k)] = make_float2(a.amplitude * c, a.amplitude * s);
   }
   if (tid < n_tok) live[tid] = a.pos[tok0 + tid] >= 0;
   __syncthreads();
@@ -224,13 +224,12 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
   }
 }
 
-template <typename T, int VEC, int ALIGN>
+template <typename T, int VEC, bool HALF, int ALIGN>
 cudaError_t launch_rope_t(cudaStream_t st, RopeArgs& a, int num_sms, bool in_place, int* n_launch) {
   const int r = a.rope_dim, D = a.head_dim;
-  const bool half = a.layout == CSA2_ROPE_HALF;
-  a.units_rope = half ? (r / 2) / VEC : (r + VEC - 1) / VEC;
+  a.units_rope = HALF ? (r / 2) / VEC : (r + VEC - 1) / VEC;
   // in place the channels that stay need no copy
-  a.units_pass = in_place ? 0 : (half ? (D - r) / VEC : D / VEC - a.units_rope);
+  a.units_pass = in_place ? 0 : (HALF ? (D - r) / VEC : D / VEC - a.units_rope);
   const int units = a.units_rope + a.units_pass;
   if (units == 0) return cudaSuccess;
   const int pairs = r / 2;
@@ -248,8 +247,7 @@ cudaError_t launch_rope_t(cudaStream_t st, RopeArgs& a, int num_sms, bool in_pla
   a.heads_per_cta = hpc;
   if (gx > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)gx, (unsigned)((a.n_heads + hpc - 1) / hpc));
-  if (half) rope_kernel<T, VEC, true, ALIGN><<<grid, kRopeThreads, 0, st>>>(a);
-  else rope_kernel<T, (VEC < 2 ? 2 : VEC), false, ALIGN><<<grid, kRopeThreads, 0, st>>>(a);
+  rope_kernel<T, VEC, HALF, ALIGN><<<grid, kRopeThreads, 0, st>>>(a);
   *n_launch += 1;
   return cudaGetLastError();
 }
@@ -268,10 +266,13 @@ cudaError_t launch_rope_type(cudaStream_t st, RopeArgs& a, int num_sms, bool in_
            mult(a.x_tok) && mult(a.x_head) && mult(a.o_tok) && mult(a.o_head) && mult(a.head_dim) &&
            mult(a.offset) && (!half || mult(a.rope_dim / 2));
   };
-  if (fits(W)) return launch_rope_t<T, W, 16>(st, a, num_sms, in_place, n_launch);
-  if (half) return launch_rope_t<T, 1, (int)sizeof(T)>(st, a, num_sms, in_place, n_launch);
-  if (fits(2)) return launch_rope_t<T, 2, 2 * (int)sizeof(T)>(st, a, num_sms, in_place, n_launch);
-  return launch_rope_t<T, 2, (int)sizeof(T)>(st, a, num_sms, in_place, n_launch);
+  constexpr int S = (int)sizeof(T);
+  if (half)
+    return fits(W) ? launch_rope_t<T, W, true, 16>(st, a, num_sms, in_place, n_launch)
+                   : launch_rope_t<T, 1, true, S>(st, a, num_sms, in_place, n_launch);
+  if (fits(W)) return launch_rope_t<T, W, false, 16>(st, a, num_sms, in_place, n_launch);
+  return fits(2) ? launch_rope_t<T, 2, false, 2 * S>(st, a, num_sms, in_place, n_launch)
+                 : launch_rope_t<T, 2, false, S>(st, a, num_sms, in_place, n_launch);
 }
 
 // ---------------------------------------------------------------------------
