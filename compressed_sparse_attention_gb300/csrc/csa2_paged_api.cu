@@ -336,7 +336,8 @@ csa2_status csa2_rope_table_init(csa2_rope_table* t, int32_t rope_dim, int32_t o
   if (scaling < CSA2_ROPE_NONE || scaling > CSA2_ROPE_YARN) return CSA2_ERR_INVALID_ARG;
   if (!(theta > 0) || !std::isfinite(theta) || !(factor >= 1) || !std::isfinite(factor) || !std::isfinite(amplitude))
     return CSA2_ERR_INVALID_ARG;
-  if (scaling == CSA2_ROPE_YARN && (!(theta > 1) || !(orig_len > 0) || !(beta_fast > 0) || !(beta_slow > 0)))
+  if (scaling == CSA2_ROPE_YARN &&
+      (!(theta > 1) || !(orig_len > 0) || !std::isfinite(orig_len) || !(beta_fast > 0) || !(beta_slow > 0)))
     return CSA2_ERR_INVALID_ARG;
   t->rope_dim = rope_dim;
   t->offset = offset;

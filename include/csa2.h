@@ -754,7 +754,8 @@ typedef struct csa2_rope_table {
   double freq[CSA2_ROPE_MAX_PAIRS];
 } csa2_rope_table;
 /* rope_dim even, 0..512; offset even; theta > 0 (> 1 for yarn), factor >= 1,
- * amplitude finite; orig_len and the betas > 0 (read for yarn only). Host only. */
+ * amplitude finite; orig_len and the betas > 0, orig_len finite (read for yarn
+ * only). Host only. */
 csa2_status csa2_rope_table_init(csa2_rope_table* table, int32_t rope_dim, int32_t offset, int32_t layout, double theta,
                                  int32_t scaling, double factor, double orig_len, double beta_fast, double beta_slow,
                                  double amplitude);

@@ -133,3 +133,13 @@ def test_page_arrays_are_checked_against_the_pool(lib):
     for bad in (good[:5], good[:, :4], good[:, :, 0], torch.zeros(6)):
         with pytest.raises(ValueError):
             c._page_arrays(pool, [bad])
+
+
+def test_yarn_tables_of_an_infinite_length(lib):
+    # the ramp would begin at infinity and make every frequency a NaN
+    with pytest.raises(binding.Csa2Error) as e:
+        binding.rope_table(64, scaling="yarn", factor=4.0, orig_len=math.inf)
+    assert e.value.status == 1
+    assert binding.rope_table(64, scaling="linear", factor=4.0, orig_len=math.inf).freq[0] == 0.25  # not read
+    # an infinite beta only puts an end of the ramp at the first pair
+    assert all(0 < f <= 1 for f in binding.rope_table(64, scaling="yarn", factor=4.0, beta_fast=math.inf).freq[:32])
