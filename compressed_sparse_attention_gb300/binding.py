@@ -486,7 +486,18 @@ class Context:
         a.table, a.table_ld = self._strided(table, torch.int32, "table")
         a.n_seq, a.max_pages = table.shape
         a.n_pages, a.page_size = pages.shape[:2]
-        return PagedKV(a, (pages, scales, table))
+        return PagedKV(a, (pages, scales, table), fmt, self.device)
+
+    def _kv(self, kv: "PagedKV"):
+        """The block of a cache whose rows this context reads: of its format and on its device."""
+        if kv.fmt != self.cfg.kv_format or kv.device != self.device:
+            raise ValueError(f"kv is of format {kv.fmt} on {kv.device}, the context of format {self.cfg.kv_format} on {self.device}")
+        return C.byref(kv.args)
+
+    def _pool(self, pool: "PagePool"):
+        if pool.device != self.device:
+            raise ValueError(f"pool is on {pool.device}, the context on {self.device}")
+        return C.byref(pool.args)
 
     def attend_paged_workspace_size(self, n_query) -> int:
         return int(self.lib.csa2_attend_paged_workspace_size(self.h, n_query))
@@ -502,7 +513,7 @@ class Context:
         self._shape(lse, (n, 64), "lse")
         self._shape(lo, (kv.args.n_seq,), "lo")
         return PreparedCall(self, "csa2_attend_paged", (
-            C.byref(kv.args), n, self._p(q, torch.bfloat16, "q"), self._p(q_pos, torch.int64, "q_pos"),
+            self._kv(kv), n, self._p(q, torch.bfloat16, "q"), self._p(q_pos, torch.int64, "q_pos"),
             self._p(seq_of_q, torch.int32, "seq_of_q"), self._p(lo, torch.int64, "lo"), int(window), int(n_first),
             self._p(sink, torch.float32, "sink"), self._p(out, torch.bfloat16, "out"),
             self._p(lse, torch.float32, "lse"), self._p(workspace, None, "workspace"),
@@ -519,7 +530,7 @@ class Context:
         self._shape(tok_off, (kv.args.n_seq + 1,), "tok_off")
         self._shape(first_pos, (kv.args.n_seq,), "first_pos")
         return PreparedCall(self, "csa2_append_paged", (
-            C.byref(kv.args), DTYPE_CODES.get(rows.dtype, -1), self._p(rows, (torch.bfloat16, torch.float32), "rows"),
+            self._kv(kv), DTYPE_CODES.get(rows.dtype, -1), self._p(rows, (torch.bfloat16, torch.float32), "rows"),
             rows.shape[0], self._p(tok_off, torch.int64, "tok_off"), self._p(first_pos, torch.int64, "first_pos")),
             (kv, rows, tok_off, first_pos))
 
@@ -538,7 +549,7 @@ class Context:
         a.seq_len = self._p(seq_len, torch.int64, "seq_len")
         a.ref = self._p(ref, torch.int32, "ref")
         a.n_pages, a.page_size = ref.numel(), page_size
-        return PagePool(a, (table, seq_len, ref))
+        return PagePool(a, (table, seq_len, ref), self.device)
 
     def pages_workspace_size(self, pool: "PagePool") -> int:
         return int(self.lib.csa2_pages_workspace_size(self.h, C.byref(pool.args)))
@@ -558,7 +569,7 @@ class Context:
     def prepare_pages_extend(self, pool, seqs, new_len, workspace) -> "PreparedCall":
         self._shape(new_len, (seqs.shape[0],), "new_len")
         return PreparedCall(self, "csa2_pages_extend", (
-            C.byref(pool.args), seqs.shape[0], self._p(seqs, torch.int32, "seqs"),
+            self._pool(pool), seqs.shape[0], self._p(seqs, torch.int32, "seqs"),
             self._p(new_len, torch.int64, "new_len"), *self._ws(workspace)), (pool, seqs, new_len, workspace))
 
     def pages_extend(self, pool, seqs, new_len, workspace):
@@ -569,7 +580,7 @@ class Context:
         self._shape(children, (parents.shape[0],), "children")
         c = self._page_arrays(pool, arrays)
         return PreparedCall(self, "csa2_pages_fork", (
-            C.byref(pool.args), parents.shape[0], self._p(parents, torch.int32, "parents"),
+            self._pool(pool), parents.shape[0], self._p(parents, torch.int32, "parents"),
             self._p(children, torch.int32, "children"), 1 if deep else 0, len(arrays), c, *self._ws(workspace)),
             (pool, parents, children, tuple(arrays), c, workspace))
 
@@ -578,7 +589,7 @@ class Context:
         self.prepare_pages_fork(pool, parents, children, arrays, workspace, deep).run()
 
     def prepare_pages_free(self, pool, seqs) -> "PreparedCall":
-        return PreparedCall(self, "csa2_pages_free", (C.byref(pool.args), seqs.shape[0],
+        return PreparedCall(self, "csa2_pages_free", (self._pool(pool), seqs.shape[0],
                                                       self._p(seqs, torch.int32, "seqs")), (pool, seqs))
 
     def pages_free(self, pool, seqs):
@@ -588,7 +599,7 @@ class Context:
     def prepare_pages_trim(self, pool, seqs, window, n_first=0, lo=None) -> "PreparedCall":
         self._shape(lo, (pool.args.n_seq,), "lo")
         return PreparedCall(self, "csa2_pages_trim", (
-            C.byref(pool.args), seqs.shape[0], self._p(seqs, torch.int32, "seqs"), int(window), int(n_first),
+            self._pool(pool), seqs.shape[0], self._p(seqs, torch.int32, "seqs"), int(window), int(n_first),
             self._p(lo, torch.int64, "lo")), (pool, seqs, lo))
 
     def pages_trim(self, pool, seqs, window, n_first=0, lo=None):
@@ -599,7 +610,7 @@ class Context:
         c = self._page_arrays(pool, arrays)
         self._shape(n_live, (1,), "n_live")
         return PreparedCall(self, "csa2_pages_compact", (
-            C.byref(pool.args), len(arrays), c, self._p(n_live, torch.int32, "n_live"), *self._ws(workspace)),
+            self._pool(pool), len(arrays), c, self._p(n_live, torch.int32, "n_live"), *self._ws(workspace)),
             (pool, tuple(arrays), c, n_live, workspace))
 
     def pages_compact(self, pool, arrays, n_live, workspace):
@@ -688,17 +699,19 @@ class Context:
 
 
 class PagedKV:
-    """A csa2_paged_kv block kept alive with the tensors it points at."""
+    """A csa2_paged_kv block kept alive with the tensors it points at, and the
+    row format and device that it was made for."""
 
-    def __init__(self, args: PagedKVArgs, tensors):
-        self.args, self._keep = args, tensors
+    def __init__(self, args: PagedKVArgs, tensors, fmt, device):
+        self.args, self._keep, self.fmt, self.device = args, tensors, fmt, device
 
 
 class PagePool:
-    """A csa2_page_pool block kept alive with the tensors it points at."""
+    """A csa2_page_pool block kept alive with the tensors it points at, and
+    their device."""
 
-    def __init__(self, args: PagePoolArgs, tensors):
-        self.args, self._keep = args, tensors
+    def __init__(self, args: PagePoolArgs, tensors, device):
+        self.args, self._keep, self.device = args, tensors, device
 
 
 class PreparedCall:

@@ -143,3 +143,32 @@ def test_yarn_tables_of_an_infinite_length(lib):
     assert binding.rope_table(64, scaling="linear", factor=4.0, orig_len=math.inf).freq[0] == 0.25  # not read
     # an infinite beta only puts an end of the ramp at the first pair
     assert all(0 < f <= 1 for f in binding.rope_table(64, scaling="yarn", factor=4.0, beta_fast=math.inf).freq[:32])
+
+
+def test_blocks_of_another_format_or_device_are_refused(lib):
+    # pages of several layers side by side: an fp8 cache's page stride also passes for a bf16 page, whose reads would
+    # leave the tensor behind the last one
+    bf16, f8 = _Cpu(), _Cpu(1)
+    cache = torch.zeros((10, 3, 16, 512), dtype=torch.uint8)
+    tab = torch.zeros((2, 3), dtype=torch.int32)
+    kv = f8.paged_kv(cache[:, 2], tab, torch.zeros((10, 16, 16), dtype=torch.uint8))
+    q = torch.zeros((1, 64, 512), dtype=torch.bfloat16)
+    pos, seq = torch.zeros(1, dtype=torch.int64), torch.zeros(1, dtype=torch.int32)
+    ws, off, first = torch.zeros(8), torch.zeros(3, dtype=torch.int64), torch.zeros(2, dtype=torch.int64)
+    f8.prepare_attend_paged(kv, q, pos, seq, q.clone(), ws)
+    f8.prepare_append_paged(kv, torch.zeros((1, 512)), off, first)
+    pool = bf16.page_pool(tab, first, torch.zeros(10, dtype=torch.int32), 16)
+    other = _Cpu(1)
+    other.device = torch.device("meta")
+    for c in (bf16, other):
+        with pytest.raises(ValueError):
+            c.prepare_attend_paged(kv, q, pos, seq, q.clone(), ws)
+        with pytest.raises(ValueError):
+            c.prepare_append_paged(kv, torch.zeros((1, 512)), off, first)
+    ids = torch.zeros(1, dtype=torch.int32, device="meta")
+    for call in (lambda: other.prepare_pages_free(pool, ids), lambda: other.prepare_pages_trim(pool, ids, 4),
+                 lambda: other.prepare_pages_extend(pool, ids, ids.long(), ids),
+                 lambda: other.prepare_pages_fork(pool, ids, ids, [], ids),
+                 lambda: other.prepare_pages_compact(pool, [], None, ids)):
+        with pytest.raises(ValueError):
+            call()
