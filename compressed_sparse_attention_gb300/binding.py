@@ -567,6 +567,7 @@ class Context:
                                                        workspace.numel() * workspace.element_size())
 
     def prepare_pages_extend(self, pool, seqs, new_len, workspace) -> "PreparedCall":
+        self._shape(seqs, (seqs.numel(),), "seqs")
         self._shape(new_len, (seqs.shape[0],), "new_len")
         return PreparedCall(self, "csa2_pages_extend", (
             self._pool(pool), seqs.shape[0], self._p(seqs, torch.int32, "seqs"),
@@ -577,6 +578,7 @@ class Context:
         self.prepare_pages_extend(pool, seqs, new_len, workspace).run()
 
     def prepare_pages_fork(self, pool, parents, children, arrays, workspace, deep=False) -> "PreparedCall":
+        self._shape(parents, (parents.numel(),), "parents")
         self._shape(children, (parents.shape[0],), "children")
         c = self._page_arrays(pool, arrays)
         return PreparedCall(self, "csa2_pages_fork", (
@@ -589,6 +591,7 @@ class Context:
         self.prepare_pages_fork(pool, parents, children, arrays, workspace, deep).run()
 
     def prepare_pages_free(self, pool, seqs) -> "PreparedCall":
+        self._shape(seqs, (seqs.numel(),), "seqs")
         return PreparedCall(self, "csa2_pages_free", (self._pool(pool), seqs.shape[0],
                                                       self._p(seqs, torch.int32, "seqs")), (pool, seqs))
 
@@ -597,6 +600,7 @@ class Context:
         self.prepare_pages_free(pool, seqs).run()
 
     def prepare_pages_trim(self, pool, seqs, window, n_first=0, lo=None) -> "PreparedCall":
+        self._shape(seqs, (seqs.numel(),), "seqs")
         self._shape(lo, (pool.args.n_seq,), "lo")
         return PreparedCall(self, "csa2_pages_trim", (
             self._pool(pool), seqs.shape[0], self._p(seqs, torch.int32, "seqs"), int(window), int(n_first),

@@ -172,3 +172,20 @@ def test_blocks_of_another_format_or_device_are_refused(lib):
                  lambda: other.prepare_pages_compact(pool, [], None, ids)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_entries_are_one_axis(lib):
+    # of a [2, 3] tensor of sequences only the first two would be taken
+    c = _Cpu()
+    pool = c.page_pool(torch.zeros((8, 3), dtype=torch.int32), torch.zeros(8, dtype=torch.int64),
+                       torch.zeros(10, dtype=torch.int32), 16)
+    ids, ws = torch.zeros((2, 3), dtype=torch.int32), torch.zeros(8)
+    one = torch.zeros(2, dtype=torch.int32)
+    for call in (lambda v: c.prepare_pages_free(pool, v), lambda v: c.prepare_pages_trim(pool, v, 4),
+                 lambda v: c.prepare_pages_extend(pool, v, one.long(), ws),
+                 lambda v: c.prepare_pages_fork(pool, v, one, [], ws)):
+        call(one)
+        with pytest.raises(ValueError):
+            call(ids)
+        with pytest.raises(ValueError):
+            call(torch.zeros((), dtype=torch.int32))
