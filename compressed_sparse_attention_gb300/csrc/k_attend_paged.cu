@@ -788,7 +788,9 @@ __device__ __forceinline__ void issue_role(const Issuer<SPLIT>& mma, Cursor cur,
 // the same relative precision as weights below 1, and rows whose weight
 // underflows are 2^-126 of the reference's. With 2^8 a few rows four times as
 // large as the others moved some head's reference in nearly every tile, at
-// 1.0 us a move (decode of 128K rows, fp8).
+// 1.0 us a move (decode of 128K rows, fp8). The price: an output sums up to 2^32
+// times what it would with the exact maximum before it is divided, so n rows
+// above 2^95 / n in size can overflow to an infinity.
 constexpr float kRefSlack = 32.f;
 // What scores are taken against while no row has set a head's reference (its
 // rows so far are missing, or -inf or NaN): the first finite one exceeds it.

@@ -628,7 +628,9 @@ typedef struct csa2_paged_kv {
  * A query that sees no row (q_pos -1, or t < lo_b) gives 0, lse = the sink (-inf
  * without one). A visible row whose page is missing is left out and recorded
  * as CSA2_FLAG_BAD_PAGE. The denominator sums fp32 weights, the products take
- * them rounded to bf16; partials of split sequences are fp32.
+ * them rounded to bf16; partials of split sequences are fp32. Weights reach 2^32
+ * before the sums are divided: the n rows that a query sees must lie below
+ * 2^95 / n in size (2^75 for a million), or their sum can overflow.
  * The result does not depend on timing. Two launches for every 4,096 queries.
  *   workspace of csa2_attend_paged_workspace_size bytes (whatever the number
  *   of queries); calls that may overlap on the GPU need one each

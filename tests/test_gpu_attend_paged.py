@@ -567,3 +567,12 @@ def test_the_last_rows_of_the_largest_table(fmt, page):
 
 def test_one_position_asked_for_by_several_queries():
     Case([900, 40], page=16, queries=[(0, 899), (1, 39), (0, 899), (0, 899), (1, 39)], seed=50).run().check()
+
+
+@pytest.mark.parametrize("power", [80, -80])
+def test_rows_far_from_unit_size(power):
+    # weights reach 2^32 before a reference moves: 600 rows of size 4 sum to 2^(80 + 2 + 32 + 10) at most
+    c = Case([600, 200, 3], page=16, seed=51, q_scale=30.0)
+    c.codes *= 2.0 ** power
+    c.q *= 2.0 ** -power
+    c.run().check()
