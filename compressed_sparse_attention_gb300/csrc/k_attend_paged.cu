@@ -22,10 +22,10 @@
 // waits between them, with one tile in shared memory at a time. fp8 and fp4
 // rows: the same chain with the conversion's stores in it, 8,700 cycles. Short
 // calls: launch, cut, first rows and join, 14 us together. Calls of many short
-// queries: an output leaves an SM at 32 bytes a clock, 2,000 cycles (a partial
-// 4,000), and its Q takes as long to arrive. Measured: 32 ragged sequences to
-// 8K 48 us (3.2 TB/s), 8 x 128K fp8 261 us, 1,200 prompt queries under a
-// window of 512 167 us, one query over 2K rows 14.4 us.
+// queries: 6,000 cycles an output (reading tensor memory, scaling, exchanging
+// between lanes; with its stores left out it takes as long). Measured: 32
+// ragged sequences to 8K 48.5 us (3.2 TB/s), 8 x 128K fp8 262 us, 1,200 prompt
+// queries under a window of 512 167 us, one query over 2K rows 14.6 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <atomic>
@@ -244,9 +244,9 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
 }
 // CTAs that share a tile, each with as many of its output dims: with fewer
 // tiles than half or a quarter of the CTAs two or four of them form the same
-// scores, and each has a share of the output's products and stores (a partial
-// leaves an SM in 4,600 cycles whole and 1,200 in quarters; one query over 2K
-// rows 16.6 -> 14.5 us). As a shift: 2, 1 or 0.
+// scores, and each has a share of the output's products and of its way out
+// of tensor memory (a partial takes 4,600 cycles whole and 1,200 in quarters; one
+// query over 2K rows 16.6 -> 14.5 us). As a shift: 2, 1 or 0.
 __device__ __forceinline__ int dim_shift(int64_t tiles, int grid) { return 4 * tiles <= grid ? 2 : (2 * tiles <= grid ? 1 : 0); }
 struct RunCut {
   int64_t cost;
@@ -579,7 +579,8 @@ __device__ __forceinline__ void fp4_to_bf16(uint32_t lo, uint32_t hi, uint32_t s
 // memory with the products, and a pair's registers are loaded again only when
 // they have been converted. More pairs ahead spill (128 registers a thread);
 // converted pairs kept in the free columns of tensor memory spill too and took
-// 274 to 333 us where this takes 265 (8 x 128K rows). Of a pair of blocks thread t has 16
+// 274 to 333 us where this took 265 (8 x 128K rows; fp4 as it stands spills 76
+// bytes a thread, fp8 nothing). Of a pair of blocks thread t has 16
 // channels, chunk t & 7, of rows t >> 3, + 32, ...: a load takes whole 128-byte
 // lines (fp8) of four rows.
 template <int KVF, int N>

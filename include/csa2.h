@@ -685,8 +685,9 @@ typedef struct csa2_page_array {
 
 /* The page operations. Free pages are handed out lowest index first, in the
  * order of the entries; n (the entries) is at most n_seq. An entry naming
- * sequence -1 is skipped. An entry that cannot be carried out (a sequence out
- * of range or named before in the same call, a length that does not fit) is
+ * sequence -1 (a fork: as its child) is skipped. An entry that cannot be carried
+ * out (a sequence out of range or named before in the same call, a fork's parent
+ * of -1, a length that does not fit) is
  * left out whole and recorded as CSA2_FLAG_BAD_SEQ; one whose pages are not
  * there, and every later one that needs any, as CSA2_FLAG_OUT_OF_PAGES. The
  * state decides on the device: a captured call replays on the state of then.
