@@ -87,3 +87,54 @@ def test_serving_loop(fmt, window, n_first):
             append({1: rng.randint(10, 20), 0: 16})
     ctx.pages_free(pool, ids(list(range(n_seq))))
     assert ctx.check()[0] == 0 and (ref == 0).all() and (table == -1).all() and (seq_len == 0).all()
+
+
+def test_every_operator_from_a_host_thread_without_cuda_calls():
+    # a serving loop's worker thread: its first CUDA call is the library's
+    import threading
+    from compressed_sparse_attention_gb300 import binding
+    require_gpu()
+    ctx = context()
+    g = torch.Generator().manual_seed(5)
+    pages = torch.randn((12, 16, 512), generator=g).to(torch.bfloat16).to(DEV)
+    table = torch.full((2, 4), -1, dtype=torch.int32, device=DEV)
+    seq_len, ref = torch.zeros(2, dtype=torch.int64, device=DEV), torch.zeros(12, dtype=torch.int32, device=DEV)
+    pool, kv = ctx.page_pool(table, seq_len, ref, 16), ctx.paged_kv(pages, table)
+    i32, i64 = (lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)), (lambda *v: torch.tensor(v, device=DEV))
+    ws = binding.workspace(ctx.pages_workspace_size(pool), DEV)
+    rows = torch.randn((40, 512), generator=g).to(DEV)
+    x = torch.randn((4, 2, 64), generator=g).to(DEV)
+    out, turned = torch.zeros((1, 64, 512), dtype=torch.bfloat16, device=DEV), torch.zeros_like(x)
+    q = torch.randn((1, 64, 512), generator=g).to(torch.bfloat16).to(DEV)
+    calls = [ctx.prepare_pages_extend(pool, i32(0), i64(40), ws), ctx.prepare_append_paged(kv, rows, i64(0, 40, 40), i64(0, 0)),
+             ctx.prepare_pages_fork(pool, i32(0), i32(1), [pages], ws), ctx.prepare_pages_compact(pool, [pages], i32(0), ws),
+             ctx.prepare_attend_paged(kv, q, i64(39), i32(1), out, binding.workspace(ctx.attend_paged_workspace_size(1), DEV)),
+             ctx.prepare_pages_trim(pool, i32(0), 16), ctx.prepare_pages_free(pool, i32(0, 1)),
+             ctx.prepare_rope(binding.rope_table(64), x, i64(1, 2, 3, 4), turned)]
+
+    def all_of_them(each):
+        seq_len.zero_(), ref.zero_(), table.fill_(-1), out.zero_(), turned.zero_()
+        torch.cuda.synchronize()
+        for c in calls:
+            each(c)
+            torch.cuda.synchronize()
+        return out.clone(), turned.clone(), ref.clone(), table.clone()
+
+    bad = []
+
+    def in_a_thread(c):
+        def work():
+            try:
+                c.run()
+            except Exception as e:  # noqa: BLE001
+                bad.append(e)
+        t = threading.Thread(target=work)
+        t.start()
+        t.join()
+
+    want = all_of_them(lambda c: c.run())
+    got = all_of_them(in_a_thread)
+    assert not bad, bad
+    assert ctx.check()[0] == 0 and want[0].abs().max() > 0 and (want[3] == -1).all()
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
