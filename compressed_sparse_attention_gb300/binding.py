@@ -34,6 +34,7 @@ FLAG_BAD_QUERY = 0x20
 FLAG_BAD_PAGE = 0x40
 FLAG_OUT_OF_PAGES = 0x80
 FLAG_BAD_SEQ = 0x100
+FLAG_BATCH_FULL = 0x200
 
 DTYPE_CODES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}  # csa2_dtype
 ROPE_LAYOUTS = {"interleaved": 0, "half": 1}  # csa2_rope_layout
@@ -92,6 +93,11 @@ class PagePoolArgs(C.Structure):
 
 class PageArray(C.Structure):
     _fields_ = [("base", C.c_void_p), ("page_stride", C.c_int64), ("row_bytes", C.c_int32), ("reserved", C.c_int32)]
+
+
+class BatchArgs(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("table_ld", C.c_int64), ("tok_off", C.c_void_p), ("first_pos", C.c_void_p),
+                ("req_of_tok", C.c_void_p), ("tok_pos", C.c_void_p), ("tok_slot", C.c_void_p), ("max_tokens", C.c_int64)]
 
 
 class RopeTable(C.Structure):
@@ -161,6 +167,17 @@ SIGNATURES = {
                                     C.c_void_p, C.c_size_t]),
     "csa2_append_paged": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(PagedKVArgs), C.c_int32, C.c_void_p, C.c_int64,
                                     C.c_void_p, C.c_void_p]),
+    "csa2_append_slots": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(PagedKVArgs), C.c_int32, C.c_void_p, C.c_int64,
+                                    C.c_void_p, C.c_void_p]),
+    "csa2_batch_tables": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(PagePoolArgs), C.c_int32, C.c_void_p, C.c_void_p,
+                                    C.POINTER(BatchArgs)]),
+    "csa2_query_groups": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int64, C.c_int32, C.c_int32, C.c_int32,
+                                    C.c_int32, C.c_int32, C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_void_p,
+                                    C.c_void_p, C.c_void_p]),
+    "csa2_attend_shared_workspace_size": (C.c_size_t, [C.c_void_p, C.c_int32]),
+    "csa2_attend_shared": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(PagedKVArgs), C.c_int32, C.c_void_p, C.c_void_p,
+                                     C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                     C.c_void_p, C.c_size_t]),
     "csa2_pages_workspace_size": (C.c_size_t, [C.c_void_p, C.POINTER(PagePoolArgs)]),
     "csa2_pages_extend": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(PagePoolArgs), C.c_int32, C.c_void_p, C.c_void_p,
                                     C.c_void_p, C.c_size_t]),
@@ -466,12 +483,13 @@ class Context:
             raise ValueError(f"{name}: pages overlap")
         return t.data_ptr(), stride * size, inner // max(1, t.shape[1]) * size
 
-    def paged_kv(self, pages, table, scales=None) -> "PagedKV":
+    def paged_kv(self, pages, table=None, scales=None) -> "PagedKV":
         """A cache in pages: `pages` [n_pages, page_size, 512] bf16, or uint8
         codes [.., 512] (fp8) / [.., 256] (fp4) with uint8 `scales` [n_pages,
         page_size, 16 / 32] (the page axis may be strided: pages of several
         layers side by side); `table` int32 [n_seq, max_pages], the page of
-        each run of page_size positions, -1 for none."""
+        each run of page_size positions, -1 for none (None: a cache for
+        append_slots, which reads no table)."""
         fmt = self.cfg.kv_format
         dtype, width, sw = {KV_BF16: (torch.bfloat16, 512, 0), KV_FP8: (torch.uint8, 512, 16),
                             KV_FP4: (torch.uint8, 256, 32)}[fmt]
@@ -483,8 +501,9 @@ class Context:
             if scales is None or scales.dtype != torch.uint8 or tuple(scales.shape) != (*pages.shape[:2], sw):
                 raise ValueError(f"scales must be uint8 [n_pages, page_size, {sw}]")
             a.scales, a.scale_stride, _ = self._page_array(scales, "scales")
-        a.table, a.table_ld = self._strided(table, torch.int32, "table")
-        a.n_seq, a.max_pages = table.shape
+        if table is not None:
+            a.table, a.table_ld = self._strided(table, torch.int32, "table")
+            a.n_seq, a.max_pages = table.shape
         a.n_pages, a.page_size = pages.shape[:2]
         return PagedKV(a, (pages, scales, table), fmt, self.device)
 
@@ -537,6 +556,93 @@ class Context:
     def append_paged(self, kv, rows, tok_off, first_pos):
         """csa2_append_paged: rows [n, 512] rotated at their positions and stored in their pages."""
         self.prepare_append_paged(kv, rows, tok_off, first_pos).run()
+
+    def prepare_append_slots(self, kv: "PagedKV", rows, pos, slots) -> "PreparedCall":
+        n = rows.shape[0]
+        self._shape(rows, (n, 512), "rows")
+        self._shape(pos, (n,), "pos")
+        self._shape(slots, (n,), "slots")
+        return PreparedCall(self, "csa2_append_slots", (
+            self._kv(kv), DTYPE_CODES.get(rows.dtype, -1), self._p(rows, (torch.bfloat16, torch.float32), "rows"), n,
+            self._p(pos, torch.int64, "pos"), self._p(slots, torch.int64, "slots")), (kv, rows, pos, slots))
+
+    def append_slots(self, kv, rows, pos, slots):
+        """csa2_append_slots: rows [n, 512] rotated at pos (None: as they are) and stored at their slots (-1: not)."""
+        self.prepare_append_slots(kv, rows, pos, slots).run()
+
+    def prepare_batch_tables(self, pool: "PagePool", seqs, n_new, table, tok_off, first_pos, req_of_tok, tok_pos,
+                             tok_slot) -> "PreparedCall":
+        n = seqs.numel()
+        self._shape(seqs, (n,), "seqs")
+        self._shape(n_new, (n,), "n_new")
+        self._shape(table, (n, pool.args.max_pages), "table")
+        self._shape(tok_off, (n + 1,), "tok_off")
+        self._shape(first_pos, (n,), "first_pos")
+        tokens = req_of_tok.numel()
+        for t, name in ((req_of_tok, "req_of_tok"), (tok_pos, "tok_pos"), (tok_slot, "tok_slot")):
+            self._shape(t, (tokens,), name)
+        a = BatchArgs()
+        a.table, a.table_ld = self._strided(table, torch.int32, "table")
+        a.tok_off, a.first_pos = self._p(tok_off, torch.int64, "tok_off"), self._p(first_pos, torch.int64, "first_pos")
+        a.req_of_tok = self._p(req_of_tok, torch.int32, "req_of_tok")
+        a.tok_pos, a.tok_slot = self._p(tok_pos, torch.int64, "tok_pos"), self._p(tok_slot, torch.int64, "tok_slot")
+        a.max_tokens = tokens
+        return PreparedCall(self, "csa2_batch_tables", (
+            self._pool(pool), n, self._p(seqs, torch.int32, "seqs"), self._p(n_new, torch.int64, "n_new"), C.byref(a)),
+            (pool, seqs, n_new, a, table, tok_off, first_pos, req_of_tok, tok_pos, tok_slot))
+
+    def batch_tables(self, pool, seqs, n_new, table, tok_off, first_pos, req_of_tok, tok_pos, tok_slot):
+        """csa2_batch_tables: of the requests `seqs` of the pool with n_new new
+        tokens each, the page table [n, max_pages], the offsets and first
+        positions of the new tokens, and each token's request, position and slot
+        (their length is the batch's capacity; -1 behind the last token)."""
+        self.prepare_batch_tables(pool, seqs, n_new, table, tok_off, first_pos, req_of_tok, tok_pos, tok_slot).run()
+
+    def prepare_query_groups(self, table, page_size, n_pages, q_pos, seq_of_q, min_shared, order, head, shared,
+                             n_groups=None) -> "PreparedCall":
+        n = q_pos.numel()
+        for t, name in ((q_pos, "q_pos"), (seq_of_q, "seq_of_q"), (order, "order"), (head, "head"), (shared, "shared")):
+            self._shape(t, (n,), name)
+        self._shape(n_groups, (1,), "n_groups")
+        ptr, ld = self._strided(table, torch.int32, "table")
+        return PreparedCall(self, "csa2_query_groups", (
+            ptr, ld, table.shape[1], n_pages, page_size, table.shape[0], n, self._p(q_pos, torch.int64, "q_pos"),
+            self._p(seq_of_q, torch.int32, "seq_of_q"), int(min_shared), self._p(order, torch.int32, "order"),
+            self._p(head, torch.int32, "head"), self._p(shared, torch.int64, "shared"),
+            self._p(n_groups, torch.int32, "n_groups")),
+            (table, q_pos, seq_of_q, order, head, shared, n_groups))
+
+    def query_groups(self, table, page_size, n_pages, q_pos, seq_of_q, min_shared, order, head, shared, n_groups=None):
+        """csa2_query_groups: queries whose sequences share at least min_shared
+        leading positions (whole pages) placed group by group, as attend_shared
+        takes them: order, head and shared [n]."""
+        self.prepare_query_groups(table, page_size, n_pages, q_pos, seq_of_q, min_shared, order, head, shared,
+                                  n_groups).run()
+
+    def attend_shared_workspace_size(self, n_query) -> int:
+        return int(self.lib.csa2_attend_shared_workspace_size(self.h, n_query))
+
+    def prepare_attend_shared(self, kv: "PagedKV", q, q_pos, seq_of_q, order, head, shared, out, workspace, *, sink=None,
+                              lse=None) -> "PreparedCall":
+        n = q.shape[0]
+        self._shape(q, (n, 64, 512), "q")
+        self._shape(out, (n, 64, 512), "out")
+        for t, name in ((q_pos, "q_pos"), (seq_of_q, "seq_of_q"), (order, "order"), (head, "head"), (shared, "shared")):
+            self._shape(t, (n,), name)
+        self._shape(sink, (64,), "sink")
+        self._shape(lse, (n, 64), "lse")
+        return PreparedCall(self, "csa2_attend_shared", (
+            self._kv(kv), n, self._p(q, torch.bfloat16, "q"), self._p(q_pos, torch.int64, "q_pos"),
+            self._p(seq_of_q, torch.int32, "seq_of_q"), self._p(order, torch.int32, "order"),
+            self._p(head, torch.int32, "head"), self._p(shared, torch.int64, "shared"),
+            self._p(sink, torch.float32, "sink"), self._p(out, torch.bfloat16, "out"), self._p(lse, torch.float32, "lse"),
+            *self._ws(workspace)), (kv, q, q_pos, seq_of_q, order, head, shared, sink, out, lse, workspace))
+
+    def attend_shared(self, kv, q, q_pos, seq_of_q, order, head, shared, out, workspace, *, sink=None, lse=None):
+        """csa2_attend_shared: q [n, 64, 512] over every row up to q_pos; query
+        order[k] at place k, groups of places from head[k] on, the rows below
+        shared[head[k]] read (and multiplied) once for two queries."""
+        self.prepare_attend_shared(kv, q, q_pos, seq_of_q, order, head, shared, out, workspace, sink=sink, lse=lse).run()
 
     def page_pool(self, table, seq_len, ref, page_size) -> "PagePool":
         """The state of the page operations: `table` int32 [n_seq, max_pages],

@@ -56,6 +56,14 @@ int page_shift(int32_t page_size) {
   return s;
 }
 
+csa2_status check_pages(csa2_ctx* c, const std::string& where, int32_t n_pages, int32_t page_size) {
+  if (page_shift(page_size) < 0)
+    return fail(c, CSA2_ERR_UNSUPPORTED, where + ": page_size must be a power of two, 1..4096");
+  if (n_pages < 1) return fail(c, CSA2_ERR_INVALID_ARG, where + ": n_pages");
+  if (n_pages > 1 << 30) return fail(c, CSA2_ERR_UNSUPPORTED, where + ": at most 2^30 pages");
+  return CSA2_OK;
+}
+
 // the table's shape, common to caches and pools
 csa2_status check_table(csa2_ctx* c, const std::string& where, const void* table, int64_t ld, int32_t max_pages,
                         int32_t n_pages, int32_t page_size, int32_t n_seq) {
@@ -72,9 +80,11 @@ csa2_status check_table(csa2_ctx* c, const std::string& where, const void* table
   return CSA2_OK;
 }
 
-csa2_status check_kv(csa2_ctx* c, const std::string& where, const csa2_paged_kv* kv, csa2::PagedView* v) {
+// table: whether the call reads it
+csa2_status check_kv(csa2_ctx* c, const std::string& where, const csa2_paged_kv* kv, csa2::PagedView* v, bool table = true) {
   if (!kv) return fail(c, CSA2_ERR_INVALID_ARG, where + ": no cache");
-  const csa2_status s = check_table(c, where, kv->table, kv->table_ld, kv->max_pages, kv->n_pages, kv->page_size, kv->n_seq);
+  const csa2_status s = table ? check_table(c, where, kv->table, kv->table_ld, kv->max_pages, kv->n_pages, kv->page_size, kv->n_seq)
+                              : check_pages(c, where, kv->n_pages, kv->page_size);
   if (s != CSA2_OK) return s;
   const int f = c->cfg.kv_format;
   const int64_t code = f == CSA2_KV_BF16 ? 1024 : (f == CSA2_KV_FP8_E4M3_B32 ? 512 : 256);
@@ -226,6 +236,143 @@ csa2_status csa2_append_paged(csa2_ctx* ctx, void* stream, const csa2_paged_kv* 
                                                   tok_off, first_pos, v, ctx->cfg.kv_format, ctx->rope, ctx->d_flags);
   if (e != cudaSuccess) return cuda_fail(ctx, e, "append_paged");
   ctx->last_launches = 1;
+  return CSA2_OK;
+}
+
+csa2_status csa2_append_slots(csa2_ctx* ctx, void* stream, const csa2_paged_kv* kv, int32_t dtype, const void* rows,
+                              int64_t n_tokens, const int64_t* pos, const int64_t* slots) {
+  if (!ctx) return CSA2_ERR_INVALID_ARG;
+  csa2_status s = begin(ctx, "append_slots");
+  if (s != CSA2_OK) return s;
+  csa2::PagedView v{};
+  if ((s = check_kv(ctx, "append_slots", kv, &v, false)) != CSA2_OK) return s;
+  if (dtype != CSA2_DTYPE_BF16 && dtype != CSA2_DTYPE_FP32)
+    return fail(ctx, CSA2_ERR_UNSUPPORTED, "append_slots: rows must be bf16 or fp32");
+  if (n_tokens < 0) return fail(ctx, CSA2_ERR_INVALID_ARG, "append_slots: n_tokens");
+  if (n_tokens == 0) return CSA2_OK;
+  if (!rows || !slots || !aligned(rows, 16) || !aligned_all(8, pos, slots))
+    return fail(ctx, CSA2_ERR_INVALID_ARG, "append_slots: null or misaligned buffer");
+  const cudaError_t e = csa2::launch_append_slots(reinterpret_cast<cudaStream_t>(stream), dtype, rows, n_tokens, pos, slots, v,
+                                                  ctx->cfg.kv_format, ctx->rope, ctx->d_flags);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "append_slots");
+  ctx->last_launches = 1;
+  return CSA2_OK;
+}
+
+csa2_status csa2_batch_tables(csa2_ctx* ctx, void* stream, const csa2_page_pool* pool, int32_t n_req, const int32_t* seqs,
+                              const int64_t* n_new, const csa2_batch* batch) {
+  if (!ctx) return CSA2_ERR_INVALID_ARG;
+  csa2_status s = begin(ctx, "batch_tables");
+  if (s != CSA2_OK) return s;
+  csa2::BatchParams p{};
+  if ((s = check_pool(ctx, "batch_tables", pool, 0, &p.pool)) != CSA2_OK) return s;
+  if (!batch || n_req < 0 || batch->max_tokens < 0) return fail(ctx, CSA2_ERR_INVALID_ARG, "batch_tables: n_req or max_tokens");
+  if (n_req > 1 << 20 || batch->max_tokens > (int64_t)1 << 32)
+    return fail(ctx, CSA2_ERR_UNSUPPORTED, "batch_tables: at most 2^20 requests and 2^32 tokens");
+  if (!batch->tok_off || !aligned(batch->tok_off, 8)) return fail(ctx, CSA2_ERR_INVALID_ARG, "batch_tables: tok_off");
+  if (n_req > 0 && (!seqs || !n_new || !batch->table || !batch->first_pos || !aligned_all(4, seqs, batch->table) ||
+                    !aligned_all(8, n_new, batch->first_pos) || batch->table_ld < pool->max_pages))
+    return fail(ctx, CSA2_ERR_INVALID_ARG, "batch_tables: null or misaligned buffer, or table_ld below the pool's max_pages");
+  if (batch->max_tokens > 0 && (!batch->req_of_tok || !batch->tok_pos || !batch->tok_slot || !aligned(batch->req_of_tok, 4) ||
+                                !aligned_all(8, batch->tok_pos, batch->tok_slot)))
+    return fail(ctx, CSA2_ERR_INVALID_ARG, "batch_tables: null or misaligned token arrays");
+  p.seqs = seqs;
+  p.n_new = n_new;
+  p.table = batch->table;
+  p.table_ld = batch->table_ld;
+  p.tok_off = batch->tok_off;
+  p.first_pos = batch->first_pos;
+  p.req_of_tok = batch->req_of_tok;
+  p.tok_pos = batch->tok_pos;
+  p.tok_slot = batch->tok_slot;
+  p.max_tokens = batch->max_tokens;
+  p.n_req = n_req;
+  const cudaError_t e = csa2::launch_batch_tables(reinterpret_cast<cudaStream_t>(stream), p);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "batch_tables");
+  ctx->last_launches = 1;
+  return CSA2_OK;
+}
+
+csa2_status csa2_query_groups(csa2_ctx* ctx, void* stream, const int32_t* table, int64_t table_ld, int32_t max_pages,
+                              int32_t n_pages, int32_t page_size, int32_t n_seq, int32_t n_query, const int64_t* q_pos,
+                              const int32_t* seq_of_q, int64_t min_shared, int32_t* order, int32_t* head, int64_t* shared,
+                              int32_t* n_groups) {
+  if (!ctx) return CSA2_ERR_INVALID_ARG;
+  csa2_status s = begin(ctx, "query_groups");
+  if (s != CSA2_OK) return s;
+  if ((s = check_table(ctx, "query_groups", table, table_ld, max_pages, n_pages, page_size, n_seq)) != CSA2_OK) return s;
+  if (n_query < 0 || min_shared < 1) return fail(ctx, CSA2_ERR_INVALID_ARG, "query_groups: n_query or min_shared");
+  if (n_query > csa2::kMaxGroupQueries)
+    return fail(ctx, CSA2_ERR_UNSUPPORTED, "query_groups: at most " + std::to_string(csa2::kMaxGroupQueries) + " queries");
+  if (!aligned(n_groups, 4)) return fail(ctx, CSA2_ERR_INVALID_ARG, "query_groups: misaligned n_groups");
+  if (n_query == 0) return CSA2_OK;
+  if (!q_pos || !seq_of_q || !order || !head || !shared || !aligned_all(8, q_pos, shared) || !aligned_all(4, seq_of_q, order, head))
+    return fail(ctx, CSA2_ERR_INVALID_ARG, "query_groups: null or misaligned buffer");
+  csa2::GroupParams p{};
+  p.table = table;
+  p.table_ld = table_ld;
+  p.q_pos = q_pos;
+  p.seq_of_q = seq_of_q;
+  p.order = order;
+  p.head = head;
+  p.shared = shared;
+  p.n_groups = n_groups;
+  p.flags = ctx->d_flags;
+  p.n_query = n_query;
+  p.n_seq = n_seq;
+  p.max_pages = max_pages;
+  p.n_pages = n_pages;
+  p.page_shift = page_shift(page_size);
+  // more columns than a table has: no groups
+  p.columns = (int)std::min((min_shared - 1) / page_size + 1, (int64_t)max_pages + 1);
+  const cudaError_t e = csa2::launch_query_groups(reinterpret_cast<cudaStream_t>(stream), p);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "query_groups");
+  ctx->last_launches = 2;
+  return CSA2_OK;
+}
+
+size_t csa2_attend_shared_workspace_size(const csa2_ctx* ctx, int32_t n_query) {
+  return ctx != nullptr && n_query > 0 ? csa2::attend_shared_workspace_bytes(ctx->num_sms, n_query) : 0;
+}
+
+csa2_status csa2_attend_shared(csa2_ctx* ctx, void* stream, const csa2_paged_kv* kv, int32_t n_query, const uint16_t* q,
+                               const int64_t* q_pos, const int32_t* seq_of_q, const int32_t* order, const int32_t* head,
+                               const int64_t* shared, const float* sink, uint16_t* out, float* lse, void* workspace,
+                               size_t workspace_bytes) {
+  if (!ctx) return CSA2_ERR_INVALID_ARG;
+  csa2_status s = begin(ctx, "attend_shared");
+  if (s != CSA2_OK) return s;
+  csa2::PagedView v{};
+  if ((s = check_kv(ctx, "attend_shared", kv, &v)) != CSA2_OK) return s;
+  if (n_query < 0) return fail(ctx, CSA2_ERR_INVALID_ARG, "attend_shared: n_query must not be negative");
+  if (n_query > 1 << 20) return fail(ctx, CSA2_ERR_UNSUPPORTED, "attend_shared: at most 2^20 queries");
+  if (n_query == 0) return CSA2_OK;
+  if (!q || !q_pos || !seq_of_q || !order || !head || !shared || !out || !aligned_all(16, q, out) ||
+      !aligned_all(8, q_pos, shared) || !aligned_all(4, seq_of_q, order, head, sink, lse))
+    return fail(ctx, CSA2_ERR_INVALID_ARG, "attend_shared: null or misaligned buffer");
+  // a pair of CTAs may store one query's out before another has read its q
+  const uint64_t qb = reinterpret_cast<uintptr_t>(q), ob = reinterpret_cast<uintptr_t>(out);
+  if ((ob > qb ? ob - qb : qb - ob) < (uint64_t)n_query * csa2::kHeads * csa2::kDim * 2)
+    return fail(ctx, CSA2_ERR_INVALID_ARG, "attend_shared: out overlaps q");
+  s = check_ws(ctx, "attend_shared", workspace, workspace_bytes, csa2::attend_shared_workspace_bytes(ctx->num_sms, n_query));
+  if (s != CSA2_OK) return s;
+  csa2::AttendParams a{};
+  a.q = q;
+  a.q_pos = q_pos;
+  a.seq_of_q = seq_of_q;
+  a.sink = sink;
+  a.out = out;
+  a.lse = lse;
+  a.flags = ctx->d_flags;
+  a.n_seq = kv->n_seq;
+  a.n_query = n_query;
+  a.scale_log2 = ctx->cfg.softmax_scale * 1.4426950408889634f;
+  a.rp = ctx->rope;
+  int nl = 0;
+  const cudaError_t e = csa2::launch_attend_shared(reinterpret_cast<cudaStream_t>(stream), ctx->num_sms, ctx->cfg.kv_format,
+                                                   a, v, order, head, shared, workspace, &nl);
+  if (e != cudaSuccess) return cuda_fail(ctx, e, "attend_shared");
+  ctx->last_launches = nl;
   return CSA2_OK;
 }
 

@@ -33,6 +33,7 @@
 
 #include "attend_tile.cuh"
 #include "paged.cuh"
+#include "tile_pipe.cuh"
 
 namespace csa2 {
 
@@ -126,51 +127,6 @@ constexpr uint32_t kPagedSmemBytes = SM_PAGED_TOTAL + 1024;
 
 enum Bar : uint32_t { kFull = 0, kEmpty = 8, kQFull = 12, kQEmpty = 13, kScores = 14, kOut = 15, kWeights = 16, kDrained = 17, kCleared = 18, kBars = 22 };
 
-// Bounded wait on an mbarrier phase: 100,000 suspensions of up to 20 us, then
-// CSA2_FLAG_WAIT_TIMEOUT and false. (mbar_wait with its clock is 40
-// instructions at each of a dozen places; see the note on code size below.)
-__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t phase, uint32_t* flags) {
-#pragma unroll 1
-  for (int i = 0; i < 100000; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{\n.reg .pred p;\n"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        "selp.u32 %0, 1, 0, p;\n}"
-        : "=r"(ok)
-        : "r"(bar), "r"(phase), "r"(20000u)
-        : "memory");
-    if (ok != 0u) return true;
-  }
-  set_flag(flags, CSA2_FLAG_WAIT_TIMEOUT);
-  return false;
-}
-// A warp arrives once, and waits, by its first lane (an arrival of every lane
-// is one atomic each, in turn).
-__device__ __forceinline__ void warp_arrive(uint32_t bar) {
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0)
-    asm volatile("{\n.reg .b64 t;\nmbarrier.arrive.shared::cta.b64 t, [%0];\n}" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t phase, uint32_t* flags) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = wait_phase(bar, phase, flags);
-  return __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-}
-// Tensor-core and TMA instructions take their operands from uniform registers:
-// the warps that issue them run the issuing code whole, one lane's predicate
-// on the instruction itself. (Inside a branch that one thread takes, every
-// operand is moved over one by one: a product took 95 cycles instead of 48, a
-// block's copy 230. The same holds for loops and branches on values that come
-// from memory, which the compiler cannot know to be the same in every lane:
-// they go through a shuffle or a vote first.)
-__device__ __forceinline__ int uniform(int v, int lane = 0) { return __shfl_sync(0xffffffffu, v, lane); }
-__device__ __forceinline__ bool uniform(bool v) { return __any_sync(0xffffffffu, v) != 0; }
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t r;
-  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(r));
-  return r;
-}
 __device__ __forceinline__ void mma_one(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                         uint32_t accumulate) {
   asm volatile(
@@ -186,23 +142,6 @@ __device__ __forceinline__ void commit_one(uint32_t leader, uint32_t bar) {
       "{\n.reg .pred e;\nsetp.ne.u32 e, %1, 0;\n"
       "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar), "r"(leader)
       : "memory");
-}
-__device__ __forceinline__ uint32_t phase_done(uint32_t bar, uint32_t phase) {
-  uint32_t ok;
-  asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-               : "=r"(ok)
-               : "r"(bar), "r"(phase)
-               : "memory");
-  return ok;
-}
-// wait_phase by every lane of a warp
-__device__ __forceinline__ bool wait_all_lanes(uint32_t bar, uint32_t phase, uint32_t* flags) {
-  return __all_sync(0xffffffffu, wait_phase(bar, phase, flags)) != 0;
-}
-__device__ __forceinline__ float exp2_approx(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
 }
 // largest value of the warp's lanes
 __device__ __forceinline__ float warp_max(float x) {
@@ -300,28 +239,6 @@ struct Run {
 };
 static_assert(sizeof(Run) <= 256, "SM_RUN");
 
-__device__ __forceinline__ void expect_one(uint32_t leader, uint32_t bar, uint32_t bytes) {
-  asm volatile(
-      "{\n.reg .b64 t;\n.reg .pred e;\nsetp.ne.u32 e, %2, 0;\n@e mbarrier.arrive.expect_tx.shared::cta.b64 t, [%0], %1;\n}" ::"r"(bar),
-      "r"(bytes), "r"(leader)
-      : "memory");
-}
-__device__ __forceinline__ void tma_2d_one(uint32_t leader, uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
-  asm volatile(
-      "{\n.reg .pred e;\nsetp.ne.u32 e, %5, 0;\n"
-      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(bar), "r"(leader)
-      : "memory");
-}
-__device__ __forceinline__ void tma_3d_one(uint32_t leader, uint32_t dst, const CUtensorMap* map, int x, int y, int z,
-                                           uint32_t bar) {
-  asm volatile(
-      "{\n.reg .pred e;\nsetp.ne.u32 e, %6, 0;\n"
-      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(leader)
-      : "memory");
-}
-
 // Q of a query: its plain 64-channel blocks by TMA, its rope channels (the
 // last block) rotated and split into hi + lo (see q_rope_split) by the
 // producer threads (t: index among N, warp: a uniform register's t / 32). The
@@ -409,11 +326,6 @@ __device__ __forceinline__ RowAt row_at(const PagedAttendParams& p, const Cursor
 __device__ __forceinline__ void zero16_if(uint32_t hit, uint32_t dst) {
   asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %0, 0;\n@p st.shared.v4.u32 [%1], {%2, %2, %2, %2};\n}" ::"r"(hit), "r"(dst), "r"(0u)
                : "memory");
-}
-
-__device__ __forceinline__ void prefetch_l2_line(const void* ptr) { asm volatile("prefetch.global.L2 [%0];" ::"l"(ptr)); }
-__device__ __forceinline__ void prefetch_l2(const void* ptr, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(ptr), "r"(bytes) : "memory");
 }
 
 // bf16 producers. Thread t finds row t of a tile one tile ahead and the first
@@ -535,39 +447,6 @@ __device__ __forceinline__ void produce_bf16(const PagedAttendParams& p, uint8_t
   if (!live && TMA && n > 0) {  // no copy may still be landing when the CTA exits
     warp_wait(bars + 8 * kQFull, (seg - 1) & 1u, p.a.flags);
     for (int b = 0; b < 8 && warp_wait(bars + 8 * (kFull + b), (n - 1) & 1u, p.a.flags); ++b) {}
-  }
-}
-
-// 16 bf16 channels (two 16-byte chunks) from 16 e4m3 codes and their scale, by
-// the hardware's conversions (72 cycles a warp and 16 values; assembling the
-// bits with integer operations and one bf16 product took 91).
-__device__ __forceinline__ void fp8_to_bf16(const uint4& codes, uint32_t scale, uint32_t (&o)[8]) {
-  const float sc = ue8m0_value(scale);
-  const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 a = e4m3x2_to_float2((uint16_t)(cw[k] & 0xFFFFu));
-    const float2 b = e4m3x2_to_float2((uint16_t)(cw[k] >> 16));
-    o[2 * k] = pack_bf16(a.x * sc, a.y * sc);
-    o[2 * k + 1] = pack_bf16(b.x * sc, b.y * sc);
-  }
-}
-// 16 bf16 channels from 16 E2M1 codes and their e4m3 scale (at most 6
-// significant bits: exact)
-__device__ __forceinline__ void fp4_to_bf16(uint32_t lo, uint32_t hi, uint32_t scale, uint32_t (&o)[8]) {
-  const float sc = e4m3_value(scale);
-  uint32_t h[4];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    e2m1x8_to_f16x2x4_cvt(k == 0 ? lo : hi, h);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      __half2_raw r;
-      r.x = (unsigned short)(h[u] & 0xFFFFu);
-      r.y = (unsigned short)(h[u] >> 16);
-      const float2 f = __half22float2(__half2(r));
-      o[4 * k + u] = pack_bf16(f.x * sc, f.y * sc);
-    }
   }
 }
 
@@ -783,19 +662,6 @@ __device__ __forceinline__ void issue_role(const Issuer<SPLIT>& mma, Cursor cur,
   }
   if (!live) mma.drain();
 }
-
-// A head's reference moves only when a row's score exceeds it by more than
-// this (log2 units). Weights then reach 2^32, which bf16 and fp32 hold with
-// the same relative precision as weights below 1, and rows whose weight
-// underflows are 2^-126 of the reference's. With 2^8 a few rows four times as
-// large as the others moved some head's reference in nearly every tile, at
-// 1.0 us a move (decode of 128K rows, fp8). The price: an output sums up to 2^32
-// times what it would with the exact maximum before it is divided, so n rows
-// above 2^95 / n in size can overflow to an infinity.
-constexpr float kRefSlack = 32.f;
-// What scores are taken against while no row has set a head's reference (its
-// rows so far are missing, or -inf or NaN): the first finite one exceeds it.
-constexpr float kNoRef = -1e38f;
 
 // Softmax of one tile (thread: row = TMEM lane, heads 32 hh .. +31 of warp w,
 // hh = w / 4) and, at a query's end, its output or partial. Most tiles need
@@ -1312,8 +1178,6 @@ __global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS, GROUPS == 1 ?
   }
 }
 
-namespace {
-constexpr size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 // Tensor map of bf16 rows, boxes of 64 channels (128 bytes, the swizzle's width).
 cudaError_t encode_bf16_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
                             const uint32_t* box) {
@@ -1355,6 +1219,9 @@ cudaError_t encode_bf16_map(CUtensorMap* map, int rank, const void* base, const 
   }
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
+
+namespace {
+constexpr size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 // Every CTA sums the tile counts of all queries before it starts: 16 a thread
 // at this many. More queries go in launches of this many, one after another.
 constexpr int kMaxQueries = 4096;

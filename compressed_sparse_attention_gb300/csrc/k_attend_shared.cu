@@ -1,0 +1,1166 @@
+// csa2_attend_shared: attention of a batch whose queries share rows.
+//
+// Places k = 0 .. n_query - 1 hold the queries group by group (order), head[k]
+// is the first place of k's group and shared[head[k]] the number of leading
+// positions whose rows the group shares: position p < shared is read through
+// the table row of the group's first query, any other through the query's own.
+// Query i at t = q_pos[i] sees every p <= t; formula as for csa2_attend_paged.
+//
+// A row serves the 64 heads of one query with 128 operations a byte, fewer
+// than the GPU has for a byte from memory (284) and, from the L2, with two
+// products of 128 x 64 x 16 that take 48 cycles each where the operations take
+// 32 (shared memory delivers 128 bytes a clock). Two queries that share it make it
+// a matrix product. So two neighbouring places of a group are one unit of work,
+// given to a pair of CTAs (a cluster of two, on two SMs that work on one
+// tcgen05 product): CTA r has query r, its 64 heads being its rows of both
+// products, M = 128 over the pair:
+//   S [64 heads x 256 rows]  = Q [64 x 512] KV^T          N = 256, K = 512
+//   O [64 heads x 512 dims] += P [64 x 256] KV            N = 256 twice, K = 256
+// Of the second operand each CTA brings half of N: of a tile's 256 rows, 128
+// whole ones for S, and all 256 in half of their dims for O. Both halves
+// stream through one ring of 16 KB slots in the order in which the products
+// use them. Tensor memory holds O (256 columns) and two S (128 each), so that
+// the next tile's scores come while this one's weights are formed.
+//
+// Tile: 256 rows of the unit's list, which are groups of 64 aligned positions:
+// those that both queries see, then those that only the first sees, then the
+// second's. Products of a group that one query does not see leave the other
+// CTA's lanes of O alone (disable-output-lane), so that a NaN in a row reaches
+// only the queries that see it.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <type_traits>
+
+#include "launchers.cuh"
+#include "tile_pipe.cuh"
+
+namespace csa2 {
+
+namespace {
+
+constexpr int kGroupRows = 64;   // aligned positions of a row group
+constexpr int kTileGroups = 4;   // row groups of a tile
+constexpr int kRing = 7;         // slots
+constexpr uint32_t kSlotBytes = 16384;
+constexpr int kMaxPairs2 = 256;  // pairs of CTAs, at most
+constexpr int kPlanThreads = 1024;
+
+// Two places of a group (or its last one alone).
+struct alignas(16) SharedUnit {
+  int32_t q[2];       // the queries; -1: none
+  int32_t seq[2];     // their sequences
+  int32_t end[2];     // one past the last position that each sees, inside the table; 0: sees nothing
+  int32_t head_seq;   // positions below len are read through its table row
+  int32_t len;
+  int32_t common;     // positions below it are seen by both (or by the only one that sees any)
+  int32_t n[3];       // row groups: common, the first query's own, the second's
+  int32_t tiles;
+  int32_t pad[3];
+};
+static_assert(sizeof(SharedUnit) == 64, "SharedUnit");
+
+struct SharedRun {
+  int64_t tile;    // number of its first tile among all
+  int32_t unit;    // its unit
+  int32_t first;   // number of that tile in its unit
+};
+
+struct SharedParams {
+  CUtensorMap q_map;   // Q: [64 n_query heads][512], boxes of 64 heads x 64 channels
+  CUtensorMap kv_map;  // bf16 pages: [n_pages][page_size][512], boxes of one piece x 64 channels
+  const uint16_t* q;
+  const int64_t* q_pos;
+  const int32_t* seq_of_q;
+  const int32_t* order;
+  const int32_t* head;
+  const int64_t* shared;
+  const float* sink;
+  uint16_t* out;
+  float* lse;
+  uint32_t* flags;
+  PagedView kv;
+  RopeParams rp;
+  float scale_log2;
+  int n_query;
+  int pairs;  // of CTAs
+  SharedUnit* units;
+  SharedRun* runs;   // [pairs + 1]
+  int4* joins;       // [pairs]: unit, first and last run of a unit that run c begins and does not end; -1: none
+  float* part_o;     // [2 pairs slots][2][512 / 4][64 heads][4]
+  float* part_m;     // [2 pairs slots][2][64]
+  float* part_l;
+};
+
+// Slots of the partials: run c leaves at most two, as in csa2_attend_paged.
+__device__ __forceinline__ int64_t shared_slot(int c, bool begins, int rank) { return 2 * (2 * (int64_t)c + (begins ? 1 : 0)) + rank; }
+
+// rows of a piece: what one copy takes of a page
+__host__ __device__ __forceinline__ int piece_shift(int page_shift) { return page_shift < 6 ? page_shift : 6; }
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// The plan, one CTA: places -> units, and the units' tiles cut into runs of
+// equal cost, one a pair of CTAs. A thread takes a share of the places and, when
+// a scan has placed its units, finds the cuts that fall into them.
+// ---------------------------------------------------------------------------
+constexpr int kTileCost2 = 4, kUnitCost = 3;  // a unit: its Q, its outputs
+
+namespace {
+struct PlanUnit {
+  SharedUnit u;
+  bool begins;
+};
+// The unit that place k begins, if it does. bad: flags to record.
+__device__ __forceinline__ PlanUnit unit_at(const SharedParams& p, int k, uint32_t& bad) {
+  PlanUnit r;
+  const int n = p.n_query;
+  auto head_of = [&](int at) {
+    const int h = p.head[at];
+    return h >= 0 && h <= at ? h : at;
+  };
+  const int h = head_of(k), hn = k + 1 < n ? head_of(k + 1) : -1;
+  r.begins = ((k - h) & 1) == 0;
+  if (!r.begins) {
+    if (head_of(k - 1) != h) bad |= CSA2_FLAG_BAD_QUERY;
+    return r;
+  }
+  const int32_t cap = p.kv.max_pages << p.kv.page_shift;  // at most 2^30
+  SharedUnit& u = r.u;
+  int64_t len = p.shared[h];
+  auto query = [&](int at) {
+    const int q = p.order[at];
+    if (q < -1 || q >= n) bad |= CSA2_FLAG_BAD_QUERY;
+    return q >= 0 && q < n ? q : -1;
+  };
+  const int qh = query(h);
+  u.q[0] = query(k);
+  u.q[1] = hn == h ? query(k + 1) : -1;
+  u.head_seq = qh >= 0 ? p.seq_of_q[qh] : -1;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    u.seq[x] = -1;
+    u.end[x] = 0;
+    if (u.q[x] < 0) continue;
+    const int b = p.seq_of_q[u.q[x]];
+    const int64_t t = p.q_pos[u.q[x]];
+    if (b == -1) {
+      u.q[x] = -1;  // a padding query
+      continue;
+    }
+    if (b < 0 || b >= p.kv.n_seq || t < -1) {
+      bad |= CSA2_FLAG_BAD_QUERY;
+      continue;
+    }
+    u.seq[x] = b;
+    if (t >= cap) bad |= CSA2_FLAG_BAD_PAGE;
+    u.end[x] = (int32_t)(t >= cap ? cap : t + 1);
+  }
+  if (u.head_seq < 0 || u.head_seq >= p.kv.n_seq) len = 0;
+  len = len < 0 ? 0 : (len > cap ? cap : len);
+  u.len = (int32_t)len & ~((1 << p.kv.page_shift) - 1);  // sequences share whole pages
+  const bool a = u.end[0] > 0, b = u.end[1] > 0;
+  u.n[1] = u.n[2] = 0;
+  if (a && b) {
+    u.common = min(u.end[0], u.end[1]);
+    if (u.seq[0] != u.seq[1]) u.common = min(u.common, u.len);
+    const int f = u.common >> 6;
+    u.n[1] = u.end[0] > u.common ? ((u.end[0] + 63) >> 6) - f : 0;
+    u.n[2] = u.end[1] > u.common ? ((u.end[1] + 63) >> 6) - f : 0;
+  } else {
+    u.common = max(u.end[0], u.end[1]);
+  }
+  u.n[0] = (u.common + 63) >> 6;
+  u.tiles = max(1, (u.n[0] + u.n[1] + u.n[2] + kTileGroups - 1) / kTileGroups);
+  u.pad[0] = u.pad[1] = u.pad[2] = 0;
+  return r;
+}
+}  // namespace
+
+__global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(const __grid_constant__ SharedParams p) {
+  __shared__ int64_t sum_t[32];
+  __shared__ int sum_u[32];
+  __shared__ int64_t total_t;
+  __shared__ int total_u;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  pdl_trigger();
+  pdl_wait();
+  const int per = (p.n_query + kPlanThreads - 1) / kPlanThreads;
+  const int lo = min(p.n_query, tid * per), hi = min(p.n_query, lo + per);
+  int64_t tiles = 0;
+  int units = 0;
+  uint32_t bad = 0, unused = 0;
+  PlanUnit one;
+  one.begins = false;
+  for (int k = lo; k < hi; ++k) {
+    one = unit_at(p, k, bad);
+    if (one.begins) {
+      tiles += one.u.tiles;
+      ++units;
+    }
+  }
+  if (bad) set_flag(p.flags, bad);
+  if (tid < p.pairs) p.joins[tid] = make_int4(-1, 0, 0, 0);
+  // exclusive scan over the threads
+  int64_t it = tiles;
+  int iu = units;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t a = __shfl_up_sync(0xffffffffu, it, o);
+    const int b = __shfl_up_sync(0xffffffffu, iu, o);
+    if (lane >= o) it += a, iu += b;
+  }
+  if (lane == 31) sum_t[warp] = it, sum_u[warp] = iu;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t a = sum_t[lane];
+    int b = sum_u[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, a, o);
+      const int y = __shfl_up_sync(0xffffffffu, b, o);
+      if (lane >= o) a += x, b += y;
+    }
+    if (lane == 31) total_t = a, total_u = b;
+    sum_t[lane] = a;
+    sum_u[lane] = b;
+  }
+  __syncthreads();
+  int64_t t0 = it - tiles + (warp > 0 ? sum_t[warp - 1] : 0);
+  int u0 = iu - units + (warp > 0 ? sum_u[warp - 1] : 0);
+  const int64_t T = total_t;
+  const int U = total_u;
+  // On a line where a tile is kTileCost2 long and a unit starts with kUnitCost,
+  // run c has the tiles that start in the c-th of R equal parts (none of them
+  // empty: a part is longer than a unit's start and a tile).
+  const int start = T > 2 * (int64_t)p.pairs ? kUnitCost : 0;
+  const int64_t cost = kTileCost2 * T + (int64_t)start * U;
+  const int R = (int)min((int64_t)p.pairs, T);
+  for (int k = lo; k < hi; ++k) {
+    if (per > 1) one = unit_at(p, k, unused);
+    if (!one.begins) continue;
+    const SharedUnit& u = one.u;
+    p.units[u0] = u;
+    const int64_t c0 = kTileCost2 * t0 + (int64_t)start * u0, c1 = c0 + start + (int64_t)kTileCost2 * u.tiles;
+    // the cuts c cost / R in [c0, c1)
+    int first = -1, last = -1;
+    for (int64_t c = (c0 * R + cost - 1) / cost; c < R && c * cost < c1 * R; ++c) {
+      const int64_t left = c * cost - R * (c0 + start), step = (int64_t)kTileCost2 * R;
+      const int j = left <= 0 ? 0 : (int)((left + step - 1) / step);  // the first tile from the cut on
+      SharedRun r;
+      r.tile = t0 + j;
+      r.unit = j < u.tiles ? u0 : u0 + 1;
+      r.first = j < u.tiles ? j : 0;
+      p.runs[c] = r;
+      if (j > 0 && j < u.tiles) {
+        if (first < 0) first = (int)c;
+        last = (int)c;
+      }
+    }
+    if (first > 0) p.joins[first - 1] = make_int4(u0, first - 1, last, 0);
+    t0 += u.tiles;
+    ++u0;
+  }
+  if (tid >= R && tid <= p.pairs) {
+    SharedRun r;
+    r.tile = T;
+    r.unit = U;
+    r.first = 0;
+    p.runs[tid] = r;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The tile kernel. Roles of a CTA's warps:
+//   0 .. 7   math: softmax, outputs
+//   8 ..     producers: a slot of the ring each in turn
+//   then 2   Q, its rope channels rotated
+//   last     issues the pair's products (in CTA 0 of the pair)
+// Waits are bounded; barriers that the issuer waits for lie in CTA 0, to which
+// CTA 1 arrives over the cluster, and the issuer's commits arrive in both.
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int kMathWarps = 8;
+constexpr int kQWarps = 2;
+template <bool TMA>
+struct SharedRoles {
+  // warps that copy or convert rows themselves are one a slot. (No more: a warp's
+  // next slot but one of the ring must come after slots that it has waited for,
+  // or its wait could take the parity of the use before the last.)
+  static constexpr int kProducers = TMA ? 4 : kRing;
+  static_assert(kProducers <= kRing);
+  static constexpr int kQ = kMathWarps + kProducers;
+  static constexpr int kIssuer = kQ + kQWarps;
+  static constexpr int kThreads = 32 * (kIssuer + 1);
+};
+
+constexpr uint32_t S_Q = 0;                           // [9 blocks][64 heads][128 B]; block 8: rope residual
+constexpr uint32_t S_P = S_Q + 9 * 8192;              // [4 row groups][64 heads][128 B]
+constexpr uint32_t S_RING = S_P + 4 * 8192;           // [kRing][16 KB]
+constexpr uint32_t S_BAR = S_RING + kRing * kSlotBytes;
+constexpr uint32_t S_RED = S_BAR + 256;               // float [4 row groups][64 heads]
+constexpr uint32_t S_ROPE = S_RED + 1024;             // float2 [2 halves of the heads][32]
+constexpr uint32_t S_QROPE = S_ROPE + 512;            // float2 [32]
+constexpr uint32_t S_MISC = S_QROPE + 256;
+constexpr uint32_t kSharedSmemBytes = S_MISC + 64 + 1024;
+static_assert(kSharedSmemBytes <= 232448, "shared memory");
+
+enum SBar : uint32_t { bFull = 0, bEmpty = 7, bQFull = 14, bQEmpty = 15, bScores = 16, bWeights = 18, bPFree = 19, bOFree = 20, bDrained = 21, kSBars = 22 };
+
+constexpr uint32_t kIdescS = idesc_bf16(128, 256, 0, 0);
+constexpr uint32_t kIdescO = idesc_bf16(128, 256, 0, 1);
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the address of the same place in CTA 0 of the pair
+__device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
+  return r;
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void warp_arrive_cluster(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) arrive_cluster(bar);
+}
+__device__ __forceinline__ void expect_cluster_one(uint32_t leader, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n.reg .pred e;\nsetp.ne.u32 e, %2, 0;\n@e mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;\n}" ::"r"(bar),
+      "r"(bytes), "r"(leader)
+      : "memory");
+}
+// wait_phase for arrivals of both CTAs
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t phase, uint32_t* flags) {
+#pragma unroll 1
+  for (int i = 0; i < 100000; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n.reg .pred p;\n"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+        "selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(phase), "r"(20000u)
+        : "memory");
+    if (ok != 0u) return true;
+  }
+  set_flag(flags, CSA2_FLAG_WAIT_TIMEOUT);
+  return false;
+}
+__device__ __forceinline__ bool wait_cluster_all_lanes(uint32_t bar, uint32_t phase, uint32_t* flags) {
+  return __all_sync(0xffffffffu, wait_cluster(bar, phase, flags)) != 0;
+}
+// copies into this CTA whose bytes are counted by a barrier of CTA 0
+__device__ __forceinline__ void tma_pair_2d(uint32_t leader, uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred e;\nsetp.ne.u32 e, %5, 0;\n"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3}], [%4];\n}" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void tma_pair_3d(uint32_t leader, uint32_t dst, const CUtensorMap* map, int x, int y, int z,
+                                            uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred e;\nsetp.ne.u32 e, %6, 0;\n"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];\n}" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(leader)
+      : "memory");
+}
+__device__ __forceinline__ void mma_pair(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n.reg .pred p, e;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 e, %5, 0;\n"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader)
+      : "memory");
+}
+// off0, off1: all ones leave CTA 0's, CTA 1's lanes of D as they are
+__device__ __forceinline__ void mma_pair_lanes(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc,
+                                               uint32_t off0, uint32_t off1) {
+  asm volatile(
+      "{\n.reg .pred p, e;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 e, %5, 0;\n"
+      "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, {%6, %6, %6, %6, %7, %7, %7, %7}, p;\n}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc), "r"(leader), "r"(off0), "r"(off1)
+      : "memory");
+}
+__device__ __forceinline__ void commit_pair(uint32_t leader, uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred e;\n.reg .b16 m;\nmov.b16 m, 3;\nsetp.ne.u32 e, %1, 0;\n"
+      "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}" ::"r"(bar), "r"(leader)
+      : "memory");
+}
+
+// Where a row group of a unit's list lies: 64 positions from 64 * block on, of
+// which [from, to) are its own; who: 0 both queries see them, 1 the first
+// alone, 2 the second alone; seq: the sequence of positions at or past len.
+struct RowGroup {
+  bool present;
+  int who, block, from, to, seq;
+};
+__device__ __forceinline__ RowGroup row_group(const SharedUnit& u, int j) {
+  RowGroup g;
+  g.present = j < u.n[0] + u.n[1] + u.n[2];
+  const int f = u.common >> 6;
+  if (j < u.n[0]) {
+    g.who = 0;
+    g.block = j;
+    g.from = 0;
+    g.to = u.common;
+    g.seq = u.end[0] > 0 ? u.seq[0] : u.seq[1];
+  } else if (j < u.n[0] + u.n[1]) {
+    g.who = 1;
+    g.block = f + j - u.n[0];
+    g.from = u.common;
+    g.to = u.end[0];
+    g.seq = u.seq[0];
+  } else {
+    g.who = 2;
+    g.block = f + j - u.n[0] - u.n[1];
+    g.from = u.common;
+    g.to = u.end[1];
+    g.seq = u.seq[1];
+  }
+  return g;
+}
+__device__ __forceinline__ int row_groups(const SharedUnit& u, int tile) {
+  return min(kTileGroups, u.n[0] + u.n[1] + u.n[2] - kTileGroups * tile);
+}
+// page of position p of a group (-1: none)
+__device__ __forceinline__ int32_t group_page(const SharedParams& p, const SharedUnit& u, const RowGroup& g, int pos) {
+  return g.present && pos >= g.from && pos < g.to ? page_of(p.kv, pos < u.len ? u.head_seq : g.seq, pos) : -1;
+}
+
+__device__ __forceinline__ SharedUnit load_unit(const SharedUnit* at) {
+  SharedUnit u;
+  const int4* s = reinterpret_cast<const int4*>(at);
+  int4* d = reinterpret_cast<int4*>(&u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) d[i] = s[i];
+  return u;
+}
+
+// A pair's run: its units, and of each the tiles [first, last).
+struct SharedWalk {
+  int64_t left;  // tiles of the run that are left, this unit's included
+  int unit, first, last;
+  bool begins, ends;
+  SharedUnit u;
+  __device__ __forceinline__ void start(const SharedParams& p, const SharedRun& r, int64_t tiles) {
+    left = tiles;
+    unit = uniform(r.unit);
+    first = uniform(r.first);
+    if (left > 0) load(p);
+  }
+  __device__ __forceinline__ void load(const SharedParams& p) {
+    u = load_unit(p.units + unit);
+    begins = uniform(first == 0);
+    last = uniform((int)min((int64_t)u.tiles, first + left));
+    ends = uniform(last == u.tiles);
+  }
+  __device__ __forceinline__ bool next(const SharedParams& p) {
+    left -= last - first;
+    ++unit;
+    first = 0;
+    if (left > 0) load(p);
+    return left > 0;
+  }
+};
+
+// place in the ring
+struct RingAt {
+  uint32_t slot, phase;
+  __device__ __forceinline__ void step(uint32_t n) {
+    slot += n;
+    if (slot >= (uint32_t)kRing) {
+      slot -= kRing;
+      phase ^= 1u;
+    }
+  }
+};
+
+// A slot's rows by the warp itself. K: channels 64 b .. of the 128 rows of the
+// tile's groups 2 rank and 2 rank + 1; V: dims d0 .. d0 + 127 of group g's 64
+// rows. Rows that are not the group's become zeros (in V: their weights are 0,
+// but 0 times a NaN is not).
+template <int KVF, bool IS_K>
+__device__ __forceinline__ void fill_slot(const SharedParams& p, const SharedUnit& u, int tile, int g0, int d0, uint32_t dst_s,
+                                          uint8_t* dst, int lane) {
+  constexpr int kRows = IS_K ? 128 : 64;
+  const int page_mask = (1 << p.kv.page_shift) - 1;
+  if constexpr (KVF == 0) {
+    constexpr int kChunks = IS_K ? 8 : 16;  // of 16 bytes, of a row
+    const int c = lane % kChunks;
+#pragma unroll 8
+    for (int r = lane / kChunks; r < kRows; r += 32 / kChunks) {
+      const RowGroup g = row_group(u, kTileGroups * tile + g0 + (r >> 6));
+      const int pos = 64 * g.block + (r & 63);
+      const int32_t page = group_page(p, u, g, pos);
+      const uint8_t* src = page >= 0 ? p.kv.pages + page * p.kv.page_stride + (int64_t)(pos & page_mask) * 1024 + 2 * d0 + 16 * c
+                                     : p.kv.pages;
+      cp_async16(dst_s + (uint32_t)(c >> 3) * 8192u + (uint32_t)r * 128u + ((uint32_t)((c & 7) ^ (r & 7)) << 4), src, page >= 0 ? 16u : 0u);
+    }
+    cp_async_wait_all();
+  } else {
+    constexpr int kRowBytes = KVF == 1 ? 512 : 256, kScaleBytes = KVF == 1 ? 16 : 32;
+    constexpr int kChunks = IS_K ? 4 : 8;  // of 16 channels, of a row
+    constexpr int kBatch = 4;              // rows of a thread under way at once
+    using Code = typename std::conditional<KVF == 1, uint4, uint2>::type;
+    const int c = lane % kChunks, ch = d0 + 16 * c;
+#pragma unroll 1
+    for (int r0 = lane / kChunks; r0 < kRows; r0 += kBatch * (32 / kChunks)) {
+      Code code[kBatch];
+      uint8_t scale[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + i * (32 / kChunks);
+        const RowGroup g = row_group(u, kTileGroups * tile + g0 + (r >> 6));
+        const int pos = 64 * g.block + (r & 63);
+        const int32_t page = group_page(p, u, g, pos);
+        if constexpr (KVF == 1) code[i] = make_uint4(0u, 0u, 0u, 0u);
+        else code[i] = make_uint2(0u, 0u);
+        scale[i] = 0;
+        if (page >= 0) {
+          const uint8_t* src = p.kv.pages + page * p.kv.page_stride + (int64_t)(pos & page_mask) * kRowBytes;
+          const uint8_t* sc = p.kv.scales + page * p.kv.scale_stride + (int64_t)(pos & page_mask) * kScaleBytes;
+          if constexpr (KVF == 1) code[i] = ldg_stream16(src + ch);
+          else code[i] = ldg_stream8(src + ch / 2);
+          scale[i] = __ldg(sc + (KVF == 1 ? ch / 32 : ch / 16));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = r0 + i * (32 / kChunks);
+        uint32_t o[8];
+        if constexpr (KVF == 1) fp8_to_bf16(code[i], scale[i], o);
+        else fp4_to_bf16(code[i].x, code[i].y, scale[i], o);
+        uint8_t* at = dst + (uint32_t)(c >> 2) * 8192u + (uint32_t)r * 128u;
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          *reinterpret_cast<uint4*>(at + (((2 * (c & 3) + k) ^ (r & 7)) << 4)) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      }
+    }
+  }
+  fence_proxy_async_smem();
+}
+
+// Producer warp w of a CTA: every kProducers-th slot of the ring.
+template <int KVF, bool TMA>
+__device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm, uint32_t base_s, SharedWalk walk, int w, int rank) {
+  constexpr int NP = SharedRoles<TMA>::kProducers;
+  const int lane = threadIdx.x & 31;
+  const uint32_t bars = base_s + S_BAR, full0 = in_leader(bars + 8 * bFull);
+  const uint32_t leader = elect_one();
+  const int ps = p.kv.page_shift, pc = piece_shift(ps);
+  RingAt at{0, 0};
+  uint32_t s = 0;  // slots so far, of all warps
+  bool live = true;
+  // a slot for this warp to fill
+  auto take = [&]() {
+    if (s >= (uint32_t)kRing) live = live && wait_all_lanes(bars + 8 * (bEmpty + at.slot), at.phase ^ 1u, p.flags);
+    return live;
+  };
+  // lane 8 g + i: the page of piece i of the tile's group g (TMA)
+  auto look_up = [&](const SharedUnit& u, int tile) {
+    const RowGroup g = row_group(u, kTileGroups * tile + (lane >> 3));
+    const int pos = 64 * g.block + ((lane & 7) << pc);
+    int32_t page = -1;
+    if ((lane & 7) << pc < kGroupRows && g.present && pos < g.to && pos + (1 << pc) > g.from)
+      page = page_of(p.kv, max(pos, g.from) < u.len ? u.head_seq : g.seq, pos);
+    return page >= 0 ? page : p.kv.n_pages;  // past the end: zeros
+  };
+  auto keys = [&](const SharedUnit& u, int tile, int32_t pages) {
+    const int mine = min(2, max(0, row_groups(u, tile) - 2 * rank));  // row groups of this CTA's half
+#pragma unroll 1
+    for (int b = 0; b < 8; ++b, ++s, at.step(1)) {
+      if ((int)(s % NP) != w || !take()) continue;
+      const uint32_t bar = full0 + 8 * at.slot, dst = base_s + S_RING + at.slot * kSlotBytes;
+      if (TMA) {
+        expect_cluster_one(leader, bar, 8192u * (uint32_t)mine);
+#pragma unroll 1
+        for (int g = 0; g < mine; ++g) {
+          const int row0 = (64 * row_group(u, kTileGroups * tile + 2 * rank + g).block) & ((1 << ps) - 1);
+#pragma unroll 1
+          for (int i = 0; (i << pc) < kGroupRows; ++i)
+            tma_pair_3d(leader, dst + 8192u * (uint32_t)g + ((uint32_t)i << (7 + pc)), &p.kv_map, 64 * b,
+                        uniform(row0), uniform(pages, 8 * (2 * rank + g) + i), bar);
+        }
+      } else {
+        if (mine > 0) fill_slot<KVF, true>(p, u, tile, 2 * rank, 64 * b, dst, sm + (dst - base_s), lane);
+        warp_arrive_cluster(bar);
+      }
+    }
+  };
+  auto values = [&](const SharedUnit& u, int tile, int32_t pages) {
+    const int n = row_groups(u, tile);
+#pragma unroll 1
+    for (int i = 0; i < 2 * n; ++i, ++s, at.step(1)) {
+      if ((int)(s % NP) != w || !take()) continue;
+      const int g = i >> 1, d0 = 256 * (i & 1) + 128 * rank;
+      const RowGroup rg = row_group(u, kTileGroups * tile + g);
+      const uint32_t bar = full0 + 8 * at.slot, dst = base_s + S_RING + at.slot * kSlotBytes;
+      // (a group's end inside a page: rows behind it hold anything)
+      if (TMA && uniform(rg.from <= 64 * rg.block && rg.to >= 64 * rg.block + 64)) {
+        expect_cluster_one(leader, bar, kSlotBytes);
+        const int row0 = uniform((64 * rg.block) & ((1 << ps) - 1));
+#pragma unroll 1
+        for (int k = 0; (k << pc) < kGroupRows; ++k) {
+          const int page = uniform(pages, 8 * g + k);
+          tma_pair_3d(leader, dst + ((uint32_t)k << (7 + pc)), &p.kv_map, d0, row0, page, bar);
+          tma_pair_3d(leader, dst + 8192u + ((uint32_t)k << (7 + pc)), &p.kv_map, d0 + 64, row0, page, bar);
+        }
+      } else {
+        fill_slot<KVF, false>(p, u, tile, g, d0, dst, sm + (dst - base_s), lane);
+        warp_arrive_cluster(bar);
+      }
+    }
+  };
+  if (walk.left <= 0) return;
+  do {
+    const SharedUnit& u = walk.u;
+    int32_t now = TMA ? look_up(u, walk.first) : 0;
+    keys(u, walk.first, now);
+#pragma unroll 1
+    for (int t = walk.first; t < walk.last; ++t) {
+      int32_t ahead = now;
+      if (t + 1 < walk.last) {
+        if (TMA) ahead = look_up(u, t + 1);
+        keys(u, t + 1, ahead);
+      }
+      values(u, t, now);
+      now = ahead;
+    }
+  } while (walk.next(p));
+}
+
+// Q of this CTA's query: plain blocks by TMA, the rope block rotated and split
+// into bf16 hi + lo by the 64 threads (see csa2_attend_paged).
+__device__ __forceinline__ void q_role(const SharedParams& p, uint8_t* sm, uint32_t base_s, SharedWalk walk, int t, int rank) {
+  const uint32_t bars = base_s + S_BAR, bar = in_leader(bars + 8 * bQFull);
+  const uint32_t leader = elect_one();
+  const bool rope = p.rp.pairs > 0;
+  const double freq = t < p.rp.pairs ? p.rp.freq[t & 31] : 0.0;
+  bool live = true;
+  if (walk.left <= 0) return;
+  uint32_t seg = 0;
+  do {
+    const int qi = uniform(walk.u.q[rank]);
+    // (a wait that ran out is recorded; the barriers below are met all the same)
+    if (seg > 0) live = live && wait_all_lanes(bars + 8 * bQEmpty, (seg & 1u) ^ 1u, p.flags);
+    if (t < 32 && live) {
+      const int plain = qi < 0 ? 0 : (rope ? 7 : 8);
+      expect_cluster_one(leader, bar, 8192u * (uint32_t)plain);
+#pragma unroll 1
+      for (int b = 0; b < plain; ++b) tma_pair_2d(leader, base_s + S_Q + 8192u * (uint32_t)b, &p.q_map, 64 * b, kHeads * qi, bar);
+    }
+    if (rope && qi >= 0) {
+      // thread: chunk 56 + (t & 7) of heads t >> 3, + 8, ...: always the same four pairs
+      uint4 v[8];
+      const uint16_t* q = p.q + (int64_t)qi * kHeads * kDim + 8 * (56 + (t & 7));
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4*>(q + (int64_t)((t >> 3) + 8 * i) * kDim);
+      float2* table = reinterpret_cast<float2*>(sm + S_QROPE);
+      asm volatile("bar.sync 3, 64;" ::: "memory");  // the last query's table has been read
+      if (t < 32) {
+        float cs, sn;
+        angle_cs((double)max(p.q_pos[qi], (int64_t)0) * freq, cs, sn);
+        table[t] = make_float2(cs, sn);
+      }
+      asm volatile("bar.sync 3, 64;" ::: "memory");
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int h = (t >> 3) + 8 * i;
+        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, lo[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 cs = table[4 * (t & 7) + k];
+          const float x0 = bf16lo(w[k]), x1 = bf16hi(w[k]);
+          const float y0 = x0 * cs.x - x1 * cs.y, y1 = x0 * cs.y + x1 * cs.x;
+          w[k] = pack_bf16(y0, y1);
+          lo[k] = pack_bf16(y0 - bf16lo(w[k]), y1 - bf16hi(w[k]));
+        }
+        const uint32_t off = (uint32_t)h * 128u + ((uint32_t)((t & 7) ^ (h & 7)) << 4);
+        *reinterpret_cast<uint4*>(sm + S_Q + 7u * 8192u + off) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(sm + S_Q + 8u * 8192u + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      }
+      fence_proxy_async_smem();
+    }
+    if (live) warp_arrive_cluster(bar);
+    ++seg;
+  } while (walk.next(p));
+}
+
+// The pair's products, by a warp of CTA 0.
+__device__ __forceinline__ void issue_shared(const SharedParams& p, uint32_t base_s, uint32_t tmem_s, uint32_t tmem_o, SharedWalk walk) {
+  const uint32_t bars = base_s + S_BAR, leader = elect_one();
+  uint32_t* flags = p.flags;
+  const bool rope = p.rp.pairs > 0;
+  const uint64_t qd = sdesc_sw128(base_s + S_Q, 16u, 1024u), pd = sdesc_sw128(base_s + S_P, 16u, 1024u);
+  const uint64_t kd = sdesc_sw128(base_s + S_RING, 16u, 1024u), vd = sdesc_sw128(base_s + S_RING, 8192u, 1024u);
+  RingAt at{0, 0};
+  uint32_t n = 0, done = 0, seg = 0;  // tiles scored, tiles whose outputs were issued, units
+  bool live = true;
+  auto scores = [&](bool last) {
+    const uint32_t d = tmem_s + 128u * (n & 1u);
+#pragma unroll 1
+    for (uint32_t b = 0; b < 8; ++b, at.step(1)) {
+      live = live && wait_cluster_all_lanes(bars + 8 * (bFull + at.slot), at.phase, flags);
+      if (!live) return;
+      tc_fence_after();
+      const uint64_t k0 = sdesc_add(kd, at.slot * kSlotBytes);
+#pragma unroll
+      for (uint32_t k = 0; k < 4; ++k) mma_pair(leader, d, sdesc_add(qd, b * 8192u + 32u * k), sdesc_add(k0, 32u * k), kIdescS, b | k);
+      if (rope && b == 7) {
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) mma_pair(leader, d, sdesc_add(qd, 8u * 8192u + 32u * k), sdesc_add(k0, 32u * k), kIdescS, 1u);
+      }
+      commit_pair(leader, bars + 8 * (bEmpty + at.slot));
+    }
+    commit_pair(leader, bars + 8 * (bScores + (n & 1u)));
+    if (last) commit_pair(leader, bars + 8 * bQEmpty);
+    ++n;
+  };
+  if (walk.left > 0) {
+    do {
+      live = live && wait_cluster_all_lanes(bars + 8 * bQFull, seg & 1u, flags);
+      tc_fence_after();
+      if (live) scores(walk.first + 1 == walk.last);
+      uint32_t begun = 0;  // whose lanes of O hold a sum (bits)
+#pragma unroll 1
+      for (int t = walk.first; t < walk.last && live; ++t) {
+        if (t + 1 < walk.last) scores(t + 2 == walk.last);
+        live = live && wait_cluster_all_lanes(bars + 8 * bWeights, done & 1u, flags);
+        if (t == walk.first && seg > 0) live = live && wait_cluster_all_lanes(bars + 8 * bOFree, (seg & 1u) ^ 1u, flags);
+        tc_fence_after();
+        const int ng = uniform(row_groups(walk.u, t));
+#pragma unroll 1
+        for (int g = 0; g < ng && live; ++g) {
+          const int who = uniform(row_group(walk.u, kTileGroups * t + g).who);
+          const uint32_t lanes = who == 0 ? 3u : (uint32_t)who;
+          const bool fresh = (begun & lanes) == 0u;
+          begun |= lanes;
+#pragma unroll 1
+          for (uint32_t j = 0; j < 2; ++j, at.step(1)) {
+            live = live && wait_cluster_all_lanes(bars + 8 * (bFull + at.slot), at.phase, flags);
+            if (!live) break;
+            tc_fence_after();
+            const uint64_t v0 = sdesc_add(vd, at.slot * kSlotBytes), p0 = sdesc_add(pd, 8192u * (uint32_t)g);
+            if (who == 0) {
+#pragma unroll
+              for (uint32_t k = 0; k < 4; ++k)
+                mma_pair(leader, tmem_o + 128u * j, sdesc_add(p0, 32u * k), sdesc_add(v0, 2048u * k), kIdescO, k > 0 || !fresh ? 1u : 0u);
+            } else {
+#pragma unroll
+              for (uint32_t k = 0; k < 4; ++k)
+                mma_pair_lanes(leader, tmem_o + 128u * j, sdesc_add(p0, 32u * k), sdesc_add(v0, 2048u * k), kIdescO,
+                               k > 0 || !fresh ? 1u : 0u, who == 1 ? 0u : ~0u, who == 1 ? ~0u : 0u);
+            }
+            commit_pair(leader, bars + 8 * (bEmpty + at.slot));
+          }
+        }
+        if (live) commit_pair(leader, bars + 8 * bPFree);
+        ++done;
+      }
+      ++seg;
+    } while (walk.next(p) && live);
+  }
+  if (!live) {  // products still in flight land before tensor memory is freed
+    commit_pair(leader, bars + 8 * bDrained);
+    wait_phase(bars + 8 * bDrained, 0u, flags);
+  }
+}
+
+// Softmax of a tile and, at a unit's end, its output or partial. Warp w: TMEM
+// lanes 32 (w & 3) .., which hold heads 32 (w & 1) .. + 31, of S its columns
+// 128 ((w >> 1) & 1) .. (the upper lanes hold the second half of N), of which
+// the warp takes 64 (w >> 2) ..: a thread has one head and the 64 rows of row
+// group 2 ((w >> 1) & 1) + (w >> 2). Four threads share a head, the four warps of
+// its half of the heads a barrier.
+__device__ __forceinline__ void math_shared(const SharedParams& p, uint8_t* sm, uint32_t base_s, uint32_t tmem_s, uint32_t tmem_o,
+                                            SharedWalk walk, int c, int warp, int rank) {
+  const uint32_t bars = base_s + S_BAR;
+  const uint32_t weights = in_leader(bars + 8 * bWeights), o_free = in_leader(bars + 8 * bOFree);
+  const int lane = threadIdx.x & 31, hb = warp & 1, upper = (warp >> 1) & 1, cols = warp >> 2;
+  const int head = 32 * hb + lane, group = 2 * upper + cols;
+  const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
+  float* red = reinterpret_cast<float*>(sm + S_RED);
+  float2* rope_tab = reinterpret_cast<float2*>(sm + S_ROPE) + 32 * hb;
+  const float scale = p.scale_log2;
+  auto sync_half = [&] { asm volatile("bar.sync %0, 128;" ::"r"(1 + hb) : "memory"); };
+  auto any_half = [&](bool v) {
+    uint32_t r;
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 p, %1, 0;\nbar.red.or.pred q, %2, 128, p;\nselp.u32 %0, 1, 0, q;\n}"
+                 : "=r"(r)
+                 : "r"((uint32_t)v), "r"(1 + hb)
+                 : "memory");
+    return r != 0;
+  };
+  if (walk.left <= 0) return;
+  bool live = true;  // a wait that ran out is recorded; the loop then only runs out
+  uint32_t n = 0;
+  do {
+    const SharedUnit& u = walk.u;
+    const int qi = u.q[rank];
+    const int64_t t_q = qi >= 0 ? p.q_pos[qi] : 0;
+    if (upper + cols == 0 && lane < p.rp.pairs) {
+      float cs, sn;
+      rope_cs(p.rp, lane, max(t_q, (int64_t)0), cs, sn);
+      rope_tab[lane] = make_float2(cs, sn);  // read behind the barriers of the unit's end
+    }
+    float m_run = -INFINITY, m_use = kNoRef, lsum = 0.f;
+    bool seen_any = false;
+#pragma unroll 1
+    for (int t = walk.first; t < walk.last; ++t, ++n) {
+      // the rows that this query sees of the warp's group
+      uint32_t mask[2];
+      {
+        const RowGroup g = row_group(u, kTileGroups * t + group);
+        const bool mine = g.present && (g.who == 0 || g.who == rank + 1) && u.end[rank] > 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int pos = 64 * g.block + 32 * i + lane;
+          const bool seen = mine && pos >= g.from && pos < g.to;
+          const bool there = seen && group_page(p, u, g, pos) >= 0;
+          if (seen && !there) set_flag(p.flags, CSA2_FLAG_BAD_PAGE);
+          mask[i] = __ballot_sync(0xffffffffu, there);
+        }
+      }
+      seen_any = seen_any || (mask[0] | mask[1]) != 0u;
+      live = live && warp_wait(bars + 8 * (bScores + (n & 1u)), (n >> 1) & 1u, p.flags);
+      tc_fence_after();
+      const uint32_t s_at = tmem_s + 128u * (n & 1u) + lane_base + 64u * cols;
+      const bool first = t == walk.first;
+      bool move = first;
+      uint32_t packed[32];
+      float add = 0.f;
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        if (move) {
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            uint32_t r[32];
+            tmem_ld32(s_at + 32u * i, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) top = fmaxf(top, (mask[i] >> k) & 1u ? __uint_as_float(r[k]) * scale : -INFINITY);
+          }
+          red[64 * group + head] = top;
+          sync_half();
+          top = fmaxf(fmaxf(red[head], red[64 + head]), fmaxf(red[128 + head], red[192 + head]));
+          const float mn = (m_run == -INFINITY || top > m_run + kRefSlack) ? fmaxf(m_run, top) : m_run;
+          const float al = m_run == -INFINITY ? 1.f : exp2f(m_run - mn);
+          m_run = mn;
+          m_use = mn == -INFINITY ? kNoRef : mn;
+          if (any_half(al != 1.f)) {
+            lsum *= al;
+            // the products of the tile before are complete
+            if (!first) live = live && warp_wait(bars + 8 * bPFree, (n & 1u) ^ 1u, p.flags);
+            tc_fence_after();
+#pragma unroll 1
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t a = tmem_o + lane_base + 128u * cols + 32u * i;
+              uint32_t r[32];
+              tmem_ld32(a, r);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * al);
+              tmem_st32(a, r);
+            }
+            tmem_wait_st();
+          }
+        }
+        float over = -INFINITY;
+        add = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          uint32_t r[32];
+          tmem_ld32(s_at + 32u * i, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            float x0 = fmaf(__uint_as_float(r[k]), scale, -m_use), x1 = fmaf(__uint_as_float(r[k + 1]), scale, -m_use);
+            if (!((mask[i] >> k) & 1u)) x0 = -INFINITY;
+            if (!((mask[i] >> (k + 1)) & 1u)) x1 = -INFINITY;
+            over = fmaxf(over, fmaxf(x0, x1));
+            x0 = exp2_approx(x0);
+            x1 = exp2_approx(x1);
+            add += x0 + x1;
+            packed[16 * i + k / 2] = pack_bf16(x0, x1);
+          }
+        }
+        move = any_half(over > kRefSlack);
+        if (!move) break;
+      }
+      lsum += add;
+      // the products of the tile before have read its weights
+      if (n > 0) live = live && warp_wait(bars + 8 * bPFree, (n & 1u) ^ 1u, p.flags);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        *reinterpret_cast<uint4*>(sm + S_P + 8192u * (uint32_t)group + 128u * (uint32_t)head + (uint32_t)((k ^ (head & 7)) << 4)) =
+            make_uint4(packed[4 * k], packed[4 * k + 1], packed[4 * k + 2], packed[4 * k + 3]);
+      fence_proxy_async_smem();
+      tc_fence_before();
+      warp_arrive_cluster(weights);
+    }
+    // ---- the unit's end: the four threads' sums of a head, then O
+    red[64 * group + head] = lsum;
+    sync_half();
+    const float l = red[head] + red[64 + head] + red[128 + head] + red[192 + head];
+    const bool none = m_run == -INFINITY && l == l;  // no row seen (scores that are all NaN set no reference either)
+    live = live && warp_wait(bars + 8 * bPFree, (n & 1u) ^ 1u, p.flags);
+    tc_fence_after();
+    const bool whole = walk.begins && walk.ends;
+    // dims of the warp's columns: N runs over CTA 0's 128 dims of a half, then CTA 1's
+    const int dim0 = 256 * cols + 128 * upper;
+    if (whole) {
+      const float sk = p.sink != nullptr ? p.sink[head] : -INFINITY, sk2 = sk * 1.4426950408889634f;
+      const float M = fmaxf(m_run, sk2);
+      float fo = 0.f, lse = sk;
+      if (!none) {
+        const float em = exp2f(m_run - M);
+        const float den = l * em + exp2f(sk2 - M);
+        fo = em / den;
+        lse = (M + log2f(den)) * 0.6931471805599453f;
+      }
+      if (qi >= 0 && group == 0 && p.lse != nullptr) p.lse[(int64_t)qi * kHeads + head] = lse;
+      const int first_rope = kDim - 2 * p.rp.pairs;
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        uint32_t r[32];
+        tmem_ld32(tmem_o + lane_base + 128u * cols + 32u * i, r);
+        tmem_wait_ld();
+        const int d = dim0 + 32 * i;
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) {
+          float x0 = none ? 0.f : __uint_as_float(r[k]) * fo, x1 = none ? 0.f : __uint_as_float(r[k + 1]) * fo;
+          if (d >= first_rope) {  // rotated back by -t
+            const float2 cs = rope_tab[(d + k - first_rope) >> 1];
+            const float y = x0 * cs.x + x1 * cs.y;
+            x1 = x1 * cs.x - x0 * cs.y;
+            x0 = y;
+          }
+          r[k / 2] = pack_bf16(x0, x1);
+        }
+        if (qi >= 0) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + ((int64_t)qi * kHeads + head) * kDim + d);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) dst[k] = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+        }
+      }
+    } else {
+      const int64_t slot = shared_slot(c, walk.begins, rank);
+      if (group == 0) {
+        p.part_m[slot * kHeads + head] = none ? -INFINITY : m_run;
+        p.part_l[slot * kHeads + head] = l;
+      }
+      float4* po = reinterpret_cast<float4*>(p.part_o) + slot * (kDim / 4) * kHeads;
+#pragma unroll 1
+      for (int i = 0; i < 4; ++i) {
+        uint32_t r[32];
+        tmem_ld32(tmem_o + lane_base + 128u * cols + 32u * i, r);
+        tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float4 v = make_float4(__uint_as_float(r[4 * k]), __uint_as_float(r[4 * k + 1]), __uint_as_float(r[4 * k + 2]),
+                                 __uint_as_float(r[4 * k + 3]));
+          if (none) v = make_float4(0.f, 0.f, 0.f, 0.f);  // nothing was summed into these lanes
+          po[(dim0 / 4 + 8 * i + k) * kHeads + head] = v;
+        }
+      }
+    }
+    tc_fence_before();  // O has been read
+    warp_arrive_cluster(o_free);
+    sync_half();  // red and the rope table are free for the next unit
+  } while (walk.next(p));
+}
+
+template <int KVF, bool TMA>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SharedRoles<TMA>::kThreads, 1)
+    attend_shared_kernel(const __grid_constant__ SharedParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  using Roles = SharedRoles<TMA>;
+  const uint32_t raw_s = smem_u32(smem_raw);
+  const uint32_t base_s = (raw_s + 1023u) & ~1023u;
+  uint8_t* sm = smem_raw + (base_s - raw_s);
+  const uint32_t bars = base_s + S_BAR;
+  const int tid = threadIdx.x;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int rank = (int)cluster_rank(), c = (int)blockIdx.x >> 1;
+  pdl_trigger();
+  if (warp == 0) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(base_s + S_MISC) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  if (tid == 32 * kMathWarps) {
+    for (uint32_t b = 0; b < kSBars; ++b) {
+      uint32_t count = 1;
+      if (b < bEmpty) count = 2;                                      // each CTA once
+      else if (b == bQFull) count = 2 * (1 + kQWarps);                // the copies, and the warps
+      else if (b == bWeights || b == bOFree) count = 2 * kMathWarps;
+      mbar_init(bars + 8 * b, count);
+    }
+    fence_mbar_init();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = (uint32_t)uniform((int)*reinterpret_cast<uint32_t*>(sm + S_MISC));
+  const uint32_t tmem_o = tmem, tmem_s = tmem + 256;
+  pdl_wait();
+  const SharedRun run = p.runs[c];
+  SharedWalk walk;
+  walk.start(p, run, p.runs[c + 1].tile - run.tile);
+  if (warp < kMathWarps) {
+    math_shared(p, sm, base_s, tmem_s, tmem_o, walk, c, warp, rank);
+  } else if (warp < Roles::kQ) {
+    produce_role<KVF, TMA>(p, sm, base_s, walk, warp - kMathWarps, rank);
+  } else if (warp < Roles::kIssuer) {
+    q_role(p, sm, base_s, walk, tid - 32 * Roles::kQ, rank);
+  } else if (rank == 0) {
+    issue_shared(p, base_s, tmem_s, tmem_o, walk);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // neither CTA's memory goes while the other may use it
+  if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// Join of a split unit's partials, the formula of csa2_attend_paged's join. A
+// thread has one head and 16 dims (a sector of the output): the parts' values
+// are next to each other over the heads.
+constexpr int kJoinDims = 16;
+__global__ void __launch_bounds__(256) attend_shared_join_kernel(const __grid_constant__ SharedParams p) {
+  const int head = threadIdx.x & 63, d0 = kJoinDims * ((int)blockIdx.y * 4 + (threadIdx.x >> 6)), rank = (int)blockIdx.z;
+  pdl_wait();
+  const int4 jn = p.joins[blockIdx.x];
+  if (jn.x < 0) return;
+  const int qi = p.units[jn.x].q[rank];
+  if (qi < 0) return;
+  const int n = jn.z - jn.y + 1;
+  auto slot = [&](int k) { return shared_slot(jn.y + k, k == 0, rank); };
+  const float sk = p.sink != nullptr ? p.sink[head] : -INFINITY, sk2 = sk * 1.4426950408889634f;
+  float M = -INFINITY;
+  for (int k = 0; k < n; ++k) M = fmaxf(M, p.part_m[slot(k) * kHeads + head]);
+  const bool none = M == -INFINITY;
+  M = fmaxf(M, sk2);
+  float den = none ? 1.f : exp2f(sk2 - M);
+  float o[kJoinDims];
+#pragma unroll
+  for (int i = 0; i < kJoinDims; ++i) o[i] = 0.f;
+  for (int k = 0; k < n; ++k) {
+    const float m = p.part_m[slot(k) * kHeads + head];
+    const float e = m == -INFINITY ? 0.f : exp2f(m - M);
+    den += e * p.part_l[slot(k) * kHeads + head];
+    const float4* v = reinterpret_cast<const float4*>(p.part_o) + (slot(k) * (kDim / 4) + d0 / 4) * kHeads + head;
+#pragma unroll
+    for (int i = 0; i < kJoinDims / 4; ++i) {
+      const float4 x = v[i * kHeads];
+      o[4 * i] = fmaf(e, x.x, o[4 * i]);
+      o[4 * i + 1] = fmaf(e, x.y, o[4 * i + 1]);
+      o[4 * i + 2] = fmaf(e, x.z, o[4 * i + 2]);
+      o[4 * i + 3] = fmaf(e, x.w, o[4 * i + 3]);
+    }
+  }
+  const float inv = none && den == 1.f ? 0.f : 1.f / den;
+  if (d0 == 0 && p.lse != nullptr) p.lse[(int64_t)qi * kHeads + head] = none && den == 1.f ? sk : (M + log2f(den)) * 0.6931471805599453f;
+  const int first_rope = kDim - 2 * p.rp.pairs;
+  uint32_t w[kJoinDims / 2];
+#pragma unroll
+  for (int i = 0; i < kJoinDims; i += 2) {
+    float x0 = o[i] * inv, x1 = o[i + 1] * inv;
+    if (d0 >= first_rope) {
+      float cs, sn;
+      rope_cs(p.rp, (d0 + i - first_rope) >> 1, p.q_pos[qi], cs, sn);
+      const float y = x0 * cs + x1 * sn;
+      x1 = x1 * cs - x0 * sn;
+      x0 = y;
+    }
+    w[i / 2] = pack_bf16(x0, x1);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(p.out + ((int64_t)qi * kHeads + head) * kDim + d0);
+  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+constexpr size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
+}  // namespace
+
+static int attend_shared_pairs(int num_sms) { return std::min(num_sms / 2, kMaxPairs2); }
+
+size_t attend_shared_workspace_bytes(int num_sms, int n_query) {
+  const size_t pairs = (size_t)attend_shared_pairs(num_sms), slots = 4 * pairs;
+  return al256(slots * kHeads * kDim * 4) + 2 * al256(slots * kHeads * 4) + al256((pairs + 1) * sizeof(SharedRun)) +
+         al256(pairs * sizeof(int4)) + al256((size_t)n_query * sizeof(SharedUnit));
+}
+
+cudaError_t launch_attend_shared(cudaStream_t st, int num_sms, int kv_fmt, const AttendParams& a, const PagedView& kv,
+                                 const int32_t* order, const int32_t* head, const int64_t* shared, void* ws, int* n_launch) {
+  SharedParams p{};
+  p.pairs = attend_shared_pairs(num_sms);
+  const size_t slots = 4 * (size_t)p.pairs;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  auto part = [&](size_t bytes) {
+    uint8_t* at = w;
+    w += al256(bytes);
+    return at;
+  };
+  p.part_o = reinterpret_cast<float*>(part(slots * kHeads * kDim * 4));
+  p.part_m = reinterpret_cast<float*>(part(slots * kHeads * 4));
+  p.part_l = reinterpret_cast<float*>(part(slots * kHeads * 4));
+  p.runs = reinterpret_cast<SharedRun*>(part((p.pairs + 1) * sizeof(SharedRun)));
+  p.joins = reinterpret_cast<int4*>(part(p.pairs * sizeof(int4)));
+  p.units = reinterpret_cast<SharedUnit*>(part((size_t)a.n_query * sizeof(SharedUnit)));
+  p.q = a.q;
+  p.q_pos = a.q_pos;
+  p.seq_of_q = a.seq_of_q;
+  p.order = order;
+  p.head = head;
+  p.shared = shared;
+  p.sink = a.sink;
+  p.out = a.out;
+  p.lse = a.lse;
+  p.flags = a.flags;
+  p.kv = kv;
+  p.rp = a.rp;
+  p.scale_log2 = a.scale_log2;
+  p.n_query = a.n_query;
+  const int piece = 1 << piece_shift(kv.page_shift);
+  const uint64_t q_dims[2] = {(uint64_t)kDim, (uint64_t)kHeads * a.n_query}, q_strides[1] = {2u * kDim};
+  const uint32_t q_box[2] = {64u, (uint32_t)kHeads};
+  const uint64_t kv_dims[3] = {(uint64_t)kDim, 1ull << kv.page_shift, (uint64_t)kv.n_pages};
+  const uint64_t kv_strides[2] = {2u * kDim, (uint64_t)kv.page_stride};
+  const uint32_t kv_box[3] = {64u, (uint32_t)piece, 1u};
+  cudaError_t e = encode_bf16_map(&p.q_map, 2, a.q, q_dims, q_strides, q_box);
+  if (e == cudaSuccess && kv_fmt == 0) e = encode_bf16_map(&p.kv_map, 3, kv.pages, kv_dims, kv_strides, kv_box);
+  if (e != cudaSuccess) return e;
+  e = launch_ex(attend_shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, true, 0, p);
+  if (e != cudaSuccess) return e;
+#define CSA2_SHARED(F, T)                                                                                               \
+  do {                                                                                                                 \
+    e = cudaFuncSetAttribute(attend_shared_kernel<F, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSharedSmemBytes); \
+    if (e == cudaSuccess)                                                                                              \
+      e = launch_ex(attend_shared_kernel<F, T>, dim3(2 * p.pairs), dim3(SharedRoles<T>::kThreads), kSharedSmemBytes, st, true, 0, p); \
+  } while (0)
+  // (TMA: pieces of at least the 8 rows of a swizzle atom)
+  if (kv_fmt == 0 && piece >= 8) CSA2_SHARED(0, true);
+  else if (kv_fmt == 0) CSA2_SHARED(0, false);
+  else if (kv_fmt == 1) CSA2_SHARED(1, false);
+  else CSA2_SHARED(2, false);
+#undef CSA2_SHARED
+  if (e != cudaSuccess) return e;
+  e = launch_ex(attend_shared_join_kernel, dim3((unsigned)p.pairs, kDim / kJoinDims / 4, 2), dim3(256), 0, st, true, 0, p);
+  if (e != cudaSuccess) return e;
+  *n_launch += 3;
+  return cudaGetLastError();
+}
+
+}  // namespace csa2

@@ -285,15 +285,8 @@ cudaError_t launch_rope_type(cudaStream_t st, RopeArgs& a, int num_sms, bool in_
 // without them, of which 4.5 are the bytes. Four rows a warp under one lookup
 // (14.3 us) or two (13.8) leave too few warps to hide either.
 // ---------------------------------------------------------------------------
-template <typename T, int FMT>
-__global__ void __launch_bounds__(256) append_paged_kernel(const T* __restrict__ rows, int64_t n_rows, int n_seq,
-                                                           const int64_t* __restrict__ tok_off,
-                                                           const int64_t* __restrict__ first_pos, const PagedView kv,
-                                                           const RopeParams rp, uint32_t* flags) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  if (row >= n_rows) return;
-  float v[16];
+template <typename T>
+__device__ __forceinline__ void load_row(const T* __restrict__ rows, int64_t row, int lane, float (&v)[16]) {
   const T* src = rows + row * kDim + lane * 16;
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
@@ -313,15 +306,10 @@ __global__ void __launch_bounds__(256) append_paged_kernel(const T* __restrict__
       }
     }
   }
-  const int b = find_segment(tok_off, n_seq, row);
-  const int64_t t0 = tok_off[b];
-  if (row < t0 || row >= tok_off[b + 1]) return;  // past the last sequence: left as it was
-  const int64_t p = first_pos[b] + (row - t0);
-  const int32_t g = p >= 0 ? page_of(kv, b, p) : -1;
-  if (g < 0) {
-    if (lane == 0) set_flag(flags, CSA2_FLAG_BAD_PAGE);
-    return;
-  }
+}
+
+// The layer's RoPE at position p on a row held as above.
+__device__ __forceinline__ void rotate_row(const RopeParams& rp, int64_t p, int lane, float (&v)[16]) {
   if (rp.pairs > 0) {
     float c = 1.f, s = 0.f;
     if (lane < rp.pairs) rope_cs(rp, lane, p, c, s);
@@ -338,9 +326,59 @@ __global__ void __launch_bounds__(256) append_paged_kernel(const T* __restrict__
       }
     }
   }
-  const int64_t r = p & ((1 << kv.page_shift) - 1);
+}
+
+// The row into row r of page g.
+template <int FMT>
+__device__ __forceinline__ void put_row(const PagedView& kv, int32_t g, int64_t r, int lane, const float (&v)[16]) {
   store_row<kDim, FMT>(v, lane, kv.pages + g * kv.page_stride + r * row_code_bytes(kDim, FMT),
                        FMT == 0 ? nullptr : kv.scales + g * kv.scale_stride + r * row_scale_bytes(kDim, FMT));
+}
+
+template <typename T, int FMT>
+__global__ void __launch_bounds__(256) append_paged_kernel(const T* __restrict__ rows, int64_t n_rows, int n_seq,
+                                                           const int64_t* __restrict__ tok_off,
+                                                           const int64_t* __restrict__ first_pos, const PagedView kv,
+                                                           const RopeParams rp, uint32_t* flags) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (row >= n_rows) return;
+  float v[16];
+  load_row(rows, row, lane, v);
+  const int b = find_segment(tok_off, n_seq, row);
+  const int64_t t0 = tok_off[b];
+  if (row < t0 || row >= tok_off[b + 1]) return;  // past the last sequence: left as it was
+  const int64_t p = first_pos[b] + (row - t0);
+  const int32_t g = p >= 0 ? page_of(kv, b, p) : -1;
+  if (g < 0) {
+    if (lane == 0) set_flag(flags, CSA2_FLAG_BAD_PAGE);
+    return;
+  }
+  rotate_row(rp, p, lane, v);
+  put_row<FMT>(kv, g, p & ((1 << kv.page_shift) - 1), lane, v);
+}
+
+// csa2_append_slots: the same, the row's place given: row slot mod page_size
+// of page slot / page_size.
+template <typename T, int FMT>
+__global__ void __launch_bounds__(256) append_slots_kernel(const T* __restrict__ rows, int64_t n_rows,
+                                                           const int64_t* __restrict__ pos,
+                                                           const int64_t* __restrict__ slots, const PagedView kv,
+                                                           const RopeParams rp, uint32_t* flags) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (row >= n_rows) return;
+  const int64_t slot = slots[row], p = pos != nullptr ? pos[row] : 0;
+  float v[16];
+  load_row(rows, row, lane, v);
+  if (slot == -1) return;  // padding
+  const int64_t g = slot >> kv.page_shift;
+  if (slot < 0 || g >= kv.n_pages || p < 0) {
+    if (lane == 0) set_flag(flags, CSA2_FLAG_BAD_PAGE);
+    return;
+  }
+  if (pos != nullptr) rotate_row(rp, p, lane, v);
+  put_row<FMT>(kv, (int32_t)g, slot & ((1 << kv.page_shift) - 1), lane, v);
 }
 
 }  // namespace
@@ -379,6 +417,25 @@ cudaError_t launch_append_paged(cudaStream_t st, int dtype, const void* rows, in
   const dim3 grid((unsigned)((n_rows + 7) / 8));
 #define CSA2_APPEND(T, F) \
   append_paged_kernel<T, F><<<grid, 256, 0, st>>>(static_cast<const T*>(rows), n_rows, n_seq, tok_off, first_pos, kv, rp, flags)
+#define CSA2_APPEND_F(T)                \
+  do {                                  \
+    if (kv_fmt == 0) CSA2_APPEND(T, 0); \
+    else if (kv_fmt == 1) CSA2_APPEND(T, 1); \
+    else CSA2_APPEND(T, 2);             \
+  } while (0)
+  if (dtype == CSA2_DTYPE_FP32) CSA2_APPEND_F(float);
+  else CSA2_APPEND_F(uint16_t);
+#undef CSA2_APPEND_F
+#undef CSA2_APPEND
+  return cudaGetLastError();
+}
+
+cudaError_t launch_append_slots(cudaStream_t st, int dtype, const void* rows, int64_t n_rows, const int64_t* pos,
+                                const int64_t* slots, const PagedView& kv, int kv_fmt, const RopeParams& rp, uint32_t* flags) {
+  if ((n_rows + 7) / 8 > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)((n_rows + 7) / 8));
+#define CSA2_APPEND(T, F) \
+  append_slots_kernel<T, F><<<grid, 256, 0, st>>>(static_cast<const T*>(rows), n_rows, pos, slots, kv, rp, flags)
 #define CSA2_APPEND_F(T)                \
   do {                                  \
     if (kv_fmt == 0) CSA2_APPEND(T, 0); \

@@ -1,7 +1,10 @@
 // Internal launcher declarations shared by the kernel files and the C-ABI host
 // code (not part of the public interface).
 #pragma once
+#include <cuda.h>
+
 #include "common.cuh"
+#include "batch.cuh"
 #include "paged.cuh"
 #include "pages.cuh"
 
@@ -214,6 +217,9 @@ cudaError_t launch_topk_merge(cudaStream_t st, int n_query, int n_lists, int k_i
 // one CTA waiting on an mbarrier nothing arrives at, for limit_ns (csa2_debug_wait_timeout)
 cudaError_t launch_wait_probe(cudaStream_t st, uint32_t* flags, uint64_t limit_ns);
 
+// Tensor map of bf16 rows, boxes of 64 channels (128 bytes, the swizzle's width)
+cudaError_t encode_bf16_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                            const uint32_t* box);
 // paged caches (csa2_attend_paged, csa2_append_paged, csa2_pages_*)
 size_t attend_paged_workspace_bytes(int num_sms);
 cudaError_t launch_attend_paged(cudaStream_t st, int num_sms, int kv_fmt, AttendParams a, const PagedView& kv,
@@ -221,6 +227,15 @@ cudaError_t launch_attend_paged(cudaStream_t st, int num_sms, int kv_fmt, Attend
 cudaError_t launch_append_paged(cudaStream_t st, int dtype, const void* rows, int64_t n_rows, int n_seq,
                                 const int64_t* tok_off, const int64_t* first_pos, const PagedView& kv, int kv_fmt,
                                 const RopeParams& rp, uint32_t* flags);
+// rows i at positions pos[i] (nullable: not rotated) into rows slots[i] of the pages
+cudaError_t launch_append_slots(cudaStream_t st, int dtype, const void* rows, int64_t n_rows, const int64_t* pos,
+                                const int64_t* slots, const PagedView& kv, int kv_fmt, const RopeParams& rp, uint32_t* flags);
+// queries that share rows, place by place: a.n_query places
+size_t attend_shared_workspace_bytes(int num_sms, int n_query);
+cudaError_t launch_attend_shared(cudaStream_t st, int num_sms, int kv_fmt, const AttendParams& a, const PagedView& kv,
+                                 const int32_t* order, const int32_t* head, const int64_t* shared, void* ws, int* n_launch);
+cudaError_t launch_batch_tables(cudaStream_t st, BatchParams p);
+cudaError_t launch_query_groups(cudaStream_t st, const GroupParams& p);
 size_t pages_workspace_bytes(int n_seq, int n_pages);
 cudaError_t launch_pages_extend(cudaStream_t st, const PagePool& P, int n, const int32_t* seqs, const int64_t* new_len,
                                 void* ws);

@@ -98,6 +98,7 @@ typedef enum csa2_kv_format {
 #define CSA2_FLAG_OUT_OF_PAGES     0x80u /* an entry refused: not enough free pages  */
 #define CSA2_FLAG_BAD_SEQ          0x100u /* an entry refused: sequence out of range,
                                             named twice, or of the wrong length      */
+#define CSA2_FLAG_BATCH_FULL       0x200u /* requests left without tokens: max_tokens    */
 
 /* Geometry and numerics of one CSA2 layer ("DeepSeek-V4.1-Flash on WASTE",
  * section "The shape"; PocketLLM page, geometry table). Supported values:
@@ -657,6 +658,18 @@ typedef enum csa2_dtype { CSA2_DTYPE_BF16 = 0, CSA2_DTYPE_FP16 = 1, CSA2_DTYPE_F
 csa2_status csa2_append_paged(csa2_ctx* ctx, void* stream, const csa2_paged_kv* kv, int32_t dtype, const void* rows,
                               int64_t n_tokens, const int64_t* tok_off, const int64_t* first_pos);
 
+/* csa2_append_slots: new rows rotated at pos [n_tokens] int64 (nullable: rows
+ * that are not to be rotated) with the context's RoPE and stored in kv_format in
+ * row slot[i] mod page_size of page slot[i] / page_size (as csa2_batch_tables
+ * makes slots; csa2_append_paged's rounding and bits). kv's table is not read
+ * (nullable, with its sizes).
+ *   rows   [n_tokens, 512] bf16 or fp32 (dtype), 16-byte aligned
+ *   slots  [n_tokens] int64; -1: padding, not stored; one outside the pages, or
+ *          with a negative position, is skipped and recorded as
+ *          CSA2_FLAG_BAD_PAGE. No slot must be named twice. One launch. */
+csa2_status csa2_append_slots(csa2_ctx* ctx, void* stream, const csa2_paged_kv* kv, int32_t dtype, const void* rows,
+                              int64_t n_tokens, const int64_t* pos, const int64_t* slots);
+
 /* csa2_page_pool (host struct): the state the page operations work on, all of
  * it the caller's device memory: table as in csa2_paged_kv (written here),
  * seq_len [n_seq] int64 tokens of each sequence, ref [n_pages] int32 the
@@ -723,6 +736,87 @@ csa2_status csa2_pages_trim(csa2_ctx* ctx, void* stream, const csa2_page_pool* p
                             int64_t window, int64_t n_first, const int64_t* lo);
 csa2_status csa2_pages_compact(csa2_ctx* ctx, void* stream, const csa2_page_pool* pool, int32_t n_arrays,
                                const csa2_page_array* arrays, int32_t* n_live, void* workspace,
+                               size_t workspace_bytes);
+
+/* ------------------------------------------------------------------------
+ * A batch over a page pool: the tables that a serving step's calls read, made on
+ * the device from the requests' lengths, so that a captured step follows the
+ * pool's state; and attention that reads the rows its sequences share once.
+ *
+ * csa2_batch_tables: request i < n_req is sequence seqs[i] of the pool, the last
+ * n_new[i] of its seq_len tokens being new (csa2_pages_extend has made room for
+ * them). Written, all of it the caller's device memory (csa2_batch, host struct):
+ *   table       [n_req, table_ld] int32, table_ld >= the pool's max_pages: the
+ *               requests' table rows (max_pages columns, -1 behind a sequence's
+ *               last page), a copy: page operations on the pool may go on while
+ *               the step reads it. With n_seq = n_req it is a csa2_paged_kv table.
+ *   tok_off     [n_req + 1] int64, first_pos [n_req] int64: the new tokens
+ *               packed request by request, as csa2_append_paged takes them
+ *   req_of_tok  [max_tokens] int32, tok_pos [max_tokens] int64: each new token's
+ *               request (row of `table`) and position, as csa2_attend_paged
+ *               takes them for seq_of_q and q_pos; -1 from tok_off[n_req] on
+ *   tok_slot    [max_tokens] int64: page * page_size + row in it, -1 where the
+ *               page is missing (recorded as CSA2_FLAG_BAD_PAGE) and for padding
+ * A request of sequence -1 has no tokens and an empty table row; one that cannot
+ * be carried out (another sequence out of range, n_new negative or above the
+ * length, a length past the table) neither, recorded as CSA2_FLAG_BAD_SEQ. A
+ * request whose tokens do not all fit into max_tokens has none, nor has any later
+ * one (CSA2_FLAG_BATCH_FULL). Two requests may name one sequence. One launch. */
+typedef struct csa2_batch {
+  int32_t* table;
+  int64_t table_ld;
+  int64_t* tok_off;
+  int64_t* first_pos;
+  int32_t* req_of_tok;
+  int64_t* tok_pos;
+  int64_t* tok_slot;
+  int64_t max_tokens;
+} csa2_batch;
+csa2_status csa2_batch_tables(csa2_ctx* ctx, void* stream, const csa2_page_pool* pool, int32_t n_req, const int32_t* seqs,
+                              const int64_t* n_new, const csa2_batch* batch);
+
+/* csa2_query_groups: the plan of csa2_attend_shared, from a page table (as in
+ * csa2_paged_kv). With K = ceil(min_shared / page_size), min_shared >= 1: the
+ * queries that see K whole pages (q_pos + 1 >= K page_size) and whose sequences
+ * name the same page in column K - 1 form a group; any other query is a group of
+ * its own. Groups stand in the order of their lowest query, queries in a group in
+ * ascending order, at places k = 0 .. n_query - 1:
+ *   order   [n_query] int32: the query at place k
+ *   head    [n_query] int32: the first place of k's group
+ *   shared  [n_query] int64: at a head, for a group of more than one query,
+ *           page_size times the number of leading columns at which all of its
+ *           queries' rows name the same page, wholly seen by each; else 0
+ *   n_groups [1] int32 (nullable)
+ *   q_pos [n_query] int64, seq_of_q [n_query] int32 as for csa2_attend_paged
+ *           (bad ones recorded as CSA2_FLAG_BAD_QUERY, groups of their own)
+ * n_query at most 4,096. Two launches. */
+csa2_status csa2_query_groups(csa2_ctx* ctx, void* stream, const int32_t* table, int64_t table_ld, int32_t max_pages,
+                              int32_t n_pages, int32_t page_size, int32_t n_seq, int32_t n_query, const int64_t* q_pos,
+                              const int32_t* seq_of_q, int64_t min_shared, int32_t* order, int32_t* head, int64_t* shared,
+                              int32_t* n_groups);
+
+/* csa2_attend_shared: csa2_attend_paged's attention over every position 0 ..
+ * q_pos[i] (no window, no left padding), for queries that share rows. Place k <
+ * n_query has query order[k] (-1: none; each query at one place), head[k] <= k is
+ * the first place of its group, whose places follow one another, and
+ * len = shared[head[k]], rounded down to whole pages, the group's common
+ * beginning: a row at a position below len is read through the table row of the
+ * query at place head[k] (one without a sequence: len 0), the others through the
+ * query's own. Two queries at neighbouring places of a group are worked on
+ * together: their common rows are read, and multiplied, once.
+ *   q, q_pos, seq_of_q, sink, out, lse: as for csa2_attend_paged (padding and bad
+ *   queries, missing pages and empty rows alike; an order outside [-1, n_query)
+ *   is recorded as CSA2_FLAG_BAD_QUERY and skipped, and so is a place whose
+ *   group does not begin where head says). A query at no place keeps its out.
+ * Results do not depend on timing. The limits on the size of rows are
+ * csa2_attend_paged's. n_query at most 2^20. Three launches.
+ *   workspace of csa2_attend_shared_workspace_size bytes; calls that may overlap
+ *   on the GPU need one each
+ * q, pages, scales and out must be 16-byte aligned; out must not overlap q. */
+size_t csa2_attend_shared_workspace_size(const csa2_ctx* ctx, int32_t n_query);
+csa2_status csa2_attend_shared(csa2_ctx* ctx, void* stream, const csa2_paged_kv* kv, int32_t n_query, const uint16_t* q,
+                               const int64_t* q_pos, const int32_t* seq_of_q, const int32_t* order, const int32_t* head,
+                               const int64_t* shared, const float* sink, uint16_t* out, float* lse, void* workspace,
                                size_t workspace_bytes);
 
 /* ------------------------------------------------------------------------
