@@ -355,6 +355,14 @@ __device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t phase, uint3
   set_flag(flags, CSA2_FLAG_WAIT_TIMEOUT);
   return false;
 }
+__device__ __forceinline__ uint32_t done_cluster(uint32_t bar, uint32_t phase) {
+  uint32_t ok;
+  asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
+               : "=r"(ok)
+               : "r"(bar), "r"(phase)
+               : "memory");
+  return ok;
+}
 __device__ __forceinline__ bool wait_cluster_all_lanes(uint32_t bar, uint32_t phase, uint32_t* flags) {
   return __all_sync(0xffffffffu, wait_cluster(bar, phase, flags)) != 0;
 }
@@ -437,12 +445,24 @@ __device__ __forceinline__ int32_t group_page(const SharedParams& p, const Share
   return g.present && pos >= g.from && pos < g.to ? page_of(p.kv, pos < u.len ? u.head_seq : g.seq, pos) : -1;
 }
 
+// (field by field: a struct filled through a cast lives in local memory)
 __device__ __forceinline__ SharedUnit load_unit(const SharedUnit* at) {
+  const int4* v = reinterpret_cast<const int4*>(at);
+  const int4 a = v[0], b = v[1], c = v[2];
   SharedUnit u;
-  const int4* s = reinterpret_cast<const int4*>(at);
-  int4* d = reinterpret_cast<int4*>(&u);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) d[i] = s[i];
+  u.q[0] = a.x;
+  u.q[1] = a.y;
+  u.seq[0] = a.z;
+  u.seq[1] = a.w;
+  u.end[0] = b.x;
+  u.end[1] = b.y;
+  u.head_seq = b.z;
+  u.len = b.w;
+  u.common = c.x;
+  u.n[0] = c.y;
+  u.n[1] = c.z;
+  u.n[2] = c.w;
+  u.tiles = reinterpret_cast<const int32_t*>(at)[12];
   return u;
 }
 
@@ -476,11 +496,14 @@ struct SharedWalk {
 // place in the ring
 struct RingAt {
   uint32_t slot, phase;
-  __device__ __forceinline__ void step(uint32_t n) {
+  __device__ __forceinline__ void step(uint32_t n) {  // n <= 2 kRing - slot
     slot += n;
-    if (slot >= (uint32_t)kRing) {
-      slot -= kRing;
-      phase ^= 1u;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (slot >= (uint32_t)kRing) {
+        slot -= kRing;
+        phase ^= 1u;
+      }
     }
   }
 };
@@ -550,90 +573,120 @@ __device__ __forceinline__ void fill_slot(const SharedParams& p, const SharedUni
   fence_proxy_async_smem();
 }
 
-// Producer warp w of a CTA: every kProducers-th slot of the ring.
+// Producer warp w of a CTA: every kProducers-th slot of the ring. What a tile's
+// copies need is found once a tile, before the waits for its slots: with the look-up
+// behind them the warps took 1,300 cycles to issue a slot's two copies.
 template <int KVF, bool TMA>
 __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm, uint32_t base_s, SharedWalk walk, int w, int rank) {
-  constexpr int NP = SharedRoles<TMA>::kProducers;
+  constexpr uint32_t NP = SharedRoles<TMA>::kProducers;
   const int lane = threadIdx.x & 31;
   const uint32_t bars = base_s + S_BAR, full0 = in_leader(bars + 8 * bFull);
   const uint32_t leader = elect_one();
   const int ps = p.kv.page_shift, pc = piece_shift(ps);
-  RingAt at{0, 0};
-  uint32_t s = 0;  // slots so far, of all warps
+  const int pieces = kGroupRows >> pc;
+  RingAt base{0, 0};  // the next slot of all warps, and the slots before it
+  uint32_t s = 0;
   bool live = true;
-  // a slot for this warp to fill
-  auto take = [&]() {
-    if (s >= (uint32_t)kRing) live = live && wait_all_lanes(bars + 8 * (bEmpty + at.slot), at.phase ^ 1u, p.flags);
-    return live;
+  // Of a tile: the number of its row groups; of lane 8 g + i piece i of group
+  // g, its page and the row in it; and which groups lie whole in it (bits 8 g).
+  struct Source {
+    int n;
+    int32_t page, row;
+    uint32_t whole;
   };
-  // lane 8 g + i: the page of piece i of the tile's group g (TMA)
-  auto look_up = [&](const SharedUnit& u, int tile) {
+  auto look_up = [&](int tile) {
+    const SharedUnit& u = walk.u;
+    Source src;
+    src.n = uniform(row_groups(u, tile));
+    src.page = p.kv.n_pages;  // past the end: zeros
+    src.row = 0;
+    src.whole = 0;
+    if (!TMA) return src;
     const RowGroup g = row_group(u, kTileGroups * tile + (lane >> 3));
     const int pos = 64 * g.block + ((lane & 7) << pc);
-    int32_t page = -1;
-    if ((lane & 7) << pc < kGroupRows && g.present && pos < g.to && pos + (1 << pc) > g.from)
-      page = page_of(p.kv, max(pos, g.from) < u.len ? u.head_seq : g.seq, pos);
-    return page >= 0 ? page : p.kv.n_pages;  // past the end: zeros
-  };
-  auto keys = [&](const SharedUnit& u, int tile, int32_t pages) {
-    const int mine = min(2, max(0, row_groups(u, tile) - 2 * rank));  // row groups of this CTA's half
-#pragma unroll 1
-    for (int b = 0; b < 8; ++b, ++s, at.step(1)) {
-      if ((int)(s % NP) != w || !take()) continue;
-      const uint32_t bar = full0 + 8 * at.slot, dst = base_s + S_RING + at.slot * kSlotBytes;
-      if (TMA) {
-        expect_cluster_one(leader, bar, 8192u * (uint32_t)mine);
-#pragma unroll 1
-        for (int g = 0; g < mine; ++g) {
-          const int row0 = (64 * row_group(u, kTileGroups * tile + 2 * rank + g).block) & ((1 << ps) - 1);
-#pragma unroll 1
-          for (int i = 0; (i << pc) < kGroupRows; ++i)
-            tma_pair_3d(leader, dst + 8192u * (uint32_t)g + ((uint32_t)i << (7 + pc)), &p.kv_map, 64 * b,
-                        uniform(row0), uniform(pages, 8 * (2 * rank + g) + i), bar);
-        }
-      } else {
-        if (mine > 0) fill_slot<KVF, true>(p, u, tile, 2 * rank, 64 * b, dst, sm + (dst - base_s), lane);
-        warp_arrive_cluster(bar);
-      }
+    if ((lane & 7) < pieces && g.present && pos < g.to && pos + (1 << pc) > g.from) {
+      const int32_t page = page_of(p.kv, max(pos, g.from) < u.len ? u.head_seq : g.seq, pos);
+      if (page >= 0) src.page = page;
     }
+    src.row = pos & ((1 << ps) - 1);
+    src.whole = __ballot_sync(0xffffffffu, (lane & 7) == 0 && g.present && g.from <= 64 * g.block && g.to >= 64 * g.block + 64);
+    return src;
   };
-  auto values = [&](const SharedUnit& u, int tile, int32_t pages) {
-    const int n = row_groups(u, tile);
+  // this warp's slots of the next `count`: fill(i, its place)
+  auto each = [&](uint32_t count, auto&& fill) {
 #pragma unroll 1
-    for (int i = 0; i < 2 * n; ++i, ++s, at.step(1)) {
-      if ((int)(s % NP) != w || !take()) continue;
+    for (uint32_t i = (w + NP - s % NP) % NP; i < count; i += NP) {
+      RingAt at = base;
+      at.step(i);
+      if (s + i >= (uint32_t)kRing) live = live && wait_all_lanes(bars + 8 * (bEmpty + at.slot), at.phase ^ 1u, p.flags);
+      if (live) fill((int)i, full0 + 8 * at.slot, at.slot * kSlotBytes + S_RING);
+    }
+    base.step(count);
+    s += count;
+  };
+  auto keys = [&](int tile, const Source& src) {
+    const int n = min(2, max(0, src.n - 2 * rank));  // row groups of this CTA's half
+    const int page0 = uniform(src.page, 16 * rank), page1 = uniform(src.page, 16 * rank + 8);
+    const int row0 = uniform(src.row, 16 * rank), row1 = uniform(src.row, 16 * rank + 8);
+    each(8, [&](int b, uint32_t bar, uint32_t slot) {
+      const uint32_t dst = base_s + slot;
+      if (!TMA) {
+        if (n > 0) fill_slot<KVF, true>(p, walk.u, tile, 2 * rank, 64 * b, dst, sm + slot, lane);
+        warp_arrive_cluster(bar);
+        return;
+      }
+      expect_cluster_one(leader, bar, 8192u * (uint32_t)n);
+      if (pieces == 1) {
+        if (n > 0) tma_pair_3d(leader, dst, &p.kv_map, 64 * b, row0, page0, bar);
+        if (n > 1) tma_pair_3d(leader, dst + 8192u, &p.kv_map, 64 * b, row1, page1, bar);
+      } else {
+#pragma unroll 1
+        for (int g = 0; g < n; ++g) {
+#pragma unroll 1
+          for (int i = 0; i < pieces; ++i)
+            tma_pair_3d(leader, dst + 8192u * (uint32_t)g + ((uint32_t)i << (7 + pc)), &p.kv_map, 64 * b, 0,
+                        uniform(src.page, 8 * (2 * rank + g) + i), bar);
+        }
+      }
+    });
+  };
+  auto values = [&](int tile, const Source& src) {
+    each(2 * (uint32_t)src.n, [&](int i, uint32_t bar, uint32_t slot) {
       const int g = i >> 1, d0 = 256 * (i & 1) + 128 * rank;
-      const RowGroup rg = row_group(u, kTileGroups * tile + g);
-      const uint32_t bar = full0 + 8 * at.slot, dst = base_s + S_RING + at.slot * kSlotBytes;
+      const uint32_t dst = base_s + slot;
       // (a group's end inside a page: rows behind it hold anything)
-      if (TMA && uniform(rg.from <= 64 * rg.block && rg.to >= 64 * rg.block + 64)) {
-        expect_cluster_one(leader, bar, kSlotBytes);
-        const int row0 = uniform((64 * rg.block) & ((1 << ps) - 1));
-#pragma unroll 1
-        for (int k = 0; (k << pc) < kGroupRows; ++k) {
-          const int page = uniform(pages, 8 * g + k);
-          tma_pair_3d(leader, dst + ((uint32_t)k << (7 + pc)), &p.kv_map, d0, row0, page, bar);
-          tma_pair_3d(leader, dst + 8192u + ((uint32_t)k << (7 + pc)), &p.kv_map, d0 + 64, row0, page, bar);
-        }
-      } else {
-        fill_slot<KVF, false>(p, u, tile, g, d0, dst, sm + (dst - base_s), lane);
+      if (!TMA || ((src.whole >> (8 * g)) & 1u) == 0u) {
+        fill_slot<KVF, false>(p, walk.u, tile, g, d0, dst, sm + slot, lane);
         warp_arrive_cluster(bar);
+        return;
       }
-    }
+      expect_cluster_one(leader, bar, kSlotBytes);
+      if (pieces == 1) {
+        const int page = uniform(src.page, 8 * g), row = uniform(src.row, 8 * g);
+        tma_pair_3d(leader, dst, &p.kv_map, d0, row, page, bar);
+        tma_pair_3d(leader, dst + 8192u, &p.kv_map, d0 + 64, row, page, bar);
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < pieces; ++k) {
+          const int page = uniform(src.page, 8 * g + k);
+          tma_pair_3d(leader, dst + ((uint32_t)k << (7 + pc)), &p.kv_map, d0, 0, page, bar);
+          tma_pair_3d(leader, dst + 8192u + ((uint32_t)k << (7 + pc)), &p.kv_map, d0 + 64, 0, page, bar);
+        }
+      }
+    });
   };
   if (walk.left <= 0) return;
   do {
-    const SharedUnit& u = walk.u;
-    int32_t now = TMA ? look_up(u, walk.first) : 0;
-    keys(u, walk.first, now);
+    Source now = look_up(walk.first);
+    keys(walk.first, now);
 #pragma unroll 1
     for (int t = walk.first; t < walk.last; ++t) {
-      int32_t ahead = now;
+      Source ahead = now;
       if (t + 1 < walk.last) {
-        if (TMA) ahead = look_up(u, t + 1);
-        keys(u, t + 1, ahead);
+        ahead = look_up(t + 1);
+        keys(t + 1, ahead);
       }
-      values(u, t, now);
+      values(t, now);
       now = ahead;
     }
   } while (walk.next(p));
@@ -650,7 +703,7 @@ __device__ __forceinline__ void q_role(const SharedParams& p, uint8_t* sm, uint3
   if (walk.left <= 0) return;
   uint32_t seg = 0;
   do {
-    const int qi = uniform(walk.u.q[rank]);
+    const int qi = uniform(rank == 0 ? walk.u.q[0] : walk.u.q[1]);
     // (a wait that ran out is recorded; the barriers below are met all the same)
     if (seg > 0) live = live && wait_all_lanes(bars + 8 * bQEmpty, (seg & 1u) ^ 1u, p.flags);
     if (t < 32 && live) {
@@ -706,13 +759,23 @@ __device__ __forceinline__ void issue_shared(const SharedParams& p, uint32_t bas
   RingAt at{0, 0};
   uint32_t n = 0, done = 0, seg = 0;  // tiles scored, tiles whose outputs were issued, units
   bool live = true;
+  // The slot whose turn it is, waited for. Its barrier was looked at while the
+  // products of the slot before were issued: a look takes some 300 cycles from
+  // the instruction to the branch, longer than a slot's products run.
+  uint32_t landed = 0;
+  auto ready = [&]() {
+    if (!uniform(landed != 0u)) live = live && wait_cluster_all_lanes(bars + 8 * (bFull + at.slot), at.phase, flags);
+    tc_fence_after();
+    RingAt next = at;
+    next.step(1);
+    landed = done_cluster(bars + 8 * (bFull + next.slot), next.phase);
+    return live;
+  };
   auto scores = [&](bool last) {
     const uint32_t d = tmem_s + 128u * (n & 1u);
 #pragma unroll 1
     for (uint32_t b = 0; b < 8; ++b, at.step(1)) {
-      live = live && wait_cluster_all_lanes(bars + 8 * (bFull + at.slot), at.phase, flags);
-      if (!live) return;
-      tc_fence_after();
+      if (!ready()) return;
       const uint64_t k0 = sdesc_add(kd, at.slot * kSlotBytes);
 #pragma unroll
       for (uint32_t k = 0; k < 4; ++k) mma_pair(leader, d, sdesc_add(qd, b * 8192u + 32u * k), sdesc_add(k0, 32u * k), kIdescS, b | k);
@@ -747,9 +810,7 @@ __device__ __forceinline__ void issue_shared(const SharedParams& p, uint32_t bas
           begun |= lanes;
 #pragma unroll 1
           for (uint32_t j = 0; j < 2; ++j, at.step(1)) {
-            live = live && wait_cluster_all_lanes(bars + 8 * (bFull + at.slot), at.phase, flags);
-            if (!live) break;
-            tc_fence_after();
+            if (!ready()) break;
             const uint64_t v0 = sdesc_add(vd, at.slot * kSlotBytes), p0 = sdesc_add(pd, 8192u * (uint32_t)g);
             if (who == 0) {
 #pragma unroll
@@ -806,7 +867,7 @@ __device__ __forceinline__ void math_shared(const SharedParams& p, uint8_t* sm, 
   uint32_t n = 0;
   do {
     const SharedUnit& u = walk.u;
-    const int qi = u.q[rank];
+    const int qi = rank == 0 ? u.q[0] : u.q[1];
     const int64_t t_q = qi >= 0 ? p.q_pos[qi] : 0;
     if (upper + cols == 0 && lane < p.rp.pairs) {
       float cs, sn;
@@ -821,7 +882,7 @@ __device__ __forceinline__ void math_shared(const SharedParams& p, uint8_t* sm, 
       uint32_t mask[2];
       {
         const RowGroup g = row_group(u, kTileGroups * t + group);
-        const bool mine = g.present && (g.who == 0 || g.who == rank + 1) && u.end[rank] > 0;
+        const bool mine = g.present && (g.who == 0 || g.who == rank + 1) && (rank == 0 ? u.end[0] : u.end[1]) > 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int pos = 64 * g.block + 32 * i + lane;
