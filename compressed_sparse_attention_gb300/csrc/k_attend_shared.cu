@@ -332,9 +332,11 @@ __device__ __forceinline__ void warp_arrive_cluster(uint32_t bar) {
   __syncwarp();
   if ((threadIdx.x & 31) == 0) arrive_cluster(bar);
 }
+// (relaxed: there is nothing before it to be seen behind it, and a release waits
+// for the warp's loads and stores, some 1,000 cycles)
 __device__ __forceinline__ void expect_cluster_one(uint32_t leader, uint32_t bar, uint32_t bytes) {
   asm volatile(
-      "{\n.reg .pred e;\nsetp.ne.u32 e, %2, 0;\n@e mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;\n}" ::"r"(bar),
+      "{\n.reg .pred e;\nsetp.ne.u32 e, %2, 0;\n@e mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;\n}" ::"r"(bar),
       "r"(bytes), "r"(leader)
       : "memory");
 }
