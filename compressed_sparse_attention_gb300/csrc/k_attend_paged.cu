@@ -176,11 +176,6 @@ __device__ __forceinline__ void sync_producers() {
 // left out: one tile a CTA where they suffice. Parts of a query lie in
 // neighbouring CTAs, none of them empty: the parts are longer than a tile.
 constexpr int kTileCost = 4, kQueryCost = 5;
-// a / b of values >= 0: 32-bit where they fit (a 64-bit division is several
-// hundred cycles, before any row is asked for)
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-  return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
 // CTAs that share a tile, each with as many of its output dims: with fewer
 // tiles than half or a quarter of the CTAs two or four of them form the same
 // scores, and each has a share of the output's products and of its way out

@@ -42,7 +42,7 @@ constexpr int kGroupRows = 64;   // aligned positions of a row group
 constexpr int kTileGroups = 4;   // row groups of a tile
 constexpr int kRing = 7;         // slots
 constexpr uint32_t kSlotBytes = 16384;
-constexpr int kMaxPairs2 = 256;  // pairs of CTAs, at most
+constexpr int kMaxPairs2 = 128;  // pairs of CTAs, at most
 constexpr int kPlanThreads = 1024;
 
 // Two places of a group (or its last one alone).
@@ -85,7 +85,7 @@ struct SharedParams {
   int pairs;  // of CTAs
   SharedUnit* units;
   SharedRun* runs;   // [pairs + 1]
-  int4* joins;       // [pairs]: unit, first and last run of a unit that run c begins and does not end; -1: none
+  int4* joins;       // [pairs]: of a unit that run c begins and does not end its queries, c and its last run; third -1: none
   float* part_o;     // [2 pairs slots][2][512 / 4][64 heads][4]
   float* part_m;     // [2 pairs slots][2][64]
   float* part_l;
@@ -178,10 +178,10 @@ __device__ __forceinline__ PlanUnit unit_at(const SharedParams& p, int k, uint32
 }  // namespace
 
 __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(const __grid_constant__ SharedParams p) {
-  __shared__ int64_t sum_t[32];
-  __shared__ int sum_u[32];
-  __shared__ int64_t total_t;
-  __shared__ int total_u;
+  __shared__ int64_t sum_t[32], share_t[kPlanThreads];  // tiles, units before a thread's share
+  __shared__ int sum_u[32], share_u[kPlanThreads];
+  __shared__ SharedRun runs[kMaxPairs2 + 1];
+  __shared__ uint32_t on[kMaxPairs2 / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
   pdl_wait();
@@ -200,7 +200,6 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(con
     }
   }
   if (bad) set_flag(p.flags, bad);
-  if (tid < p.pairs) p.joins[tid] = make_int4(-1, 0, 0, 0);
   // exclusive scan over the threads
   int64_t it = tiles;
   int iu = units;
@@ -212,61 +211,86 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(con
   }
   if (lane == 31) sum_t[warp] = it, sum_u[warp] = iu;
   __syncthreads();
-  if (warp == 0) {
-    int64_t a = sum_t[lane];
-    int b = sum_u[lane];
+  // (every warp scans the warps' sums for itself)
+  int64_t at = sum_t[lane];
+  int au = sum_u[lane];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t x = __shfl_up_sync(0xffffffffu, a, o);
-      const int y = __shfl_up_sync(0xffffffffu, b, o);
-      if (lane >= o) a += x, b += y;
-    }
-    if (lane == 31) total_t = a, total_u = b;
-    sum_t[lane] = a;
-    sum_u[lane] = b;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, at, o);
+    const int y = __shfl_up_sync(0xffffffffu, au, o);
+    if (lane >= o) at += x, au += y;
+  }
+  const int64_t T = __shfl_sync(0xffffffffu, at, 31);
+  const int U = __shfl_sync(0xffffffffu, au, 31);
+  const int64_t bt = __shfl_sync(0xffffffffu, at, max(warp, 1) - 1);
+  const int bu = __shfl_sync(0xffffffffu, au, max(warp, 1) - 1);
+  share_t[tid] = it - tiles + (warp > 0 ? bt : 0);
+  share_u[tid] = iu - units + (warp > 0 ? bu : 0);
+  int u0 = share_u[tid];
+  for (int k = lo; k < hi; ++k) {
+    if (per > 1) one = unit_at(p, k, unused);
+    if (one.begins) p.units[u0++] = one.u;
   }
   __syncthreads();
-  int64_t t0 = it - tiles + (warp > 0 ? sum_t[warp - 1] : 0);
-  int u0 = iu - units + (warp > 0 ? sum_u[warp - 1] : 0);
-  const int64_t T = total_t;
-  const int U = total_u;
   // On a line where a tile is kTileCost2 long and a unit starts with kUnitCost,
   // run c has the tiles that start in the c-th of R equal parts (none of them
-  // empty: a part is longer than a unit's start and a tile).
+  // empty: a part is longer than a unit's start and a tile). Thread c finds the
+  // first tile from the c-th cut on.
   const int start = T > 2 * (int64_t)p.pairs ? kUnitCost : 0;
   const int64_t cost = kTileCost2 * T + (int64_t)start * U;
   const int R = (int)min((int64_t)p.pairs, T);
-  for (int k = lo; k < hi; ++k) {
-    if (per > 1) one = unit_at(p, k, unused);
-    if (!one.begins) continue;
-    const SharedUnit& u = one.u;
-    p.units[u0] = u;
-    const int64_t c0 = kTileCost2 * t0 + (int64_t)start * u0, c1 = c0 + start + (int64_t)kTileCost2 * u.tiles;
-    // the cuts c cost / R in [c0, c1)
-    int first = -1, last = -1;
-    for (int64_t c = (c0 * R + cost - 1) / cost; c < R && c * cost < c1 * R; ++c) {
-      const int64_t left = c * cost - R * (c0 + start), step = (int64_t)kTileCost2 * R;
-      const int j = left <= 0 ? 0 : (int)((left + step - 1) / step);  // the first tile from the cut on
-      SharedRun r;
-      r.tile = t0 + j;
-      r.unit = j < u.tiles ? u0 : u0 + 1;
-      r.first = j < u.tiles ? j : 0;
-      p.runs[c] = r;
-      if (j > 0 && j < u.tiles) {
-        if (first < 0) first = (int)c;
-        last = (int)c;
+  if (tid <= p.pairs) {
+    SharedRun r{T, U, 0};
+    if (tid < R) {
+      const int64_t y = tid * cost;  // R-fold, as are all places below
+      int i = 0, end = kPlanThreads;  // the last share that begins at or before y
+      while (end - i > 1) {
+        const int mid = (i + end) >> 1;
+        if (R * (kTileCost2 * share_t[mid] + (int64_t)start * share_u[mid]) <= y) i = mid;
+        else end = mid;
+      }
+      int64_t t = share_t[i];
+      int u = share_u[i];
+      for (;; ++u) {
+        const int n = p.units[u].tiles;
+        const int64_t left = y - R * (kTileCost2 * t + (int64_t)start * (u + 1)), step = (int64_t)kTileCost2 * R;
+        const int64_t j = left <= 0 ? 0 : quotient(left + step - 1, step);
+        if (j < n) {
+          r = SharedRun{t + j, u, (int32_t)j};
+          break;
+        }
+        t += n;
+        if (u + 1 == U) break;  // (a cut behind the last tile's start)
       }
     }
-    if (first > 0) p.joins[first - 1] = make_int4(u0, first - 1, last, 0);
-    t0 += u.tiles;
-    ++u0;
-  }
-  if (tid >= R && tid <= p.pairs) {
-    SharedRun r;
-    r.tile = T;
-    r.unit = U;
-    r.first = 0;
+    runs[tid] = r;
     p.runs[tid] = r;
+  }
+  __syncthreads();
+  // a unit that begins in run c and goes on: its last run is the one behind
+  // those that it fills from end to end
+  if (tid < kMaxPairs2) {
+    const bool through = tid < R && runs[tid + 1].first > 0 && runs[tid + 1].unit == runs[tid].unit;
+    const uint32_t w = __ballot_sync(0xffffffffu, through);
+    if (lane == 0) on[warp] = w;
+  }
+  __syncthreads();
+  if (tid < p.pairs) {
+    int4 jn = make_int4(-1, -1, -1, 0);
+    if (tid < R && runs[tid + 1].first > 0 && (runs[tid].unit < runs[tid + 1].unit || runs[tid].first == 0)) {
+      int c = tid + 1;
+      while (c < kMaxPairs2) {
+        const uint32_t off = ~on[c >> 5] >> (c & 31);
+        if (off != 0u) {
+          c += __ffs((int)off) - 1;
+          break;
+        }
+        c = (c | 31) + 1;
+      }
+      const SharedUnit& u = p.units[runs[tid + 1].unit];
+      jn = make_int4(u.q[0], u.q[1], tid, c);
+    }
+    p.joins[tid] = jn;
   }
 }
 
@@ -325,8 +349,13 @@ __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
   return r;
 }
+// An arrival in CTA 0 for what this CTA's warps left in their own shared memory
+// (made visible to the tensor core by a proxy fence before) or read from their
+// own tensor memory: the products that follow read and write those on this SM,
+// so that its own order suffices. A release at cluster scope would wait for all
+// of the warp's accesses to global memory too, 1,500 cycles.
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void warp_arrive_cluster(uint32_t bar) {
   __syncwarp();
@@ -796,36 +825,42 @@ __device__ __forceinline__ void issue_shared(const SharedParams& p, uint32_t bas
       live = live && wait_cluster_all_lanes(bars + 8 * bQFull, seg & 1u, flags);
       tc_fence_after();
       if (live) scores(walk.first + 1 == walk.last);
-      uint32_t begun = 0;  // whose lanes of O hold a sum (bits)
+      uint32_t holds = 0;  // whose lanes of O hold a sum (bits)
 #pragma unroll 1
       for (int t = walk.first; t < walk.last && live; ++t) {
         if (t + 1 < walk.last) scores(t + 2 == walk.last);
+        // who sees the tile's row groups, and (in the same places) whether their
+        // lanes of O hold a sum already
+        uint32_t whose = 0, begun = 0;
+        const uint32_t ng = (uint32_t)uniform(row_groups(walk.u, t));
+#pragma unroll
+        for (int g = 0; g < kTileGroups; ++g) {
+          const uint32_t who = (uint32_t)row_group(walk.u, kTileGroups * t + g).who, lanes = who == 0u ? 3u : who;
+          whose |= who << (2 * g);
+          begun |= ((holds & lanes) != 0u ? 1u : 0u) << (2 * g);
+          if (g < (int)ng) holds |= lanes;
+        }
+        whose = (uint32_t)uniform((int)whose);
+        begun = (uint32_t)uniform((int)begun);
         live = live && wait_cluster_all_lanes(bars + 8 * bWeights, done & 1u, flags);
         if (t == walk.first && seg > 0) live = live && wait_cluster_all_lanes(bars + 8 * bOFree, (seg & 1u) ^ 1u, flags);
         tc_fence_after();
-        const int ng = uniform(row_groups(walk.u, t));
 #pragma unroll 1
-        for (int g = 0; g < ng && live; ++g) {
-          const int who = uniform(row_group(walk.u, kTileGroups * t + g).who);
-          const uint32_t lanes = who == 0 ? 3u : (uint32_t)who;
-          const bool fresh = (begun & lanes) == 0u;
-          begun |= lanes;
-#pragma unroll 1
-          for (uint32_t j = 0; j < 2; ++j, at.step(1)) {
-            if (!ready()) break;
-            const uint64_t v0 = sdesc_add(vd, at.slot * kSlotBytes), p0 = sdesc_add(pd, 8192u * (uint32_t)g);
-            if (who == 0) {
+        for (uint32_t i = 0; i < 2u * ng; ++i, at.step(1)) {
+          if (!ready()) break;
+          const uint32_t g = i >> 1, who = (whose >> (2u * g)) & 3u;
+          const uint64_t v0 = sdesc_add(vd, at.slot * kSlotBytes), p0 = sdesc_add(pd, 8192u * g);
+          const uint32_t d = tmem_o + 128u * (i & 1u), keep = (begun >> (2u * g)) & 1u;
+          if (who == 0u) {
 #pragma unroll
-              for (uint32_t k = 0; k < 4; ++k)
-                mma_pair(leader, tmem_o + 128u * j, sdesc_add(p0, 32u * k), sdesc_add(v0, 2048u * k), kIdescO, k > 0 || !fresh ? 1u : 0u);
-            } else {
+            for (uint32_t k = 0; k < 4; ++k) mma_pair(leader, d, sdesc_add(p0, 32u * k), sdesc_add(v0, 2048u * k), kIdescO, k | keep);
+          } else {
 #pragma unroll
-              for (uint32_t k = 0; k < 4; ++k)
-                mma_pair_lanes(leader, tmem_o + 128u * j, sdesc_add(p0, 32u * k), sdesc_add(v0, 2048u * k), kIdescO,
-                               k > 0 || !fresh ? 1u : 0u, who == 1 ? 0u : ~0u, who == 1 ? ~0u : 0u);
-            }
-            commit_pair(leader, bars + 8 * (bEmpty + at.slot));
+            for (uint32_t k = 0; k < 4; ++k)
+              mma_pair_lanes(leader, d, sdesc_add(p0, 32u * k), sdesc_add(v0, 2048u * k), kIdescO, k | keep, who == 1u ? 0u : ~0u,
+                             who == 1u ? ~0u : 0u);
           }
+          commit_pair(leader, bars + 8 * (bEmpty + at.slot));
         }
         if (live) commit_pair(leader, bars + 8 * bPFree);
         ++done;
@@ -1098,53 +1133,93 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SharedRoles<TMA>::kT
 }
 
 // Join of a split unit's partials, the formula of csa2_attend_paged's join. A
-// thread has one head and 16 dims (a sector of the output): the parts' values
-// are next to each other over the heads.
+// thread has one head and 16 dims (a sector of the output; the parts' values lie
+// next to each other over the heads), a CTA 64 of the dims: the parts' weights
+// go through its shared memory, and two parts' values are under way at once.
 constexpr int kJoinDims = 16;
-__global__ void __launch_bounds__(256) attend_shared_join_kernel(const __grid_constant__ SharedParams p) {
-  const int head = threadIdx.x & 63, d0 = kJoinDims * ((int)blockIdx.y * 4 + (threadIdx.x >> 6)), rank = (int)blockIdx.z;
+constexpr int kJoinParts = 2;
+__global__ void __launch_bounds__(256, 4) attend_shared_join_kernel(const __grid_constant__ SharedParams p) {
+  __shared__ float weight[kMaxPairs2][kHeads];
+  __shared__ float red[2][4][kHeads];
+  __shared__ float2 turn[32];
+  const int head = threadIdx.x & 63, quarter = threadIdx.x >> 6, rank = (int)blockIdx.z;
+  const int d0 = kJoinDims * ((int)blockIdx.y * 4 + quarter), first_rope = kDim - 2 * p.rp.pairs;
+  const bool rope = kJoinDims * ((int)blockIdx.y * 4 + 4) > first_rope;  // of the CTA
+  const double freq = rope && threadIdx.x < (unsigned)p.rp.pairs ? p.rp.freq[threadIdx.x] : 0.0;
   pdl_wait();
   const int4 jn = p.joins[blockIdx.x];
-  if (jn.x < 0) return;
-  const int qi = p.units[jn.x].q[rank];
-  if (qi < 0) return;
-  const int n = jn.z - jn.y + 1;
-  auto slot = [&](int k) { return shared_slot(jn.y + k, k == 0, rank); };
+  const int qi = rank == 0 ? jn.x : jn.y;
+  if (jn.z < 0 || qi < 0) return;
+  const int n = jn.w - jn.z + 1;
+  auto slot = [&](int k) { return shared_slot(jn.z + k, k == 0, rank); };
+  const float4* parts = reinterpret_cast<const float4*>(p.part_o) + (int64_t)(d0 / 4) * kHeads + head;
+  float4 v[kJoinParts][kJoinDims / 4];
+  auto fetch = [&](int k0) {
+#pragma unroll
+    for (int u = 0; u < kJoinParts; ++u) {
+#pragma unroll
+      for (int i = 0; i < kJoinDims / 4; ++i)
+        v[u][i] = k0 + u < n ? parts[(slot(k0 + u) * (kDim / 4) + i) * kHeads] : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  fetch(0);
+  // references and sums of this thread's quarter of the parts
   const float sk = p.sink != nullptr ? p.sink[head] : -INFINITY, sk2 = sk * 1.4426950408889634f;
+  if (threadIdx.x < 32 && rope) {
+    float cs, sn;
+    angle_cs((double)p.q_pos[qi] * freq, cs, sn);
+    turn[threadIdx.x] = make_float2(cs, sn);
+  }
   float M = -INFINITY;
-  for (int k = 0; k < n; ++k) M = fmaxf(M, p.part_m[slot(k) * kHeads + head]);
+  for (int k = quarter; k < n; k += 4) {
+    const float m = p.part_m[slot(k) * kHeads + head];
+    weight[k][head] = m;
+    M = fmaxf(M, m);
+  }
+  red[0][quarter][head] = M;
+  __syncthreads();
+  M = fmaxf(fmaxf(red[0][0][head], red[0][1][head]), fmaxf(red[0][2][head], red[0][3][head]));
   const bool none = M == -INFINITY;
   M = fmaxf(M, sk2);
-  float den = none ? 1.f : exp2f(sk2 - M);
+  float den = 0.f;
+  for (int k = quarter; k < n; k += 4) {
+    const float m = weight[k][head], e = m == -INFINITY ? 0.f : exp2f(m - M);
+    den += e * p.part_l[slot(k) * kHeads + head];  // 0 times NaN stays
+    weight[k][head] = e;
+  }
+  red[1][quarter][head] = den;
+  __syncthreads();
+  den = (red[1][0][head] + red[1][1][head]) + (red[1][2][head] + red[1][3][head]);
+  const bool empty = none && den == 0.f;  // no row in any part
+  if (!none) den += exp2f(sk2 - M);
+  else if (empty) den = 1.f;
+  const float inv = empty ? 0.f : 1.f / den;
+  if (d0 == 0 && p.lse != nullptr) p.lse[(int64_t)qi * kHeads + head] = empty ? sk : (M + log2f(den)) * 0.6931471805599453f;
   float o[kJoinDims];
 #pragma unroll
   for (int i = 0; i < kJoinDims; ++i) o[i] = 0.f;
-  for (int k = 0; k < n; ++k) {
-    const float m = p.part_m[slot(k) * kHeads + head];
-    const float e = m == -INFINITY ? 0.f : exp2f(m - M);
-    den += e * p.part_l[slot(k) * kHeads + head];
-    const float4* v = reinterpret_cast<const float4*>(p.part_o) + (slot(k) * (kDim / 4) + d0 / 4) * kHeads + head;
+  for (int k0 = 0; k0 < n; k0 += kJoinParts) {
+    if (k0 > 0) fetch(k0);
 #pragma unroll
-    for (int i = 0; i < kJoinDims / 4; ++i) {
-      const float4 x = v[i * kHeads];
-      o[4 * i] = fmaf(e, x.x, o[4 * i]);
-      o[4 * i + 1] = fmaf(e, x.y, o[4 * i + 1]);
-      o[4 * i + 2] = fmaf(e, x.z, o[4 * i + 2]);
-      o[4 * i + 3] = fmaf(e, x.w, o[4 * i + 3]);
+    for (int u = 0; u < kJoinParts; ++u) {
+      const float e = k0 + u < n ? weight[k0 + u][head] : 0.f;
+#pragma unroll
+      for (int i = 0; i < kJoinDims / 4; ++i) {
+        o[4 * i] = fmaf(e, v[u][i].x, o[4 * i]);
+        o[4 * i + 1] = fmaf(e, v[u][i].y, o[4 * i + 1]);
+        o[4 * i + 2] = fmaf(e, v[u][i].z, o[4 * i + 2]);
+        o[4 * i + 3] = fmaf(e, v[u][i].w, o[4 * i + 3]);
+      }
     }
   }
-  const float inv = none && den == 1.f ? 0.f : 1.f / den;
-  if (d0 == 0 && p.lse != nullptr) p.lse[(int64_t)qi * kHeads + head] = none && den == 1.f ? sk : (M + log2f(den)) * 0.6931471805599453f;
-  const int first_rope = kDim - 2 * p.rp.pairs;
   uint32_t w[kJoinDims / 2];
 #pragma unroll
   for (int i = 0; i < kJoinDims; i += 2) {
     float x0 = o[i] * inv, x1 = o[i + 1] * inv;
-    if (d0 >= first_rope) {
-      float cs, sn;
-      rope_cs(p.rp, (d0 + i - first_rope) >> 1, p.q_pos[qi], cs, sn);
-      const float y = x0 * cs + x1 * sn;
-      x1 = x1 * cs - x0 * sn;
+    if (d0 + i >= first_rope) {
+      const float2 cs = turn[(d0 + i - first_rope) >> 1];
+      const float y = x0 * cs.x + x1 * cs.y;
+      x1 = x1 * cs.x - x0 * cs.y;
       x0 = y;
     }
     w[i / 2] = pack_bf16(x0, x1);

@@ -143,4 +143,10 @@ constexpr float kRefSlack = 32.f;
 // rows so far are missing, or -inf or NaN): the first finite one exceeds it.
 constexpr float kNoRef = -1e38f;
 
+// a / b of values >= 0: 32-bit where they fit (a 64-bit division is several
+// hundred cycles, before any row is asked for)
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 }  // namespace csa2
