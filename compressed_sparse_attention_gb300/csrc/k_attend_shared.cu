@@ -792,7 +792,9 @@ __device__ __forceinline__ void issue_shared(const SharedParams& p, uint32_t bas
   bool live = true;
   // The slot whose turn it is, waited for. Its barrier was looked at while the
   // products of the slot before were issued: a look takes some 300 cycles from
-  // the instruction to the branch, longer than a slot's products run.
+  // the instruction to the branch, longer than a slot's products run. When a
+  // wait has run out (live: false) nothing is waited for any more and the
+  // products go on, on whatever lies there, so that every role comes to its end.
   uint32_t landed = 0;
   auto ready = [&]() {
     if (!uniform(landed != 0u)) live = live && wait_cluster_all_lanes(bars + 8 * (bFull + at.slot), at.phase, flags);
@@ -800,14 +802,13 @@ __device__ __forceinline__ void issue_shared(const SharedParams& p, uint32_t bas
     RingAt next = at;
     next.step(1);
     landed = done_cluster(bars + 8 * (bFull + next.slot), next.phase);
-    return live;
   };
   auto scores = [&](bool last) {
     const uint32_t d = tmem_s + 128u * (n & 1u);
 #pragma unroll 1
     for (uint32_t b = 0; b < 8; ++b, at.step(1)) {
-      if (!ready()) return;
-      const uint64_t k0 = sdesc_add(kd, at.slot * kSlotBytes);
+      ready();
+      const uint64_t k0 = sdesc_add(kd, (uint32_t)uniform((int)at.slot) * kSlotBytes);
 #pragma unroll
       for (uint32_t k = 0; k < 4; ++k) mma_pair(leader, d, sdesc_add(qd, b * 8192u + 32u * k), sdesc_add(k0, 32u * k), kIdescS, b | k);
       if (rope && b == 7) {
@@ -824,33 +825,39 @@ __device__ __forceinline__ void issue_shared(const SharedParams& p, uint32_t bas
     do {
       live = live && wait_cluster_all_lanes(bars + 8 * bQFull, seg & 1u, flags);
       tc_fence_after();
-      if (live) scores(walk.first + 1 == walk.last);
+      scores(walk.first + 1 == walk.last);
       uint32_t holds = 0;  // whose lanes of O hold a sum (bits)
 #pragma unroll 1
-      for (int t = walk.first; t < walk.last && live; ++t) {
+      for (int t = walk.first; t < walk.last; ++t) {
         if (t + 1 < walk.last) scores(t + 2 == walk.last);
+        const uint32_t formed = done_cluster(bars + 8 * bWeights, done & 1u);
         // who sees the tile's row groups, and (in the same places) whether their
         // lanes of O hold a sum already
-        uint32_t whose = 0, begun = 0;
+        uint32_t whose = 0, begun = holds != 0u ? 0x55u : 0x54u;
         const uint32_t ng = (uint32_t)uniform(row_groups(walk.u, t));
-#pragma unroll
-        for (int g = 0; g < kTileGroups; ++g) {
-          const uint32_t who = (uint32_t)row_group(walk.u, kTileGroups * t + g).who, lanes = who == 0u ? 3u : who;
-          whose |= who << (2 * g);
-          begun |= ((holds & lanes) != 0u ? 1u : 0u) << (2 * g);
-          if (g < (int)ng) holds |= lanes;
+        const bool common = uniform(kTileGroups * (t + 1) <= walk.u.n[0]);
+        if (common) {
+          holds = 3u;
+        } else {
+          begun = 0;
+#pragma unroll 1
+          for (int g = 0; g < (int)ng; ++g) {
+            const uint32_t who = (uint32_t)row_group(walk.u, kTileGroups * t + g).who, lanes = who == 0u ? 3u : who;
+            whose |= who << (2 * g);
+            begun |= ((holds & lanes) != 0u ? 1u : 0u) << (2 * g);
+            holds |= lanes;
+          }
+          whose = (uint32_t)uniform((int)whose);
         }
-        whose = (uint32_t)uniform((int)whose);
         begun = (uint32_t)uniform((int)begun);
-        live = live && wait_cluster_all_lanes(bars + 8 * bWeights, done & 1u, flags);
+        if (!uniform(formed != 0u)) live = live && wait_cluster_all_lanes(bars + 8 * bWeights, done & 1u, flags);
         if (t == walk.first && seg > 0) live = live && wait_cluster_all_lanes(bars + 8 * bOFree, (seg & 1u) ^ 1u, flags);
         tc_fence_after();
-#pragma unroll 1
-        for (uint32_t i = 0; i < 2u * ng; ++i, at.step(1)) {
-          if (!ready()) break;
-          const uint32_t g = i >> 1, who = (whose >> (2u * g)) & 3u;
-          const uint64_t v0 = sdesc_add(vd, at.slot * kSlotBytes), p0 = sdesc_add(pd, 8192u * g);
-          const uint32_t d = tmem_o + 128u * (i & 1u), keep = (begun >> (2u * g)) & 1u;
+        // the products of a slot: half j of the dims, row group g
+        auto slot_products = [&](uint32_t g, uint32_t j, uint32_t keep, uint32_t who) {
+          ready();
+          const uint64_t v0 = sdesc_add(vd, (uint32_t)uniform((int)at.slot) * kSlotBytes), p0 = sdesc_add(pd, 8192u * g);
+          const uint32_t d = tmem_o + 128u * j;
           if (who == 0u) {
 #pragma unroll
             for (uint32_t k = 0; k < 4; ++k) mma_pair(leader, d, sdesc_add(p0, 32u * k), sdesc_add(v0, 2048u * k), kIdescO, k | keep);
@@ -861,12 +868,23 @@ __device__ __forceinline__ void issue_shared(const SharedParams& p, uint32_t bas
                              who == 1u ? ~0u : 0u);
           }
           commit_pair(leader, bars + 8 * (bEmpty + at.slot));
+          at.step(1);
+        };
+        if (common) {
+#pragma unroll 1
+          for (uint32_t g = 0; g < (uint32_t)kTileGroups; ++g) {
+            slot_products(g, 0, g != 0u || begun == 0x55u ? 1u : 0u, 0u);
+            slot_products(g, 1, g != 0u || begun == 0x55u ? 1u : 0u, 0u);
+          }
+        } else {
+#pragma unroll 1
+          for (uint32_t i = 0; i < 2u * ng; ++i) slot_products(i >> 1, i & 1u, (begun >> (i & ~1u)) & 1u, (whose >> (i & ~1u)) & 3u);
         }
-        if (live) commit_pair(leader, bars + 8 * bPFree);
+        commit_pair(leader, bars + 8 * bPFree);
         ++done;
       }
       ++seg;
-    } while (walk.next(p) && live);
+    } while (walk.next(p));
   }
   if (!live) {  // products still in flight land before tensor memory is freed
     commit_pair(leader, bars + 8 * bDrained);

@@ -2,6 +2,8 @@
 // warp-uniform issue of barrier, TMA and tensor-core instructions, prefetches,
 // and the conversion of fp8 and fp4 rows to bf16.
 #pragma once
+#include <cuda.h>
+
 #include "common.cuh"
 
 namespace csa2 {
