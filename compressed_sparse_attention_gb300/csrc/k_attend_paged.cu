@@ -1188,13 +1188,12 @@ cudaError_t encode_bf16_map(CUtensorMap* map, int rank, const void* base, const 
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
     looked_up.store(encode, std::memory_order_release);
   }
-  const uint32_t ones[3] = {1u, 1u, 1u};
-  cuuint64_t d[3], st[2];
-  cuuint32_t bx[3], es[3];
+  cuuint64_t d[4], st[3];
+  cuuint32_t bx[4], es[4];
   for (int i = 0; i < rank; ++i) {
     d[i] = dims[i];
     bx[i] = box[i];
-    es[i] = ones[i];
+    es[i] = 1u;
     if (i + 1 < rank) st[i] = strides[i];
   }
   auto fill = [&] {

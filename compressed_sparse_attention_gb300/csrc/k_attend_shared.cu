@@ -68,6 +68,7 @@ struct SharedRun {
 struct SharedParams {
   CUtensorMap q_map;   // Q: [64 n_query heads][512], boxes of 64 heads x 64 channels
   CUtensorMap kv_map;  // bf16 pages: [n_pages][page_size][512], boxes of one piece x 64 channels
+  CUtensorMap v_map;   // the same as [n_pages][8 blocks][page_size][64], boxes of two blocks of 64 rows (pages of 64 rows and more)
   const uint16_t* q;
   const int64_t* q_pos;
   const int32_t* seq_of_q;
@@ -413,6 +414,14 @@ __device__ __forceinline__ void tma_pair_3d(uint32_t leader, uint32_t dst, const
       "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(leader)
       : "memory");
 }
+__device__ __forceinline__ void tma_pair_4d(uint32_t leader, uint32_t dst, const CUtensorMap* map, int x, int y, int z, int w,
+                                            uint32_t bar) {
+  asm volatile(
+      "{\n.reg .pred e;\nsetp.ne.u32 e, %7, 0;\n"
+      "@e cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];\n}" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar), "r"(leader)
+      : "memory");
+}
 __device__ __forceinline__ void mma_pair(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n.reg .pred p, e;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 e, %5, 0;\n"
@@ -693,9 +702,7 @@ __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm,
       }
       expect_cluster_one(leader, bar, kSlotBytes);
       if (pieces == 1) {
-        const int page = uniform(src.page, 8 * g), row = uniform(src.row, 8 * g);
-        tma_pair_3d(leader, dst, &p.kv_map, d0, row, page, bar);
-        tma_pair_3d(leader, dst + 8192u, &p.kv_map, d0 + 64, row, page, bar);
+        tma_pair_4d(leader, dst, &p.v_map, 0, uniform(src.row, 8 * g), d0 / 64, uniform(src.page, 8 * g), bar);
       } else {
 #pragma unroll 1
         for (int k = 0; k < pieces; ++k) {
@@ -1297,6 +1304,12 @@ cudaError_t launch_attend_shared(cudaStream_t st, int num_sms, int kv_fmt, const
   const uint32_t kv_box[3] = {64u, (uint32_t)piece, 1u};
   cudaError_t e = encode_bf16_map(&p.q_map, 2, a.q, q_dims, q_strides, q_box);
   if (e == cudaSuccess && kv_fmt == 0) e = encode_bf16_map(&p.kv_map, 3, kv.pages, kv_dims, kv_strides, kv_box);
+  if (e == cudaSuccess && kv_fmt == 0 && piece == kGroupRows) {
+    const uint64_t v_dims[4] = {64u, 1ull << kv.page_shift, (uint64_t)kDim / 64, (uint64_t)kv.n_pages};
+    const uint64_t v_strides[3] = {2u * kDim, 128u, (uint64_t)kv.page_stride};
+    const uint32_t v_box[4] = {64u, (uint32_t)kGroupRows, 2u, 1u};
+    e = encode_bf16_map(&p.v_map, 4, kv.pages, v_dims, v_strides, v_box);
+  }
   if (e != cudaSuccess) return e;
   e = launch_ex(attend_shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, true, 0, p);
   if (e != cudaSuccess) return e;
