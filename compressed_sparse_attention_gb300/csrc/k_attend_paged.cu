@@ -317,12 +317,6 @@ __device__ __forceinline__ RowAt row_at(const PagedAttendParams& p, const Cursor
   return a;
 }
 
-// 16 zero bytes into shared memory if hit != 0, without a branch
-__device__ __forceinline__ void zero16_if(uint32_t hit, uint32_t dst) {
-  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %0, 0;\n@p st.shared.v4.u32 [%1], {%2, %2, %2, %2};\n}" ::"r"(hit), "r"(dst), "r"(0u)
-               : "memory");
-}
-
 // bf16 producers. Thread t finds row t of a tile one tile ahead and the first
 // row of each chunk asks for the chunk in L2: shared memory holds one tile, so
 // that the memory would idle between a tile's last block and its first PV;

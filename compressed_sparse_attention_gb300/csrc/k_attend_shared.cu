@@ -42,7 +42,7 @@ constexpr int kGroupRows = 64;   // aligned positions of a row group
 constexpr int kTileGroups = 4;   // row groups of a tile
 constexpr int kRing = 7;         // slots
 constexpr uint32_t kSlotBytes = 16384;
-constexpr int kMaxPairs2 = 128;  // pairs of CTAs, at most
+constexpr int kMaxPairs2 = 80;   // pairs of CTAs, at most
 constexpr int kPlanThreads = 1024;
 
 // Two places of a group (or its last one alone).
@@ -56,13 +56,21 @@ struct alignas(16) SharedUnit {
   int32_t n[3];       // row groups: common, the first query's own, the second's
   int32_t tiles;
   int32_t pad[3];
+  int64_t t[2];       // the queries' positions
 };
-static_assert(sizeof(SharedUnit) == 64, "SharedUnit");
+static_assert(sizeof(SharedUnit) == 80, "SharedUnit");
 
-struct SharedRun {
+struct alignas(16) SharedRun {
   int64_t tile;    // number of its first tile among all
   int32_t unit;    // its unit
   int32_t first;   // number of that tile in its unit
+};
+// What a pair of CTAs starts from: its run, the number of its tiles and its
+// first unit, in one place (each step through memory is 0.6 us of a short call).
+struct alignas(16) SharedStart {
+  int64_t tiles;
+  int32_t unit, first;
+  SharedUnit u;
 };
 
 struct SharedParams {
@@ -85,11 +93,10 @@ struct SharedParams {
   int n_query;
   int pairs;  // of CTAs
   SharedUnit* units;
-  SharedRun* runs;   // [pairs + 1]
+  SharedStart* starts;  // [pairs]
   int4* joins;       // [pairs]: of a unit that run c begins and does not end its queries, c and its last run; third -1: none
   float* part_o;     // [2 pairs slots][2][512 / 4][64 heads][4]
-  float* part_m;     // [2 pairs slots][2][64]
-  float* part_l;
+  float2* part_ml;   // [2 pairs slots][2][64]: reference and sum
 };
 
 // Slots of the partials: run c leaves at most two, as in csa2_attend_paged.
@@ -105,7 +112,7 @@ __host__ __device__ __forceinline__ int piece_shift(int page_shift) { return pag
 // equal cost, one a pair of CTAs. A thread takes a share of the places and, when
 // a scan has placed its units, finds the cuts that fall into them.
 // ---------------------------------------------------------------------------
-constexpr int kTileCost2 = 4, kUnitCost = 3;  // a unit: its Q, its outputs
+constexpr int kTileCost2 = 4, kUnitCost = 8;  // a unit: its Q, its first weights, its outputs
 
 namespace {
 struct PlanUnit {
@@ -142,9 +149,11 @@ __device__ __forceinline__ PlanUnit unit_at(const SharedParams& p, int k, uint32
   for (int x = 0; x < 2; ++x) {
     u.seq[x] = -1;
     u.end[x] = 0;
+    u.t[x] = 0;
     if (u.q[x] < 0) continue;
     const int b = p.seq_of_q[u.q[x]];
     const int64_t t = p.q_pos[u.q[x]];
+    u.t[x] = t;
     if (b == -1) {
       u.q[x] = -1;  // a padding query
       continue;
@@ -181,8 +190,12 @@ __device__ __forceinline__ PlanUnit unit_at(const SharedParams& p, int k, uint32
 __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(const __grid_constant__ SharedParams p) {
   __shared__ int64_t sum_t[32], share_t[kPlanThreads];  // tiles, units before a thread's share
   __shared__ int sum_u[32], share_u[kPlanThreads];
+  __shared__ int share_n[kPlanThreads];   // a share of one unit: its tiles
+  __shared__ int2 share_q[kPlanThreads];  // and queries
   __shared__ SharedRun runs[kMaxPairs2 + 1];
-  __shared__ uint32_t on[kMaxPairs2 / 32];
+  __shared__ int run_share[kMaxPairs2];
+  constexpr int kWords = (kMaxPairs2 + 31) / 32;
+  __shared__ uint32_t on[kWords];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
   pdl_wait();
@@ -227,6 +240,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(con
   const int bu = __shfl_sync(0xffffffffu, au, max(warp, 1) - 1);
   share_t[tid] = it - tiles + (warp > 0 ? bt : 0);
   share_u[tid] = iu - units + (warp > 0 ? bu : 0);
+  if (per == 1 && one.begins) {
+    share_n[tid] = one.u.tiles;
+    share_q[tid] = make_int2(one.u.q[0], one.u.q[1]);
+  }
   int u0 = share_u[tid];
   for (int k = lo; k < hi; ++k) {
     if (per > 1) one = unit_at(p, k, unused);
@@ -234,9 +251,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(con
   }
   __syncthreads();
   // On a line where a tile is kTileCost2 long and a unit starts with kUnitCost,
-  // run c has the tiles that start in the c-th of R equal parts (none of them
-  // empty: a part is longer than a unit's start and a tile). Thread c finds the
-  // first tile from the c-th cut on.
+  // run c has the tiles that start in the c-th of R equal parts (a part inside a
+  // unit's start has none). Thread c finds the first tile from the c-th cut on.
   const int start = T > 2 * (int64_t)p.pairs ? kUnitCost : 0;
   const int64_t cost = kTileCost2 * T + (int64_t)start * U;
   const int R = (int)min((int64_t)p.pairs, T);
@@ -253,7 +269,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(con
       int64_t t = share_t[i];
       int u = share_u[i];
       for (;; ++u) {
-        const int n = p.units[u].tiles;
+        const int n = per == 1 ? share_n[i] : p.units[u].tiles;
         const int64_t left = y - R * (kTileCost2 * t + (int64_t)start * (u + 1)), step = (int64_t)kTileCost2 * R;
         const int64_t j = left <= 0 ? 0 : quotient(left + step - 1, step);
         if (j < n) {
@@ -262,15 +278,19 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(con
         }
         t += n;
         if (u + 1 == U) break;  // (a cut behind the last tile's start)
+        if (per == 1) {  // the share of the next unit
+          do ++i;
+          while (share_u[i] != u + 1 || (i + 1 < kPlanThreads && share_u[i + 1] == u + 1));
+        }
       }
+      run_share[tid] = i;
     }
     runs[tid] = r;
-    p.runs[tid] = r;
   }
   __syncthreads();
   // a unit that begins in run c and goes on: its last run is the one behind
   // those that it fills from end to end
-  if (tid < kMaxPairs2) {
+  if (warp < kWords) {
     const bool through = tid < R && runs[tid + 1].first > 0 && runs[tid + 1].unit == runs[tid].unit;
     const uint32_t w = __ballot_sync(0xffffffffu, through);
     if (lane == 0) on[warp] = w;
@@ -280,7 +300,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(con
     int4 jn = make_int4(-1, -1, -1, 0);
     if (tid < R && runs[tid + 1].first > 0 && (runs[tid].unit < runs[tid + 1].unit || runs[tid].first == 0)) {
       int c = tid + 1;
-      while (c < kMaxPairs2) {
+      while (c < 32 * kWords) {
         const uint32_t off = ~on[c >> 5] >> (c & 31);
         if (off != 0u) {
           c += __ffs((int)off) - 1;
@@ -288,10 +308,19 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(con
         }
         c = (c | 31) + 1;
       }
-      const SharedUnit& u = p.units[runs[tid + 1].unit];
-      jn = make_int4(u.q[0], u.q[1], tid, c);
+      const int2 q = per == 1 ? share_q[run_share[tid + 1]] : *reinterpret_cast<const int2*>(p.units[runs[tid + 1].unit].q);
+      jn = make_int4(q.x, q.y, tid, c);
     }
     p.joins[tid] = jn;
+  }
+  // (four starts a warp)
+  const int first_c = warp * 4;
+  for (int c = first_c; c < min(p.pairs, first_c + 4); ++c) {
+    const SharedRun r = runs[c];
+    const int64_t n = runs[c + 1].tile - r.tile;
+    int4* dst = reinterpret_cast<int4*>(p.starts + c);
+    if (lane == 0) dst[0] = make_int4((int)(uint32_t)n, (int)(n >> 32), r.unit, r.first);
+    if (lane < 5 && n > 0) dst[1 + lane] = reinterpret_cast<const int4*>(p.units + r.unit)[lane];
   }
 }
 
@@ -299,7 +328,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(con
 // The tile kernel. Roles of a CTA's warps:
 //   0 .. 7   math: softmax, outputs
 //   8 ..     producers: a slot of the ring each in turn
-//   then 2   Q, its rope channels rotated
+//   then 1 or 2  Q, its rope channels rotated
 //   last     issues the pair's products (in CTA 0 of the pair)
 // Waits are bounded; barriers that the issuer waits for lie in CTA 0, to which
 // CTA 1 arrives over the cluster, and the issuer's commits arrive in both.
@@ -307,17 +336,19 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(con
 namespace {
 
 constexpr int kMathWarps = 8;
-constexpr int kQWarps = 2;
+// 15 or 16 warps: four on a scheduler, each with up to 128 registers (with a
+// seventeenth they would have 96, and the conversion of fp8 rows spill 900 bytes).
+// A warp's slots come kProducers apart, no more than the ring's: its next
+// slot but one of the ring must come after slots that it has waited for, or its
+// wait could take the parity of the use before the last.
 template <bool TMA>
 struct SharedRoles {
-  // warps that copy or convert rows themselves are one a slot. (No more: a warp's
-  // next slot but one of the ring must come after slots that it has waited for,
-  // or its wait could take the parity of the use before the last.)
-  static constexpr int kProducers = TMA ? 4 : kRing;
-  static_assert(kProducers <= kRing);
+  static constexpr int kProducers = TMA ? 4 : 6;  // threads copy, or convert, with more warps
+  static constexpr int kQWarps = TMA ? 2 : 1;
   static constexpr int kQ = kMathWarps + kProducers;
   static constexpr int kIssuer = kQ + kQWarps;
   static constexpr int kThreads = 32 * (kIssuer + 1);
+  static_assert(kProducers <= kRing && kThreads <= 512);
 };
 
 constexpr uint32_t S_Q = 0;                           // [9 blocks][64 heads][128 B]; block 8: rope residual
@@ -331,7 +362,7 @@ constexpr uint32_t S_MISC = S_QROPE + 256;
 constexpr uint32_t kSharedSmemBytes = S_MISC + 64 + 1024;
 static_assert(kSharedSmemBytes <= 232448, "shared memory");
 
-enum SBar : uint32_t { bFull = 0, bEmpty = 7, bQFull = 14, bQEmpty = 15, bScores = 16, bWeights = 18, bPFree = 19, bOFree = 20, bDrained = 21, kSBars = 22 };
+enum SBar : uint32_t { bFull = 0, bEmpty = 7, bQFull = 14, bQEmpty = 15, bScores = 16, bWeights = 18, bPFree = 19, bOFree = 20, bDrained = 21, bEdge = 22, kSBars = 26 };
 
 constexpr uint32_t kIdescS = idesc_bf16(128, 256, 0, 0);
 constexpr uint32_t kIdescO = idesc_bf16(128, 256, 0, 1);
@@ -502,7 +533,10 @@ __device__ __forceinline__ SharedUnit load_unit(const SharedUnit* at) {
   u.n[0] = c.y;
   u.n[1] = c.z;
   u.n[2] = c.w;
-  u.tiles = reinterpret_cast<const int32_t*>(at)[12];
+  u.tiles = v[3].x;
+  const int4 t = v[4];
+  u.t[0] = (int64_t)(uint32_t)t.x | (int64_t)t.y << 32;
+  u.t[1] = (int64_t)(uint32_t)t.z | (int64_t)t.w << 32;
   return u;
 }
 
@@ -512,14 +546,15 @@ struct SharedWalk {
   int unit, first, last;
   bool begins, ends;
   SharedUnit u;
-  __device__ __forceinline__ void start(const SharedParams& p, const SharedRun& r, int64_t tiles) {
-    left = tiles;
-    unit = uniform(r.unit);
-    first = uniform(r.first);
-    if (left > 0) load(p);
+  __device__ __forceinline__ void start(const SharedStart* at) {
+    const int4 a = *reinterpret_cast<const int4*>(at);
+    left = (int64_t)(uint32_t)a.x | (int64_t)a.y << 32;
+    unit = uniform(a.z);
+    first = uniform(a.w);
+    if (left > 0) load(&at->u);
   }
-  __device__ __forceinline__ void load(const SharedParams& p) {
-    u = load_unit(p.units + unit);
+  __device__ __forceinline__ void load(const SharedUnit* at) {
+    u = load_unit(at);
     begins = uniform(first == 0);
     last = uniform((int)min((int64_t)u.tiles, first + left));
     ends = uniform(last == u.tiles);
@@ -528,7 +563,7 @@ struct SharedWalk {
     left -= last - first;
     ++unit;
     first = 0;
-    if (left > 0) load(p);
+    if (left > 0) load(p.units + unit);
     return left > 0;
   }
 };
@@ -613,6 +648,90 @@ __device__ __forceinline__ void fill_slot(const SharedParams& p, const SharedUni
   fence_proxy_async_smem();
 }
 
+// What a tile's producers know of it: the number of its row groups; of lane
+// 8 g + i the page of piece i of group g (the pool's size: none) and the row of
+// it where the piece begins; and which groups lie whole in it (bits 8 g).
+struct TileSource {
+  int n;
+  int32_t page, row;
+  uint32_t whole;
+};
+
+// A slot of fp8 or fp4 rows (pages of eight rows and more), converted. A lane has 16
+// chunks of 16 channels; four of them are under way while four others are
+// converted, the first eight from before the wait for the slot on. The stores and
+// the conversions (72 cycles a warp and chunk) bound it.
+template <int KVF, bool IS_K>
+struct CodeSlot {
+  static constexpr int kRowBytes = KVF == 1 ? 512 : 256, kScaleBytes = KVF == 1 ? 16 : 32;
+  static constexpr int kChunks = IS_K ? 4 : 8;          // of a row
+  static constexpr int kStep = 32 / kChunks;            // rows of a load
+  static constexpr int kBatch = 4;
+  using Code = typename std::conditional<KVF == 1, uint4, uint2>::type;
+  Code code[2][kBatch];
+  uint8_t scale[2][kBatch];
+  int row0, c, ch;
+  int from[2], to[2];  // rows of the slot's groups that are theirs
+  int in_page[2];      // place of a group's first row in its page
+  __device__ __forceinline__ void start(const SharedParams& p, const SharedUnit& u, const TileSource& src, int tile, int g0, int d0, int lane) {
+    row0 = lane / kChunks;
+    c = lane % kChunks;
+    ch = d0 + 16 * c;
+#pragma unroll
+    for (int k = 0; k < (IS_K ? 2 : 1); ++k) {
+      const RowGroup g = row_group(u, kTileGroups * tile + g0 + k);
+      from[k] = g.present ? g.from - 64 * g.block : 64;
+      to[k] = g.present ? g.to - 64 * g.block : 0;
+      in_page[k] = (64 * g.block) & ((1 << p.kv.page_shift) - 1);
+    }
+    load(p, src, g0, 0, 0);
+    load(p, src, g0, 1, 1);
+  }
+  __device__ __forceinline__ void load(const SharedParams& p, const TileSource& src, int g0, int batch, int into) {
+    const int pc = piece_shift(p.kv.page_shift), page_mask = (1 << p.kv.page_shift) - 1;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int first = (batch * kBatch + i) * kStep, k = IS_K ? first >> 6 : 0;  // the load's first row, its group
+      const int r = (first & 63) + row0;
+      const int page = uniform(src.page, 8 * (g0 + k) + ((first & 63) >> pc));
+      const int at = (in_page[IS_K ? k : 0] + r) & page_mask;
+      const bool there = page < p.kv.n_pages && r >= from[IS_K ? k : 0] && r < to[IS_K ? k : 0];
+      const uint8_t* codes = p.kv.pages + page * p.kv.page_stride + (int64_t)at * kRowBytes;
+      const uint8_t* sc = p.kv.scales + page * p.kv.scale_stride + (int64_t)at * kScaleBytes;
+      if constexpr (KVF == 1) {
+        code[into][i] = there ? ldg_stream16(codes + ch) : make_uint4(0u, 0u, 0u, 0u);
+        scale[into][i] = there ? __ldg(sc + ch / 32) : 0;
+      } else {
+        code[into][i] = there ? ldg_stream8(codes + ch / 2) : make_uint2(0u, 0u);
+        scale[into][i] = there ? __ldg(sc + ch / 16) : 0;
+      }
+    }
+  }
+  __device__ __forceinline__ void store(int batch, int from_set, uint8_t* dst) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = (batch * kBatch + i) * kStep + row0;
+      uint32_t o[8];
+      if constexpr (KVF == 1) fp8_to_bf16(code[from_set][i], scale[from_set][i], o);
+      else fp4_to_bf16(code[from_set][i].x, code[from_set][i].y, scale[from_set][i], o);
+      uint8_t* at = dst + (uint32_t)(c >> 2) * 8192u + (uint32_t)r * 128u;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        *reinterpret_cast<uint4*>(at + (((2 * (c & 3) + k) ^ (r & 7)) << 4)) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+    }
+  }
+  __device__ __forceinline__ void finish(const SharedParams& p, const TileSource& src, int g0, uint8_t* dst) {
+#pragma unroll 1
+    for (int b = 0; b < 4; b += 2) {
+      store(b, 0, dst);
+      if (b == 0) load(p, src, g0, 2, 0);
+      store(b + 1, 1, dst);
+      if (b == 0) load(p, src, g0, 3, 1);
+    }
+    fence_proxy_async_smem();
+  }
+};
+
 // Producer warp w of a CTA: every kProducers-th slot of the ring. What a tile's
 // copies need is found once a tile, before the waits for its slots: with the look-up
 // behind them the warps took 1,300 cycles to issue a slot's two copies.
@@ -625,53 +744,62 @@ __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm,
   const int ps = p.kv.page_shift, pc = piece_shift(ps);
   const int pieces = kGroupRows >> pc;
   RingAt base{0, 0};  // the next slot of all warps, and the slots before it
-  uint32_t s = 0;
+  uint32_t s = 0, edges = 0;
   bool live = true;
-  // Of a tile: the number of its row groups; of lane 8 g + i piece i of group
-  // g, its page and the row in it; and which groups lie whole in it (bits 8 g).
-  struct Source {
-    int n;
-    int32_t page, row;
-    uint32_t whole;
-  };
+  const bool pieced = pc >= 3;  // a tile's pages fit the warp's lanes
   auto look_up = [&](int tile) {
     const SharedUnit& u = walk.u;
-    Source src;
+    TileSource src;
     src.n = uniform(row_groups(u, tile));
     src.page = p.kv.n_pages;  // past the end: zeros
     src.row = 0;
     src.whole = 0;
-    if (!TMA) return src;
+    if (!pieced) return src;
     const RowGroup g = row_group(u, kTileGroups * tile + (lane >> 3));
     const int pos = 64 * g.block + ((lane & 7) << pc);
     if ((lane & 7) < pieces && g.present && pos < g.to && pos + (1 << pc) > g.from) {
       const int32_t page = page_of(p.kv, max(pos, g.from) < u.len ? u.head_seq : g.seq, pos);
-      if (page >= 0) src.page = page;
+      if (page >= 0) {
+        src.page = page;
+        // (codes on their way to the L2, half of the tile's rows by either CTA)
+        if (KVF != 0 && w == 0 && (lane >> 4) == rank) {
+          constexpr uint32_t kRow = KVF == 1 ? 512u : 256u, kScale = KVF == 1 ? 16u : 32u;
+          const int64_t at = pos & ((1 << ps) - 1);
+          prefetch_l2(p.kv.pages + page * p.kv.page_stride + at * kRow, kRow << pc);
+          prefetch_l2(p.kv.scales + page * p.kv.scale_stride + at * kScale, kScale << pc);
+        }
+      }
     }
     src.row = pos & ((1 << ps) - 1);
     src.whole = __ballot_sync(0xffffffffu, (lane & 7) == 0 && g.present && g.from <= 64 * g.block && g.to >= 64 * g.block + 64);
     return src;
   };
-  // this warp's slots of the next `count`: fill(i, its place)
-  auto each = [&](uint32_t count, auto&& fill) {
+  // this warp's slots of the next `count`: ask(i), then fill(i, its place)
+  auto each = [&](uint32_t count, auto&& ask, auto&& fill) {
 #pragma unroll 1
     for (uint32_t i = (w + NP - s % NP) % NP; i < count; i += NP) {
       RingAt at = base;
       at.step(i);
+      ask((int)i);
       if (s + i >= (uint32_t)kRing) live = live && wait_all_lanes(bars + 8 * (bEmpty + at.slot), at.phase ^ 1u, p.flags);
       if (live) fill((int)i, full0 + 8 * at.slot, at.slot * kSlotBytes + S_RING);
     }
     base.step(count);
     s += count;
   };
-  auto keys = [&](int tile, const Source& src) {
+  auto keys = [&](int tile, const TileSource& src) {
     const int n = min(2, max(0, src.n - 2 * rank));  // row groups of this CTA's half
     const int page0 = uniform(src.page, 16 * rank), page1 = uniform(src.page, 16 * rank + 8);
     const int row0 = uniform(src.row, 16 * rank), row1 = uniform(src.row, 16 * rank + 8);
-    each(8, [&](int b, uint32_t bar, uint32_t slot) {
+    CodeSlot<KVF, true> codes;
+    auto ask = [&](int b) {
+      if (KVF != 0 && pieced && n > 0) codes.start(p, walk.u, src, tile, 2 * rank, 64 * b, lane);
+    };
+    each(8, ask, [&](int b, uint32_t bar, uint32_t slot) {
       const uint32_t dst = base_s + slot;
       if (!TMA) {
-        if (n > 0) fill_slot<KVF, true>(p, walk.u, tile, 2 * rank, 64 * b, dst, sm + slot, lane);
+        if (KVF != 0 && pieced && n > 0) codes.finish(p, src, 2 * rank, sm + slot);
+        else if (n > 0) fill_slot<KVF, true>(p, walk.u, tile, 2 * rank, 64 * b, dst, sm + slot, lane);
         warp_arrive_cluster(bar);
         return;
       }
@@ -690,13 +818,48 @@ __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm,
       }
     });
   };
-  auto values = [&](int tile, const Source& src) {
-    each(2 * (uint32_t)src.n, [&](int i, uint32_t bar, uint32_t slot) {
+  auto values = [&](int tile, const TileSource& src) {
+    CodeSlot<KVF, false> codes;
+    auto ask = [&](int i) {
+      if (KVF != 0 && pieced) codes.start(p, walk.u, src, tile, i >> 1, 256 * (i & 1) + 128 * rank, lane);
+    };
+    each(2 * (uint32_t)src.n, ask, [&](int i, uint32_t bar, uint32_t slot) {
       const int g = i >> 1, d0 = 256 * (i & 1) + 128 * rank;
       const uint32_t dst = base_s + slot;
-      // (a group's end inside a page: rows behind it hold anything)
-      if (!TMA || ((src.whole >> (8 * g)) & 1u) == 0u) {
-        fill_slot<KVF, false>(p, walk.u, tile, g, d0, dst, sm + slot, lane);
+      if (!TMA) {
+        if (KVF != 0 && pieced) codes.finish(p, src, g, sm + slot);
+        else fill_slot<KVF, false>(p, walk.u, tile, g, d0, dst, sm + slot, lane);
+        warp_arrive_cluster(bar);
+        return;
+      }
+      if (((src.whole >> (8 * g)) & 1u) == 0u) {
+        // A group that ends inside its 64 positions: the rows behind it hold
+        // anything, and are cleared once they have landed (their weights are 0, but
+        // 0 times a NaN is not). Copied by the warp itself such a slot took it
+        // 2 us, and the ring with it.
+        const RowGroup rg = row_group(walk.u, kTileGroups * tile + g);
+        const uint32_t here = bars + 8 * (bEdge + (uint32_t)w);
+        expect_one(leader, here, kSlotBytes);
+        if (pieces == 1) {
+          const int page = uniform(src.page, 8 * g), row = uniform(src.row, 8 * g);
+          tma_3d_one(leader, dst, &p.kv_map, d0, row, page, here);
+          tma_3d_one(leader, dst + 8192u, &p.kv_map, d0 + 64, row, page, here);
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < pieces; ++k) {
+            const int page = uniform(src.page, 8 * g + k);
+            tma_3d_one(leader, dst + ((uint32_t)k << (7 + pc)), &p.kv_map, d0, 0, page, here);
+            tma_3d_one(leader, dst + 8192u + ((uint32_t)k << (7 + pc)), &p.kv_map, d0 + 64, 0, page, here);
+          }
+        }
+        live = live && wait_all_lanes(here, edges & 1u, p.flags);
+        ++edges;
+        // lanes 0 .. 15 a row's 256 bytes, lanes 16 .. 31 the next one's
+        const uint32_t chunk = dst + 8192u * ((lane >> 3) & 1) + 16u * (lane & 7);
+        const int from = rg.from - 64 * rg.block, to = rg.to - 64 * rg.block;
+#pragma unroll 4
+        for (int r = lane >> 4; r < kGroupRows; r += 2) zero16_if(r < from || r >= to ? 1u : 0u, chunk + 128u * (uint32_t)r);
+        fence_proxy_async_smem();
         warp_arrive_cluster(bar);
         return;
       }
@@ -715,11 +878,11 @@ __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm,
   };
   if (walk.left <= 0) return;
   do {
-    Source now = look_up(walk.first);
+    TileSource now = look_up(walk.first);
     keys(walk.first, now);
 #pragma unroll 1
     for (int t = walk.first; t < walk.last; ++t) {
-      Source ahead = now;
+      TileSource ahead = now;
       if (t + 1 < walk.last) {
         ahead = look_up(t + 1);
         keys(t + 1, ahead);
@@ -731,7 +894,8 @@ __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm,
 }
 
 // Q of this CTA's query: plain blocks by TMA, the rope block rotated and split
-// into bf16 hi + lo by the 64 threads (see csa2_attend_paged).
+// into bf16 hi + lo by the role's threads (see csa2_attend_paged).
+template <int WARPS>
 __device__ __forceinline__ void q_role(const SharedParams& p, uint8_t* sm, uint32_t base_s, SharedWalk walk, int t, int rank) {
   const uint32_t bars = base_s + S_BAR, bar = in_leader(bars + 8 * bQFull);
   const uint32_t leader = elect_one();
@@ -742,6 +906,7 @@ __device__ __forceinline__ void q_role(const SharedParams& p, uint8_t* sm, uint3
   uint32_t seg = 0;
   do {
     const int qi = uniform(rank == 0 ? walk.u.q[0] : walk.u.q[1]);
+    const int64_t t_q = rank == 0 ? walk.u.t[0] : walk.u.t[1];
     // (a wait that ran out is recorded; the barriers below are met all the same)
     if (seg > 0) live = live && wait_all_lanes(bars + 8 * bQEmpty, (seg & 1u) ^ 1u, p.flags);
     if (t < 32 && live) {
@@ -751,34 +916,40 @@ __device__ __forceinline__ void q_role(const SharedParams& p, uint8_t* sm, uint3
       for (int b = 0; b < plain; ++b) tma_pair_2d(leader, base_s + S_Q + 8192u * (uint32_t)b, &p.q_map, 64 * b, kHeads * qi, bar);
     }
     if (rope && qi >= 0) {
-      // thread: chunk 56 + (t & 7) of heads t >> 3, + 8, ...: always the same four pairs
-      uint4 v[8];
-      const uint16_t* q = p.q + (int64_t)qi * kHeads * kDim + 8 * (56 + (t & 7));
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4*>(q + (int64_t)((t >> 3) + 8 * i) * kDim);
+      // thread: chunk 56 + (t & 7) of every 4 WARPS-th head: always the same four pairs
+      constexpr int kStep = 4 * WARPS;
       float2* table = reinterpret_cast<float2*>(sm + S_QROPE);
-      asm volatile("bar.sync 3, 64;" ::: "memory");  // the last query's table has been read
-      if (t < 32) {
-        float cs, sn;
-        angle_cs((double)max(p.q_pos[qi], (int64_t)0) * freq, cs, sn);
-        table[t] = make_float2(cs, sn);
-      }
-      asm volatile("bar.sync 3, 64;" ::: "memory");
+      const uint16_t* q = p.q + (int64_t)qi * kHeads * kDim + 8 * (56 + (t & 7));
+#pragma unroll 1
+      for (int h0 = t >> 3; h0 < kHeads; h0 += 8 * kStep) {
+        uint4 v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int h = (t >> 3) + 8 * i;
-        uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, lo[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 cs = table[4 * (t & 7) + k];
-          const float x0 = bf16lo(w[k]), x1 = bf16hi(w[k]);
-          const float y0 = x0 * cs.x - x1 * cs.y, y1 = x0 * cs.y + x1 * cs.x;
-          w[k] = pack_bf16(y0, y1);
-          lo[k] = pack_bf16(y0 - bf16lo(w[k]), y1 - bf16hi(w[k]));
+        for (int i = 0; i < 8; ++i) v[i] = *reinterpret_cast<const uint4*>(q + (int64_t)(h0 + kStep * i) * kDim);
+        if (h0 < kStep) {
+          asm volatile("bar.sync 3, %0;" ::"n"(32 * WARPS) : "memory");  // the last query's table has been read
+          if (t < 32) {
+            float cs, sn;
+            angle_cs((double)max(t_q, (int64_t)0) * freq, cs, sn);
+            table[t] = make_float2(cs, sn);
+          }
+          asm volatile("bar.sync 3, %0;" ::"n"(32 * WARPS) : "memory");
         }
-        const uint32_t off = (uint32_t)h * 128u + ((uint32_t)((t & 7) ^ (h & 7)) << 4);
-        *reinterpret_cast<uint4*>(sm + S_Q + 7u * 8192u + off) = make_uint4(w[0], w[1], w[2], w[3]);
-        *reinterpret_cast<uint4*>(sm + S_Q + 8u * 8192u + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int h = h0 + kStep * i;
+          uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, lo[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 cs = table[4 * (t & 7) + k];
+            const float x0 = bf16lo(w[k]), x1 = bf16hi(w[k]);
+            const float y0 = x0 * cs.x - x1 * cs.y, y1 = x0 * cs.y + x1 * cs.x;
+            w[k] = pack_bf16(y0, y1);
+            lo[k] = pack_bf16(y0 - bf16lo(w[k]), y1 - bf16hi(w[k]));
+          }
+          const uint32_t off = (uint32_t)h * 128u + ((uint32_t)((t & 7) ^ (h & 7)) << 4);
+          *reinterpret_cast<uint4*>(sm + S_Q + 7u * 8192u + off) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(sm + S_Q + 8u * 8192u + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
       }
       fence_proxy_async_smem();
     }
@@ -930,7 +1101,7 @@ __device__ __forceinline__ void math_shared(const SharedParams& p, uint8_t* sm, 
   do {
     const SharedUnit& u = walk.u;
     const int qi = rank == 0 ? u.q[0] : u.q[1];
-    const int64_t t_q = qi >= 0 ? p.q_pos[qi] : 0;
+    const int64_t t_q = rank == 0 ? u.t[0] : u.t[1];
     if (upper + cols == 0 && lane < p.rp.pairs) {
       float cs, sn;
       rope_cs(p.rp, lane, max(t_q, (int64_t)0), cs, sn);
@@ -1080,11 +1251,10 @@ __device__ __forceinline__ void math_shared(const SharedParams& p, uint8_t* sm, 
     } else {
       const int64_t slot = shared_slot(c, walk.begins, rank);
       if (group == 0) {
-        p.part_m[slot * kHeads + head] = none ? -INFINITY : m_run;
-        p.part_l[slot * kHeads + head] = l;
+        p.part_ml[slot * kHeads + head] = make_float2(m_run, l);
       }
       float4* po = reinterpret_cast<float4*>(p.part_o) + slot * (kDim / 4) * kHeads;
-#pragma unroll 1
+#pragma unroll 2
       for (int i = 0; i < 4; ++i) {
         uint32_t r[32];
         tmem_ld32(tmem_o + lane_base + 128u * cols + 32u * i, r);
@@ -1125,7 +1295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SharedRoles<TMA>::kT
     for (uint32_t b = 0; b < kSBars; ++b) {
       uint32_t count = 1;
       if (b < bEmpty) count = 2;                                      // each CTA once
-      else if (b == bQFull) count = 2 * (1 + kQWarps);                // the copies, and the warps
+      else if (b == bQFull) count = 2 * (1 + Roles::kQWarps);                // the copies, and the warps
       else if (b == bWeights || b == bOFree) count = 2 * kMathWarps;
       mbar_init(bars + 8 * b, count);
     }
@@ -1138,15 +1308,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SharedRoles<TMA>::kT
   const uint32_t tmem = (uint32_t)uniform((int)*reinterpret_cast<uint32_t*>(sm + S_MISC));
   const uint32_t tmem_o = tmem, tmem_s = tmem + 256;
   pdl_wait();
-  const SharedRun run = p.runs[c];
   SharedWalk walk;
-  walk.start(p, run, p.runs[c + 1].tile - run.tile);
+  walk.start(p.starts + c);
   if (warp < kMathWarps) {
     math_shared(p, sm, base_s, tmem_s, tmem_o, walk, c, warp, rank);
   } else if (warp < Roles::kQ) {
     produce_role<KVF, TMA>(p, sm, base_s, walk, warp - kMathWarps, rank);
   } else if (warp < Roles::kIssuer) {
-    q_role(p, sm, base_s, walk, tid - 32 * Roles::kQ, rank);
+    q_role<Roles::kQWarps>(p, sm, base_s, walk, tid - 32 * Roles::kQ, rank);
   } else if (rank == 0) {
     issue_shared(p, base_s, tmem_s, tmem_o, walk);
   }
@@ -1159,17 +1328,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SharedRoles<TMA>::kT
 
 // Join of a split unit's partials, the formula of csa2_attend_paged's join. A
 // thread has one head and 16 dims (a sector of the output; the parts' values lie
-// next to each other over the heads), a CTA 64 of the dims: the parts' weights
-// go through its shared memory, and two parts' values are under way at once.
+// next to each other over the heads). GROUPS 1: a CTA has 64 dims. GROUPS 4:
+// it has 16, and its quarters take every fourth part, for the few queries that
+// have many parts: what a thread waits for is one round trip for two parts.
 constexpr int kJoinDims = 16;
-constexpr int kJoinParts = 2;
+constexpr int kJoinParts = 2;  // whose values are under way at once
+template <int GROUPS>
 __global__ void __launch_bounds__(256, 4) attend_shared_join_kernel(const __grid_constant__ SharedParams p) {
-  __shared__ float weight[kMaxPairs2][kHeads];
+  __shared__ float2 weight[kMaxPairs2][kHeads];  // reference and sum, then the weight
   __shared__ float red[2][4][kHeads];
   __shared__ float2 turn[32];
-  const int head = threadIdx.x & 63, quarter = threadIdx.x >> 6, rank = (int)blockIdx.z;
-  const int d0 = kJoinDims * ((int)blockIdx.y * 4 + quarter), first_rope = kDim - 2 * p.rp.pairs;
-  const bool rope = kJoinDims * ((int)blockIdx.y * 4 + 4) > first_rope;  // of the CTA
+  const int head = threadIdx.x & 63, quarter = threadIdx.x >> 6, rank = (int)blockIdx.z, group = GROUPS == 1 ? 0 : quarter;
+  const int d0 = kJoinDims * (GROUPS == 1 ? (int)blockIdx.y * 4 + quarter : (int)blockIdx.y), first_rope = kDim - 2 * p.rp.pairs;
+  const bool rope = GROUPS == 1 ? 64 * ((int)blockIdx.y + 1) > first_rope : d0 + kJoinDims > first_rope;  // of the CTA
   const double freq = rope && threadIdx.x < (unsigned)p.rp.pairs ? p.rp.freq[threadIdx.x] : 0.0;
   pdl_wait();
   const int4 jn = p.joins[blockIdx.x];
@@ -1182,35 +1353,39 @@ __global__ void __launch_bounds__(256, 4) attend_shared_join_kernel(const __grid
   auto fetch = [&](int k0) {
 #pragma unroll
     for (int u = 0; u < kJoinParts; ++u) {
+      const int k = k0 + u * GROUPS;
 #pragma unroll
       for (int i = 0; i < kJoinDims / 4; ++i)
-        v[u][i] = k0 + u < n ? parts[(slot(k0 + u) * (kDim / 4) + i) * kHeads] : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[u][i] = k < n ? parts[(slot(k) * (kDim / 4) + i) * kHeads] : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   };
-  fetch(0);
-  // references and sums of this thread's quarter of the parts
+  fetch(group);
   const float sk = p.sink != nullptr ? p.sink[head] : -INFINITY, sk2 = sk * 1.4426950408889634f;
-  if (threadIdx.x < 32 && rope) {
-    float cs, sn;
-    angle_cs((double)p.q_pos[qi] * freq, cs, sn);
-    turn[threadIdx.x] = make_float2(cs, sn);
-  }
+  const int64_t t = rope && threadIdx.x < 32 ? p.q_pos[qi] : 0;
+  // the largest reference, each quarter over its share of the parts
   float M = -INFINITY;
+#pragma unroll 4
   for (int k = quarter; k < n; k += 4) {
-    const float m = p.part_m[slot(k) * kHeads + head];
-    weight[k][head] = m;
-    M = fmaxf(M, m);
+    const float2 ml = p.part_ml[slot(k) * kHeads + head];
+    weight[k][head] = ml;
+    M = fmaxf(M, ml.x);
   }
   red[0][quarter][head] = M;
+  if (threadIdx.x < 32 && rope) {
+    float cs, sn;
+    angle_cs((double)t * freq, cs, sn);
+    turn[threadIdx.x] = make_float2(cs, sn);
+  }
   __syncthreads();
   M = fmaxf(fmaxf(red[0][0][head], red[0][1][head]), fmaxf(red[0][2][head], red[0][3][head]));
   const bool none = M == -INFINITY;
   M = fmaxf(M, sk2);
   float den = 0.f;
   for (int k = quarter; k < n; k += 4) {
-    const float m = weight[k][head], e = m == -INFINITY ? 0.f : exp2f(m - M);
-    den += e * p.part_l[slot(k) * kHeads + head];  // 0 times NaN stays
-    weight[k][head] = e;
+    const float2 ml = weight[k][head];
+    const float e = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+    den += e * ml.y;  // 0 times NaN stays
+    weight[k][head].x = e;
   }
   red[1][quarter][head] = den;
   __syncthreads();
@@ -1219,15 +1394,16 @@ __global__ void __launch_bounds__(256, 4) attend_shared_join_kernel(const __grid
   if (!none) den += exp2f(sk2 - M);
   else if (empty) den = 1.f;
   const float inv = empty ? 0.f : 1.f / den;
-  if (d0 == 0 && p.lse != nullptr) p.lse[(int64_t)qi * kHeads + head] = empty ? sk : (M + log2f(den)) * 0.6931471805599453f;
+  if (d0 == 0 && group == 0 && p.lse != nullptr)
+    p.lse[(int64_t)qi * kHeads + head] = empty ? sk : (M + log2f(den)) * 0.6931471805599453f;
   float o[kJoinDims];
 #pragma unroll
   for (int i = 0; i < kJoinDims; ++i) o[i] = 0.f;
-  for (int k0 = 0; k0 < n; k0 += kJoinParts) {
-    if (k0 > 0) fetch(k0);
+  for (int k0 = group; k0 < n; k0 += kJoinParts * GROUPS) {
+    if (k0 > group) fetch(k0);
 #pragma unroll
     for (int u = 0; u < kJoinParts; ++u) {
-      const float e = k0 + u < n ? weight[k0 + u][head] : 0.f;
+      const float e = k0 + u * GROUPS < n ? weight[k0 + u * GROUPS][head].x : 0.f;
 #pragma unroll
       for (int i = 0; i < kJoinDims / 4; ++i) {
         o[4 * i] = fmaf(e, v[u][i].x, o[4 * i]);
@@ -1235,6 +1411,22 @@ __global__ void __launch_bounds__(256, 4) attend_shared_join_kernel(const __grid
         o[4 * i + 2] = fmaf(e, v[u][i].z, o[4 * i + 2]);
         o[4 * i + 3] = fmaf(e, v[u][i].w, o[4 * i + 3]);
       }
+    }
+  }
+  if constexpr (GROUPS > 1) {
+    float(*acc)[kJoinDims][kHeads] = reinterpret_cast<float(*)[kJoinDims][kHeads]>(&weight[0][0]);
+    static_assert(sizeof(float) * (GROUPS - 1) * kJoinDims * kHeads <= sizeof(weight));
+    __syncthreads();  // the weights have been read
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < kJoinDims; ++i) acc[group - 1][i][head] = o[i];
+    }
+    __syncthreads();
+    if (group > 0) return;
+#pragma unroll
+    for (int g = 0; g < GROUPS - 1; ++g) {
+#pragma unroll
+      for (int i = 0; i < kJoinDims; ++i) o[i] += acc[g][i][head];
     }
   }
   uint32_t w[kJoinDims / 2];
@@ -1261,7 +1453,7 @@ static int attend_shared_pairs(int num_sms) { return std::min(num_sms / 2, kMaxP
 
 size_t attend_shared_workspace_bytes(int num_sms, int n_query) {
   const size_t pairs = (size_t)attend_shared_pairs(num_sms), slots = 4 * pairs;
-  return al256(slots * kHeads * kDim * 4) + 2 * al256(slots * kHeads * 4) + al256((pairs + 1) * sizeof(SharedRun)) +
+  return al256(slots * kHeads * kDim * 4) + al256(slots * kHeads * 8) + al256(pairs * sizeof(SharedStart)) +
          al256(pairs * sizeof(int4)) + al256((size_t)n_query * sizeof(SharedUnit));
 }
 
@@ -1277,9 +1469,8 @@ cudaError_t launch_attend_shared(cudaStream_t st, int num_sms, int kv_fmt, const
     return at;
   };
   p.part_o = reinterpret_cast<float*>(part(slots * kHeads * kDim * 4));
-  p.part_m = reinterpret_cast<float*>(part(slots * kHeads * 4));
-  p.part_l = reinterpret_cast<float*>(part(slots * kHeads * 4));
-  p.runs = reinterpret_cast<SharedRun*>(part((p.pairs + 1) * sizeof(SharedRun)));
+  p.part_ml = reinterpret_cast<float2*>(part(slots * kHeads * 8));
+  p.starts = reinterpret_cast<SharedStart*>(part(p.pairs * sizeof(SharedStart)));
   p.joins = reinterpret_cast<int4*>(part(p.pairs * sizeof(int4)));
   p.units = reinterpret_cast<SharedUnit*>(part((size_t)a.n_query * sizeof(SharedUnit)));
   p.q = a.q;
@@ -1326,7 +1517,12 @@ cudaError_t launch_attend_shared(cudaStream_t st, int num_sms, int kv_fmt, const
   else CSA2_SHARED(2, false);
 #undef CSA2_SHARED
   if (e != cudaSuccess) return e;
-  e = launch_ex(attend_shared_join_kernel, dim3((unsigned)p.pairs, kDim / kJoinDims / 4, 2), dim3(256), 0, st, true, 0, p);
+  // few queries: many parts a unit, few units to be joined
+  const unsigned joins = (unsigned)std::min(p.pairs, p.n_query);
+  if (4 * joins <= (unsigned)p.pairs)
+    e = launch_ex(attend_shared_join_kernel<4>, dim3((unsigned)p.pairs, kDim / kJoinDims, 2), dim3(256), 0, st, true, 0, p);
+  else
+    e = launch_ex(attend_shared_join_kernel<1>, dim3((unsigned)p.pairs, kDim / kJoinDims / 4, 2), dim3(256), 0, st, true, 0, p);
   if (e != cudaSuccess) return e;
   *n_launch += 3;
   return cudaGetLastError();

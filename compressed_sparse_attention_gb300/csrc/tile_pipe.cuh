@@ -151,4 +151,10 @@ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
+// 16 zero bytes into shared memory if hit != 0, without a branch
+__device__ __forceinline__ void zero16_if(uint32_t hit, uint32_t dst) {
+  asm volatile("{\n.reg .pred p;\nsetp.ne.u32 p, %0, 0;\n@p st.shared.v4.u32 [%1], {%2, %2, %2, %2};\n}" ::"r"(hit), "r"(dst), "r"(0u)
+               : "memory");
+}
+
 }  // namespace csa2
