@@ -1168,8 +1168,8 @@ __global__ void __launch_bounds__(GROUPS == 1 ? 128 : 32 * GROUPS, GROUPS == 1 ?
 }
 
 // Tensor map of bf16 rows, boxes of 64 channels (128 bytes, the swizzle's width).
-cudaError_t encode_bf16_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
-                            const uint32_t* box) {
+static cudaError_t encode_map(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, int rank, const void* base,
+                              const uint64_t* dims, const uint64_t* strides, const uint32_t* box) {
   // looked up by the first call; host threads with contexts of their own may make it at once
   static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> looked_up{nullptr};
   PFN_cuTensorMapEncodeTiled_v12000 encode = looked_up.load(std::memory_order_acquire);
@@ -1191,9 +1191,8 @@ cudaError_t encode_bf16_map(CUtensorMap* map, int rank, const void* base, const 
     if (i + 1 < rank) st[i] = strides[i];
   }
   auto fill = [&] {
-    return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank, const_cast<void*>(base), d, st, bx, es,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return encode(map, type, (cuuint32_t)rank, const_cast<void*>(base), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
   CUresult r = fill();
   if (r == CUDA_ERROR_INVALID_CONTEXT) {
@@ -1206,6 +1205,15 @@ cudaError_t encode_bf16_map(CUtensorMap* map, int rank, const void* base, const 
     r = fill();
   }
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t encode_bf16_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                            const uint32_t* box) {
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, rank, base, dims, strides, box);
+}
+cudaError_t encode_byte_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                            const uint32_t* box) {
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_NONE, rank, base, dims, strides, box);
 }
 
 namespace {

@@ -77,6 +77,7 @@ struct SharedParams {
   CUtensorMap q_map;   // Q: [64 n_query heads][512], boxes of 64 heads x 64 channels
   CUtensorMap kv_map;  // bf16 pages: [n_pages][page_size][512], boxes of one piece x 64 channels
   CUtensorMap v_map;   // the same as [n_pages][8 blocks][page_size][64], boxes of two blocks of 64 rows (pages of 64 rows and more)
+  CUtensorMap code_map;  // fp8, fp4 codes: [n_pages][page_size][row bytes], boxes of one piece x 64 channels
   const uint16_t* q;
   const int64_t* q_pos;
   const int32_t* seq_of_q;
@@ -362,7 +363,7 @@ constexpr uint32_t S_MISC = S_QROPE + 256;
 constexpr uint32_t kSharedSmemBytes = S_MISC + 64 + 1024;
 static_assert(kSharedSmemBytes <= 232448, "shared memory");
 
-enum SBar : uint32_t { bFull = 0, bEmpty = 7, bQFull = 14, bQEmpty = 15, bScores = 16, bWeights = 18, bPFree = 19, bOFree = 20, bDrained = 21, bEdge = 22, kSBars = 26 };
+enum SBar : uint32_t { bFull = 0, bEmpty = 7, bQFull = 14, bQEmpty = 15, bScores = 16, bWeights = 18, bPFree = 19, bOFree = 20, bDrained = 21, bEdge = 22, kSBars = 28 };
 
 constexpr uint32_t kIdescS = idesc_bf16(128, 256, 0, 0);
 constexpr uint32_t kIdescO = idesc_bf16(128, 256, 0, 1);
@@ -650,87 +651,217 @@ __device__ __forceinline__ void fill_slot(const SharedParams& p, const SharedUni
 
 // What a tile's producers know of it: the number of its row groups; of lane
 // 8 g + i the page of piece i of group g (the pool's size: none) and the row of
-// it where the piece begins; and which groups lie whole in it (bits 8 g).
+// it where the piece begins (fp8, fp4: also where its scales do, -1: none); and
+// which groups lie whole in it (bits 8 g).
 struct TileSource {
   int n;
   int32_t page, row;
+  int64_t scales;
   uint32_t whole;
 };
+__device__ __forceinline__ int64_t from_lane(int64_t v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }
 
-// A slot of fp8 or fp4 rows (pages of eight rows and more), converted. A lane has 16
-// chunks of 16 channels; four of them are under way while four others are
-// converted, the first eight from before the wait for the slot on. The stores and
-// the conversions (72 cycles a warp and chunk) bound it.
-template <int KVF, bool IS_K>
-struct CodeSlot {
-  static constexpr int kRowBytes = KVF == 1 ? 512 : 256, kScaleBytes = KVF == 1 ? 16 : 32;
-  static constexpr int kChunks = IS_K ? 4 : 8;          // of a row
-  static constexpr int kStep = 32 / kChunks;            // rows of a load
-  static constexpr int kBatch = 4;
-  using Code = typename std::conditional<KVF == 1, uint4, uint2>::type;
-  Code code[2][kBatch];
-  uint8_t scale[2][kBatch];
-  int row0, c, ch;
-  int from[2], to[2];  // rows of the slot's groups that are theirs
-  int in_page[2];      // place of a group's first row in its page
-  __device__ __forceinline__ void start(const SharedParams& p, const SharedUnit& u, const TileSource& src, int tile, int g0, int d0, int lane) {
-    row0 = lane / kChunks;
-    c = lane % kChunks;
-    ch = d0 + 16 * c;
+// fp8 and fp4 rows (pages of eight rows and more). A slot's codes, 128 runs of 64
+// channels, are copied into the end of the slot itself and converted in place,
+// from the front: 8 runs of bf16 take as much room as 16 (fp8) of codes leave, so
+// that no code is overwritten before it has been read. A warp's next slot is on
+// its way while it converts one (72 cycles a warp and 16 channels a lane, which
+// is what bounds it: with the codes in registers, loaded four at a time, a slot
+// took a warp 9,500 cycles, most of them waiting for the L2).
+// Codes times their block's scale in bf16, exact: codes have at most 4 (e2m1: 2)
+// significant bits, scales 1 (4), and the product is rounded like a float's.
+__device__ __forceinline__ uint32_t scaled_pair(uint32_t f16x2, __nv_bfloat162 sc) {
+  const __half2_raw h{(unsigned short)(f16x2 & 0xFFFFu), (unsigned short)(f16x2 >> 16)};
+  const __nv_bfloat162 v = __hmul2(__float22bfloat162_rn(__half22float2(__half2(h))), sc);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ void scaled_e4m3(const uint4& codes, uint32_t scale, uint32_t (&o)[8]) {
+  const __nv_bfloat162 sc = __float2bfloat162_rn(ue8m0_value(scale));
+  const uint32_t cw[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
-    for (int k = 0; k < (IS_K ? 2 : 1); ++k) {
-      const RowGroup g = row_group(u, kTileGroups * tile + g0 + k);
-      from[k] = g.present ? g.from - 64 * g.block : 64;
-      to[k] = g.present ? g.to - 64 * g.block : 0;
-      in_page[k] = (64 * g.block) & ((1 << p.kv.page_shift) - 1);
-    }
-    load(p, src, g0, 0, 0);
-    load(p, src, g0, 1, 1);
+  for (int k = 0; k < 4; ++k) {
+    o[2 * k] = scaled_pair(e4m3x2_to_f16x2(cw[k] & 0xFFFFu), sc);
+    o[2 * k + 1] = scaled_pair(e4m3x2_to_f16x2(cw[k] >> 16), sc);
   }
-  __device__ __forceinline__ void load(const SharedParams& p, const TileSource& src, int g0, int batch, int into) {
-    const int pc = piece_shift(p.kv.page_shift), page_mask = (1 << p.kv.page_shift) - 1;
+}
+__device__ __forceinline__ void scaled_e2m1(const uint2& codes, uint32_t scale, uint32_t (&o)[8]) {
+  const __nv_bfloat162 sc = __float2bfloat162_rn(e4m3_value(scale));
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int first = (batch * kBatch + i) * kStep, k = IS_K ? first >> 6 : 0;  // the load's first row, its group
-      const int r = (first & 63) + row0;
-      const int page = uniform(src.page, 8 * (g0 + k) + ((first & 63) >> pc));
-      const int at = (in_page[IS_K ? k : 0] + r) & page_mask;
-      const bool there = page < p.kv.n_pages && r >= from[IS_K ? k : 0] && r < to[IS_K ? k : 0];
-      const uint8_t* codes = p.kv.pages + page * p.kv.page_stride + (int64_t)at * kRowBytes;
-      const uint8_t* sc = p.kv.scales + page * p.kv.scale_stride + (int64_t)at * kScaleBytes;
-      if constexpr (KVF == 1) {
-        code[into][i] = there ? ldg_stream16(codes + ch) : make_uint4(0u, 0u, 0u, 0u);
-        scale[into][i] = there ? __ldg(sc + ch / 32) : 0;
-      } else {
-        code[into][i] = there ? ldg_stream8(codes + ch / 2) : make_uint2(0u, 0u);
-        scale[into][i] = there ? __ldg(sc + ch / 16) : 0;
+  for (int k = 0; k < 2; ++k) {
+    uint32_t h[4];
+    e2m1x8_to_f16x2x4_cvt(k == 0 ? codes.x : codes.y, h);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) o[4 * k + u] = scaled_pair(h[u], sc);
+  }
+}
+
+template <int KVF>
+struct CodeProducer {
+  static constexpr uint32_t NP = SharedRoles<false>::kProducers;
+  static constexpr int kRowBytes = KVF == 1 ? 512 : 256, kScaleBytes = KVF == 1 ? 16 : 32;
+  static constexpr uint32_t kRun = KVF == 1 ? 64u : 32u;  // code bytes of 64 channels
+  using Code = typename std::conditional<KVF == 1, uint4, uint2>::type;
+  const SharedParams& p;
+  uint8_t* sm;
+  uint32_t base_s, bars, full0, leader, here;
+  int w, rank, lane, pc, pieces;
+  SharedWalk& walk;
+  RingAt base{0, 0};  // the next slot of all warps, and the slots before it
+  uint32_t s = 0, asked = 0;
+  bool live = true;
+  // A slot whose codes are on their way: its place (bar 0: none); of runs 32 i +
+  // lane their scales (two bytes, fp4: four), which nothing touches before the slot
+  // is converted, and which runs are there (bits).
+  struct Asked {
+    uint32_t slot, bar, scales[4], there[4];
+  };
+  Asked on{0u, 0u, {0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
+
+  __device__ __forceinline__ TileSource look_up(int tile) const {
+    const SharedUnit& u = walk.u;
+    TileSource src;
+    src.n = uniform(row_groups(u, tile));
+    const RowGroup g = row_group(u, kTileGroups * tile + (lane >> 3));
+    const int pos = 64 * g.block + ((lane & 7) << pc), in_page = pos & ((1 << p.kv.page_shift) - 1);
+    int32_t page = -1;
+    if ((lane & 7) < pieces && g.present && pos < g.to && pos + (1 << pc) > g.from)
+      page = page_of(p.kv, max(pos, g.from) < u.len ? u.head_seq : g.seq, pos);
+    src.page = page >= 0 ? page : p.kv.n_pages;  // past the end: zeros
+    src.row = in_page;
+    src.scales = page >= 0 ? page * p.kv.scale_stride + (int64_t)in_page * kScaleBytes : -1;
+    src.whole = 0;
+    // (on their way to the L2, half of the tile's rows by either CTA)
+    if (page >= 0 && w == 0 && (lane >> 4) == rank) {
+      prefetch_l2(p.kv.pages + page * p.kv.page_stride + (int64_t)in_page * kRowBytes, (uint32_t)kRowBytes << pc);
+      prefetch_l2(p.kv.scales + src.scales, (uint32_t)kScaleBytes << pc);
+    }
+    return src;
+  }
+  // Runs 64 k .. of a slot, k < n: row group g0 + k's (K), or of one group its
+  // dims d0 + 64 k .. (V).
+  __device__ __forceinline__ void ask(const TileSource& src, int tile, bool is_k, int n, int g0, int d0, uint32_t slot, uint32_t bar) {
+    on.slot = slot;
+    on.bar = bar;
+    const uint32_t dst = base_s + slot + kSlotBytes - 128u * kRun;
+    expect_one(leader, here, 64u * kRun * (uint32_t)n);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int g = is_k ? g0 + k : g0, ch = is_k ? d0 : d0 + 64 * k;
+      if (k < n) {
+#pragma unroll 1
+        for (int i = 0; i < pieces; ++i)
+          tma_3d_one(leader, dst + (64u * (uint32_t)k + (uint32_t)(i << pc)) * kRun, &p.code_map, ch * (int)kRun / 64,
+                     uniform(src.row, 8 * g + i), uniform(src.page, 8 * g + i), here);
+      }
+      const RowGroup rg = row_group(walk.u, kTileGroups * tile + g);
+      const int from = rg.from - 64 * rg.block, to = k < n && rg.present ? rg.to - 64 * rg.block : 0;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = 32 * i + lane;
+        const int64_t at = __shfl_sync(0xffffffffu, src.scales, 8 * (g & 3) + (r >> pc));
+        const bool there = at >= 0 && r >= from && r < to;
+        const uint8_t* sp = p.kv.scales + at + (uint32_t)((r & ((1 << pc) - 1)) * kScaleBytes + ch / (KVF == 1 ? 32 : 16));
+        uint32_t sc = 0u;
+        if constexpr (KVF == 1) {
+          if (there) sc = __ldg(reinterpret_cast<const uint16_t*>(sp));
+        } else {
+          if (there) sc = __ldg(reinterpret_cast<const uint32_t*>(sp));
+        }
+        on.scales[2 * k + i] = sc;
+        on.there[2 * k + i] = __ballot_sync(0xffffffffu, there);
       }
     }
+    ++asked;
   }
-  __device__ __forceinline__ void store(int batch, int from_set, uint8_t* dst) {
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = (batch * kBatch + i) * kStep + row0;
-      uint32_t o[8];
-      if constexpr (KVF == 1) fp8_to_bf16(code[from_set][i], scale[from_set][i], o);
-      else fp4_to_bf16(code[from_set][i].x, code[from_set][i].y, scale[from_set][i], o);
-      uint8_t* at = dst + (uint32_t)(c >> 2) * 8192u + (uint32_t)r * 128u;
-#pragma unroll
-      for (int k = 0; k < 2; ++k)
-        *reinterpret_cast<uint4*>(at + (((2 * (c & 3) + k) ^ (r & 7)) << 4)) = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-    }
-  }
-  __device__ __forceinline__ void finish(const SharedParams& p, const TileSource& src, int g0, uint8_t* dst) {
+  // (asked for one after another on one barrier: each has landed before the next is counted)
+  __device__ __forceinline__ void landed() { live = live && wait_all_lanes(here, (asked - 1u) & 1u, p.flags); }
+  // A lane has channels 16 (lane & 3) .. of runs lane >> 2, + 8, ...
+  __device__ __forceinline__ void convert(const Asked& a) const {
+    const uint8_t* code_at = sm + a.slot + kSlotBytes - 128u * kRun + (kRun / 4u) * (uint32_t)lane;
+    const int r = lane >> 2, c = lane & 3;
+    uint8_t* out = sm + a.slot + 128u * (uint32_t)r;
 #pragma unroll 1
-    for (int b = 0; b < 4; b += 2) {
-      store(b, 0, dst);
-      if (b == 0) load(p, src, g0, 2, 0);
-      store(b + 1, 1, dst);
-      if (b == 0) load(p, src, g0, 3, 1);
+    for (int j4 = 0; j4 < 4; ++j4) {
+      Code code[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) code[i] = *reinterpret_cast<const Code*>(code_at + 8u * kRun * (uint32_t)(4 * j4 + i));
+      __syncwarp();  // all lanes have read what the stores below may overwrite
+      const uint32_t scales = j4 == 0 ? a.scales[0] : (j4 == 1 ? a.scales[1] : (j4 == 2 ? a.scales[2] : a.scales[3]));
+      const uint32_t there = j4 == 0 ? a.there[0] : (j4 == 1 ? a.there[1] : (j4 == 2 ? a.there[2] : a.there[3]));
+      const bool all = there == 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t word = __shfl_sync(0xffffffffu, scales, 8 * i + r);
+        const uint32_t sc = (word >> (KVF == 1 ? 8 * (c >> 1) : 8 * c)) & 255u;
+        if (!all && ((there >> (8 * i + r)) & 1u) == 0u) {  // rows that are not the group's: zeros
+          if constexpr (KVF == 1) code[i] = make_uint4(0u, 0u, 0u, 0u);
+          else code[i] = make_uint2(0u, 0u);
+        }
+        uint32_t o[8];
+        if constexpr (KVF == 1) scaled_e4m3(code[i], sc, o);
+        else scaled_e2m1(code[i], sc, o);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          *reinterpret_cast<uint4*>(out + 1024u * (uint32_t)(4 * j4 + i) + (((2 * c + k) ^ r) << 4)) =
+              make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      }
     }
     fence_proxy_async_smem();
+    warp_arrive_cluster(a.bar);
+  }
+  __device__ __forceinline__ void flush() {
+    if (on.bar == 0u) return;
+    landed();
+    convert(on);
+    on.bar = 0u;
+  }
+  // this warp's slots of the next `count`
+  __device__ __forceinline__ void slots(uint32_t count, int tile, const TileSource& src, bool is_k) {
+    const int n = is_k ? min(2, max(0, src.n - 2 * rank)) : 2;
+#pragma unroll 1
+    for (uint32_t i = (w + NP - s % NP) % NP; i < count; i += NP) {
+      RingAt at = base;
+      at.step(i);
+      const uint32_t empty = bars + 8 * (bEmpty + at.slot);
+      if (s + i >= (uint32_t)kRing) {
+        // (not free yet: the one on its way is converted meanwhile)
+        if (!uniform(phase_done(empty, at.phase ^ 1u) != 0u)) flush();
+        live = live && wait_all_lanes(empty, at.phase ^ 1u, p.flags);
+      }
+      if (on.bar != 0u) landed();
+      const Asked last = on;
+      ask(src, tile, is_k, n, is_k ? 2 * rank : (int)i >> 1, is_k ? 64 * (int)i : 256 * ((int)i & 1) + 128 * rank,
+          S_RING + at.slot * kSlotBytes, full0 + 8 * at.slot);
+      if (last.bar != 0u) convert(last);
+    }
+    base.step(count);
+    s += count;
   }
 };
+
+template <int KVF>
+__device__ __forceinline__ void produce_codes(const SharedParams& p, uint8_t* sm, uint32_t base_s, SharedWalk walk, int w, int rank) {
+  if (walk.left <= 0) return;
+  const uint32_t bars = base_s + S_BAR;
+  const int pc = piece_shift(p.kv.page_shift);
+  CodeProducer<KVF> c{p, sm, base_s, bars, in_leader(bars + 8 * bFull), elect_one(), bars + 8 * (bEdge + (uint32_t)w), w, rank,
+                      (int)(threadIdx.x & 31), pc, kGroupRows >> pc, walk};
+  do {
+    TileSource now = c.look_up(walk.first);
+    c.slots(8, walk.first, now, true);
+#pragma unroll 1
+    for (int t = walk.first; t < walk.last; ++t) {
+      TileSource ahead = now;
+      if (t + 1 < walk.last) {
+        ahead = c.look_up(t + 1);
+        c.slots(8, t + 1, ahead, true);
+      }
+      c.slots(2u * (uint32_t)now.n, t, now, false);
+      now = ahead;
+    }
+  } while (walk.next(p));
+  c.flush();
+}
 
 // Producer warp w of a CTA: every kProducers-th slot of the ring. What a tile's
 // copies need is found once a tile, before the waits for its slots: with the look-up
@@ -746,41 +877,31 @@ __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm,
   RingAt base{0, 0};  // the next slot of all warps, and the slots before it
   uint32_t s = 0, edges = 0;
   bool live = true;
-  const bool pieced = pc >= 3;  // a tile's pages fit the warp's lanes
   auto look_up = [&](int tile) {
     const SharedUnit& u = walk.u;
     TileSource src;
     src.n = uniform(row_groups(u, tile));
     src.page = p.kv.n_pages;  // past the end: zeros
     src.row = 0;
+    src.scales = -1;
     src.whole = 0;
-    if (!pieced) return src;
+    if (!TMA) return src;
     const RowGroup g = row_group(u, kTileGroups * tile + (lane >> 3));
     const int pos = 64 * g.block + ((lane & 7) << pc);
     if ((lane & 7) < pieces && g.present && pos < g.to && pos + (1 << pc) > g.from) {
       const int32_t page = page_of(p.kv, max(pos, g.from) < u.len ? u.head_seq : g.seq, pos);
-      if (page >= 0) {
-        src.page = page;
-        // (codes on their way to the L2, half of the tile's rows by either CTA)
-        if (KVF != 0 && w == 0 && (lane >> 4) == rank) {
-          constexpr uint32_t kRow = KVF == 1 ? 512u : 256u, kScale = KVF == 1 ? 16u : 32u;
-          const int64_t at = pos & ((1 << ps) - 1);
-          prefetch_l2(p.kv.pages + page * p.kv.page_stride + at * kRow, kRow << pc);
-          prefetch_l2(p.kv.scales + page * p.kv.scale_stride + at * kScale, kScale << pc);
-        }
-      }
+      if (page >= 0) src.page = page;
     }
     src.row = pos & ((1 << ps) - 1);
     src.whole = __ballot_sync(0xffffffffu, (lane & 7) == 0 && g.present && g.from <= 64 * g.block && g.to >= 64 * g.block + 64);
     return src;
   };
-  // this warp's slots of the next `count`: ask(i), then fill(i, its place)
-  auto each = [&](uint32_t count, auto&& ask, auto&& fill) {
+  // this warp's slots of the next `count`: fill(i, its place)
+  auto each = [&](uint32_t count, auto&& fill) {
 #pragma unroll 1
     for (uint32_t i = (w + NP - s % NP) % NP; i < count; i += NP) {
       RingAt at = base;
       at.step(i);
-      ask((int)i);
       if (s + i >= (uint32_t)kRing) live = live && wait_all_lanes(bars + 8 * (bEmpty + at.slot), at.phase ^ 1u, p.flags);
       if (live) fill((int)i, full0 + 8 * at.slot, at.slot * kSlotBytes + S_RING);
     }
@@ -791,15 +912,10 @@ __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm,
     const int n = min(2, max(0, src.n - 2 * rank));  // row groups of this CTA's half
     const int page0 = uniform(src.page, 16 * rank), page1 = uniform(src.page, 16 * rank + 8);
     const int row0 = uniform(src.row, 16 * rank), row1 = uniform(src.row, 16 * rank + 8);
-    CodeSlot<KVF, true> codes;
-    auto ask = [&](int b) {
-      if (KVF != 0 && pieced && n > 0) codes.start(p, walk.u, src, tile, 2 * rank, 64 * b, lane);
-    };
-    each(8, ask, [&](int b, uint32_t bar, uint32_t slot) {
+    each(8, [&](int b, uint32_t bar, uint32_t slot) {
       const uint32_t dst = base_s + slot;
       if (!TMA) {
-        if (KVF != 0 && pieced && n > 0) codes.finish(p, src, 2 * rank, sm + slot);
-        else if (n > 0) fill_slot<KVF, true>(p, walk.u, tile, 2 * rank, 64 * b, dst, sm + slot, lane);
+        if (n > 0) fill_slot<KVF, true>(p, walk.u, tile, 2 * rank, 64 * b, dst, sm + slot, lane);
         warp_arrive_cluster(bar);
         return;
       }
@@ -819,16 +935,11 @@ __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm,
     });
   };
   auto values = [&](int tile, const TileSource& src) {
-    CodeSlot<KVF, false> codes;
-    auto ask = [&](int i) {
-      if (KVF != 0 && pieced) codes.start(p, walk.u, src, tile, i >> 1, 256 * (i & 1) + 128 * rank, lane);
-    };
-    each(2 * (uint32_t)src.n, ask, [&](int i, uint32_t bar, uint32_t slot) {
+    each(2 * (uint32_t)src.n, [&](int i, uint32_t bar, uint32_t slot) {
       const int g = i >> 1, d0 = 256 * (i & 1) + 128 * rank;
       const uint32_t dst = base_s + slot;
       if (!TMA) {
-        if (KVF != 0 && pieced) codes.finish(p, src, g, sm + slot);
-        else fill_slot<KVF, false>(p, walk.u, tile, g, d0, dst, sm + slot, lane);
+        fill_slot<KVF, false>(p, walk.u, tile, g, d0, dst, sm + slot, lane);
         warp_arrive_cluster(bar);
         return;
       }
@@ -1313,7 +1424,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SharedRoles<TMA>::kT
   if (warp < kMathWarps) {
     math_shared(p, sm, base_s, tmem_s, tmem_o, walk, c, warp, rank);
   } else if (warp < Roles::kQ) {
-    produce_role<KVF, TMA>(p, sm, base_s, walk, warp - kMathWarps, rank);
+    if (KVF != 0 && p.kv.page_shift >= 3) produce_codes<KVF>(p, sm, base_s, walk, warp - kMathWarps, rank);
+    else produce_role<KVF, TMA>(p, sm, base_s, walk, warp - kMathWarps, rank);
   } else if (warp < Roles::kIssuer) {
     q_role<Roles::kQWarps>(p, sm, base_s, walk, tid - 32 * Roles::kQ, rank);
   } else if (rank == 0) {
@@ -1500,6 +1612,13 @@ cudaError_t launch_attend_shared(cudaStream_t st, int num_sms, int kv_fmt, const
     const uint64_t v_strides[3] = {2u * kDim, 128u, (uint64_t)kv.page_stride};
     const uint32_t v_box[4] = {64u, (uint32_t)kGroupRows, 2u, 1u};
     e = encode_bf16_map(&p.v_map, 4, kv.pages, v_dims, v_strides, v_box);
+  }
+  if (e == cudaSuccess && kv_fmt != 0 && piece >= 8) {
+    const uint32_t run = kv_fmt == 1 ? 64u : 32u;
+    const uint64_t c_dims[3] = {8u * run, 1ull << kv.page_shift, (uint64_t)kv.n_pages};
+    const uint64_t c_strides[2] = {8u * run, (uint64_t)kv.page_stride};
+    const uint32_t c_box[3] = {run, (uint32_t)piece, 1u};
+    e = encode_byte_map(&p.code_map, 3, kv.pages, c_dims, c_strides, c_box);
   }
   if (e != cudaSuccess) return e;
   e = launch_ex(attend_shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, true, 0, p);

@@ -220,6 +220,9 @@ cudaError_t launch_wait_probe(cudaStream_t st, uint32_t* flags, uint64_t limit_n
 // Tensor map of bf16 rows, boxes of 64 channels (128 bytes, the swizzle's width)
 cudaError_t encode_bf16_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
                             const uint32_t* box);
+// of bytes, laid out plainly
+cudaError_t encode_byte_map(CUtensorMap* map, int rank, const void* base, const uint64_t* dims, const uint64_t* strides,
+                            const uint32_t* box);
 // paged caches (csa2_attend_paged, csa2_append_paged, csa2_pages_*)
 size_t attend_paged_workspace_bytes(int num_sms);
 cudaError_t launch_attend_paged(cudaStream_t st, int num_sms, int kv_fmt, AttendParams a, const PagedView& kv,
