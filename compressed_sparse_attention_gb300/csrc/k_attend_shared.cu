@@ -93,6 +93,7 @@ struct SharedParams {
   float scale_log2;
   int n_query;
   int pairs;  // of CTAs
+  int planned;  // whether a launch of its own has made the plan (units, starts, joins)
   SharedUnit* units;
   SharedStart* starts;  // [pairs]
   int4* joins;       // [pairs]: of a unit that run c begins and does not end its queries, c and its last run; third -1: none
@@ -109,11 +110,38 @@ __host__ __device__ __forceinline__ int piece_shift(int page_shift) { return pag
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// The plan, one CTA: places -> units, and the units' tiles cut into runs of
-// equal cost, one a pair of CTAs. A thread takes a share of the places and, when
-// a scan has placed its units, finds the cuts that fall into them.
+// The plan: places -> units, and the units' tiles cut into runs of equal cost, one
+// a pair of CTAs. Of up to kPlanHere places every pair of CTAs makes it for itself,
+// a thread a place (three round trips to the L2); of more, one CTA in a launch of
+// its own, a thread a share of the places (a launch, and what it costs to hand
+// the plan over, 3 us of a call).
+//
+// On a line where a tile is kTileCost2 long and a unit starts with kUnitCost, run
+// c has the tiles that start in the c-th of R equal parts (a part inside a unit's
+// start has none).
 // ---------------------------------------------------------------------------
 constexpr int kTileCost2 = 4, kUnitCost = 8;  // a unit: its Q, its first weights, its outputs
+constexpr int kPlanHere = 96;                 // units that fit shared memory beside the tiles
+struct RunLine {
+  int64_t cost;
+  int runs, start;
+  __device__ __forceinline__ RunLine(int64_t tiles, int units, int pairs) {
+    start = tiles > 2 * (int64_t)pairs ? kUnitCost : 0;
+    cost = kTileCost2 * tiles + (int64_t)start * units;
+    runs = (int)min((int64_t)pairs, tiles);
+  }
+  // where unit u begins, t tiles coming before it, runs-fold
+  __device__ __forceinline__ int64_t at(int64_t t, int u) const { return runs * (kTileCost2 * t + (int64_t)start * u); }
+  // of unit u the first tile from cut c on
+  __device__ __forceinline__ int64_t tile_from(int c, int64_t t, int u) const {
+    const int64_t left = c * cost - at(t, u + 1), step = (int64_t)kTileCost2 * runs;
+    return left <= 0 ? 0 : quotient(left + step - 1, step);
+  }
+  // run of tile j of unit u
+  __device__ __forceinline__ int run_of(int64_t t, int u, int j) const {
+    return (int)quotient(at(t, u + 1) + (int64_t)kTileCost2 * runs * j, cost);
+  }
+};
 
 namespace {
 struct PlanUnit {
@@ -191,12 +219,7 @@ __device__ __forceinline__ PlanUnit unit_at(const SharedParams& p, int k, uint32
 __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(const __grid_constant__ SharedParams p) {
   __shared__ int64_t sum_t[32], share_t[kPlanThreads];  // tiles, units before a thread's share
   __shared__ int sum_u[32], share_u[kPlanThreads];
-  __shared__ int share_n[kPlanThreads];   // a share of one unit: its tiles
-  __shared__ int2 share_q[kPlanThreads];  // and queries
   __shared__ SharedRun runs[kMaxPairs2 + 1];
-  __shared__ int run_share[kMaxPairs2];
-  constexpr int kWords = (kMaxPairs2 + 31) / 32;
-  __shared__ uint32_t on[kWords];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
   pdl_wait();
@@ -241,76 +264,45 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(con
   const int bu = __shfl_sync(0xffffffffu, au, max(warp, 1) - 1);
   share_t[tid] = it - tiles + (warp > 0 ? bt : 0);
   share_u[tid] = iu - units + (warp > 0 ? bu : 0);
-  if (per == 1 && one.begins) {
-    share_n[tid] = one.u.tiles;
-    share_q[tid] = make_int2(one.u.q[0], one.u.q[1]);
-  }
   int u0 = share_u[tid];
   for (int k = lo; k < hi; ++k) {
     if (per > 1) one = unit_at(p, k, unused);
     if (one.begins) p.units[u0++] = one.u;
   }
   __syncthreads();
-  // On a line where a tile is kTileCost2 long and a unit starts with kUnitCost,
-  // run c has the tiles that start in the c-th of R equal parts (a part inside a
-  // unit's start has none). Thread c finds the first tile from the c-th cut on.
-  const int start = T > 2 * (int64_t)p.pairs ? kUnitCost : 0;
-  const int64_t cost = kTileCost2 * T + (int64_t)start * U;
-  const int R = (int)min((int64_t)p.pairs, T);
+  const RunLine line(T, U, p.pairs);
+  // thread c finds the first tile from the c-th cut on
   if (tid <= p.pairs) {
     SharedRun r{T, U, 0};
-    if (tid < R) {
-      const int64_t y = tid * cost;  // R-fold, as are all places below
+    if (tid < line.runs) {
+      const int64_t y = tid * line.cost;
       int i = 0, end = kPlanThreads;  // the last share that begins at or before y
       while (end - i > 1) {
         const int mid = (i + end) >> 1;
-        if (R * (kTileCost2 * share_t[mid] + (int64_t)start * share_u[mid]) <= y) i = mid;
+        if (line.at(share_t[mid], share_u[mid]) <= y) i = mid;
         else end = mid;
       }
       int64_t t = share_t[i];
-      int u = share_u[i];
-      for (;; ++u) {
-        const int n = per == 1 ? share_n[i] : p.units[u].tiles;
-        const int64_t left = y - R * (kTileCost2 * t + (int64_t)start * (u + 1)), step = (int64_t)kTileCost2 * R;
-        const int64_t j = left <= 0 ? 0 : quotient(left + step - 1, step);
+      for (int u = share_u[i]; u < U; ++u) {
+        const int n = p.units[u].tiles;
+        const int64_t j = line.tile_from(tid, t, u);
         if (j < n) {
           r = SharedRun{t + j, u, (int32_t)j};
           break;
         }
         t += n;
-        if (u + 1 == U) break;  // (a cut behind the last tile's start)
-        if (per == 1) {  // the share of the next unit
-          do ++i;
-          while (share_u[i] != u + 1 || (i + 1 < kPlanThreads && share_u[i + 1] == u + 1));
-        }
       }
-      run_share[tid] = i;
     }
     runs[tid] = r;
   }
   __syncthreads();
-  // a unit that begins in run c and goes on: its last run is the one behind
-  // those that it fills from end to end
-  if (warp < kWords) {
-    const bool through = tid < R && runs[tid + 1].first > 0 && runs[tid + 1].unit == runs[tid].unit;
-    const uint32_t w = __ballot_sync(0xffffffffu, through);
-    if (lane == 0) on[warp] = w;
-  }
-  __syncthreads();
   if (tid < p.pairs) {
     int4 jn = make_int4(-1, -1, -1, 0);
-    if (tid < R && runs[tid + 1].first > 0 && (runs[tid].unit < runs[tid + 1].unit || runs[tid].first == 0)) {
-      int c = tid + 1;
-      while (c < 32 * kWords) {
-        const uint32_t off = ~on[c >> 5] >> (c & 31);
-        if (off != 0u) {
-          c += __ffs((int)off) - 1;
-          break;
-        }
-        c = (c | 31) + 1;
-      }
-      const int2 q = per == 1 ? share_q[run_share[tid + 1]] : *reinterpret_cast<const int2*>(p.units[runs[tid + 1].unit].q);
-      jn = make_int4(q.x, q.y, tid, c);
+    // a unit that begins in run c and goes on
+    const SharedRun next = runs[tid + 1];
+    if (next.first > 0 && (runs[tid].unit < next.unit || runs[tid].first == 0)) {
+      const SharedUnit& u = p.units[next.unit];
+      jn = make_int4(u.q[0], u.q[1], tid, line.run_of(next.tile - next.first, next.unit, u.tiles - 1));
     }
     p.joins[tid] = jn;
   }
@@ -360,7 +352,9 @@ constexpr uint32_t S_RED = S_BAR + 256;               // float [4 row groups][64
 constexpr uint32_t S_ROPE = S_RED + 1024;             // float2 [2 halves of the heads][32]
 constexpr uint32_t S_QROPE = S_ROPE + 512;            // float2 [32]
 constexpr uint32_t S_MISC = S_QROPE + 256;
-constexpr uint32_t kSharedSmemBytes = S_MISC + 64 + 1024;
+constexpr uint32_t S_UNITS = S_MISC + 64;              // SharedUnit [kPlanHere]
+constexpr uint32_t S_SUMS = S_UNITS + kPlanHere * (uint32_t)sizeof(SharedUnit);  // int64 [4], int [4], SharedRun [2]
+constexpr uint32_t kSharedSmemBytes = S_SUMS + 96 + 1024;
 static_assert(kSharedSmemBytes <= 232448, "shared memory");
 
 enum SBar : uint32_t { bFull = 0, bEmpty = 7, bQFull = 14, bQEmpty = 15, bScores = 16, bWeights = 18, bPFree = 19, bOFree = 20, bDrained = 21, bEdge = 22, kSBars = 28 };
@@ -546,13 +540,24 @@ struct SharedWalk {
   int64_t left;  // tiles of the run that are left, this unit's included
   int unit, first, last;
   bool begins, ends;
+  const SharedUnit* units;
   SharedUnit u;
-  __device__ __forceinline__ void start(const SharedStart* at) {
+  // from the plan in memory
+  __device__ __forceinline__ void start(const SharedUnit* all, const SharedStart* at) {
+    units = all;
     const int4 a = *reinterpret_cast<const int4*>(at);
     left = (int64_t)(uint32_t)a.x | (int64_t)a.y << 32;
     unit = uniform(a.z);
     first = uniform(a.w);
     if (left > 0) load(&at->u);
+  }
+  // from the CTA's own
+  __device__ __forceinline__ void start(const SharedUnit* all, const SharedRun& r, int64_t tiles) {
+    units = all;
+    left = tiles;
+    unit = uniform(r.unit);
+    first = uniform(r.first);
+    if (left > 0) load(units + unit);
   }
   __device__ __forceinline__ void load(const SharedUnit* at) {
     u = load_unit(at);
@@ -560,11 +565,11 @@ struct SharedWalk {
     last = uniform((int)min((int64_t)u.tiles, first + left));
     ends = uniform(last == u.tiles);
   }
-  __device__ __forceinline__ bool next(const SharedParams& p) {
+  __device__ __forceinline__ bool next() {
     left -= last - first;
     ++unit;
     first = 0;
-    if (left > 0) load(p.units + unit);
+    if (left > 0) load(units + unit);
     return left > 0;
   }
 };
@@ -659,7 +664,6 @@ struct TileSource {
   int64_t scales;
   uint32_t whole;
 };
-__device__ __forceinline__ int64_t from_lane(int64_t v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }
 
 // fp8 and fp4 rows (pages of eight rows and more). A slot's codes, 128 runs of 64
 // channels, are copied into the end of the slot itself and converted in place,
@@ -859,7 +863,7 @@ __device__ __forceinline__ void produce_codes(const SharedParams& p, uint8_t* sm
       c.slots(2u * (uint32_t)now.n, t, now, false);
       now = ahead;
     }
-  } while (walk.next(p));
+  } while (walk.next());
   c.flush();
 }
 
@@ -1001,7 +1005,7 @@ __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm,
       values(t, now);
       now = ahead;
     }
-  } while (walk.next(p));
+  } while (walk.next());
 }
 
 // Q of this CTA's query: plain blocks by TMA, the rope block rotated and split
@@ -1066,7 +1070,7 @@ __device__ __forceinline__ void q_role(const SharedParams& p, uint8_t* sm, uint3
     }
     if (live) warp_arrive_cluster(bar);
     ++seg;
-  } while (walk.next(p));
+  } while (walk.next());
 }
 
 // The pair's products, by a warp of CTA 0.
@@ -1173,7 +1177,7 @@ __device__ __forceinline__ void issue_shared(const SharedParams& p, uint32_t bas
         ++done;
       }
       ++seg;
-    } while (walk.next(p));
+    } while (walk.next());
   }
   if (!live) {  // products still in flight land before tensor memory is freed
     commit_pair(leader, bars + 8 * bDrained);
@@ -1382,7 +1386,70 @@ __device__ __forceinline__ void math_shared(const SharedParams& p, uint8_t* sm, 
     tc_fence_before();  // O has been read
     warp_arrive_cluster(o_free);
     sync_half();  // red and the rope table are free for the next unit
-  } while (walk.next(p));
+  } while (walk.next());
+}
+
+// The plan of up to kPlanHere places by the CTA's own threads, and this pair's run.
+__device__ __forceinline__ void plan_here(const SharedParams& p, uint8_t* sm, SharedWalk& walk, int c, int rank) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = kPlanHere / 32;
+  SharedUnit* units = reinterpret_cast<SharedUnit*>(sm + S_UNITS);
+  int64_t* sum_t = reinterpret_cast<int64_t*>(sm + S_SUMS);
+  int* sum_u = reinterpret_cast<int*>(sm + S_SUMS + 32);
+  SharedRun* cut = reinterpret_cast<SharedRun*>(sm + S_SUMS + 48);
+  PlanUnit one;
+  one.begins = false;
+  uint32_t bad = 0;
+  int64_t it = 0;
+  int iu = 0;
+  if (warp < kWarps) {
+    if (tid < p.n_query) one = unit_at(p, tid, bad);
+    if (bad && blockIdx.x == 0) set_flag(p.flags, bad);
+    it = one.begins ? one.u.tiles : 0;
+    iu = one.begins ? 1 : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t a = __shfl_up_sync(0xffffffffu, it, o);
+      const int b = __shfl_up_sync(0xffffffffu, iu, o);
+      if (lane >= o) it += a, iu += b;
+    }
+    if (lane == 31) sum_t[warp] = it, sum_u[warp] = iu;
+  }
+  __syncthreads();
+  int64_t T = 0, t0 = it - (one.begins ? one.u.tiles : 0);
+  int U = 0, u0 = iu - (one.begins ? 1 : 0);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) t0 += sum_t[w], u0 += sum_u[w];
+    T += sum_t[w];
+    U += sum_u[w];
+  }
+  const RunLine line(T, U, p.pairs);
+  if (tid == 0) {
+    if (c >= line.runs) cut[0] = SharedRun{T, U, 0};
+    if (c + 1 >= line.runs) cut[1] = SharedRun{T, U, 0};
+  }
+  if (one.begins) {
+    units[u0] = one.u;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int64_t y = (c + e) * line.cost;
+      if (c + e < line.runs && y >= line.at(t0, u0) && y < line.at(t0 + one.u.tiles, u0 + 1)) {
+        const int64_t j = line.tile_from(c + e, t0, u0);
+        cut[e] = j < one.u.tiles ? SharedRun{t0 + j, u0, (int32_t)j} : SharedRun{t0 + one.u.tiles, u0 + 1, 0};
+      }
+    }
+  }
+  __syncthreads();
+  const SharedRun from = cut[0], to = cut[1];
+  // a unit that begins in this run and goes on
+  const bool goes_on = one.begins && t0 >= from.tile && t0 < to.tile && t0 + one.u.tiles > to.tile;
+  const bool any = __syncthreads_or(goes_on) != 0;
+  if (rank == 0) {
+    if (goes_on) p.joins[c] = make_int4(one.u.q[0], one.u.q[1], c, line.run_of(t0, u0, one.u.tiles - 1));
+    else if (!any && tid == 0) p.joins[c] = make_int4(-1, -1, -1, 0);
+  }
+  walk.start(units, from, to.tile - from.tile);
 }
 
 template <int KVF, bool TMA>
@@ -1420,7 +1487,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SharedRoles<TMA>::kT
   const uint32_t tmem_o = tmem, tmem_s = tmem + 256;
   pdl_wait();
   SharedWalk walk;
-  walk.start(p.starts + c);
+  if (p.planned) walk.start(p.units, p.starts + c);
+  else plan_here(p, sm, walk, c, rank);
   if (warp < kMathWarps) {
     math_shared(p, sm, base_s, tmem_s, tmem_o, walk, c, warp, rank);
   } else if (warp < Roles::kQ) {
@@ -1621,8 +1689,11 @@ cudaError_t launch_attend_shared(cudaStream_t st, int num_sms, int kv_fmt, const
     e = encode_byte_map(&p.code_map, 3, kv.pages, c_dims, c_strides, c_box);
   }
   if (e != cudaSuccess) return e;
-  e = launch_ex(attend_shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, true, 0, p);
-  if (e != cudaSuccess) return e;
+  p.planned = a.n_query > kPlanHere;
+  if (p.planned) {
+    e = launch_ex(attend_shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, true, 0, p);
+    if (e != cudaSuccess) return e;
+  }
 #define CSA2_SHARED(F, T)                                                                                               \
   do {                                                                                                                 \
     e = cudaFuncSetAttribute(attend_shared_kernel<F, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSharedSmemBytes); \
@@ -1643,7 +1714,7 @@ cudaError_t launch_attend_shared(cudaStream_t st, int num_sms, int kv_fmt, const
   else
     e = launch_ex(attend_shared_join_kernel<1>, dim3((unsigned)p.pairs, kDim / kJoinDims / 4, 2), dim3(256), 0, st, true, 0, p);
   if (e != cudaSuccess) return e;
-  *n_launch += 3;
+  *n_launch += p.planned ? 3 : 2;
   return cudaGetLastError();
 }
 
