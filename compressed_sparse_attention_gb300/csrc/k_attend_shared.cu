@@ -96,7 +96,8 @@ struct SharedParams {
   int planned;  // whether a launch of its own has made the plan (units, starts, joins)
   SharedUnit* units;
   SharedStart* starts;  // [pairs]
-  int4* joins;       // [pairs]: of a unit that run c begins and does not end its queries, c and its last run; third -1: none
+  int4* joins;       // [min(n_query, pairs)]: of a split unit its queries, first and last run; third -1: none. The index is
+                     // the unit, or with as many queries as pairs or more the run that begins it and does not end it
   float* part_o;     // [2 pairs slots][2][512 / 4][64 heads][4]
   float2* part_ml;   // [2 pairs slots][2][64]: reference and sum
 };
@@ -1444,10 +1445,13 @@ __device__ __forceinline__ void plan_here(const SharedParams& p, uint8_t* sm, Sh
   const SharedRun from = cut[0], to = cut[1];
   // a unit that begins in this run and goes on
   const bool goes_on = one.begins && t0 >= from.tile && t0 < to.tile && t0 + one.u.tiles > to.tile;
-  const bool any = __syncthreads_or(goes_on) != 0;
-  if (rank == 0) {
-    if (goes_on) p.joins[c] = make_int4(one.u.q[0], one.u.q[1], c, line.run_of(t0, u0, one.u.tiles - 1));
-    else if (!any && tid == 0) p.joins[c] = make_int4(-1, -1, -1, 0);
+  const int4 jn = goes_on ? make_int4(one.u.q[0], one.u.q[1], c, line.run_of(t0, u0, one.u.tiles - 1)) : make_int4(-1, -1, -1, 0);
+  if (p.n_query >= p.pairs) {
+    const bool any = __syncthreads_or(goes_on) != 0;
+    if (rank == 0 && (goes_on || (!any && tid == 0))) p.joins[c] = jn;
+  } else if (rank == 0) {
+    if (one.begins && t0 >= from.tile && t0 < to.tile) p.joins[u0] = jn;
+    if (c == 0 && tid >= U && tid < p.n_query) p.joins[tid] = make_int4(-1, -1, -1, 0);
   }
   walk.start(units, from, to.tile - from.tile);
 }
@@ -1689,7 +1693,8 @@ cudaError_t launch_attend_shared(cudaStream_t st, int num_sms, int kv_fmt, const
     e = encode_byte_map(&p.code_map, 3, kv.pages, c_dims, c_strides, c_box);
   }
   if (e != cudaSuccess) return e;
-  p.planned = a.n_query > kPlanHere;
+  p.planned = a.n_query > kPlanHere;  // (then there are as many queries as pairs: kPlanHere is more than those)
+  static_assert(kPlanHere >= kMaxPairs2);
   if (p.planned) {
     e = launch_ex(attend_shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, true, 0, p);
     if (e != cudaSuccess) return e;
@@ -1707,12 +1712,13 @@ cudaError_t launch_attend_shared(cudaStream_t st, int num_sms, int kv_fmt, const
   else CSA2_SHARED(2, false);
 #undef CSA2_SHARED
   if (e != cudaSuccess) return e;
-  // few queries: many parts a unit, few units to be joined
+  // few queries: many parts a unit, few units to be joined (CTAs without one cost
+  // their start, 1.6 ns each)
   const unsigned joins = (unsigned)std::min(p.pairs, p.n_query);
   if (4 * joins <= (unsigned)p.pairs)
-    e = launch_ex(attend_shared_join_kernel<4>, dim3((unsigned)p.pairs, kDim / kJoinDims, 2), dim3(256), 0, st, true, 0, p);
+    e = launch_ex(attend_shared_join_kernel<4>, dim3(joins, kDim / kJoinDims, 2), dim3(256), 0, st, true, 0, p);
   else
-    e = launch_ex(attend_shared_join_kernel<1>, dim3((unsigned)p.pairs, kDim / kJoinDims / 4, 2), dim3(256), 0, st, true, 0, p);
+    e = launch_ex(attend_shared_join_kernel<1>, dim3(joins, kDim / kJoinDims / 4, 2), dim3(256), 0, st, true, 0, p);
   if (e != cudaSuccess) return e;
   *n_launch += p.planned ? 3 : 2;
   return cudaGetLastError();
