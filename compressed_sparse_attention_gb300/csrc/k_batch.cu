@@ -43,6 +43,8 @@ __global__ void __launch_bounds__(kBatchThreads) batch_tables_kernel(const __gri
   __shared__ int64_t sums[kBatchThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   uint32_t bad = 0;
+  pdl_trigger();
+  pdl_wait();
   if ((int)blockIdx.x >= p.tok_ctas) {
     const int64_t at = (int64_t)blockIdx.x - p.tok_ctas;
     const int i = (int)(at / p.row_ctas), c0 = (int)(at % p.row_ctas) * kRowCols;
@@ -84,8 +86,7 @@ __global__ void __launch_bounds__(kBatchThreads) batch_tables_kernel(const __gri
       all += sums[w];
     }
     // A request whose tokens do not all fit has none, nor has any later one:
-    // `end` is the end of the last that fits.
-    int64_t end = full ? before : -1;
+    // the next one's offset is the end of the last that fits.
 #pragma unroll
     for (int k = 0; k < kPer; ++k) {
       const int e = kPer * tid + k;
@@ -104,7 +105,7 @@ __global__ void __launch_bounds__(kBatchThreads) batch_tables_kernel(const __gri
         if (off[mid] <= p.max_tokens) lo = mid;
         else hi = mid;
       }
-      end = off[lo];
+      const int64_t end = off[lo];
       __syncthreads();
       for (int e = lo + tid; e <= kBatchReqs; e += kBatchThreads) off[e] = end;
       if (blockIdx.x == 0 && tid == 0) bad |= CSA2_FLAG_BATCH_FULL;
@@ -161,8 +162,7 @@ cudaError_t launch_batch_tables(cudaStream_t st, BatchParams p) {
   const int64_t ctas = tok + (int64_t)p.n_req * p.row_ctas;
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
   p.tok_ctas = (int)tok;
-  batch_tables_kernel<<<(unsigned)ctas, kBatchThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  return launch_ex(batch_tables_kernel, dim3((unsigned)ctas), dim3(kBatchThreads), 0, st, true, 0, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -187,6 +187,35 @@ __device__ __forceinline__ int64_t whole_pages(const GroupParams& p, int i, int3
   const int64_t t = p.q_pos[i];
   seq = b >= 0 && b < p.n_seq && t >= 0 ? b : -1;
   return seq < 0 ? 0 : min((t + 1) >> p.page_shift, (int64_t)p.max_pages);
+}
+
+// The columns at which the rows of queries i and j (both keyed: both have
+// sequences) name the same page, from the first column on, bounded by the whole
+// pages that both see; by a warp.
+__device__ __forceinline__ int64_t common_columns(const GroupParams& p, int i, int j, int lane) {
+  int32_t seq, first;
+  const int64_t mine = whole_pages(p, i, seq);
+  const int64_t run = min(mine, whole_pages(p, j, first));
+  const int32_t* a = p.table + (int64_t)seq * p.table_ld;
+  const int32_t* b = p.table + (int64_t)first * p.table_ld;
+  constexpr int kAhead = 4;
+  for (int64_t c0 = 0; c0 < run; c0 += 32 * kAhead) {
+    int32_t x[kAhead], y[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t c = c0 + 32 * u + lane;
+      x[u] = c < run ? a[c] : -1;
+      y[u] = c < run ? b[c] : -1;
+    }
+    int64_t stop = run;
+#pragma unroll
+    for (int u = kAhead - 1; u >= 0; --u) {
+      const uint32_t off = __ballot_sync(0xffffffffu, x[u] != y[u] || (uint32_t)x[u] >= (uint32_t)p.n_pages);
+      if (off) stop = min(run, c0 + 32 * u + __ffs((int)off) - 1);
+    }
+    if (stop < run) return stop;
+  }
+  return run;
 }
 
 }  // namespace
@@ -310,53 +339,14 @@ __global__ void __launch_bounds__(kGroupThreads, 1) query_groups_kernel(const __
   if (tid == 0 && p.n_groups != nullptr) *p.n_groups = groups;
 }
 
-// A warp a place: the columns at which its query's row and its group's first
-// one name the same page, from the first column on, bounded by the whole pages
-// that the query sees.
+// A warp a place: the common run of its query and its group's first.
 __global__ void __launch_bounds__(256) query_groups_run_kernel(const __grid_constant__ GroupParams p) {
   const int lane = threadIdx.x & 31, k = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
   pdl_wait();
   if (k >= p.n_query) return;
   const int h = p.head[k];
   if (h == k) return;
-  int32_t seq, first;
-  const int i = p.order[k], j = p.order[h];
-  const int64_t mine = whole_pages(p, i, seq);
-  int64_t run = min(mine, whole_pages(p, j, first));  // (both keyed: both have sequences)
-  const int32_t* a = p.table + (int64_t)seq * p.table_ld;
-  const int32_t* b = p.table + (int64_t)first * p.table_ld;
-  constexpr int kAhead = 4;
-  if (seq != first) {
-    for (int64_t c0 = 0; c0 < run; c0 += 32 * kAhead) {
-      int32_t x[kAhead], y[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int64_t c = c0 + 32 * u + lane;
-        x[u] = c < run ? a[c] : -1;
-        y[u] = c < run ? b[c] : -1;
-      }
-      int64_t stop = run;
-#pragma unroll
-      for (int u = kAhead - 1; u >= 0; --u) {
-        const uint32_t off = __ballot_sync(0xffffffffu, x[u] != y[u] || (uint32_t)x[u] >= (uint32_t)p.n_pages);
-        if (off) stop = c0 + 32 * u + __ffs((int)off) - 1;
-      }
-      if (stop < run) {
-        run = stop;
-        break;
-      }
-    }
-  } else {
-    // one sequence twice: the pages that are there
-    for (int64_t c0 = 0; c0 < run; c0 += 32) {
-      const int64_t c = c0 + lane;
-      const uint32_t off = __ballot_sync(0xffffffffu, c >= run || (uint32_t)a[c] >= (uint32_t)p.n_pages);
-      if (off) {
-        run = min(run, c0 + __ffs((int)off) - 1);
-        break;
-      }
-    }
-  }
+  const int64_t run = common_columns(p, p.order[k], p.order[h], lane);
   if (lane == 0) atomicMin(reinterpret_cast<long long*>(p.shared + h), (long long)(run << p.page_shift));
 }
 
@@ -364,7 +354,9 @@ cudaError_t launch_query_groups(cudaStream_t st, const GroupParams& p) {
   int slots = 64;
   while (slots < 2 * p.n_query) slots *= 2;
   const size_t smem = query_groups_smem(p.n_query);
-  cudaError_t e = cudaFuncSetAttribute(query_groups_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)query_groups_smem(kMaxGroupQueries));
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024)
+    e = cudaFuncSetAttribute(query_groups_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)query_groups_smem(kMaxGroupQueries));
   if (e != cudaSuccess) return e;
   e = launch_ex(query_groups_kernel, dim3(1), dim3(kGroupThreads), smem, st, true, 0, p, slots);
   if (e != cudaSuccess) return e;

@@ -367,6 +367,8 @@ __global__ void __launch_bounds__(256) append_slots_kernel(const T* __restrict__
                                                            const RopeParams rp, uint32_t* flags) {
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  pdl_trigger();
+  pdl_wait();
   if (row >= n_rows) return;
   const int64_t slot = slots[row], p = pos != nullptr ? pos[row] : 0;
   float v[16];
@@ -435,7 +437,7 @@ cudaError_t launch_append_slots(cudaStream_t st, int dtype, const void* rows, in
   if ((n_rows + 7) / 8 > 0x7FFFFFFF) return cudaErrorInvalidValue;
   const dim3 grid((unsigned)((n_rows + 7) / 8));
 #define CSA2_APPEND(T, F) \
-  append_slots_kernel<T, F><<<grid, 256, 0, st>>>(static_cast<const T*>(rows), n_rows, pos, slots, kv, rp, flags)
+  return launch_ex(append_slots_kernel<T, F>, grid, dim3(256), 0, st, true, 0, static_cast<const T*>(rows), n_rows, pos, slots, kv, rp, flags)
 #define CSA2_APPEND_F(T)                \
   do {                                  \
     if (kv_fmt == 0) CSA2_APPEND(T, 0); \
@@ -446,7 +448,6 @@ cudaError_t launch_append_slots(cudaStream_t st, int dtype, const void* rows, in
   else CSA2_APPEND_F(uint16_t);
 #undef CSA2_APPEND_F
 #undef CSA2_APPEND
-  return cudaGetLastError();
 }
 
 }  // namespace csa2
