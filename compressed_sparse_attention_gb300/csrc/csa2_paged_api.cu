@@ -276,6 +276,11 @@ csa2_status csa2_batch_tables(csa2_ctx* ctx, void* stream, const csa2_page_pool*
   if (batch->max_tokens > 0 && (!batch->req_of_tok || !batch->tok_pos || !batch->tok_slot || !aligned(batch->req_of_tok, 4) ||
                                 !aligned_all(8, batch->tok_pos, batch->tok_slot)))
     return fail(ctx, CSA2_ERR_INVALID_ARG, "batch_tables: null or misaligned token arrays");
+  // rows are copied by many CTAs at once: from one table into another
+  const uint64_t pb = reinterpret_cast<uintptr_t>(pool->table), bb = reinterpret_cast<uintptr_t>(batch->table);
+  const uint64_t pe = pb + 4 * ((uint64_t)(pool->n_seq - 1) * (uint64_t)pool->table_ld + (uint64_t)pool->max_pages);
+  const uint64_t be = bb + 4 * ((uint64_t)std::max(n_req - 1, 0) * (uint64_t)batch->table_ld + (uint64_t)pool->max_pages);
+  if (n_req > 0 && pb < be && bb < pe) return fail(ctx, CSA2_ERR_INVALID_ARG, "batch_tables: the batch's table overlaps the pool's");
   p.seqs = seqs;
   p.n_new = n_new;
   p.table = batch->table;

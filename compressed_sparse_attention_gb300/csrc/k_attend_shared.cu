@@ -24,9 +24,22 @@
 //
 // Tile: 256 rows of the unit's list, which are groups of 64 aligned positions:
 // those that both queries see, then those that only the first sees, then the
-// second's. Products of a group that one query does not see leave the other
+// second's. Products of a group that one query does not see leave that query's
 // CTA's lanes of O alone (disable-output-lane), so that a NaN in a row reaches
 // only the queries that see it.
+//
+// What bounds it. A tile's products run 4,352 cycles at best (36 of N = 256 and
+// K = 16 for S, rope residual included, 32 for O, 64 cycles each; all operations
+// would take 4,096). Their operands take 3,264 of shared memory's cycles and
+// what is copied into it and written as weights 2,300: 5,570 together. Measured
+// tiles take 5,700 to 5,900 in a long run: 64 queries over 32K common bf16 rows
+// 171 us, 1.62 PFLOP/s, where csa2_attend_paged takes 332. The ring's seven slots
+// just cover a copy's 1,100 to 1,500 cycles: what was between the products at
+// first (copies looked up behind the wait for a slot, arrivals with a cluster-wide
+// release, a barrier not looked at ahead: 9,800 cycles a tile) is off that path.
+// fp8 and fp4 rows: their conversion, 14,400 cycles a tile. Short calls: plan 2.2
+// us, Q 2, a tile's scores, first weights and products 4.5, partial 2 (128 KB a
+// CTA, 32 bytes a clock), join 5: four queries over 2K rows 18.8 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <type_traits>
@@ -42,7 +55,7 @@ constexpr int kGroupRows = 64;   // aligned positions of a row group
 constexpr int kTileGroups = 4;   // row groups of a tile
 constexpr int kRing = 7;         // slots
 constexpr uint32_t kSlotBytes = 16384;
-constexpr int kMaxPairs2 = 80;   // pairs of CTAs, at most
+constexpr int kMaxCtaPairs = 80;   // pairs of CTAs, at most
 constexpr int kPlanThreads = 1024;
 
 // Two places of a group (or its last one alone).
@@ -117,30 +130,30 @@ __host__ __device__ __forceinline__ int piece_shift(int page_shift) { return pag
 // its own, a thread a share of the places (a launch, and what it costs to hand
 // the plan over, 3 us of a call).
 //
-// On a line where a tile is kTileCost2 long and a unit starts with kUnitCost, run
+// On a line where a tile is kTilePlace long and a unit starts with kUnitPlace, run
 // c has the tiles that start in the c-th of R equal parts (a part inside a unit's
 // start has none).
 // ---------------------------------------------------------------------------
-constexpr int kTileCost2 = 4, kUnitCost = 8;  // a unit: its Q, its first weights, its outputs
+constexpr int kTilePlace = 4, kUnitPlace = 8;  // a unit: its Q, its first weights, its outputs
 constexpr int kPlanHere = 96;                 // units that fit shared memory beside the tiles
 struct RunLine {
   int64_t cost;
   int runs, start;
   __device__ __forceinline__ RunLine(int64_t tiles, int units, int pairs) {
-    start = tiles > 2 * (int64_t)pairs ? kUnitCost : 0;
-    cost = kTileCost2 * tiles + (int64_t)start * units;
+    start = tiles > 2 * (int64_t)pairs ? kUnitPlace : 0;
+    cost = kTilePlace * tiles + (int64_t)start * units;
     runs = (int)min((int64_t)pairs, tiles);
   }
   // where unit u begins, t tiles coming before it, runs-fold
-  __device__ __forceinline__ int64_t at(int64_t t, int u) const { return runs * (kTileCost2 * t + (int64_t)start * u); }
+  __device__ __forceinline__ int64_t at(int64_t t, int u) const { return runs * (kTilePlace * t + (int64_t)start * u); }
   // of unit u the first tile from cut c on
   __device__ __forceinline__ int64_t tile_from(int c, int64_t t, int u) const {
-    const int64_t left = c * cost - at(t, u + 1), step = (int64_t)kTileCost2 * runs;
+    const int64_t left = c * cost - at(t, u + 1), step = (int64_t)kTilePlace * runs;
     return left <= 0 ? 0 : quotient(left + step - 1, step);
   }
   // run of tile j of unit u
   __device__ __forceinline__ int run_of(int64_t t, int u, int j) const {
-    return (int)quotient(at(t, u + 1) + (int64_t)kTileCost2 * runs * j, cost);
+    return (int)quotient(at(t, u + 1) + (int64_t)kTilePlace * runs * j, cost);
   }
 };
 
@@ -220,7 +233,7 @@ __device__ __forceinline__ PlanUnit unit_at(const SharedParams& p, int k, uint32
 __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(const __grid_constant__ SharedParams p) {
   __shared__ int64_t sum_t[32], share_t[kPlanThreads];  // tiles, units before a thread's share
   __shared__ int sum_u[32], share_u[kPlanThreads];
-  __shared__ SharedRun runs[kMaxPairs2 + 1];
+  __shared__ SharedRun runs[kMaxCtaPairs + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
   pdl_wait();
@@ -590,7 +603,8 @@ struct RingAt {
   }
 };
 
-// A slot's rows by the warp itself. K: channels 64 b .. of the 128 rows of the
+// A slot's rows by the warp itself: pages of less than the eight rows of a copy's
+// swizzle atom, row by row. K: channels 64 b .. of the 128 rows of the
 // tile's groups 2 rank and 2 rank + 1; V: dims d0 .. d0 + 127 of group g's 64
 // rows. Rows that are not the group's become zeros (in V: their weights are 0,
 // but 0 times a NaN is not).
@@ -1519,7 +1533,7 @@ constexpr int kJoinDims = 16;
 constexpr int kJoinParts = 2;  // whose values are under way at once
 template <int GROUPS>
 __global__ void __launch_bounds__(256, 4) attend_shared_join_kernel(const __grid_constant__ SharedParams p) {
-  __shared__ float2 weight[kMaxPairs2][kHeads];  // reference and sum, then the weight
+  __shared__ float2 weight[kMaxCtaPairs][kHeads];  // reference and sum, then the weight
   __shared__ float red[2][4][kHeads];
   __shared__ float2 turn[32];
   const int head = threadIdx.x & 63, quarter = threadIdx.x >> 6, rank = (int)blockIdx.z, group = GROUPS == 1 ? 0 : quarter;
@@ -1633,7 +1647,7 @@ __global__ void __launch_bounds__(256, 4) attend_shared_join_kernel(const __grid
 constexpr size_t al256(size_t x) { return (x + 255) & ~(size_t)255; }
 }  // namespace
 
-static int attend_shared_pairs(int num_sms) { return std::min(num_sms / 2, kMaxPairs2); }
+static int attend_shared_pairs(int num_sms) { return std::min(num_sms / 2, kMaxCtaPairs); }
 
 size_t attend_shared_workspace_bytes(int num_sms, int n_query) {
   const size_t pairs = (size_t)attend_shared_pairs(num_sms), slots = 4 * pairs;
@@ -1694,7 +1708,7 @@ cudaError_t launch_attend_shared(cudaStream_t st, int num_sms, int kv_fmt, const
   }
   if (e != cudaSuccess) return e;
   p.planned = a.n_query > kPlanHere;  // (then there are as many queries as pairs: kPlanHere is more than those)
-  static_assert(kPlanHere >= kMaxPairs2);
+  static_assert(kPlanHere >= kMaxCtaPairs);
   if (p.planned) {
     e = launch_ex(attend_shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, st, true, 0, p);
     if (e != cudaSuccess) return e;

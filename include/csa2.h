@@ -761,7 +761,9 @@ csa2_status csa2_pages_compact(csa2_ctx* ctx, void* stream, const csa2_page_pool
  * be carried out (another sequence out of range, n_new negative or above the
  * length, a length past the table) neither, recorded as CSA2_FLAG_BAD_SEQ. A
  * request whose tokens do not all fit into max_tokens has none, nor has any later
- * one (CSA2_FLAG_BATCH_FULL). Two requests may name one sequence. One launch. */
+ * one (CSA2_FLAG_BATCH_FULL). Two requests may name one sequence. `table` must
+ * not overlap the pool's (refused). n_req at most 2^20, max_tokens at most 2^32.
+ * One launch. */
 typedef struct csa2_batch {
   int32_t* table;
   int64_t table_ld;
@@ -809,7 +811,8 @@ csa2_status csa2_query_groups(csa2_ctx* ctx, void* stream, const int32_t* table,
  *   is recorded as CSA2_FLAG_BAD_QUERY and skipped, and so is a place whose
  *   group does not begin where head says). A query at no place keeps its out.
  * Results do not depend on timing. The limits on the size of rows are
- * csa2_attend_paged's. n_query at most 2^20. Three launches.
+ * csa2_attend_paged's. n_query at most 2^20. Two launches, three for more than 96
+ * queries.
  *   workspace of csa2_attend_shared_workspace_size bytes; calls that may overlap
  *   on the GPU need one each
  * q, pages, scales and out must be 16-byte aligned; out must not overlap q. */

@@ -501,3 +501,106 @@ def test_many_queries():
     c = Case([(0, [40 + rng.randint(0, 100)]) for _ in range(50)], page=16, seed=38,
              queries=[(i % 50, rng.randint(0, 39)) for i in range(n)])
     c.run().check(only=rng.sample(range(n), 40))
+
+
+@pytest.mark.parametrize("n", [75, 76, 77, 95, 96, 97, 200])
+def test_numbers_of_queries_around_the_plans(n):
+    # the plan is made by every pair of CTAs or by a launch of its own, and joins are kept by unit or by run
+    rng = random.Random(n)
+    groups, left = [], n
+    while left:
+        k = min(left, rng.choice([1, 1, 2, 3, 8, 20]))
+        whole = rng.choice([0, 3, 12, 60])
+        groups.append((whole, [16 * whole + rng.randint(1, 300) for _ in range(k)]))
+        left -= k
+    c = Case(groups, page=16, seed=n, shuffle=True).run()
+    c.check(only=rng.sample(range(n), 30))
+
+
+@pytest.mark.parametrize("n", [100, 1100, 2300])
+def test_one_long_query_among_many_short_ones(n):
+    # units that other runs begin and end in, and one over many pairs of CTAs
+    lens = [9000] + [1 + i % 40 for i in range(19)]
+    queries = [(1 + i % 19, (i % 19) % 40) for i in range(n - 1)]
+    queries.insert(n // 2, (0, 8999))
+    c = Case([(0, [m]) for m in lens], page=16, seed=n, queries=queries)
+    c.run().check(only=[0, 1, n // 2 - 1, n // 2, n // 2 + 1, n - 1])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+def test_groups_ends_in_every_place_of_a_page(fmt):
+    # tails that end 1 .. 64 rows into their last group, in one call
+    Case([(4, [256 + 1 + i for i in range(0, 64, 3)])], fmt=fmt, page=64, seed=40).run().check()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("page", [8, 32, 128, 4096])
+def test_empty_and_single_row_queries_beside_long_ones(fmt, page):
+    Case([(0, [1, 2 * page, 300])], fmt=fmt, page=page, queries=[(0, -1), (2, 299), (0, 0), (1, 0), (1, 2 * page - 1), (2, 64)],
+         seed=41).run().check()
+
+
+@pytest.mark.parametrize("fmt", ["fp8", "fp4"])
+def test_nan_codes_are_not_numbers(fmt):
+    # a visible row of NaN codes or scales reaches the queries that see it, and no others
+    c = Case([(3, [64 * 3 + 20, 64 * 3 + 50, 64 * 3 + 5])], fmt=fmt, page=64, seed=42)
+    clean = page_values(c.codes, c.scales, c.fmt)
+    at = c.lens[1] - 2
+    (c.codes if fmt == "fp8" else c.scales)[c.table_rows[1][at // 64], at % 64] = 0x7F
+    c.run().check(only=[0, 2], values=clean)
+    assert torch.isnan(c.out[1]).any()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_the_first_call_of_a_host_thread(fmt):
+    import threading
+    c = Case([(3, [100, 200])], fmt=fmt, page=16, seed=43).run()
+    want, call, bad = c.out.clone(), c.call(), []
+    c.out.zero_()
+    torch.cuda.synchronize()
+
+    def work():
+        try:
+            call.run()
+        except Exception as e:  # noqa: BLE001
+            bad.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not bad, bad
+    assert torch.equal(c.out, want)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+def test_agrees_with_attend_paged_on_its_own_groups(fmt):
+    """Groups found by csa2_query_groups, the result against csa2_attend_paged's
+    on the same queries: both within their bounds of the exact result."""
+    c = Case([(7, [16 * 7 + 30, 16 * 7 + 9, 16 * 7 + 77]), (5, [16 * 5 + 3, 16 * 5 + 40]), (0, [90])], fmt=fmt, page=16, per=2, seed=44)
+    n = len(c.seq)
+    order, head = torch.empty(n, dtype=torch.int32, device=DEV), torch.empty(n, dtype=torch.int32, device=DEV)
+    shared = torch.empty(n, dtype=torch.int64, device=DEV)
+    c.ctx.query_groups(c.table, 16, c.codes.shape[0], c.pos_d, c.seq_d, 40, order, head, shared)
+    c.order, c.head, c.shared = order.tolist(), head.tolist(), shared.tolist()
+    assert c.shared[0] == 16 * 7 and c.shared[6] == 16 * 5
+    c.plan()
+    c.run().check()
+    out, lse = torch.empty_like(c.out), torch.empty_like(c.lse)
+    ws = c.b.workspace(c.ctx.attend_paged_workspace_size(n), DEV)
+    c.ctx.attend_paged(c.kv, c.q, c.pos_d, c.seq_d, out, ws, sink=c.sink, lse=lse)
+    # twice attend_one's lse bound: 40 U32 of a score's sum of sizes (below 64 here), 2^-21 and 8 U32 of its own size
+    assert ((lse - c.lse).abs() <= 2 * (40 * U32 * 64 + 2.0 ** -16 * 4 + 2.0 ** -21 + 8 * U32 * (1 + lse.abs()))).all()
+
+
+def test_misaligned_buffers_are_refused():
+    c = Case([(1, [20, 30])])
+    lib, p = c.b.load_library(), lambda t: t.data_ptr()
+    import ctypes as C
+    good = [p(c.q), p(c.pos_d), p(c.seq_d), p(c.order_d), p(c.head_d), p(c.shared_d), p(c.sink), p(c.out), p(c.lse)]
+    for i, step in enumerate((8, 4, 2, 2, 2, 4, 2, 8, 2)):
+        a = list(good)
+        a[i] += step
+        st = lib.csa2_attend_shared(c.ctx.h, None, C.byref(c.kv.args), 2, *a, p(c.ws), c.ws.numel())
+        assert st == 1, i
+        assert c.ctx.last_launch_count == 0

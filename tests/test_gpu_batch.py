@@ -530,3 +530,74 @@ def test_a_serving_step_from_lengths_alone(fmt):
     codes2, scales2 = codes.clone(), None if scales is None else scales.clone()
     ctx.append_paged(ctx.paged_kv(codes2, batch["table"], scales2), rows, batch["tok_off"], batch["first_pos"])
     assert torch.equal(codes.view(torch.uint8), codes2.view(torch.uint8))
+
+
+def test_a_batchs_table_over_the_pools_is_refused():
+    p = Pool([20, 30, 40])
+    b = __import__("compressed_sparse_attention_gb300.binding", fromlist=["x"])
+    n, w = 2, len(p.rows[0])
+    both = torch.zeros((6, w), dtype=torch.int32, device=DEV)
+    both[:3] = p.table
+    pool = p.ctx.page_pool(both[:3], p.seq_len, p.ref, p.page)
+    rest = (i64([0] * 3), i64([0] * 2), i32([0] * 4), i64([0] * 4), i64([0] * 4))
+    for at in (0, 1, 2):
+        with pytest.raises(b.Csa2Error, match="overlaps"):
+            p.ctx.batch_tables(pool, i32([0, 1]), i64([1, 1]), both[at:at + 2], *rest)
+    p.ctx.batch_tables(pool, i32([0, 1]), i64([1, 1]), both[3:5], *rest)
+    assert p.ctx.check()[0] == 0 and both[3:5].tolist() == p.rows[:2]
+
+
+def test_batch_calls_from_a_host_thread_without_cuda_calls():
+    import threading
+    p = Pool([20, 30, 10])
+    ctx = p.ctx
+    table, off, first = torch.zeros((2, 2), dtype=torch.int32, device=DEV), i64([0] * 3), i64([0] * 2)
+    req, pos, slot = i32([0] * 4), i64([0] * 4), i64([0] * 4)
+    order, head, shared = i32([0] * 4), i32([0] * 4), i64([0] * 4)
+    pages = torch.zeros((p.n_pages, 16, DIM), dtype=torch.bfloat16, device=DEV)
+    rows = torch.randn((4, DIM), device=DEV).to(torch.bfloat16)
+    calls = [ctx.prepare_batch_tables(p.pool, i32([2, 0]), i64([1, 2]), table, off, first, req, pos, slot),
+             ctx.prepare_append_slots(ctx.paged_kv(pages), rows, pos, slot),
+             ctx.prepare_query_groups(table, 16, p.n_pages, pos, req, 1, order, head, shared)]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        try:
+            for c in calls:
+                c.run()
+        except Exception as e:  # noqa: BLE001
+            bad.append(e)
+
+    t = threading.Thread(target=work)
+    t.start()
+    t.join()
+    torch.cuda.synchronize()
+    assert not bad, bad
+    want = p.plain([2, 0], [1, 2], 4)
+    assert list(zip(req.tolist(), pos.tolist(), slot.tolist())) == want[3]
+    assert order.tolist() == [0, 1, 2, 3] and head.tolist() == [0, 1, 1, 3] and shared.tolist() == [0, 16, 0, 0]
+    assert int((pages != 0).any(-1).sum()) == 3
+
+
+@pytest.mark.parametrize("n", [1, 5, 40])
+def test_two_streams_at_once(n):
+    """Each stream its own context and outputs, one table read by both."""
+    require_gpu()
+    from compressed_sparse_attention_gb300 import binding
+    rows, lens, n_pages = forked(50, 3, 16, 9, n)
+    table, seq, pos = i32(rows), i32(list(range(50))), i64([m - 1 for m in lens])
+    made = []
+    for _ in range(2):
+        ctx = binding.Context()
+        out = [i32([0] * 50), i32([0] * 50), i64([0] * 50), i32([0])]
+        made.append((ctx.prepare_query_groups(table, 16, n_pages, pos, seq, n, *out), out, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for call, _, s in made:
+            with torch.cuda.stream(s):
+                call.run()
+    torch.cuda.synchronize()
+    want = plain_groups(rows, 16, n_pages, pos.tolist(), list(range(50)), n)
+    for _, out, _ in made:
+        assert [o.tolist() for o in out] == [want[0], want[1], want[2], [want[3]]]
