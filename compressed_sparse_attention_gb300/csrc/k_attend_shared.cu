@@ -670,15 +670,51 @@ __device__ __forceinline__ void fill_slot(const SharedParams& p, const SharedUni
 }
 
 // What a tile's producers know of it: the number of its row groups; of lane
-// 8 g + i the page of piece i of group g (the pool's size: none) and the row of
-// it where the piece begins (fp8, fp4: also where its scales do, -1: none); and
-// which groups lie whole in it (bits 8 g).
+// 8 g + i the table's entry for piece i of group g (as it was read; -1: not
+// wanted) and the row of that page where the piece begins; and which groups lie
+// whole in the tile (bits 8 g). Read a tile before it is used, and not touched before
+// that: 800 cycles of a round trip to the L2.
 struct TileSource {
   int n;
-  int32_t page, row;
-  int64_t scales;
+  int32_t entry, row;
   uint32_t whole;
+  // the page, past the end of the pages (where copies read zeros) for none
+  __device__ __forceinline__ int32_t page(const SharedParams& p) const {
+    return (uint32_t)entry < (uint32_t)p.kv.n_pages ? entry : p.kv.n_pages;
+  }
 };
+__device__ __forceinline__ TileSource look_up(const SharedParams& p, const SharedUnit& u, int tile, int lane) {
+  const int pc = piece_shift(p.kv.page_shift);
+  TileSource src;
+  src.n = uniform(row_groups(u, tile));
+  const RowGroup g = row_group(u, kTileGroups * tile + (lane >> 3));
+  const int pos = 64 * g.block + ((lane & 7) << pc), column = pos >> p.kv.page_shift;
+  src.entry = -1;
+  if ((lane & 7) < (kGroupRows >> pc) && g.present && pos < g.to && pos + (1 << pc) > g.from && column < p.kv.max_pages)
+    src.entry = p.kv.table[(int64_t)(max(pos, g.from) < u.len ? u.head_seq : g.seq) * p.kv.table_ld + column];
+  src.row = pos & ((1 << p.kv.page_shift) - 1);
+  src.whole = __ballot_sync(0xffffffffu, (lane & 7) == 0 && g.present && g.from <= 64 * g.block && g.to >= 64 * g.block + 64);
+  return src;
+}
+// A producer's way through its pair's run: keys(tile, source), values(tile,
+// source) in the order of the products, look(tile) a tile ahead of both.
+template <class Look, class Keys, class Values>
+__device__ __forceinline__ void produce_tiles(SharedWalk& walk, Look&& look, Keys&& keys, Values&& values) {
+  do {
+    TileSource now = look(walk.first), ahead = now;
+    if (walk.first + 1 < walk.last) ahead = look(walk.first + 1);
+    keys(walk.first, now);
+#pragma unroll 1
+    for (int t = walk.first; t < walk.last; ++t) {
+      TileSource next = ahead;
+      if (t + 2 < walk.last) next = look(t + 2);
+      if (t + 1 < walk.last) keys(t + 1, ahead);
+      values(t, now);
+      now = ahead;
+      ahead = next;
+    }
+  } while (walk.next());
+}
 
 // fp8 and fp4 rows (pages of eight rows and more). A slot's codes, 128 runs of 64
 // channels, are copied into the end of the slot itself and converted in place,
@@ -736,31 +772,12 @@ struct CodeProducer {
   };
   Asked on{0u, 0u, {0u, 0u, 0u, 0u}, {0u, 0u, 0u, 0u}};
 
-  __device__ __forceinline__ TileSource look_up(int tile) const {
-    const SharedUnit& u = walk.u;
-    TileSource src;
-    src.n = uniform(row_groups(u, tile));
-    const RowGroup g = row_group(u, kTileGroups * tile + (lane >> 3));
-    const int pos = 64 * g.block + ((lane & 7) << pc), in_page = pos & ((1 << p.kv.page_shift) - 1);
-    int32_t page = -1;
-    if ((lane & 7) < pieces && g.present && pos < g.to && pos + (1 << pc) > g.from)
-      page = page_of(p.kv, max(pos, g.from) < u.len ? u.head_seq : g.seq, pos);
-    src.page = page >= 0 ? page : p.kv.n_pages;  // past the end: zeros
-    src.row = in_page;
-    src.scales = page >= 0 ? page * p.kv.scale_stride + (int64_t)in_page * kScaleBytes : -1;
-    src.whole = 0;
-    // (on their way to the L2, half of the tile's rows by either CTA)
-    if (page >= 0 && w == 0 && (lane >> 4) == rank) {
-      prefetch_l2(p.kv.pages + page * p.kv.page_stride + (int64_t)in_page * kRowBytes, (uint32_t)kRowBytes << pc);
-      prefetch_l2(p.kv.scales + src.scales, (uint32_t)kScaleBytes << pc);
-    }
-    return src;
-  }
   // Runs 64 k .. of a slot, k < n: row group g0 + k's (K), or of one group its
   // dims d0 + 64 k .. (V).
   __device__ __forceinline__ void ask(const TileSource& src, int tile, bool is_k, int n, int g0, int d0, uint32_t slot, uint32_t bar) {
     on.slot = slot;
     on.bar = bar;
+    const int32_t page = src.page(p);
     const uint32_t dst = base_s + slot + kSlotBytes - 128u * kRun;
     expect_one(leader, here, 64u * kRun * (uint32_t)n);
 #pragma unroll
@@ -770,16 +787,18 @@ struct CodeProducer {
 #pragma unroll 1
         for (int i = 0; i < pieces; ++i)
           tma_3d_one(leader, dst + (64u * (uint32_t)k + (uint32_t)(i << pc)) * kRun, &p.code_map, ch * (int)kRun / 64,
-                     uniform(src.row, 8 * g + i), uniform(src.page, 8 * g + i), here);
+                     uniform(src.row, 8 * g + i), uniform(page, 8 * g + i), here);
       }
       const RowGroup rg = row_group(walk.u, kTileGroups * tile + g);
       const int from = rg.from - 64 * rg.block, to = k < n && rg.present ? rg.to - 64 * rg.block : 0;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = 32 * i + lane;
-        const int64_t at = __shfl_sync(0xffffffffu, src.scales, 8 * (g & 3) + (r >> pc));
-        const bool there = at >= 0 && r >= from && r < to;
-        const uint8_t* sp = p.kv.scales + at + (uint32_t)((r & ((1 << pc) - 1)) * kScaleBytes + ch / (KVF == 1 ? 32 : 16));
+        const int of = 8 * (g & 3) + (r >> pc);  // the lane that has the run's page
+        const int32_t run_page = __shfl_sync(0xffffffffu, page, of), run_row = __shfl_sync(0xffffffffu, src.row, of);
+        const bool there = run_page < p.kv.n_pages && r >= from && r < to;
+        const uint8_t* sp = p.kv.scales + run_page * p.kv.scale_stride +
+                            (uint32_t)((run_row + (r & ((1 << pc) - 1))) * kScaleBytes + ch / (KVF == 1 ? 32 : 16));
         uint32_t sc = 0u;
         if constexpr (KVF == 1) {
           if (there) sc = __ldg(reinterpret_cast<const uint16_t*>(sp));
@@ -865,20 +884,19 @@ __device__ __forceinline__ void produce_codes(const SharedParams& p, uint8_t* sm
   const int pc = piece_shift(p.kv.page_shift);
   CodeProducer<KVF> c{p, sm, base_s, bars, in_leader(bars + 8 * bFull), elect_one(), bars + 8 * (bEdge + (uint32_t)w), w, rank,
                       (int)(threadIdx.x & 31), pc, kGroupRows >> pc, walk};
-  do {
-    TileSource now = c.look_up(walk.first);
-    c.slots(8, walk.first, now, true);
-#pragma unroll 1
-    for (int t = walk.first; t < walk.last; ++t) {
-      TileSource ahead = now;
-      if (t + 1 < walk.last) {
-        ahead = c.look_up(t + 1);
-        c.slots(8, t + 1, ahead, true);
-      }
-      c.slots(2u * (uint32_t)now.n, t, now, false);
-      now = ahead;
-    }
-  } while (walk.next());
+  produce_tiles(
+      walk,
+      [&](int tile) { return look_up(p, walk.u, tile, c.lane); },
+      [&](int tile, const TileSource& src) {
+        // codes on their way to the L2, half of the tile's rows by either CTA
+        const int32_t page = src.page(p);
+        if (w == 0 && (c.lane >> 4) == rank && page < p.kv.n_pages) {
+          prefetch_l2(p.kv.pages + page * p.kv.page_stride + (int64_t)src.row * c.kRowBytes, (uint32_t)c.kRowBytes << pc);
+          prefetch_l2(p.kv.scales + page * p.kv.scale_stride + (int64_t)src.row * c.kScaleBytes, (uint32_t)c.kScaleBytes << pc);
+        }
+        c.slots(8, tile, src, true);
+      },
+      [&](int tile, const TileSource& src) { c.slots(2u * (uint32_t)src.n, tile, src, false); });
   c.flush();
 }
 
@@ -896,24 +914,9 @@ __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm,
   RingAt base{0, 0};  // the next slot of all warps, and the slots before it
   uint32_t s = 0, edges = 0;
   bool live = true;
-  auto look_up = [&](int tile) {
-    const SharedUnit& u = walk.u;
-    TileSource src;
-    src.n = uniform(row_groups(u, tile));
-    src.page = p.kv.n_pages;  // past the end: zeros
-    src.row = 0;
-    src.scales = -1;
-    src.whole = 0;
-    if (!TMA) return src;
-    const RowGroup g = row_group(u, kTileGroups * tile + (lane >> 3));
-    const int pos = 64 * g.block + ((lane & 7) << pc);
-    if ((lane & 7) < pieces && g.present && pos < g.to && pos + (1 << pc) > g.from) {
-      const int32_t page = page_of(p.kv, max(pos, g.from) < u.len ? u.head_seq : g.seq, pos);
-      if (page >= 0) src.page = page;
-    }
-    src.row = pos & ((1 << ps) - 1);
-    src.whole = __ballot_sync(0xffffffffu, (lane & 7) == 0 && g.present && g.from <= 64 * g.block && g.to >= 64 * g.block + 64);
-    return src;
+  auto look = [&](int tile) {
+    if (TMA) return look_up(p, walk.u, tile, lane);
+    return TileSource{uniform(row_groups(walk.u, tile)), -1, 0, 0u};
   };
   // this warp's slots of the next `count`: fill(i, its place)
   auto each = [&](uint32_t count, auto&& fill) {
@@ -929,7 +932,8 @@ __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm,
   };
   auto keys = [&](int tile, const TileSource& src) {
     const int n = min(2, max(0, src.n - 2 * rank));  // row groups of this CTA's half
-    const int page0 = uniform(src.page, 16 * rank), page1 = uniform(src.page, 16 * rank + 8);
+    const int32_t page = src.page(p);
+    const int page0 = uniform(page, 16 * rank), page1 = uniform(page, 16 * rank + 8);
     const int row0 = uniform(src.row, 16 * rank), row1 = uniform(src.row, 16 * rank + 8);
     each(8, [&](int b, uint32_t bar, uint32_t slot) {
       const uint32_t dst = base_s + slot;
@@ -948,12 +952,13 @@ __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm,
 #pragma unroll 1
           for (int i = 0; i < pieces; ++i)
             tma_pair_3d(leader, dst + 8192u * (uint32_t)g + ((uint32_t)i << (7 + pc)), &p.kv_map, 64 * b, 0,
-                        uniform(src.page, 8 * (2 * rank + g) + i), bar);
+                        uniform(page, 8 * (2 * rank + g) + i), bar);
         }
       }
     });
   };
   auto values = [&](int tile, const TileSource& src) {
+    const int32_t pages = src.page(p);
     each(2 * (uint32_t)src.n, [&](int i, uint32_t bar, uint32_t slot) {
       const int g = i >> 1, d0 = 256 * (i & 1) + 128 * rank;
       const uint32_t dst = base_s + slot;
@@ -971,13 +976,13 @@ __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm,
         const uint32_t here = bars + 8 * (bEdge + (uint32_t)w);
         expect_one(leader, here, kSlotBytes);
         if (pieces == 1) {
-          const int page = uniform(src.page, 8 * g), row = uniform(src.row, 8 * g);
+          const int page = uniform(pages, 8 * g), row = uniform(src.row, 8 * g);
           tma_3d_one(leader, dst, &p.kv_map, d0, row, page, here);
           tma_3d_one(leader, dst + 8192u, &p.kv_map, d0 + 64, row, page, here);
         } else {
 #pragma unroll 1
           for (int k = 0; k < pieces; ++k) {
-            const int page = uniform(src.page, 8 * g + k);
+            const int page = uniform(pages, 8 * g + k);
             tma_3d_one(leader, dst + ((uint32_t)k << (7 + pc)), &p.kv_map, d0, 0, page, here);
             tma_3d_one(leader, dst + 8192u + ((uint32_t)k << (7 + pc)), &p.kv_map, d0 + 64, 0, page, here);
           }
@@ -995,11 +1000,11 @@ __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm,
       }
       expect_cluster_one(leader, bar, kSlotBytes);
       if (pieces == 1) {
-        tma_pair_4d(leader, dst, &p.v_map, 0, uniform(src.row, 8 * g), d0 / 64, uniform(src.page, 8 * g), bar);
+        tma_pair_4d(leader, dst, &p.v_map, 0, uniform(src.row, 8 * g), d0 / 64, uniform(pages, 8 * g), bar);
       } else {
 #pragma unroll 1
         for (int k = 0; k < pieces; ++k) {
-          const int page = uniform(src.page, 8 * g + k);
+          const int page = uniform(pages, 8 * g + k);
           tma_pair_3d(leader, dst + ((uint32_t)k << (7 + pc)), &p.kv_map, d0, 0, page, bar);
           tma_pair_3d(leader, dst + 8192u + ((uint32_t)k << (7 + pc)), &p.kv_map, d0 + 64, 0, page, bar);
         }
@@ -1007,20 +1012,7 @@ __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm,
     });
   };
   if (walk.left <= 0) return;
-  do {
-    TileSource now = look_up(walk.first);
-    keys(walk.first, now);
-#pragma unroll 1
-    for (int t = walk.first; t < walk.last; ++t) {
-      TileSource ahead = now;
-      if (t + 1 < walk.last) {
-        ahead = look_up(t + 1);
-        keys(t + 1, ahead);
-      }
-      values(t, now);
-      now = ahead;
-    }
-  } while (walk.next());
+  produce_tiles(walk, look, keys, values);
 }
 
 // Q of this CTA's query: plain blocks by TMA, the rope block rotated and split
