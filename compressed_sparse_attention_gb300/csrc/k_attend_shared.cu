@@ -1230,7 +1230,6 @@ __device__ __forceinline__ void math_shared(const SharedParams& p, uint8_t* sm, 
       rope_tab[lane] = make_float2(cs, sn);  // read behind the barriers of the unit's end
     }
     float m_run = -INFINITY, m_use = kNoRef, lsum = 0.f;
-    bool seen_any = false;
 #pragma unroll 1
     for (int t = walk.first; t < walk.last; ++t, ++n) {
       // the rows that this query sees of the warp's group
@@ -1247,7 +1246,6 @@ __device__ __forceinline__ void math_shared(const SharedParams& p, uint8_t* sm, 
           mask[i] = __ballot_sync(0xffffffffu, there);
         }
       }
-      seen_any = seen_any || (mask[0] | mask[1]) != 0u;
       live = live && warp_wait(bars + 8 * (bScores + (n & 1u)), (n >> 1) & 1u, p.flags);
       tc_fence_after();
       const uint32_t s_at = tmem_s + 128u * (n & 1u) + lane_base + 64u * cols;

@@ -186,7 +186,7 @@ __device__ __forceinline__ int64_t whole_pages(const GroupParams& p, int i, int3
   const int32_t b = p.seq_of_q[i];
   const int64_t t = p.q_pos[i];
   seq = b >= 0 && b < p.n_seq && t >= 0 ? b : -1;
-  return seq < 0 ? 0 : min((t + 1) >> p.page_shift, (int64_t)p.max_pages);
+  return seq < 0 ? 0 : min((min(t, (int64_t)1 << 40) + 1) >> p.page_shift, (int64_t)p.max_pages);
 }
 
 // The columns at which the rows of queries i and j (both keyed: both have

@@ -320,7 +320,7 @@ def test_lengths_bound_the_common_run():
 
 
 def test_positions_past_the_table_in_groups():
-    check_groups([[1, 2, 3, 4]] * 3, 16, 10, [1 << 40, 63, 1000], [0, 1, 2], 16)
+    check_groups([[1, 2, 3, 4]] * 4, 16, 10, [1 << 40, 63, 1000, (1 << 63) - 1], [0, 1, 2, 3], 16)
 
 
 def test_groups_on_another_stream_and_captured():
