@@ -826,15 +826,20 @@ struct CodeProducer {
       __syncwarp();  // all lanes have read what the stores below may overwrite
       const uint32_t scales = j4 == 0 ? a.scales[0] : (j4 == 1 ? a.scales[1] : (j4 == 2 ? a.scales[2] : a.scales[3]));
       const uint32_t there = j4 == 0 ? a.there[0] : (j4 == 1 ? a.there[1] : (j4 == 2 ? a.there[2] : a.there[3]));
-      const bool all = there == 0xFFFFFFFFu;
+      uint32_t word[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t word = __shfl_sync(0xffffffffu, scales, 8 * i + r);
-        const uint32_t sc = (word >> (KVF == 1 ? 8 * (c >> 1) : 8 * c)) & 255u;
-        if (!all && ((there >> (8 * i + r)) & 1u) == 0u) {  // rows that are not the group's: zeros
+      for (int i = 0; i < 4; ++i) word[i] = __shfl_sync(0xffffffffu, scales, 8 * i + r);
+      if (there != 0xFFFFFFFFu) {  // rows that are not the group's: zeros
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (((there >> (8 * i + r)) & 1u) != 0u) continue;
           if constexpr (KVF == 1) code[i] = make_uint4(0u, 0u, 0u, 0u);
           else code[i] = make_uint2(0u, 0u);
         }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t sc = (word[i] >> (KVF == 1 ? 8 * (c >> 1) : 8 * c)) & 255u;
         uint32_t o[8];
         if constexpr (KVF == 1) scaled_e4m3(code[i], sc, o);
         else scaled_e2m1(code[i], sc, o);
