@@ -30,14 +30,14 @@
 //
 // What bounds it. A tile's products run 4,352 cycles at best (36 of N = 256 and
 // K = 16 for S, rope residual included, 32 for O, 64 cycles each; all operations
-// would take 4,096). Their operands take 3,264 of shared memory's cycles and
-// what is copied into it and written as weights 2,300: 5,570 together. Measured
-// tiles take 5,700 to 5,900 in a long run: 64 queries over 32K common bf16 rows
-// 171 us, 1.62 PFLOP/s, where csa2_attend_paged takes 332. The ring's seven slots
-// just cover a copy's 1,100 to 1,500 cycles: what was between the products at
-// first (copies looked up behind the wait for a slot, arrivals with a cluster-wide
-// release, a barrier not looked at ahead: 9,800 cycles a tile) is off that path.
-// fp8 and fp4 rows: their conversion, 14,400 cycles a tile. Short calls: plan 2.2
+// would take 4,096). Tiles take 2.7 us in a long run, some 5,250 cycles: 64 queries
+// over 32K common bf16 rows 166 us, 1.67 PFLOP/s, where csa2_attend_paged takes
+// 332. The ring's seven slots are 1,900 cycles of products and just cover a
+// copy's 1,100 to 1,500 and the barriers around it (without copies a tile takes
+// 4,700): what was between the products at first (copies looked up behind the wait for
+// a slot, arrivals with a cluster-wide release, a barrier not looked at ahead: 9,800
+// cycles a tile) is off that path. fp8 and fp4 rows: their conversion, 14,000
+// cycles a tile. Short calls: plan 2.2
 // us, Q 2, a tile's scores, first weights and products 4.5, partial 2 (128 KB a
 // CTA, 32 bytes a clock), join 5: four queries over 2K rows 18.8 us.
 #include <cuda.h>
