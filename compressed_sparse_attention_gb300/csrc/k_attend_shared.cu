@@ -33,13 +33,13 @@
 // would take 4,096). Tiles take 2.7 us in a long run, some 5,250 cycles: 64 queries
 // over 32K common bf16 rows 166 us, 1.67 PFLOP/s, where csa2_attend_paged takes
 // 332. The ring's seven slots are 1,900 cycles of products and just cover a
-// copy's 1,100 to 1,500 and the barriers around it (without copies a tile takes
-// 4,700): what was between the products at first (copies looked up behind the wait for
+// copy's 1,100 to 1,500 and the barriers around it (without copies and weights a
+// tile takes 4,700): what was between the products at first (copies looked up behind the wait for
 // a slot, arrivals with a cluster-wide release, a barrier not looked at ahead: 9,800
 // cycles a tile) is off that path. fp8 and fp4 rows: their conversion, 14,000
 // cycles a tile. Short calls: plan 2.2
 // us, Q 2, a tile's scores, first weights and products 4.5, partial 2 (128 KB a
-// CTA, 32 bytes a clock), join 5: four queries over 2K rows 18.8 us.
+// CTA, 32 bytes a clock), join 5: four queries over 2K rows 18.1 us.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <type_traits>
@@ -1523,11 +1523,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SharedRoles<TMA>::kT
 // thread has one head and 16 dims (a sector of the output; the parts' values lie
 // next to each other over the heads). GROUPS 1: a CTA has 64 dims. GROUPS 4:
 // it has 16, and its quarters take every fourth part, for the few queries that
-// have many parts: what a thread waits for is one round trip for two parts.
+// have many parts (4 queries of 17 parts between them 18.7 us, 20.9 with GROUPS 1; 48
+// queries 37.0 and 40.4). What a thread waits for is one round trip for PARTS parts:
+// four, or for many queries with two or three parts each two, which leaves room
+// for twice the CTAs (32 queries 43.2 us with four, 45.0 with two; 48 38.1 and 37.0).
 constexpr int kJoinDims = 16;
-constexpr int kJoinParts = 2;  // whose values are under way at once
-template <int GROUPS>
-__global__ void __launch_bounds__(256, 4) attend_shared_join_kernel(const __grid_constant__ SharedParams p) {
+template <int GROUPS, int PARTS>
+__global__ void __launch_bounds__(256, 8 / PARTS) attend_shared_join_kernel(const __grid_constant__ SharedParams p) {
   __shared__ float2 weight[kMaxCtaPairs][kHeads];  // reference and sum, then the weight
   __shared__ float red[2][4][kHeads];
   __shared__ float2 turn[32];
@@ -1542,10 +1544,10 @@ __global__ void __launch_bounds__(256, 4) attend_shared_join_kernel(const __grid
   const int n = jn.w - jn.z + 1;
   auto slot = [&](int k) { return shared_slot(jn.z + k, k == 0, rank); };
   const float4* parts = reinterpret_cast<const float4*>(p.part_o) + (int64_t)(d0 / 4) * kHeads + head;
-  float4 v[kJoinParts][kJoinDims / 4];
+  float4 v[PARTS][kJoinDims / 4];
   auto fetch = [&](int k0) {
 #pragma unroll
-    for (int u = 0; u < kJoinParts; ++u) {
+    for (int u = 0; u < PARTS; ++u) {
       const int k = k0 + u * GROUPS;
 #pragma unroll
       for (int i = 0; i < kJoinDims / 4; ++i)
@@ -1592,10 +1594,10 @@ __global__ void __launch_bounds__(256, 4) attend_shared_join_kernel(const __grid
   float o[kJoinDims];
 #pragma unroll
   for (int i = 0; i < kJoinDims; ++i) o[i] = 0.f;
-  for (int k0 = group; k0 < n; k0 += kJoinParts * GROUPS) {
+  for (int k0 = group; k0 < n; k0 += PARTS * GROUPS) {
     if (k0 > group) fetch(k0);
 #pragma unroll
-    for (int u = 0; u < kJoinParts; ++u) {
+    for (int u = 0; u < PARTS; ++u) {
       const float e = k0 + u * GROUPS < n ? weight[k0 + u * GROUPS][head].x : 0.f;
 #pragma unroll
       for (int i = 0; i < kJoinDims / 4; ++i) {
@@ -1724,10 +1726,10 @@ cudaError_t launch_attend_shared(cudaStream_t st, int num_sms, int kv_fmt, const
   // few queries: many parts a unit, few units to be joined (CTAs without one cost
   // their start, 1.6 ns each)
   const unsigned joins = (unsigned)std::min(p.pairs, p.n_query);
-  if (4 * joins <= (unsigned)p.pairs)
-    e = launch_ex(attend_shared_join_kernel<4>, dim3(joins, kDim / kJoinDims, 2), dim3(256), 0, st, true, 0, p);
-  else
-    e = launch_ex(attend_shared_join_kernel<1>, dim3(joins, kDim / kJoinDims / 4, 2), dim3(256), 0, st, true, 0, p);
+  const dim3 by_quarter(joins, kDim / kJoinDims, 2), by_dims(joins, kDim / kJoinDims / 4, 2);
+  if (4 * joins <= (unsigned)p.pairs) e = launch_ex(attend_shared_join_kernel<4, 4>, by_quarter, dim3(256), 0, st, true, 0, p);
+  else if (2 * joins <= (unsigned)p.pairs) e = launch_ex(attend_shared_join_kernel<1, 4>, by_dims, dim3(256), 0, st, true, 0, p);
+  else e = launch_ex(attend_shared_join_kernel<1, 2>, by_dims, dim3(256), 0, st, true, 0, p);
   if (e != cudaSuccess) return e;
   *n_launch += p.planned ? 3 : 2;
   return cudaGetLastError();
