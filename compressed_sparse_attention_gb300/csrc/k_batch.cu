@@ -37,7 +37,9 @@ __device__ __forceinline__ Request request_at(const BatchParams& p, int i, uint3
 // token arrays each, every one with a scan over all requests of its own (their
 // lengths come from the L2 in two round trips, which is what the call takes;
 // a scan in a launch of its own would add one more); CTA 0 also writes the
-// offsets. The others copy table rows.
+// offsets. The others copy table rows. 64 requests 3.9 us (3.5 in a graph), 512
+// with rows of 2,050 columns 5.8 us; launched plainly instead of programmatically
+// 6.2 and 8.3.
 __global__ void __launch_bounds__(kBatchThreads) batch_tables_kernel(const __grid_constant__ BatchParams p) {
   __shared__ int64_t off[kBatchReqs + 1];
   __shared__ int64_t first[kBatchReqs];
