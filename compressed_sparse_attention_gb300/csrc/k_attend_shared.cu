@@ -162,31 +162,35 @@ struct PlanUnit {
   SharedUnit u;
   bool begins;
 };
+// A place as the plan sees it: its head, the next place's (kNoPlace behind the
+// last) and the first place of the run of equal heads that it lies in, which is
+// where its group begins.
+constexpr int32_t kNoPlace = INT32_MIN;
+struct PlanPlace {
+  int32_t head, next, run;
+};
 // The unit that place k begins, if it does. bad: flags to record.
-__device__ __forceinline__ PlanUnit unit_at(const SharedParams& p, int k, uint32_t& bad) {
+__device__ __forceinline__ PlanUnit unit_at(const SharedParams& p, int k, const PlanPlace& at, uint32_t& bad) {
   PlanUnit r;
-  const int n = p.n_query;
-  auto head_of = [&](int at) {
-    const int h = p.head[at];
-    return h >= 0 && h <= at ? h : at;
-  };
-  const int h = head_of(k), hn = k + 1 < n ? head_of(k + 1) : -1;
-  r.begins = ((k - h) & 1) == 0;
-  if (!r.begins) {
-    if (head_of(k - 1) != h) bad |= CSA2_FLAG_BAD_QUERY;
+  const int n = p.n_query, h = at.head;
+  r.begins = false;
+  if (h != at.run) {  // its group does not begin where its head says
+    bad |= CSA2_FLAG_BAD_QUERY;
     return r;
   }
+  r.begins = ((k - h) & 1) == 0;
+  if (!r.begins) return r;
   const int32_t cap = p.kv.max_pages << p.kv.page_shift;  // at most 2^30
   SharedUnit& u = r.u;
   int64_t len = p.shared[h];
-  auto query = [&](int at) {
-    const int q = p.order[at];
+  auto query = [&](int place) {
+    const int q = p.order[place];
     if (q < -1 || q >= n) bad |= CSA2_FLAG_BAD_QUERY;
     return q >= 0 && q < n ? q : -1;
   };
   const int qh = query(h);
   u.q[0] = query(k);
-  u.q[1] = hn == h ? query(k + 1) : -1;
+  u.q[1] = at.next == h ? query(k + 1) : -1;
   u.head_seq = qh >= 0 ? p.seq_of_q[qh] : -1;
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
@@ -233,24 +237,47 @@ __device__ __forceinline__ PlanUnit unit_at(const SharedParams& p, int k, uint32
 __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(const __grid_constant__ SharedParams p) {
   __shared__ int64_t sum_t[32], share_t[kPlanThreads];  // tiles, units before a thread's share
   __shared__ int sum_u[32], share_u[kPlanThreads];
+  __shared__ int last_run[32];
   __shared__ SharedRun runs[kMaxCtaPairs + 1];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_trigger();
   pdl_wait();
   const int per = (p.n_query + kPlanThreads - 1) / kPlanThreads;
   const int lo = min(p.n_query, tid * per), hi = min(p.n_query, lo + per);
+  // where the run of equal heads begins that goes on into the share
+  int run = -1;
+  for (int k = lo; k < hi; ++k) {
+    if (k == 0 || p.head[k] != p.head[k - 1]) run = k;
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) run = max(run, __shfl_up_sync(0xffffffffu, run, o));
+  if (lane == 31) last_run[warp] = run;
+  __syncthreads();
+  run = __shfl_up_sync(0xffffffffu, run, 1);
+  if (lane == 0) run = -1;
+  for (int w = 0; w < warp; ++w) run = max(run, last_run[w]);
+  // the units of the share in turn
+  auto each_unit = [&](uint32_t& bad, auto&& take) {
+    PlanPlace at{kNoPlace, lo < hi ? p.head[lo] : kNoPlace, run};
+    int32_t before = lo > 0 && lo < hi ? p.head[lo - 1] : kNoPlace;
+    for (int k = lo; k < hi; ++k) {
+      at.head = at.next;
+      at.next = k + 1 < p.n_query ? p.head[k + 1] : kNoPlace;
+      if (k == 0 || at.head != before) at.run = k;
+      before = at.head;
+      const PlanUnit one = unit_at(p, k, at, bad);
+      if (one.begins) take(one.u);
+    }
+  };
   int64_t tiles = 0;
   int units = 0;
   uint32_t bad = 0, unused = 0;
-  PlanUnit one;
-  one.begins = false;
-  for (int k = lo; k < hi; ++k) {
-    one = unit_at(p, k, bad);
-    if (one.begins) {
-      tiles += one.u.tiles;
-      ++units;
-    }
-  }
+  SharedUnit only;  // of a share of one place
+  each_unit(bad, [&](const SharedUnit& u) {
+    tiles += u.tiles;
+    ++units;
+    only = u;
+  });
   if (bad) set_flag(p.flags, bad);
   // exclusive scan over the threads
   int64_t it = tiles;
@@ -279,10 +306,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) attend_shared_plan_kernel(con
   share_t[tid] = it - tiles + (warp > 0 ? bt : 0);
   share_u[tid] = iu - units + (warp > 0 ? bu : 0);
   int u0 = share_u[tid];
-  for (int k = lo; k < hi; ++k) {
-    if (per > 1) one = unit_at(p, k, unused);
-    if (one.begins) p.units[u0++] = one.u;
-  }
+  if (per > 1) each_unit(unused, [&](const SharedUnit& u) { p.units[u0++] = u; });
+  else if (units > 0) p.units[u0] = only;
   __syncthreads();
   const RunLine line(T, U, p.pairs);
   // thread c finds the first tile from the c-th cut on
@@ -1413,7 +1438,28 @@ __device__ __forceinline__ void plan_here(const SharedParams& p, uint8_t* sm, Sh
   int64_t it = 0;
   int iu = 0;
   if (warp < kWarps) {
-    if (tid < p.n_query) one = unit_at(p, tid, bad);
+    // every warp looks at all places' heads: where runs of equal ones begin (bits)
+    int32_t head[kWarps];
+    uint32_t begins[kWarps];
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) head[w] = 32 * w + lane < p.n_query ? p.head[32 * w + lane] : kNoPlace;
+    PlanPlace at{kNoPlace, kNoPlace, 0};
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const int32_t up = __shfl_up_sync(0xffffffffu, head[w], 1), last = __shfl_sync(0xffffffffu, head[max(w, 1) - 1], 31);
+      const int32_t down = __shfl_down_sync(0xffffffffu, head[w], 1), first = __shfl_sync(0xffffffffu, head[min(w + 1, kWarps - 1)], 0);
+      begins[w] = __ballot_sync(0xffffffffu, lane == 0 ? w == 0 || head[w] != last : head[w] != up);
+      if (w == warp) {
+        at.head = head[w];
+        at.next = lane < 31 ? down : (w + 1 < kWarps ? first : kNoPlace);
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const uint32_t till = w < warp ? begins[w] : (w == warp ? begins[w] & (0xFFFFFFFFu >> (31 - lane)) : 0u);
+      if (till != 0u) at.run = 32 * w + 31 - __clz((int)till);
+    }
+    if (tid < p.n_query) one = unit_at(p, tid, at, bad);
     if (bad && blockIdx.x == 0) set_flag(p.flags, bad);
     it = one.begins ? one.u.tiles : 0;
     iu = one.begins ? 1 : 0;

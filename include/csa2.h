@@ -809,7 +809,9 @@ csa2_status csa2_query_groups(csa2_ctx* ctx, void* stream, const int32_t* table,
  *   q, q_pos, seq_of_q, sink, out, lse: as for csa2_attend_paged (padding and bad
  *   queries, missing pages and empty rows alike; an order outside [-1, n_query)
  *   is recorded as CSA2_FLAG_BAD_QUERY and skipped, and so is a place whose
- *   group does not begin where head says). A query at no place keeps its out.
+ *   group does not begin where head says: head[k] must be the first place of
+ *   the run of equal heads around k). A query at no place, or at a skipped one,
+ *   keeps its out and lse.
  * Results do not depend on timing. The limits on the size of rows are
  * csa2_attend_paged's. n_query at most 2^20. Two launches, three for more than 96
  * queries.
