@@ -310,7 +310,11 @@ csa2_status csa2_query_groups(csa2_ctx* ctx, void* stream, const int32_t* table,
   if (n_query > csa2::kMaxGroupQueries)
     return fail(ctx, CSA2_ERR_UNSUPPORTED, "query_groups: at most " + std::to_string(csa2::kMaxGroupQueries) + " queries");
   if (!aligned(n_groups, 4)) return fail(ctx, CSA2_ERR_INVALID_ARG, "query_groups: misaligned n_groups");
-  if (n_query == 0) return CSA2_OK;
+  if (n_query == 0) {  // no groups
+    if (n_groups == nullptr) return CSA2_OK;
+    const cudaError_t e = cudaMemsetAsync(n_groups, 0, sizeof(*n_groups), reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CSA2_OK : cuda_fail(ctx, e, "query_groups");
+  }
   if (!q_pos || !seq_of_q || !order || !head || !shared || !aligned_all(8, q_pos, shared) || !aligned_all(4, seq_of_q, order, head))
     return fail(ctx, CSA2_ERR_INVALID_ARG, "query_groups: null or misaligned buffer");
   csa2::GroupParams p{};

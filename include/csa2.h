@@ -791,7 +791,8 @@ csa2_status csa2_batch_tables(csa2_ctx* ctx, void* stream, const csa2_page_pool*
  *   n_groups [1] int32 (nullable)
  *   q_pos [n_query] int64, seq_of_q [n_query] int32 as for csa2_attend_paged
  *           (bad ones recorded as CSA2_FLAG_BAD_QUERY, groups of their own)
- * n_query at most 4,096. Two launches. */
+ * n_query at most 4,096. Two launches; without queries none, n_groups being set
+ * to 0. */
 csa2_status csa2_query_groups(csa2_ctx* ctx, void* stream, const int32_t* table, int64_t table_ld, int32_t max_pages,
                               int32_t n_pages, int32_t page_size, int32_t n_seq, int32_t n_query, const int64_t* q_pos,
                               const int32_t* seq_of_q, int64_t min_shared, int32_t* order, int32_t* head, int64_t* shared,
