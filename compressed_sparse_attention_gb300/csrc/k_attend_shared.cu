@@ -58,7 +58,7 @@ constexpr uint32_t kSlotBytes = 16384;
 constexpr int kMaxCtaPairs = 80;   // pairs of CTAs, at most
 constexpr int kPlanThreads = 1024;
 
-// Two places of a group (or its last one alone).
+// Two places of a group (or its last one alone), one of which has a query.
 struct alignas(16) SharedUnit {
   int32_t q[2];       // the queries; -1: none
   int32_t seq[2];     // their sequences
@@ -212,6 +212,10 @@ __device__ __forceinline__ PlanUnit unit_at(const SharedParams& p, int k, const 
     u.seq[x] = b;
     if (t >= cap) bad |= CSA2_FLAG_BAD_PAGE;
     u.end[x] = (int32_t)(t >= cap ? cap : t + 1);
+  }
+  if (u.q[0] < 0 && u.q[1] < 0) {  // nothing to write: padding takes no tile
+    r.begins = false;
+    return r;
   }
   if (u.head_seq < 0 || u.head_seq >= p.kv.n_seq) len = 0;
   len = len < 0 ? 0 : (len > cap ? cap : len);

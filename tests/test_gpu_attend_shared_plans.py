@@ -1,7 +1,10 @@
 """Plans that csa2_attend_shared is given: heads that do not begin where they
 say, in plans that the tile kernel makes itself and in those of a launch of
 their own."""
+import random
+
 import pytest
+import torch
 
 from test_gpu_attend_shared import Case
 
@@ -87,3 +90,56 @@ def test_one_run_over_many_shares():
     c.order, c.head, c.shared = list(range(n)), [0] * n, [32] + [0] * (n - 1)
     c.plan()
     c.run().check(only=[0, 1, 2, 3, 1023, 1024, 1025, 2598, 2599])
+
+
+# ---------------------------------------------------------------- padded batches
+
+def padded(n, live, page=16, fmt="bf16", seed=0):
+    """n queries of which those of `live` have sequences: places group by group, padding a place each, mixed."""
+    rng = random.Random(seed)
+    lens = [64 + rng.randint(1, 400) for _ in range(9)]
+    at = sorted(rng.sample(range(n), live))
+    queries = [(-1, rng.choice([-1, 5]))] * n
+    for j, i in enumerate(at):
+        queries[i] = (j % 9, lens[j % 9] - 1 - (j // 9) % 30)
+    return Case([(4, lens)], page=page, fmt=fmt, queries=queries, seed=seed), at
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("n,live", [(1, 0), (2, 1), (16, 3), (64, 5), (76, 0), (90, 7), (96, 2), (97, 0), (300, 11), (2100, 9)])
+def test_padded_batches(fmt, n, live):
+    c, at = padded(n, live, fmt=fmt, seed=n)
+    c.run().check(only=at)
+    rest = [i for i in range(n) if i not in at]
+    assert (c.out[rest] == 77).all() and (c.lse[rest] == 77).all()
+
+
+def test_padding_inside_groups():
+    # two empty places that would be a unit, one beside a query, one as the head
+    lens = [70, 90, 110, 130]
+    c = Case([(4, lens)], page=16, queries=[(0, 69), (-1, 3), (-1, 4), (1, 89), (-1, 5), (2, 109), (3, 129)], seed=104)
+    c.order, c.head, c.shared = [0, 3, 1, 2, 4, 5, 6], [0] * 7, [64] + [0] * 6
+    c.plan()
+    c.run().check(only=[0, 3, 5, 6])
+    assert (c.out[[1, 2, 4]] == 77).all()
+
+
+def test_places_without_a_query_cost_no_tile():
+    # as many places, one row each: without a query they take well under half of the time
+    n = 4096
+    empty = Case([(0, [5])], page=16, queries=[(-1, 0)] * (n - 4) + [(0, 4)] * 4, seed=105)
+    one = Case([(0, [5])], page=16, queries=[(0, 0)] * n, seed=105)
+    best = {}
+    for name, c in (("one", one), ("empty", empty)):
+        call = c.call()
+        times = []
+        for _ in range(6):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(5):
+                call.run()
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b))
+        best[name] = min(times[1:])
+    assert best["empty"] < 0.5 * best["one"], best
