@@ -292,9 +292,10 @@ csa2_status csa2_batch_tables(csa2_ctx* ctx, void* stream, const csa2_page_pool*
   p.tok_slot = batch->tok_slot;
   p.max_tokens = batch->max_tokens;
   p.n_req = n_req;
-  const cudaError_t e = csa2::launch_batch_tables(reinterpret_cast<cudaStream_t>(stream), p);
+  int nl = 0;
+  const cudaError_t e = csa2::launch_batch_tables(reinterpret_cast<cudaStream_t>(stream), p, &nl);
   if (e != cudaSuccess) return cuda_fail(ctx, e, "batch_tables");
-  ctx->last_launches = 1;
+  ctx->last_launches = nl;
   return CSA2_OK;
 }
 

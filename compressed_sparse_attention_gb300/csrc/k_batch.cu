@@ -13,6 +13,12 @@ constexpr int kBatchThreads = 256;
 constexpr int kBatchReqs = 1024;   // requests whose offsets lie in shared memory at once
 constexpr int kTokThreads = 4;     // tokens of a thread
 constexpr int kRowCols = 2048;     // table columns of a CTA
+// Scans of 1,024 requests that token CTAs make between them at most; where it would
+// be more, CTA 0 alone scans, and the others search its offsets behind a second
+// launch. Scans by all and search: 16 x 16 scans (16,384 requests, as many tokens)
+// 45.5 and 56.5 us, 3 x 98 11.8 and 18.8, 4 x 977 26.4 and 25.9, 64 x 64 180 and 186,
+// 8 x 977 46.0 and 37.0, 64 x 1,024 340 and 198.
+constexpr int64_t kMostScans = 4096;
 
 // Request i: its sequence (-1: none, or not to be carried out), its length and new tokens.
 struct Request {
@@ -30,16 +36,31 @@ __device__ __forceinline__ Request request_at(const BatchParams& p, int i, uint3
   if (r.seq != -1) bad |= CSA2_FLAG_BAD_SEQ;
   return Request{-1, 0, 0};
 }
+// Place t of the token arrays: token at pos of request i, sequence seq.
+__device__ __forceinline__ void put_token(const BatchParams& p, int64_t t, int i, int32_t seq, int64_t pos, uint32_t& bad) {
+  const int32_t page = p.pool.table[(int64_t)seq * p.pool.table_ld + (pos >> p.pool.page_shift)];
+  const bool there = (uint32_t)page < (uint32_t)p.pool.n_pages;
+  if (!there) bad |= CSA2_FLAG_BAD_PAGE;
+  p.req_of_tok[t] = i;
+  p.tok_pos[t] = pos;
+  p.tok_slot[t] = there ? ((int64_t)page << p.pool.page_shift) + (pos & ((1 << p.pool.page_shift) - 1)) : -1;
+}
+__device__ __forceinline__ void put_padding(const BatchParams& p, int64_t t) {
+  p.req_of_tok[t] = -1;
+  p.tok_pos[t] = -1;
+  p.tok_slot[t] = -1;
+}
 
 }  // namespace
 
-// csa2_batch_tables, one launch. CTAs below p.tok_ctas take 1,024 places of the
-// token arrays each, every one with a scan over all requests of its own (their
-// lengths come from the L2 in two round trips, which is what the call takes;
-// a scan in a launch of its own would add one more); CTA 0 also writes the
-// offsets. The others copy table rows. 64 requests 3.9 us (3.5 in a graph), 512
-// with rows of 2,050 columns 5.8 us; launched plainly instead of programmatically
-// 6.2 and 8.3.
+// csa2_batch_tables. CTAs below p.tok_ctas take 1,024 places of the token arrays
+// each, every one with a scan of its own over the requests up to the last that has
+// a token there (the lengths of 1,024 requests come from the L2 in two round trips,
+// which up to as many requests is what the call takes; a scan in a launch of its own
+// would add one more); CTA 0 scans all, for the offsets. The others copy table
+// rows. 64 requests 3.9 us (3.5 in a graph), 512 with rows of 2,050 columns 5.8 us;
+// launched plainly instead of programmatically 6.2 and 8.3. Each further 1,024
+// requests are 2.8 us of CTA 0.
 __global__ void __launch_bounds__(kBatchThreads) batch_tables_kernel(const __grid_constant__ BatchParams p) {
   __shared__ int64_t off[kBatchReqs + 1];
   __shared__ int64_t first[kBatchReqs];
@@ -126,7 +147,6 @@ __global__ void __launch_bounds__(kBatchThreads) batch_tables_kernel(const __gri
         p.first_pos[i0 + e] = first[e];
       }
     }
-    const int page_mask = (1 << p.pool.page_shift) - 1;
 #pragma unroll
     for (int k = 0; k < kTokThreads; ++k) {
       const int64_t t = t0 + kBatchThreads * k + tid;
@@ -137,36 +157,57 @@ __global__ void __launch_bounds__(kBatchThreads) batch_tables_kernel(const __gri
         if (off[mid] <= t) lo = mid;
         else hi = mid;
       }
-      const int64_t pos = first[lo] + (t - off[lo]);
-      const int32_t page = p.pool.table[(int64_t)seq_of[lo] * p.pool.table_ld + (pos >> p.pool.page_shift)];
-      const bool there = (uint32_t)page < (uint32_t)p.pool.n_pages;
-      if (!there) bad |= CSA2_FLAG_BAD_PAGE;
-      p.req_of_tok[t] = i0 + lo;
-      p.tok_pos[t] = pos;
-      p.tok_slot[t] = there ? ((int64_t)page << p.pool.page_shift) + (pos & page_mask) : -1;
+      put_token(p, t, i0 + lo, seq_of[lo], first[lo] + (t - off[lo]), bad);
     }
+    // (CTA 0 goes on to the last request, for the offsets)
+    if (blockIdx.x != 0 && (full || before >= t0 + kBatchThreads * kTokThreads)) break;
   }
   // places behind the last token
 #pragma unroll
   for (int k = 0; k < kTokThreads; ++k) {
     const int64_t t = t0 + kBatchThreads * k + tid;
-    if (t >= before && t < p.max_tokens) {
-      p.req_of_tok[t] = -1;
-      p.tok_pos[t] = -1;
-      p.tok_slot[t] = -1;
+    if (t >= before && t < p.max_tokens) put_padding(p, t);
+  }
+  if (blockIdx.x != 0) bad &= ~(uint32_t)CSA2_FLAG_BAD_SEQ;  // CTA 0 has seen them all
+  if (bad) set_flag(p.pool.flags, bad);
+}
+
+// Places of the token arrays from `from` on, their requests found by a search in
+// the offsets that the launch before has written.
+__global__ void __launch_bounds__(kBatchThreads) batch_tokens_kernel(const __grid_constant__ BatchParams p, int64_t from) {
+  uint32_t bad = 0;
+  pdl_trigger();
+  pdl_wait();
+  const int64_t used = p.tok_off[p.n_req];
+#pragma unroll 1
+  for (int k = 0; k < kTokThreads; ++k) {
+    const int64_t t = from + ((int64_t)blockIdx.x * kTokThreads + k) * kBatchThreads + threadIdx.x;
+    if (t >= p.max_tokens) break;
+    if (t >= used) {
+      put_padding(p, t);
+      continue;
     }
+    const int i = find_segment(p.tok_off, p.n_req, t);
+    put_token(p, t, i, p.seqs[i], p.first_pos[i] + (t - p.tok_off[i]), bad);
   }
   if (bad) set_flag(p.pool.flags, bad);
 }
 
-cudaError_t launch_batch_tables(cudaStream_t st, BatchParams p) {
+cudaError_t launch_batch_tables(cudaStream_t st, BatchParams p, int* n_launch) {
   const int64_t per = kBatchThreads * kTokThreads;
   const int64_t tok = p.max_tokens > 0 ? (p.max_tokens + per - 1) / per : 1;
+  const int64_t scans = (p.n_req + kBatchReqs - 1) / kBatchReqs;
+  const bool search = scans > 1 && tok > 1 && scans * tok > kMostScans;
   p.row_ctas = (p.pool.max_pages + kRowCols - 1) / kRowCols;
-  const int64_t ctas = tok + (int64_t)p.n_req * p.row_ctas;
+  const int64_t ctas = (search ? 1 : tok) + (int64_t)p.n_req * p.row_ctas;
   if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  p.tok_ctas = (int)tok;
-  return launch_ex(batch_tables_kernel, dim3((unsigned)ctas), dim3(kBatchThreads), 0, st, true, 0, p);
+  p.tok_ctas = search ? 1 : (int)tok;
+  cudaError_t e = launch_ex(batch_tables_kernel, dim3((unsigned)ctas), dim3(kBatchThreads), 0, st, true, 0, p);
+  ++*n_launch;
+  if (e != cudaSuccess || !search) return e;
+  e = launch_ex(batch_tokens_kernel, dim3((unsigned)(tok - 1)), dim3(kBatchThreads), 0, st, true, 0, p, per);
+  ++*n_launch;
+  return e;
 }
 
 // ---------------------------------------------------------------------------

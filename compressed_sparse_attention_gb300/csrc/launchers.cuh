@@ -237,7 +237,7 @@ cudaError_t launch_append_slots(cudaStream_t st, int dtype, const void* rows, in
 size_t attend_shared_workspace_bytes(int num_sms, int n_query);
 cudaError_t launch_attend_shared(cudaStream_t st, int num_sms, int kv_fmt, const AttendParams& a, const PagedView& kv,
                                  const int32_t* order, const int32_t* head, const int64_t* shared, void* ws, int* n_launch);
-cudaError_t launch_batch_tables(cudaStream_t st, BatchParams p);
+cudaError_t launch_batch_tables(cudaStream_t st, BatchParams p, int* n_launch);
 cudaError_t launch_query_groups(cudaStream_t st, const GroupParams& p);
 size_t pages_workspace_bytes(int n_seq, int n_pages);
 cudaError_t launch_pages_extend(cudaStream_t st, const PagePool& P, int n, const int32_t* seqs, const int64_t* new_len,

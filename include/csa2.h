@@ -763,7 +763,8 @@ csa2_status csa2_pages_compact(csa2_ctx* ctx, void* stream, const csa2_page_pool
  * request whose tokens do not all fit into max_tokens has none, nor has any later
  * one (CSA2_FLAG_BATCH_FULL). Two requests may name one sequence. `table` must
  * not overlap the pool's (refused). n_req at most 2^20, max_tokens at most 2^32.
- * One launch. */
+ * One launch; two where more than 1,024 requests come with so many places that a
+ * scan of the requests for each 1,024 of them would take longer. */
 typedef struct csa2_batch {
   int32_t* table;
   int64_t table_ld;

@@ -1,10 +1,12 @@
 """csa2_batch_tables, csa2_query_groups and csa2_append_slots at the ends of
 their ranges: nothing to do, padded batches, many requests."""
+import random
+
 import pytest
 import torch
 
 from gpu_common import context, require_gpu
-from test_gpu_batch import DEV, i32, i64
+from test_gpu_batch import BAD_SEQ, BATCH_FULL, DEV, Pool, i32, i64
 
 pytestmark = pytest.mark.gpu
 
@@ -44,3 +46,92 @@ def test_no_queries_are_no_groups_on_a_stream_and_in_a_graph():
     n_groups.fill_(9)
     g.replay()
     assert n_groups.tolist() == [0]
+
+
+# ---------------------------------------------------------------- tables
+
+def plain_tables(lens, seqs, n_new, max_tokens):
+    """Offsets, first positions and (request, position) of each place, on the host with tensors."""
+    ok = (seqs >= 0) & (seqs < lens.numel())
+    length = torch.where(ok, lens[seqs.clamp(0, lens.numel() - 1)], 0)
+    ok &= (n_new >= 0) & (n_new <= length)
+    length, new = torch.where(ok, length, 0), torch.where(ok, n_new, 0)
+    first = length - new
+    end = torch.cumsum(new, 0)
+    past = torch.nonzero(end > max_tokens)
+    if past.numel():  # from the first that does not fit on: none
+        new[int(past[0]):] = 0
+    off = torch.cat((torch.zeros(1, dtype=torch.int64), torch.cumsum(new, 0)))
+    used = int(off[-1])
+    req = torch.repeat_interleave(torch.arange(seqs.numel()), new)
+    pos = first[req] + torch.arange(used) - off[req]
+    pad = torch.full((max_tokens - used,), -1)
+    flags = (0 if bool((ok | (seqs == -1)).all()) else BAD_SEQ) | (BATCH_FULL if past.numel() else 0)
+    return off, first, torch.cat((req, pad)), torch.cat((pos, pad)), flags
+
+
+@pytest.mark.parametrize("n,per,spare,launches", [
+    (1024, 30, 0, 1), (1025, 3, 5000, 1), (3000, 40, -30000, 1), (5000, 3, 1 << 20, 2), (5000, 300, 12345, 2),
+    (20000, 40, -200000, 2), (70000, 1, 0, 1), (70000, 2, 100000, 2), (1 << 20, 1, 3, 2)])
+def test_tables_of_so_many_requests(n, per, spare, launches):
+    """Batches around the limit of what every token CTA scans for itself: every output."""
+    require_gpu()
+    ctx, page = context(), 64
+    g = torch.Generator().manual_seed(n)
+    lens = torch.randint(0, 2 * per + 3, (n + 5,), generator=g)
+    width = -(-(2 * per + 3) // page)
+    table = torch.randperm((n + 5) * width, generator=g).reshape(n + 5, width).int()
+    seqs = torch.randperm(n + 5, generator=g)[:n]
+    n_new = torch.minimum(lens[seqs], torch.randint(0, 2 * per + 1, (n,), generator=g))
+    seqs[torch.randint(0, n, (n // 50,), generator=g)] = -1
+    if n % 2 == 0:  # some that cannot be carried out
+        seqs[n // 2], n_new[n // 3] = n + 5, -4
+    max_tokens = max(0, int(n_new.clamp_min(0).sum()) + spare)
+    off, first, req, pos, flags = plain_tables(lens, seqs, n_new, max_tokens)
+    d = [x.to(DEV) for x in (table, lens, seqs.int(), n_new)]
+    pool = ctx.page_pool(d[0], d[1], torch.ones((n + 5) * width, dtype=torch.int32, device=DEV), page)
+    got = dict(table=torch.full((n, width), 77, dtype=torch.int32, device=DEV), tok_off=torch.full((n + 1,), 77, device=DEV),
+               first_pos=torch.full((n,), 77, device=DEV), req_of_tok=torch.full((max_tokens,), 77, dtype=torch.int32, device=DEV),
+               tok_pos=torch.full((max_tokens,), 77, device=DEV), tok_slot=torch.full((max_tokens,), 77, device=DEV))
+    ctx.batch_tables(pool, d[2], d[3], **got)
+    assert ctx.last_launch_count == launches
+    assert ctx.check()[0] == flags
+    assert torch.equal(got["tok_off"].cpu(), off) and torch.equal(got["first_pos"].cpu(), first)
+    assert torch.equal(got["req_of_tok"].cpu().long(), req) and torch.equal(got["tok_pos"].cpu(), pos)
+    c, at = req.clamp_min(0), pos.clamp_min(0)
+    slot = table[seqs[c].clamp_min(0), at // page].long() * page + at % page
+    assert torch.equal(got["tok_slot"].cpu(), torch.where(req >= 0, slot, -1))
+    length = torch.where((seqs >= 0) & (seqs < n + 5) & (n_new >= 0), lens[seqs.clamp(0, n + 4)], 0)
+    used = (length + page - 1) // page
+    rows = torch.where(torch.arange(width)[None] < used[:, None], table[seqs.clamp(0, n + 4)], -1)
+    assert torch.equal(got["table"].cpu(), rows)
+
+
+def test_tables_of_many_requests_in_a_graph_and_again():
+    # the second launch reads the offsets that the first has written, call after call
+    p = Pool([random.Random(i).randint(1, 9) for i in range(2000)], seed=7)
+    seqs, new = i32(list(range(2000))), i64([0] * 2000)
+    tokens = 3 << 20
+    off, first, table = i64([0] * 2001), i64([0] * 2000), torch.empty_like(p.table)
+    req, pos, slot = (torch.zeros(tokens, dtype=t, device=DEV) for t in (torch.int32, torch.int64, torch.int64))
+    call = p.ctx.prepare_batch_tables(p.pool, seqs, new, table, off, first, req, pos, slot)
+    call.run()
+    assert p.ctx.last_launch_count == 2
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call.run()
+    for part in (1, 2):
+        new.copy_(i64([m // part for m in p.lens]))
+        g.replay()
+        want = plain_tables(torch.tensor(p.lens), torch.arange(2000), new.cpu(), tokens)
+        for a, b in zip((off, first, req.long(), pos), want):
+            assert torch.equal(a.cpu(), b)
+
+
+def test_tables_of_many_bad_requests_record_them():
+    p = Pool([4, 5])
+    n = 3000
+    seqs = [0, 1] * (n // 2)
+    seqs[2900] = 2
+    p.check(seqs, [1] * n, n)
+    p.check(seqs, [1] * n, 40)
