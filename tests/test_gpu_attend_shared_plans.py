@@ -1,12 +1,14 @@
-"""Plans that csa2_attend_shared is given: heads that do not begin where they
-say, in plans that the tile kernel makes itself and in those of a launch of
-their own."""
+"""csa2_attend_shared: plans whose heads do not begin where they say, in plans
+that the tile kernel makes itself and in those of a launch of their own; padded
+batches; its outputs beside csa2_attend_paged's, the flags of lengths that are
+cut, positions far past the table, very many queries."""
 import random
 
 import pytest
 import torch
 
-from test_gpu_attend_shared import Case
+from paged_common import DIM, HEADS, U16, U32, attend_one, layer_turned, page_values
+from test_gpu_attend_shared import DEV, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +145,89 @@ def test_places_without_a_query_cost_no_tile():
             times.append(a.elapsed_time(b))
         best[name] = min(times[1:])
     assert best["empty"] < 0.5 * best["one"], best
+
+
+# ---------------------------------------------------------------- results
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+def test_outputs_of_both_attentions_on_the_same_queries(fmt):
+    """Groups found by csa2_query_groups; csa2_attend_paged's out and lse and
+    csa2_attend_shared's, each within the bounds of the exact result, and so
+    within twice them of each other."""
+    c = Case([(7, [16 * 7 + 30, 16 * 7 + 9, 16 * 7 + 77]), (5, [16 * 5 + 3, 16 * 5 + 40]), (0, [90])], fmt=fmt, page=16, per=2, seed=106)
+    n = len(c.seq)
+    order, head = (torch.empty(n, dtype=torch.int32, device=DEV) for _ in range(2))
+    shared = torch.empty(n, dtype=torch.int64, device=DEV)
+    c.ctx.query_groups(c.table, 16, c.codes.shape[0], c.pos_d, c.seq_d, 40, order, head, shared)
+    c.order, c.head, c.shared = order.tolist(), head.tolist(), shared.tolist()
+    assert c.shared[0] == 16 * 7 and c.shared[6] == 16 * 5
+    c.plan()
+    c.run().check()
+    one, one_lse = c.out.clone(), c.lse.clone()
+    ws = c.b.workspace(c.ctx.attend_paged_workspace_size(n), DEV)
+    c.out.fill_(77)
+    c.lse.fill_(77)
+    c.ctx.attend_paged(c.kv, c.q, c.pos_d, c.seq_d, c.out, ws, sink=c.sink, lse=c.lse)
+    assert c.ctx.check()[0] == 0
+    c.check()
+    v, views = page_values(c.codes, c.scales, c.fmt), c.views()
+    for i in range(n):
+        _, _, bo, bl = attend_one(v, views[i], 16, c.q[i], c.pos[i], 0, 0, 0, c.sink, c.ctx.cfg)
+        assert ((one[i] - c.out[i]).double().cpu().abs() <= 2 * bo).all()
+        assert ((one_lse[i] - c.lse[i]).double().cpu().abs() <= 2 * bl).all()
+
+
+@pytest.mark.parametrize("shared,missing", [(-(1 << 62), False), (-3, False), (0, False), (7, False), (16, False), (40, False), (64, False),
+                                            (1000, True), (1 << 40, True), ((1 << 63) - 1, True)])
+def test_flags_of_lengths_that_are_cut(shared, missing):
+    # the first query's sequence has 60 rows in four pages: of a common length past them the fourth's rows are its own,
+    # the pages behind, which only the others see, missing
+    c = Case([(3, [60, 70, 90])], page=16, seed=107)
+    c.shared[0] = shared
+    c.plan()
+    c.run(flags=c.b.FLAG_BAD_PAGE if missing else 0)
+    c.shared[0] = min(max(shared, 0), 16 * len(c.table_rows[0]))
+    c.check()
+
+
+def test_a_position_far_past_the_table():
+    # every row of the table, rotated at 2^40
+    t = 1 << 40
+    c = Case([(2, [48, 48])], page=16, queries=[(0, 47), (1, t)], seed=108)
+    c.run(flags=c.b.FLAG_BAD_PAGE).check(only=[0])
+    cfg, row = c.ctx.cfg, c.views()[1]
+    rows = page_values(c.codes, c.scales, c.fmt)[row].reshape(-1, DIM)
+    tau, r = float(cfg.softmax_scale), int(cfg.rope_dim)
+    q = layer_turned(c.q[1].double().cpu(), t, cfg)
+    z = q @ rows.T * tau
+    lse = torch.logsumexp(torch.cat((z, c.sink.double().cpu()[:, None]), -1), -1)
+    w = torch.exp(z - lse[:, None])
+    o = w @ rows
+    # attend_one's bounds, and the angles: t f, f at most 1, is off by 2^-53 of itself in each double product and by
+    # 2^-51 for frequencies two steps apart, on both sides below 2^-50 of 2^40: 2^-10 radians, which move a pair by as
+    # much of its length, scores by tau times the pairs' lengths' products, and o as other errors of scores do
+    turn = 2.0 ** -10
+    pairs = lambda x: x[:, DIM - r:].reshape(x.shape[0], -1, 2).norm(dim=-1)  # noqa: E731
+    mag, rope = tau * (q.abs() @ rows.abs().T), tau * (q[:, DIM - r:].abs() @ rows[:, DIM - r:].abs().T)
+    delta = 40 * U32 * mag + (U16 ** 2 + 4 * U32) * rope + 2.0 ** -21 + turn * tau * (pairs(q) @ pairs(rows).T)
+    # exp(delta) - 1 <= 1.1 delta, in numerator and denominator
+    assert float(delta.max()) < 0.15
+    S = torch.einsum("hn,hnd->hd", w * 1.1 * delta, (rows[None] - o[:, None]).abs()) * 1.1
+    bound = (U16 + (len(rows) / 16 + 160) * U32) * (w @ rows.abs()) + S
+    both = bound[:, DIM - r:].reshape(HEADS, -1, 2).sum(-1, keepdim=True).expand(-1, -1, 2).reshape(HEADS, r)
+    length = (1 + turn) * turn * pairs(o)[:, :, None].expand(-1, -1, 2).reshape(HEADS, r)
+    bound = torch.cat((bound[:, :DIM - r], both + length), -1)
+    o = layer_turned(o, -float(t), cfg)
+    bound = bound + U16 * (o.abs() + bound) + 1e-30
+    assert ((c.out[1].double().cpu() - o).abs() <= bound).all()
+    assert ((c.lse[1].double().cpu() - lse).abs() <= 1.1 * delta.amax(-1) + 8 * U32 * (1 + lse.abs())).all()
+
+
+def test_very_many_queries():
+    # a share of many places a thread in the plan
+    n, lens = 40000, [3 + 7 * i for i in range(11)]
+    rng = random.Random(109)
+    c = Case([(0, lens)], page=16, queries=[(i % 11, rng.randint(0, lens[i % 11] - 1)) for i in range(n)], seed=109)
+    at = [0, 1, 39, 40, 41, n - 2, n - 1] + rng.sample(range(n), 25)
+    c.run().check(only=at)
+    assert torch.isfinite(c.out).all() and torch.isfinite(c.lse).all()

@@ -135,3 +135,31 @@ def test_tables_of_many_bad_requests_record_them():
     seqs[2900] = 2
     p.check(seqs, [1] * n, n)
     p.check(seqs, [1] * n, 40)
+
+
+# ---------------------------------------------------------------- rows by slot
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "fp4"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_slots_of_a_padded_batch_hold_the_packed_rows(fmt, dtype):
+    """A pool's batch by its slots, codes and scales as csa2_append_paged leaves
+    them; half of the places are padding, whose rows are not looked at."""
+    from paged_common import FMT_NAMES, random_pages
+    page = 16
+    p = Pool([40, 70, 33, 16], page=page, seed=5)
+    ctx = context(kv_format=fmt)
+    codes, scales = random_pages(FMT_NAMES[fmt], p.n_pages, page, 6, DEV)
+    mine, mine_s = codes.clone(), None if scales is None else scales.clone()
+    seqs, new = i32([2, 0, -1, 3, 1]), i64([7, 1, 0, 16, 40])
+    n, cap, w = 5, 128, len(p.rows[0])
+    table, off, first = torch.empty((n, w), dtype=torch.int32, device=DEV), i64([0] * 6), i64([0] * 5)
+    req, pos, slot = i32([0] * cap), i64([0] * cap), i64([0] * cap)
+    pool = ctx.page_pool(p.table, p.seq_len, p.ref, page)
+    ctx.batch_tables(pool, seqs, new, table, off, first, req, pos, slot)
+    rows = torch.randn((cap, 512), generator=torch.Generator().manual_seed(7)).to(dtype).to(DEV)
+    rows[64:] = float("nan")
+    ctx.append_slots(ctx.paged_kv(mine, None, mine_s), rows, pos, slot)
+    ctx.append_paged(ctx.paged_kv(codes, table, scales), rows, off, first)
+    assert ctx.check()[0] == 0 and off.tolist()[-1] == 64
+    assert torch.equal(codes.view(torch.uint8), mine.view(torch.uint8))
+    assert scales is None or torch.equal(scales, mine_s)
