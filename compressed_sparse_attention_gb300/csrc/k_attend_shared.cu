@@ -1588,10 +1588,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(SharedRoles<TMA>::kT
 // thread has one head and 16 dims (a sector of the output; the parts' values lie
 // next to each other over the heads). GROUPS 1: a CTA has 64 dims. GROUPS 4:
 // it has 16, and its quarters take every fourth part, for the few queries that
-// have many parts (4 queries of 17 parts between them 18.7 us, 20.9 with GROUPS 1; 48
-// queries 37.0 and 40.4). What a thread waits for is one round trip for PARTS parts:
-// four, or for many queries with two or three parts each two, which leaves room
-// for twice the CTAs (32 queries 43.2 us with four, 45.0 with two; 48 38.1 and 37.0).
+// have many parts. What a thread waits for is one round trip for PARTS parts: four,
+// or for many queries with two or three parts each two, which leaves room for
+// twice the CTAs. Whole calls over 8K common rows, <4, 4>, <1, 4> and <1, 2>: 4
+// queries 22.3 and 29.8 us, 8 28.9, 32.8, 39.6, 10 27.8 and 29.0, 12 28.7 and 28.6,
+// 16 31.7, 30.7, 34.1, 19 35.6, 33.1, 35.8, 32 45.3, 39.5, 41.2, 38 49.9, 43.9, 44.2, 40
+// 52.6, 46.9, 46.5, 64 70.4, 59.8, 58.2; over 2K, 30K and in pairs, fours or without
+// common rows the same within 1 us, but that over 500 rows <4, 4> loses from 10 on.
 constexpr int kJoinDims = 16;
 template <int GROUPS, int PARTS>
 __global__ void __launch_bounds__(256, 8 / PARTS) attend_shared_join_kernel(const __grid_constant__ SharedParams p) {
@@ -1789,10 +1792,11 @@ cudaError_t launch_attend_shared(cudaStream_t st, int num_sms, int kv_fmt, const
 #undef CSA2_SHARED
   if (e != cudaSuccess) return e;
   // few queries: many parts a unit, few units to be joined (CTAs without one cost
-  // their start, 1.6 ns each)
+  // their start, 1.6 ns each). The borders are where the variants meet: 10 to 12
+  // queries and 38 to 40 on 76 pairs.
   const unsigned joins = (unsigned)std::min(p.pairs, p.n_query);
   const dim3 by_quarter(joins, kDim / kJoinDims, 2), by_dims(joins, kDim / kJoinDims / 4, 2);
-  if (4 * joins <= (unsigned)p.pairs) e = launch_ex(attend_shared_join_kernel<4, 4>, by_quarter, dim3(256), 0, st, true, 0, p);
+  if (7 * joins <= (unsigned)p.pairs) e = launch_ex(attend_shared_join_kernel<4, 4>, by_quarter, dim3(256), 0, st, true, 0, p);
   else if (2 * joins <= (unsigned)p.pairs) e = launch_ex(attend_shared_join_kernel<1, 4>, by_dims, dim3(256), 0, st, true, 0, p);
   else e = launch_ex(attend_shared_join_kernel<1, 2>, by_dims, dim3(256), 0, st, true, 0, p);
   if (e != cudaSuccess) return e;

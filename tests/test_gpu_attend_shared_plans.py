@@ -231,3 +231,11 @@ def test_very_many_queries():
     at = [0, 1, 39, 40, 41, n - 2, n - 1] + rng.sample(range(n), 25)
     c.run().check(only=at)
     assert torch.isfinite(c.out).all() and torch.isfinite(c.lse).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp4"])
+@pytest.mark.parametrize("n", [4, 9, 10, 11, 12, 13, 18, 19, 20, 37, 38, 39])
+def test_numbers_of_queries_around_the_joins(fmt, n):
+    # every query split: of one prefix, and of sequences of their own
+    Case([(40, [40 * 64 + 1 + 11 * i for i in range(n)])], fmt=fmt, page=64, seed=n).run().check(only=[0, n // 2, n - 1])
+    Case([(0, [1300 + 11 * i for i in range(n)])], fmt=fmt, page=64, seed=n + 50).run().check(only=[0, n // 2, n - 1])
