@@ -170,6 +170,40 @@ bool share_elements(int64_t delta, int64_t n_outer, int64_t outer, int64_t n_inn
   return false;
 }
 
+// Rows of `width` bytes, `stride` apart, that a call reads or writes.
+struct Extent {
+  uint64_t base, rows, stride, width;
+};
+template <class T>
+Extent extent(const T* p, int64_t n) {
+  return Extent{reinterpret_cast<uintptr_t>(p), n > 0 ? 1u : 0u, 0, (uint64_t)std::max<int64_t>(n, 0) * sizeof(T)};
+}
+Extent extent(const int32_t* table, int64_t rows, int64_t ld, int64_t columns) {
+  return Extent{reinterpret_cast<uintptr_t>(table), (uint64_t)rows, 4 * (uint64_t)ld, 4 * (uint64_t)columns};
+}
+// Whether a and b share a byte; one of them is a single row.
+bool meet(const Extent& a, const Extent& b) {
+  if (b.rows > 1) return meet(b, a);
+  if (a.rows == 0 || b.rows == 0 || a.width == 0 || b.width == 0 || b.base + b.width <= a.base) return false;
+  // the row of a that begins last before b does, and the one behind it
+  const uint64_t i = b.base < a.base || a.rows == 1 ? 0 : std::min((b.base - a.base) / a.stride, a.rows - 1);
+  const uint64_t at = a.base + i * a.stride;
+  if (b.base < at + a.width && at < b.base + b.width) return true;
+  return i + 1 < a.rows && b.base < at + a.stride + a.width && at + a.stride < b.base + b.width;
+}
+// Whether one of the outputs meets another or an input; at most one of the inputs
+// and one of the outputs (not compared with each other) have several rows.
+template <size_t O, size_t I>
+bool any_meet(const Extent (&out)[O], const Extent (&in)[I]) {
+  for (size_t i = 0; i < O; ++i) {
+    for (size_t j = 0; j < i; ++j)
+      if (meet(out[i], out[j])) return true;
+    for (size_t j = 0; j < I; ++j)
+      if (!(out[i].rows > 1 && in[j].rows > 1) && meet(out[i], in[j])) return true;
+  }
+  return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -281,6 +315,13 @@ csa2_status csa2_batch_tables(csa2_ctx* ctx, void* stream, const csa2_page_pool*
   const uint64_t pe = pb + 4 * ((uint64_t)(pool->n_seq - 1) * (uint64_t)pool->table_ld + (uint64_t)pool->max_pages);
   const uint64_t be = bb + 4 * ((uint64_t)std::max(n_req - 1, 0) * (uint64_t)batch->table_ld + (uint64_t)pool->max_pages);
   if (n_req > 0 && pb < be && bb < pe) return fail(ctx, CSA2_ERR_INVALID_ARG, "batch_tables: the batch's table overlaps the pool's");
+  // and every CTA reads the requests while others write
+  const Extent out[] = {extent(batch->table, n_req, batch->table_ld, pool->max_pages), extent(batch->tok_off, n_req + (int64_t)1),
+                        extent(batch->first_pos, n_req), extent(batch->req_of_tok, batch->max_tokens),
+                        extent(batch->tok_pos, batch->max_tokens), extent(batch->tok_slot, batch->max_tokens)};
+  const Extent in[] = {extent(pool->table, pool->n_seq, pool->table_ld, pool->max_pages), extent(pool->seq_len, pool->n_seq),
+                       extent(seqs, n_req), extent(n_new, n_req)};
+  if (any_meet(out, in)) return fail(ctx, CSA2_ERR_INVALID_ARG, "batch_tables: an output overlaps an input or another output");
   p.seqs = seqs;
   p.n_new = n_new;
   p.table = batch->table;
@@ -318,6 +359,10 @@ csa2_status csa2_query_groups(csa2_ctx* ctx, void* stream, const int32_t* table,
   }
   if (!q_pos || !seq_of_q || !order || !head || !shared || !aligned_all(8, q_pos, shared) || !aligned_all(4, seq_of_q, order, head))
     return fail(ctx, CSA2_ERR_INVALID_ARG, "query_groups: null or misaligned buffer");
+  // (the second launch reads the queries again)
+  const Extent out[] = {extent(order, n_query), extent(head, n_query), extent(shared, n_query), extent(n_groups, n_groups ? 1 : 0)};
+  const Extent in[] = {extent(table, n_seq, table_ld, max_pages), extent(q_pos, n_query), extent(seq_of_q, n_query)};
+  if (any_meet(out, in)) return fail(ctx, CSA2_ERR_INVALID_ARG, "query_groups: an output overlaps an input or another output");
   csa2::GroupParams p{};
   p.table = table;
   p.table_ld = table_ld;

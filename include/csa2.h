@@ -761,8 +761,9 @@ csa2_status csa2_pages_compact(csa2_ctx* ctx, void* stream, const csa2_page_pool
  * be carried out (another sequence out of range, n_new negative or above the
  * length, a length past the table) neither, recorded as CSA2_FLAG_BAD_SEQ. A
  * request whose tokens do not all fit into max_tokens has none, nor has any later
- * one (CSA2_FLAG_BATCH_FULL). Two requests may name one sequence. `table` must
- * not overlap the pool's (refused). n_req at most 2^20, max_tokens at most 2^32.
+ * one (CSA2_FLAG_BATCH_FULL). Two requests may name one sequence. No output must
+ * overlap an input or another output (refused; `table` also not the span of the
+ * pool's). n_req at most 2^20, max_tokens at most 2^32.
  * One launch; two where more than 1,024 requests come with so many places that a
  * scan of the requests for each 1,024 of them would take longer. */
 typedef struct csa2_batch {
@@ -792,7 +793,8 @@ csa2_status csa2_batch_tables(csa2_ctx* ctx, void* stream, const csa2_page_pool*
  *   n_groups [1] int32 (nullable)
  *   q_pos [n_query] int64, seq_of_q [n_query] int32 as for csa2_attend_paged
  *           (bad ones recorded as CSA2_FLAG_BAD_QUERY, groups of their own)
- * n_query at most 4,096. Two launches; without queries none, n_groups being set
+ * n_query at most 4,096; no output must overlap an input or another output
+ * (refused). Two launches; without queries none, n_groups being set
  * to 0. */
 csa2_status csa2_query_groups(csa2_ctx* ctx, void* stream, const int32_t* table, int64_t table_ld, int32_t max_pages,
                               int32_t n_pages, int32_t page_size, int32_t n_seq, int32_t n_query, const int64_t* q_pos,

@@ -163,3 +163,89 @@ def test_slots_of_a_padded_batch_hold_the_packed_rows(fmt, dtype):
     assert ctx.check()[0] == 0 and off.tolist()[-1] == 64
     assert torch.equal(codes.view(torch.uint8), mine.view(torch.uint8))
     assert scales is None or torch.equal(scales, mine_s)
+
+
+# ---------------------------------------------------------------- overlaps
+
+def test_tables_over_each_other_are_refused():
+    """Every pair of an output with an input or another output, in one buffer:
+    the last element of one the first of the other, and one behind the other."""
+    from compressed_sparse_attention_gb300 import binding
+    p = Pool([20, 30, 40, 50], page=16)
+    ctx, w, n, cap = p.ctx, len(p.rows[0]), 3, 9
+    size = dict(seqs=(4, n), n_new=(8, n), table=(4, n * w), tok_off=(8, n + 1), first_pos=(8, n), req_of_tok=(4, cap),
+                tok_pos=(8, cap), tok_slot=(8, cap), pool_table=(4, 4 * w), seq_len=(8, 4))
+    outs = ("table", "tok_off", "first_pos", "req_of_tok", "tok_pos", "tok_slot")
+    values = dict(seqs=i32([1, 3, 0]), n_new=i64([2, 3, 1]), pool_table=p.table.flatten(), seq_len=p.seq_len)
+
+    def call(at):
+        """Arrays at the given byte offsets of one buffer."""
+        buf = torch.zeros(1 << 14, dtype=torch.uint8, device=DEV)
+        a = {}
+        for k, o in at.items():
+            width, count = size[k]
+            a[k] = buf[o:o + width * count].view(torch.int32 if width == 4 else torch.int64)
+            if k in values:
+                a[k].copy_(values[k])
+        pool = ctx.page_pool(a["pool_table"].view(4, w), a["seq_len"], p.ref, p.page)
+        ctx.batch_tables(pool, a["seqs"], a["n_new"], a["table"].view(n, w), a["tok_off"], a["first_pos"], a["req_of_tok"],
+                         a["tok_pos"], a["tok_slot"])
+        return a
+
+    apart, o = {}, 0
+    for k, (width, count) in size.items():
+        apart[k] = o
+        o += -(-width * count // 8) * 8 + 64
+    want = p.plain([1, 3, 0], [2, 3, 1], cap)
+    a = call(apart)
+    assert a["tok_off"].tolist() == want[1] and a["first_pos"].tolist() == want[2]
+    assert list(zip(a["req_of_tok"].tolist(), a["tok_pos"].tolist(), a["tok_slot"].tolist())) == want[3]
+    for x in outs:
+        for y in size:
+            if x == y:
+                continue
+            (wx, cx), (wy, cy) = size[x], size[y]
+            # y's first bytes over x's last, and x's first over y's last
+            for first, second, end in ((x, y, wx * cx), (y, x, wy * cy)):
+                over = (end - 1) // 8 * 8
+                with pytest.raises(binding.Csa2Error, match="overlap"):
+                    call({**apart, first: 8192, second: 8192 + over})
+                call({**apart, first: 8192, second: 8192 + over + 8})
+    assert ctx.check()[0] == 0
+
+
+def test_arrays_between_the_rows_of_a_table_are_taken():
+    # rows of a wide buffer whose other columns hold the requests and the offsets
+    from compressed_sparse_attention_gb300 import binding
+    p = Pool([20, 30, 40], page=16)
+    w = len(p.rows[0])
+    buf = torch.zeros((4, 64), dtype=torch.int32, device=DEV)
+    rest = (torch.zeros(2, dtype=torch.int64, device=DEV), i32([0] * 4), i64([0] * 4), i64([0] * 4))
+    for at, good in ((0, False), (w // 2 - 1 + w % 2, False), (-(-w // 2), True), (29, True), (30, False)):
+        # (the last two 64-bit places of a row and the first of the next)
+        tok_off = buf.view(torch.int64).flatten()[32 + at:32 + at + 3]
+        if good:
+            p.ctx.batch_tables(p.pool, i32([1, 2]), i64([1, 2]), buf[1:3, :w], tok_off, *rest)
+            assert tok_off.tolist() == [0, 1, 3] and buf[1:3, :w].tolist() == p.rows[1:3]
+        else:
+            with pytest.raises(binding.Csa2Error, match="overlap"):
+                p.ctx.batch_tables(p.pool, i32([1, 2]), i64([1, 2]), buf[1:3, :w], tok_off, *rest)
+    assert p.ctx.check()[0] == 0
+
+
+def test_groups_over_their_queries_are_refused():
+    require_gpu()
+    from compressed_sparse_attention_gb300 import binding
+    ctx = context()
+    table = i32([[1, 2], [1, 3], [1, 2]])
+    pos, seq = i64([20, 20, 31]), i32([0, 1, 2])
+    order, head, shared, groups = i32([0] * 3), i32([0] * 3), i64([0] * 3), i32([0])
+    good = dict(table=table, page_size=16, n_pages=9, q_pos=pos, seq_of_q=seq, min_shared=1, order=order, head=head, shared=shared,
+                n_groups=groups)
+    for kw in (dict(shared=pos), dict(order=seq), dict(head=seq), dict(order=head), dict(n_groups=seq[2:]), dict(n_groups=order[:1]),
+               dict(order=table.flatten()[3:6]), dict(n_groups=table.flatten()[5:]), dict(q_pos=shared),
+               dict(head=shared.view(torch.int32)[3:])):
+        with pytest.raises(binding.Csa2Error, match="overlap"):
+            ctx.query_groups(**{**good, **kw})
+    ctx.query_groups(**good)
+    assert ctx.check()[0] == 0 and order.tolist() == [0, 1, 2] and head.tolist() == [0, 0, 0] and shared.tolist() == [16, 0, 0]
