@@ -30,14 +30,18 @@
 //
 // What bounds it. A tile's products run 4,352 cycles at best (36 of N = 256 and
 // K = 16 for S, rope residual included, 32 for O, 64 cycles each; all operations
-// would take 4,096). Tiles take 2.7 us in a long run, some 5,250 cycles: 64 queries
-// over 32K common bf16 rows 166 us, 1.67 PFLOP/s, where csa2_attend_paged takes
-// 332. The ring's seven slots are 1,900 cycles of products and just cover a
+// would take 4,096). Tiles take 2.7 us in a unit of many, some 5,250 cycles: 64
+// queries over 32K common bf16 rows 166 to 170 us, 1.67 PFLOP/s, where
+// csa2_attend_paged takes 332; run for seconds 187, 1.48 PFLOP/s, as the card's
+// power limit then holds the clock at 1.63 GHz instead of 2.07 (csa2_attend_paged
+// stays below it). The ring's seven slots are 1,900 cycles of products and just cover a
 // copy's 1,100 to 1,500 and the barriers around it (without copies and weights a
 // tile takes 4,700): what was between the products at first (copies looked up behind the wait for
 // a slot, arrivals with a cluster-wide release, a barrier not looked at ahead: 9,800
 // cycles a tile) is off that path. fp8 and fp4 rows: their conversion, 14,000
-// cycles a tile. Short calls: plan 2.2
+// cycles a tile: the pair converts every element twice, as a key and as a value,
+// and for one query as for two; a query alone in its unit takes half as
+// long again as with csa2_attend_paged, in bf16 a tenth. Short calls: plan 2.2
 // us, Q 2, a tile's scores, first weights and products 4.5, partial 2 (128 KB a
 // CTA, 32 bytes a clock), join 5: four queries over 2K rows 18.1 us.
 #include <cuda.h>
@@ -423,7 +427,7 @@ __device__ __forceinline__ uint32_t in_leader(uint32_t addr) {
 // (made visible to the tensor core by a proxy fence before) or read from their
 // own tensor memory, for products that CTA 0 issues. What has to be released at
 // the scope of the pair is shared memory alone, and a fence for no more than that
-// costs nothing (fp8 137.3 -> 139.1 us, bf16 as without it): an arrival that
+// costs little (fp8 136.5 -> 137.9 us, bf16 as without it): an arrival that
 // releases at cluster scope itself waits for all of the warp's accesses to global
 // memory too, 1,500 cycles (64 x 32K 169 -> 185 us, fp8 152).
 __device__ __forceinline__ void arrive_cluster(uint32_t bar) {

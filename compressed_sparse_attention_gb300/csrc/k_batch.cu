@@ -58,7 +58,7 @@ __device__ __forceinline__ void put_padding(const BatchParams& p, int64_t t) {
 // a token there (the lengths of 1,024 requests come from the L2 in two round trips,
 // which up to as many requests is what the call takes; a scan in a launch of its own
 // would add one more); CTA 0 scans all, for the offsets. The others copy table
-// rows. 64 requests 3.9 us (3.5 in a graph), 512 with rows of 2,050 columns 5.8 us;
+// rows. 64 requests 3.7 us (3.5 in a graph), 512 with rows of 2,050 columns 5.8 us;
 // launched plainly instead of programmatically 6.2 and 8.3. Each further 1,024
 // requests are 2.8 us of CTA 0.
 __global__ void __launch_bounds__(kBatchThreads) batch_tables_kernel(const __grid_constant__ BatchParams p) {
@@ -217,7 +217,7 @@ cudaError_t launch_batch_tables(cudaStream_t st, BatchParams p, int* n_launch) {
 // queries group by group: ranks within a group from sixteen warps' counts. The
 // second compares each query's row with its group's first, a warp a query, and
 // keeps the least common run. Nothing depends on timing: minima and sums of
-// whole numbers. Bound by latency: 64 queries 5.6 us, 2,047 over 313 columns 11.2.
+// whole numbers. Bound by latency: 64 queries 5.4 us, 2,047 over 313 columns 11.0.
 // ---------------------------------------------------------------------------
 namespace {
 
