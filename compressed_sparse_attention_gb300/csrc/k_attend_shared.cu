@@ -651,6 +651,18 @@ struct RingAt {
   }
 };
 
+// The ring behind its last slot, `filled` of them before: the products' arrivals
+// for all of them. Nothing is filled after these, but an arrival from the other CTA
+// must find this one's shared memory still its own.
+__device__ __forceinline__ void drain_ring(const SharedParams& p, uint32_t bars, const RingAt& end, uint32_t filled, bool live) {
+#pragma unroll 1
+  for (uint32_t i = 0; i < (uint32_t)kRing && live; ++i) {
+    RingAt at = end;
+    at.step(i);
+    if (filled + i >= (uint32_t)kRing) live = wait_cluster_all_lanes(bars + 8 * (bEmpty + at.slot), at.phase ^ 1u, p.flags);
+  }
+}
+
 // A slot's rows by the warp itself: pages of less than the eight rows of a copy's
 // swizzle atom, row by row. K: channels 64 b .. of the 128 rows of the
 // tile's groups 2 rank and 2 rank + 1; V: dims d0 .. d0 + 127 of group g's 64
@@ -906,6 +918,10 @@ struct CodeProducer {
     convert(on);
     on.bar = 0u;
   }
+  __device__ __forceinline__ void finish() {
+    flush();
+    if (w == 0) drain_ring(p, bars, base, s, live);
+  }
   // this warp's slots of the next `count`
   __device__ __forceinline__ void slots(uint32_t count, int tile, const TileSource& src, bool is_k) {
     const int n = is_k ? min(2, max(0, src.n - 2 * rank)) : 2;
@@ -950,7 +966,7 @@ __device__ __forceinline__ void produce_codes(const SharedParams& p, uint8_t* sm
         c.slots(8, tile, src, true);
       },
       [&](int tile, const TileSource& src) { c.slots(2u * (uint32_t)src.n, tile, src, false); });
-  c.flush();
+  c.finish();
 }
 
 // Producer warp w of a CTA: every kProducers-th slot of the ring. What a tile's
@@ -1066,6 +1082,7 @@ __device__ __forceinline__ void produce_role(const SharedParams& p, uint8_t* sm,
   };
   if (walk.left <= 0) return;
   produce_tiles(walk, look, keys, values);
+  if (w == 0) drain_ring(p, bars, base, s, live);
 }
 
 // Q of this CTA's query: plain blocks by TMA, the rope block rotated and split
@@ -1131,6 +1148,7 @@ __device__ __forceinline__ void q_role(const SharedParams& p, uint8_t* sm, uint3
     if (live) warp_arrive_cluster(bar);
     ++seg;
   } while (walk.next());
+  if (t < 32 && live) wait_cluster_all_lanes(bars + 8 * bQEmpty, (seg & 1u) ^ 1u, p.flags);  // (as drain_ring)
 }
 
 // The pair's products, by a warp of CTA 0.
